@@ -96,7 +96,9 @@ typedef enum {
                                       without bias2, or missing with bias2)         */
   EVO_ERR_SCRATCH_LIMIT = 11,      /* evo_attn_bwd_noalloc: the problem needs more
                                       scratch than EVO_NOALLOC_SCRATCH_BYTES         */
-  EVO_ERR_BAD_LAYOUT = 12          /* a stride of evo_layout_t breaks its rules      */
+  EVO_ERR_BAD_LAYOUT = 12,         /* a stride of evo_layout_t breaks its rules      */
+  EVO_ERR_BAD_INDEX = 13           /* evo_seq.h: an offset, length or page index in
+                                      device memory is out of range                  */
 } evo_status_t;
 
 typedef enum { EVO_F16 = 0, EVO_BF16 = 1 } evo_dtype_t;
@@ -356,7 +358,8 @@ EVO_API evo_status_t evo_attn_bwd_status(const void* workspace, void* stream);
  * Synchronises `stream`, then reads and clears the fallback device status
  * word on the current device: EVO_OK, or EVO_ERR_DEVICE_TIMEOUT if some
  * kernel of a call given no status location of its own gave up on a bounded
- * wait since the last read (its outputs are then undefined).  EVO_ERR_CUDA
+ * wait since the last read (its outputs are then undefined), or
+ * EVO_ERR_BAD_INDEX if such a call of evo_seq.h met a bad index.  EVO_ERR_CUDA
  * if the synchronisation itself failed.
  */
 EVO_API evo_status_t evo_attn_device_status(void* stream);

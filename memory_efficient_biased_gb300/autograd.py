@@ -19,6 +19,7 @@ from typing import List, Optional
 import torch
 
 from . import evo_attn as E
+from . import evo_seq as Q
 
 
 def readable_in_place(t: torch.Tensor) -> bool:
@@ -74,3 +75,43 @@ def evoformer_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 
 # The pages' name for the same call.
 DS4Sci_EvoformerAttention = evoformer_attention
+
+
+def _packed_rows(t: torch.Tensor) -> torch.Tensor:
+    """``t`` itself where the library reads its token rows in place, else a packed copy."""
+    T, H, D = t.shape
+    ok = (D == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == D) and t.data_ptr() % 16 == 0
+    ok = ok and (T <= 1 or (t.stride(0) >= H * D and t.stride(0) % 8 == 0 and t.stride(0) < 1 << 36))
+    return t if ok else t.contiguous()
+
+
+class PromptAttentionFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, scale):
+        q, k, v = _packed_rows(q), _packed_rows(k), _packed_rows(v)
+        # rows in no sequence: zero, so that whatever reads them next is defined
+        out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+        out, lse = Q.evo_prompt_fwd(q, k, v, cu_seqlens, out=out, scale=scale)
+        ctx.save_for_backward(q, k, v, cu_seqlens, out, lse)
+        ctx.scale = scale
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, cu_seqlens, out, lse = ctx.saved_tensors
+        dq, dk, dv = (torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        Q.evo_prompt_bwd(q, k, v, cu_seqlens, out, lse, _packed_rows(dout), dq, dk, dv, scale=ctx.scale)
+        return dq, dk, dv, None, None
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     scale: Optional[float] = None) -> torch.Tensor:
+    """Causal attention within each of the packed sequences, differentiable: q [T, Hq, D],
+    k, v [T, Hkv, D] with Hq a multiple of Hkv, cu_seqlens int32 [B + 1] on the device; ``scale``
+    defaults to D^-1/2.  Rows in no sequence get zeros, and zero gradients.
+
+    Strided token rows (the parts of one fused projection) are read in place.  To capture the
+    backward into a CUDA graph, run the forward inside the same capture, on the stream that is
+    being captured: PyTorch ties the accumulation of a leaf's gradient to the stream on which
+    the leaf was first used, and a capture that meets another stream's work ends with an error."""
+    return PromptAttentionFunction.apply(q, k, v, cu_seqlens, scale)

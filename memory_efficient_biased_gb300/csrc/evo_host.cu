@@ -394,6 +394,21 @@ WsLayout ws_layout(const evo_shape_t& s, bool has_bias2, bool has_db1 = false, b
 
 }  // namespace
 
+bool host_encode(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz,
+                 CUtensorMapL2promotion l2) {
+  return encode_t(m, base, dt, rank, dims, strides, box, swz, l2);
+}
+
+evo_status_t host_device(int* sms, int** status) {
+  DeviceInfo* d = nullptr;
+  const evo_status_t st = check_device(&d);
+  if (st != EVO_OK) return st;
+  *sms = d->sms;
+  *status = d->status;
+  return EVO_OK;
+}
+
 int num_sms() {
   DeviceInfo* d = device_info(nullptr);
   return (d && d->sms > 0) ? d->sms : 148;
@@ -444,6 +459,7 @@ const char* evo_status_string(evo_status_t s) {
       return "backward workspace exceeds the fixed 16 MiB scratch of evo_attn_bwd_noalloc; use evo_attn_bwd";
     case EVO_ERR_BAD_LAYOUT:
       return "a stride breaks the layout rules (multiples of 8, rows must not overlap)";
+    case EVO_ERR_BAD_INDEX: return "an offset, length or page index in device memory is out of range";
   }
   return "unknown status";
 }
@@ -776,7 +792,7 @@ evo_status_t evo_attn_device_status(void* stream) {
   if (v != 0) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_evo_status, &zero, sizeof(int)) != cudaSuccess) return EVO_ERR_CUDA;
-    return EVO_ERR_DEVICE_TIMEOUT;
+    return v == kStatusBadIndex ? EVO_ERR_BAD_INDEX : EVO_ERR_DEVICE_TIMEOUT;
   }
   return EVO_OK;
 }

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "evo_attn.h"
+
 namespace evo {
 
 constexpr int kTile = 128;  // queries (and keys) per tile
@@ -154,6 +156,14 @@ cudaError_t launch_bwd_db1_partials(const BwdArgs& a, int DP, bool bf16, bool ha
 cudaError_t launch_bwd_db1_sum(const BwdArgs& a, bool bf16, cudaStream_t st);
 
 int num_sms();
+// Shared by the ABI's translation units: a tensor map of any rank (false: the detail text is
+// set), the current device checked and made current on this thread (its SM count and fallback
+// status word), and the status of a failed CUDA call.
+bool host_encode(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swz,
+                 CUtensorMapL2promotion l2);
+evo_status_t host_device(int* sms, int** status);
+evo_status_t cuda_fail(const char* what, cudaError_t e);
 cudaError_t launch_fwd(const FwdArgs& a, int DP, bool bf16, cudaStream_t st);
 // The single-query-tile forward (DP = 64 only), for the shapes the paired kernel cannot fit.
 cudaError_t launch_fwd_single(const FwdArgs& a, bool bf16, cudaStream_t st);

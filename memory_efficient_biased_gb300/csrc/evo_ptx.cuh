@@ -10,7 +10,7 @@
 namespace evo {
 
 // Device status codes written by kernels (match evo_status_t).
-constexpr int kStatusTimeout = 8;
+constexpr int kStatusTimeout = 8, kStatusBadIndex = 13;
 
 // Shared-memory offsets of a ring of equally sized buffers: ring[s] = base + s·stride.
 // (Arithmetic rather than an array, so that a run-time stage index never forces

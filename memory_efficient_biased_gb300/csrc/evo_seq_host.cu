@@ -1,0 +1,401 @@
+// evo_seq_host.cu — the C ABI of the causal-sequence operators (include/evo_seq.h):
+// argument validation, workspace sizes and dispatch to the kernels.
+#include <cmath>
+#include <cstdint>
+#include <limits>
+
+#include "evo_seq.h"
+#include "evo_seq_internal.h"
+
+namespace evo {
+namespace {
+
+constexpr uint64_t kDefaultWaitNs = 2000000000ull;
+constexpr int64_t kMaxStride = int64_t(1) << 36;
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct Opts {
+  float scale = 0.0f;
+  uint64_t wait_ns = kDefaultWaitNs;
+  int* status = nullptr;
+};
+bool read_opts(const evo_seq_options_t* o, Opts* c) {
+  if (!o) return true;
+  if (o->size < sizeof(evo_seq_options_t) || o->flags != 0 || o->reserved != 0) return false;
+  if (o->scale != 0.0f && !(std::isfinite(o->scale) && o->scale > 0.0f)) return false;
+  c->scale = o->scale;
+  if (o->wait_limit_ns) c->wait_ns = o->wait_limit_ns < 1000 ? 1000 : o->wait_limit_ns;
+  c->status = o->status;
+  return true;
+}
+
+// needs_q: the call has query heads (every one but append and evict)
+evo_status_t check_seq_shape(const evo_seq_shape_t& s, bool needs_q) {
+  if (s.tokens < 0 || s.seqs < 0 || s.tokens > (int64_t(1) << 31) - 1024 || s.seqs > 65535) return EVO_ERR_BAD_SHAPE;
+  if (s.kv_heads < 1 || s.kv_heads > 16384 || s.head_dim < 8 || s.head_dim > 128 || s.head_dim % 8)
+    return EVO_ERR_BAD_SHAPE;
+  if (!needs_q) return EVO_OK;
+  if (s.q_heads < 1 || s.q_heads > 65535 || s.q_heads % s.kv_heads || s.q_heads / s.kv_heads > 128)
+    return EVO_ERR_BAD_SHAPE;
+  return EVO_OK;
+}
+
+evo_status_t check_cache(const evo_cache_shape_t& c, const evo_seq_shape_t& s, int64_t* k_page, int64_t* v_page) {
+  const bool page_ok = c.page_size == 16 || c.page_size == 32 || c.page_size == 64 ||
+                       (c.page_size >= 128 && c.page_size <= 1024 && c.page_size % 128 == 0);
+  if (!page_ok || c.num_pages < 1 || c.num_pages > (int64_t(1) << 31) - 2 || c.pages_per_seq < 1 ||
+      c.pages_per_seq > (int64_t(1) << 31) - 1)
+    return EVO_ERR_BAD_SHAPE;
+  const int64_t packed = c.page_size * s.kv_heads * s.head_dim;
+  *k_page = c.k_page_stride ? c.k_page_stride : packed;
+  *v_page = c.v_page_stride ? c.v_page_stride : packed;
+  for (int64_t p : {*k_page, *v_page})
+    if (p < packed || p % 8 || p >= kMaxStride) return EVO_ERR_BAD_LAYOUT;
+  return EVO_OK;
+}
+
+bool stride_ok(int64_t given, int64_t packed, long long* out) {
+  *out = given ? given : packed;
+  return given == 0 || (given >= packed && given % 8 == 0 && given < kMaxStride);
+}
+
+// The [tokens, heads, head_dim] tensors' token strides of one call.
+struct Strides {
+  long long q, k, v, out, dout, dq, dk, dv;
+};
+bool read_strides(const evo_seq_strides_t* g, const evo_seq_shape_t& s, Strides* o) {
+  const evo_seq_strides_t z{};
+  const evo_seq_strides_t& i = g ? *g : z;
+  const int64_t nq = s.q_heads * s.head_dim, nk = s.kv_heads * s.head_dim;
+  return stride_ok(i.q, nq, &o->q) && stride_ok(i.k, nk, &o->k) && stride_ok(i.v, nk, &o->v) &&
+         stride_ok(i.out, nq, &o->out) && stride_ok(i.dout, nq, &o->dout) && stride_ok(i.dq, nq, &o->dq) &&
+         stride_ok(i.dk, nk, &o->dk) && stride_ok(i.dv, nk, &o->dv);
+}
+
+// Address ranges: an output may overlap neither an input nor another output.  A strided
+// tensor is `rows` pieces of `piece` bytes, `step` bytes apart; two with the same step may
+// interleave (the parts of one projection, keys and values next to each other in a page).
+struct Span {
+  const void* p;
+  size_t bytes;  // from the first byte to one past the last
+  int64_t step, piece;
+};
+Span flat(const void* p, size_t bytes) { return {p, bytes, 0, 0}; }
+Span strided(const void* p, int64_t rows, int64_t step, int64_t piece) {  // in elements of two bytes
+  return {p, rows > 0 ? (size_t(rows - 1) * size_t(step) + size_t(piece)) * 2 : 0, step * 2, piece * 2};
+}
+bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  if (!(a0 < b0 + b.bytes && b0 < a0 + a.bytes)) return false;
+  if (a.step == 0 || a.step != b.step) return true;
+  const int64_t d = static_cast<int64_t>(b0 - a0), r = ((d % a.step) + a.step) % a.step;
+  return !(r >= a.piece && r + b.piece <= a.step);
+}
+template <int NI, int NO>
+bool aliased(const Span (&in)[NI], const Span (&out)[NO]) {
+  for (int o = 0; o < NO; ++o) {
+    for (int i = 0; i < NI; ++i)
+      if (overlap(out[o], in[i])) return true;
+    for (int p = 0; p < o; ++p)
+      if (overlap(out[o], out[p])) return true;
+  }
+  return false;
+}
+Span pages(const void* p, const evo_cache_shape_t& c, const evo_seq_shape_t& s, int64_t stride) {
+  return strided(p, c.num_pages, stride, c.page_size * s.kv_heads * s.head_dim);
+}
+
+SeqDesc desc(const evo_seq_shape_t& s, const int32_t* cu, const int32_t* lens, const int32_t* table,
+             const evo_cache_shape_t* c, int64_t weights_len, int* status) {
+  SeqDesc d{};
+  d.cu = cu;
+  d.seq_lens = lens;
+  d.table = table;
+  d.tokens = static_cast<int>(s.tokens);
+  d.seqs = static_cast<int>(s.seqs);
+  d.q_heads = static_cast<int>(s.q_heads);
+  d.kv_heads = static_cast<int>(s.kv_heads);
+  d.group = s.kv_heads ? static_cast<int>(s.q_heads / s.kv_heads) : 0;
+  d.D = static_cast<int>(s.head_dim);
+  int64_t most = d.tokens;
+  if (c) {
+    d.page = static_cast<int>(c->page_size);
+    d.pages_per_seq = static_cast<int>(c->pages_per_seq);
+    d.num_pages = static_cast<int>(c->num_pages);
+    most = c->page_size * c->pages_per_seq;
+    if (weights_len >= 0 && weights_len < most) most = weights_len;
+    const int64_t lim = std::numeric_limits<int>::max() - 1024;
+    if (most > lim) most = lim;
+  }
+  d.max_kv = static_cast<int>(most);
+  d.status = status;
+  return d;
+}
+
+float scale_of(const Opts& o, const evo_seq_shape_t& s) {
+  return o.scale != 0.0f ? o.scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(s.head_dim)));
+}
+
+}  // namespace
+}  // namespace evo
+
+using namespace evo;
+
+extern "C" {
+
+size_t evo_prompt_fwd_workspace_bytes(evo_seq_shape_t shape) {
+  if (check_seq_shape(shape, true) != EVO_OK) return 0;
+  return 256;
+}
+
+size_t evo_prompt_bwd_workspace_bytes(evo_seq_shape_t shape) {
+  if (check_seq_shape(shape, true) != EVO_OK) return 0;
+  return 256 + round256(size_t(shape.tokens) * shape.q_heads * 4);
+}
+
+size_t evo_paged_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache_shape_t cache) {
+  int64_t a, b;
+  if (check_seq_shape(shape, true) != EVO_OK || check_cache(cache, shape, &a, &b) != EVO_OK) return 0;
+  return 256;
+}
+
+evo_status_t evo_prompt_fwd(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, void* out,
+                            float* lse, void* workspace, size_t workspace_bytes, evo_seq_shape_t shape,
+                            evo_dtype_t dtype, const evo_seq_strides_t* strides, const evo_seq_options_t* opts,
+                            void* stream) {
+  Opts o;
+  if (!read_opts(opts, &o)) return EVO_ERR_BAD_ARGUMENT;
+  if (dtype != EVO_F16 && dtype != EVO_BF16) return EVO_ERR_BAD_DTYPE;
+  evo_status_t st = check_seq_shape(shape, true);
+  if (st != EVO_OK) return st;
+  Strides t;
+  if (!read_strides(strides, shape, &t)) return EVO_ERR_BAD_LAYOUT;
+  if (shape.tokens == 0 || shape.seqs == 0) return EVO_OK;
+  if (!q || !k || !v || !cu_seqlens || !out || !lse || !workspace) return EVO_ERR_NULL_POINTER;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_seqlens, 4) ||
+      !aligned(lse, 4) || !aligned(workspace, 256) || !aligned(o.status, 4))
+    return EVO_ERR_MISALIGNED;
+  if (workspace_bytes < evo_prompt_fwd_workspace_bytes(shape)) return EVO_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t T = shape.tokens, nq = shape.q_heads * shape.head_dim, nk = shape.kv_heads * shape.head_dim;
+  const Span in[] = {strided(q, T, t.q, nq), strided(k, T, t.k, nk), strided(v, T, t.v, nk),
+                     flat(cu_seqlens, size_t(shape.seqs + 1) * 4)};
+  const Span outs[] = {strided(out, T, t.out, nq), flat(lse, size_t(T) * shape.q_heads * 4),
+                       flat(workspace, workspace_bytes)};
+  if (aliased(in, outs)) return EVO_ERR_ALIASING;
+  int sms = 0;
+  int* fallback = nullptr;
+  if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
+  SeqAttnArgs a{};
+  a.s = desc(shape, cu_seqlens, nullptr, nullptr, nullptr, -1, o.status ? o.status : fallback);
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.q_stride = t.q, a.k_stride = t.k, a.v_stride = t.v, a.out_stride = t.out;
+  a.scale = scale_of(o, shape);
+  a.wait_ns = o.wait_ns;
+  const cudaError_t e = launch_seq_fwd(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EVO_OK : cuda_fail("prompt forward launch", e);
+}
+
+evo_status_t evo_prompt_bwd(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, const void* out,
+                            const float* lse, const void* dout, void* dq, void* dk, void* dv, void* workspace,
+                            size_t workspace_bytes, evo_seq_shape_t shape, evo_dtype_t dtype,
+                            const evo_seq_strides_t* strides, const evo_seq_options_t* opts, void* stream) {
+  Opts o;
+  if (!read_opts(opts, &o)) return EVO_ERR_BAD_ARGUMENT;
+  if (dtype != EVO_F16 && dtype != EVO_BF16) return EVO_ERR_BAD_DTYPE;
+  evo_status_t st = check_seq_shape(shape, true);
+  if (st != EVO_OK) return st;
+  Strides t;
+  if (!read_strides(strides, shape, &t)) return EVO_ERR_BAD_LAYOUT;
+  if (shape.tokens == 0 || shape.seqs == 0) return EVO_OK;
+  if (!q || !k || !v || !cu_seqlens || !out || !lse || !dout || !dq || !dk || !dv || !workspace)
+    return EVO_ERR_NULL_POINTER;
+  for (const void* p : {q, k, v, out, dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                        static_cast<const void*>(dv)})
+    if (!aligned(p, 16)) return EVO_ERR_MISALIGNED;
+  if (!aligned(cu_seqlens, 4) || !aligned(lse, 4) || !aligned(workspace, 256) || !aligned(o.status, 4))
+    return EVO_ERR_MISALIGNED;
+  if (workspace_bytes < evo_prompt_bwd_workspace_bytes(shape)) return EVO_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t T = shape.tokens, nq = shape.q_heads * shape.head_dim, nk = shape.kv_heads * shape.head_dim;
+  const Span in[] = {strided(q, T, t.q, nq),       strided(k, T, t.k, nk),
+                     strided(v, T, t.v, nk),       flat(cu_seqlens, size_t(shape.seqs + 1) * 4),
+                     strided(out, T, t.out, nq),   flat(lse, size_t(T) * shape.q_heads * 4),
+                     strided(dout, T, t.dout, nq)};
+  const Span outs[] = {strided(dq, T, t.dq, nq), strided(dk, T, t.dk, nk), strided(dv, T, t.dv, nk),
+                       flat(workspace, workspace_bytes)};
+  if (aliased(in, outs)) return EVO_ERR_ALIASING;
+  int sms = 0;
+  int* fallback = nullptr;
+  if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
+  SeqAttnArgs a{};
+  a.s = desc(shape, cu_seqlens, nullptr, nullptr, nullptr, -1, o.status ? o.status : fallback);
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.out = static_cast<uint16_t*>(const_cast<void*>(out));
+  a.lse = const_cast<float*>(lse);
+  a.dout = static_cast<const uint16_t*>(dout);
+  a.dq = static_cast<uint16_t*>(dq);
+  a.dk = static_cast<uint16_t*>(dk);
+  a.dv = static_cast<uint16_t*>(dv);
+  a.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  a.q_stride = t.q, a.k_stride = t.k, a.v_stride = t.v, a.out_stride = t.out, a.dout_stride = t.dout;
+  a.dq_stride = t.dq, a.dk_stride = t.dk, a.dv_stride = t.dv;
+  a.scale = scale_of(o, shape);
+  a.wait_ns = o.wait_ns;
+  const cudaError_t e = launch_prompt_bwd(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EVO_OK : cuda_fail("prompt backward launch", e);
+}
+
+evo_status_t evo_cache_append(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                              const int32_t* block_table, void* k_pages, void* v_pages, evo_seq_shape_t shape,
+                              evo_cache_shape_t cache, evo_dtype_t dtype, const evo_seq_strides_t* strides,
+                              const evo_seq_options_t* opts, void* stream) {
+  Opts o;
+  if (!read_opts(opts, &o)) return EVO_ERR_BAD_ARGUMENT;
+  if (dtype != EVO_F16 && dtype != EVO_BF16) return EVO_ERR_BAD_DTYPE;
+  evo_status_t st = check_seq_shape(shape, false);
+  if (st != EVO_OK) return st;
+  shape.q_heads = shape.kv_heads;
+  Strides t;
+  int64_t kp, vp;
+  if ((st = check_cache(cache, shape, &kp, &vp)) != EVO_OK) return st;
+  evo_seq_strides_t only{};
+  if (strides) only.k = strides->k, only.v = strides->v;
+  if (!read_strides(&only, shape, &t)) return EVO_ERR_BAD_LAYOUT;
+  if (shape.tokens == 0 || shape.seqs == 0) return EVO_OK;
+  if (!k || !v || !cu_seqlens || !seq_lens || !block_table || !k_pages || !v_pages) return EVO_ERR_NULL_POINTER;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) ||
+      !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(o.status, 4))
+    return EVO_ERR_MISALIGNED;
+  const int64_t nk = shape.kv_heads * shape.head_dim;
+  const Span in[] = {strided(k, shape.tokens, t.k, nk), strided(v, shape.tokens, t.v, nk),
+                     flat(cu_seqlens, size_t(shape.seqs + 1) * 4), flat(seq_lens, size_t(shape.seqs) * 4),
+                     flat(block_table, size_t(shape.seqs) * size_t(cache.pages_per_seq) * 4)};
+  const Span ks[] = {pages(k_pages, cache, shape, kp)}, vs[] = {pages(v_pages, cache, shape, vp)};
+  if (aliased(in, ks) || aliased(in, vs) || overlap(ks[0], vs[0]))
+    return EVO_ERR_ALIASING;
+  int sms = 0;
+  int* fallback = nullptr;
+  if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
+  AppendArgs a{};
+  a.s = desc(shape, cu_seqlens, seq_lens, block_table, &cache, -1, o.status ? o.status : fallback);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.k_pages = static_cast<uint16_t*>(k_pages);
+  a.v_pages = static_cast<uint16_t*>(v_pages);
+  a.k_stride = t.k, a.v_stride = t.v, a.k_page = kp, a.v_page = vp;
+  const cudaError_t e = launch_cache_append(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EVO_OK : cuda_fail("cache append launch", e);
+}
+
+evo_status_t evo_paged_fwd(const void* q, const void* k_pages, const void* v_pages, const int32_t* cu_seqlens,
+                           const int32_t* seq_lens, const int32_t* block_table, void* out, float* lse,
+                           float* weights, int64_t weights_len, void* workspace, size_t workspace_bytes,
+                           evo_seq_shape_t shape, evo_cache_shape_t cache, evo_dtype_t dtype,
+                           const evo_seq_strides_t* strides, const evo_seq_options_t* opts, void* stream) {
+  Opts o;
+  if (!read_opts(opts, &o)) return EVO_ERR_BAD_ARGUMENT;
+  if (dtype != EVO_F16 && dtype != EVO_BF16) return EVO_ERR_BAD_DTYPE;
+  evo_status_t st = check_seq_shape(shape, true);
+  if (st != EVO_OK) return st;
+  int64_t kp, vp;
+  if ((st = check_cache(cache, shape, &kp, &vp)) != EVO_OK) return st;
+  if (weights && (weights_len < 1 || weights_len > (int64_t(1) << 40))) return EVO_ERR_BAD_SHAPE;
+  evo_seq_strides_t only{};
+  if (strides) only.q = strides->q, only.out = strides->out;
+  Strides t;
+  if (!read_strides(&only, shape, &t)) return EVO_ERR_BAD_LAYOUT;
+  if (shape.tokens == 0 || shape.seqs == 0) return EVO_OK;
+  if (!q || !k_pages || !v_pages || !cu_seqlens || !seq_lens || !block_table || !out || !lse || !workspace)
+    return EVO_ERR_NULL_POINTER;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
+      !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(lse, 4) ||
+      !aligned(weights, 4) || !aligned(workspace, 256) || !aligned(o.status, 4))
+    return EVO_ERR_MISALIGNED;
+  if (workspace_bytes < evo_paged_fwd_workspace_bytes(shape, cache)) return EVO_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t T = shape.tokens, nq = shape.q_heads * shape.head_dim;
+  const Span in[] = {strided(q, T, t.q, nq),
+                     pages(k_pages, cache, shape, kp),
+                     pages(v_pages, cache, shape, vp),
+                     flat(cu_seqlens, size_t(shape.seqs + 1) * 4),
+                     flat(seq_lens, size_t(shape.seqs) * 4),
+                     flat(block_table, size_t(shape.seqs) * size_t(cache.pages_per_seq) * 4)};
+  const Span outs[] = {strided(out, T, t.out, nq), flat(lse, size_t(T) * shape.q_heads * 4),
+                       flat(weights, weights ? size_t(shape.seqs) * shape.kv_heads * size_t(weights_len) * 4 : 0),
+                       flat(workspace, workspace_bytes)};
+  if (aliased(in, outs)) return EVO_ERR_ALIASING;
+  int sms = 0;
+  int* fallback = nullptr;
+  if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
+  SeqAttnArgs a{};
+  a.s = desc(shape, cu_seqlens, seq_lens, block_table, &cache, weights ? weights_len : -1,
+             o.status ? o.status : fallback);
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k_pages);
+  a.v = static_cast<const uint16_t*>(v_pages);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.weights = weights;
+  a.weights_len = weights_len;
+  a.q_stride = t.q, a.out_stride = t.out, a.k_page = kp, a.v_page = vp;
+  a.scale = scale_of(o, shape);
+  a.wait_ns = o.wait_ns;
+  cudaError_t e = launch_seq_fwd(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess && weights) e = launch_seq_weights(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EVO_OK : cuda_fail("paged forward launch", e);
+}
+
+evo_status_t evo_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table, int32_t* seq_lens,
+                             float* weights, int64_t weights_len, int32_t* kept, int64_t budget, int64_t recent,
+                             evo_seq_shape_t shape, evo_cache_shape_t cache, evo_dtype_t dtype,
+                             const evo_seq_options_t* opts, void* stream) {
+  Opts o;
+  if (!read_opts(opts, &o)) return EVO_ERR_BAD_ARGUMENT;
+  if (dtype != EVO_F16 && dtype != EVO_BF16) return EVO_ERR_BAD_DTYPE;
+  shape.tokens = 0;
+  evo_status_t st = check_seq_shape(shape, false);
+  if (st != EVO_OK) return st;
+  int64_t kp, vp;
+  if ((st = check_cache(cache, shape, &kp, &vp)) != EVO_OK) return st;
+  if (weights_len < 1 || weights_len > (int64_t(1) << 40)) return EVO_ERR_BAD_SHAPE;
+  if (budget < 1 || budget > (int64_t(1) << 30) || recent < 0 || recent > budget) return EVO_ERR_BAD_ARGUMENT;
+  if (shape.seqs == 0) return EVO_OK;
+  if (!k_pages || !v_pages || !block_table || !seq_lens || !weights || !kept) return EVO_ERR_NULL_POINTER;
+  if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(weights, 4) || !aligned(kept, 4) || !aligned(o.status, 4))
+    return EVO_ERR_MISALIGNED;
+  const Span in[] = {flat(block_table, size_t(shape.seqs) * size_t(cache.pages_per_seq) * 4)};
+  const Span small[] = {flat(seq_lens, size_t(shape.seqs) * 4),
+                        flat(weights, size_t(shape.seqs) * shape.kv_heads * size_t(weights_len) * 4),
+                        flat(kept, size_t(shape.seqs) * shape.kv_heads * size_t(budget) * 4)};
+  const Span ks[] = {pages(k_pages, cache, shape, kp)}, vs[] = {pages(v_pages, cache, shape, vp)};
+  if (aliased(in, small) || aliased(in, ks) || aliased(in, vs) || aliased(small, ks) || aliased(small, vs) ||
+      overlap(ks[0], vs[0]))
+    return EVO_ERR_ALIASING;
+  int sms = 0;
+  int* fallback = nullptr;
+  if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
+  EvictArgs a{};
+  a.s = desc(shape, nullptr, seq_lens, block_table, &cache, weights_len, o.status ? o.status : fallback);
+  a.k_pages = static_cast<uint16_t*>(k_pages);
+  a.v_pages = static_cast<uint16_t*>(v_pages);
+  a.k_page = kp, a.v_page = vp;
+  a.seq_lens = seq_lens;
+  a.weights = weights;
+  a.weights_len = weights_len;
+  a.kept = kept;
+  a.budget = static_cast<int>(budget);
+  a.recent = static_cast<int>(recent);
+  const cudaError_t e = launch_cache_evict(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EVO_OK : cuda_fail("cache evict launch", e);
+}
+
+}  // extern "C"

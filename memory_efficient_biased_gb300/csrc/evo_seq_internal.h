@@ -1,0 +1,112 @@
+// evo_seq_internal.h — what the kernels of the causal-sequence operators
+// (include/evo_seq.h) share: their arguments, and how a sequence is read from
+// the offsets, lengths and block table in device memory, which are checked here.
+#pragma once
+
+#include "evo_internal.h"
+#include "evo_ptx.cuh"
+
+namespace evo {
+
+constexpr float kSeqLog2e = 1.4426950408889634f;
+constexpr float kSeqLn2 = 0.6931471805599453f;
+
+// One call's sequences.  A prompt has no seq_lens and no table: its keys are its own rows.
+struct SeqDesc {
+  const int* cu;
+  const int* seq_lens;
+  const int* table;
+  int tokens, seqs;
+  int q_heads, kv_heads, group, D;
+  int page, pages_per_seq, num_pages;
+  int max_kv;  // longest length the table (and weights) can hold
+  int* status;
+};
+
+// Sequence b: first row, new tokens, length, position of its first new token.
+struct Seq {
+  int row0, n, kv, pos0;
+};
+
+__device__ __forceinline__ void report_bad_index(int* status) { atomicExch(status, kStatusBadIndex); }
+
+__device__ __forceinline__ Seq load_seq(const SeqDesc& d, int b) {
+  const int c0 = d.cu[b], c1 = d.cu[b + 1];
+  const int kv = d.seq_lens ? d.seq_lens[b] : c1 - c0;
+  if (c0 < 0 || c1 < c0 || c1 > d.tokens || kv < 0 || kv > d.max_kv) {
+    report_bad_index(d.status);
+    return Seq{0, 0, 0, 0};
+  }
+  return Seq{c0, c1 - c0, kv, kv - (c1 - c0)};
+}
+
+// Looks every sequence over (one block's threads): a row's search below may never meet a bad one.
+__device__ __forceinline__ void check_seqs(const SeqDesc& d) {
+  for (int b = threadIdx.x; b < d.seqs; b += blockDim.x) load_seq(d, b);
+}
+
+// The sequence that holds row t, or -1 (a row in front of the first or behind the last).
+__device__ __forceinline__ int find_seq(const SeqDesc& d, int t) {
+  int lo = 0, hi = d.seqs;  // the last b with cu[b] <= t
+  if (t < d.cu[0]) return -1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (d.cu[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo < d.seqs ? lo : -1;
+}
+
+// The page that holds place j of sequence b, or -1 (recorded) when the table's entry is bad.
+__device__ __forceinline__ int page_of(const SeqDesc& d, int b, int j) {
+  const int p = d.table[static_cast<size_t>(b) * d.pages_per_seq + j / d.page];
+  if (p < 0 || p >= d.num_pages) {
+    report_bad_index(d.status);
+    return -1;
+  }
+  return p;
+}
+
+struct AppendArgs {
+  SeqDesc s;
+  const uint16_t *k, *v;
+  uint16_t *k_pages, *v_pages;
+  long long k_stride, v_stride, k_page, v_page;
+};
+
+struct EvictArgs {
+  SeqDesc s;  // cu unused
+  uint16_t *k_pages, *v_pages;
+  long long k_page, v_page;
+  int* seq_lens;
+  float* weights;
+  long long weights_len;
+  int* kept;
+  int budget, recent;
+};
+
+// Plain pointers of one attention call; keys and values are token rows or pages.
+struct SeqAttnArgs {
+  SeqDesc s;
+  const uint16_t *q, *k, *v;
+  const uint16_t* dout;
+  uint16_t *out, *dq, *dk, *dv;
+  float* lse;
+  float* delta;
+  float* weights;
+  long long weights_len;
+  long long q_stride, k_stride, v_stride, out_stride, dout_stride, dq_stride, dk_stride, dv_stride;
+  long long k_page, v_page;
+  float scale;
+  uint64_t wait_ns;
+};
+
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
+cudaError_t launch_seq_fwd(const SeqAttnArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_seq_weights(const SeqAttnArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_prompt_bwd(const SeqAttnArgs& a, bool bf16, cudaStream_t st);
+
+}  // namespace evo

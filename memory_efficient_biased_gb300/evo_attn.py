@@ -30,14 +30,17 @@ STATUS_NAMES = {
     0: "EVO_OK", 1: "EVO_ERR_NULL_POINTER", 2: "EVO_ERR_BAD_SHAPE", 3: "EVO_ERR_BAD_DTYPE",
     4: "EVO_ERR_MISALIGNED", 5: "EVO_ERR_WORKSPACE_TOO_SMALL", 6: "EVO_ERR_ARCH", 7: "EVO_ERR_CUDA",
     8: "EVO_ERR_DEVICE_TIMEOUT", 9: "EVO_ERR_ALIASING", 10: "EVO_ERR_BAD_ARGUMENT",
-    11: "EVO_ERR_SCRATCH_LIMIT", 12: "EVO_ERR_BAD_LAYOUT",
+    11: "EVO_ERR_SCRATCH_LIMIT", 12: "EVO_ERR_BAD_LAYOUT", 13: "EVO_ERR_BAD_INDEX",
 }
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 EXPORTED = ("evo_attn_abi_version", "evo_status_string", "evo_attn_fwd", "evo_attn_bwd_workspace_bytes",
             "evo_attn_bwd", "evo_attn_device_status", "evo_attn_selftest_wait_timeout",
             "evo_attn_step_host_arena_bytes", "evo_attn_step_host", "evo_attn_bwd_noalloc", "evo_attn_bwd_ex",
             "evo_attn_last_error_detail", "evo_attn_fwd_strided", "evo_attn_bwd_strided", "evo_attn_fwd_opts",
-            "evo_attn_bwd_opts", "evo_attn_bwd_status")
+            "evo_attn_bwd_opts", "evo_attn_bwd_status",
+            # include/evo_seq.h, bound in evo_seq.py
+            "evo_prompt_fwd_workspace_bytes", "evo_prompt_bwd_workspace_bytes", "evo_paged_fwd_workspace_bytes",
+            "evo_prompt_fwd", "evo_prompt_bwd", "evo_cache_append", "evo_paged_fwd", "evo_cache_evict")
 OPT_SKIP_MASKED_TILES, OPT_NO_DBIAS2 = 1, 2  # evo_options_t flags
 
 _DTYPE_CODE = {torch.float16: 0, torch.bfloat16: 1}
