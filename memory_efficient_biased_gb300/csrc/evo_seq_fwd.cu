@@ -1,0 +1,669 @@
+// evo_seq_fwd.cu — attention over causal sequences (include/evo_seq.h) on the tensor
+// cores: packed prompts, and chunks of new tokens over a paged cache.
+//
+// Mathematics, per row (token, head): S = q·kᵀ, m the running reference of s·log2e·S,
+// P = 2^(s·log2e·S - m), l = Σ P and O = Σ P v over the key tiles seen so far; at the end
+// O / l and lse = ln2·(m + log2 l).  m follows a tile's maximum only when that passes it by
+// more than 2^8 (P stays below 256), so O in tensor memory is rescaled rarely.
+//
+// Rows.  A query tile holds floor(128 / G) tokens with all G heads of their group, token by
+// token: the heads of a group share the K and V tiles, single tokens fill as much of a
+// tile as they can, and a causal border is as tight as with one head.  An item is two such
+// tiles (tile g worked on by warpgroup g) over the key tiles of 128 that they see; items are
+// shared out by evo_seq_sched.cuh.
+//
+// Roles (12 warps, one CTA per SM, persistent over its share of the work):
+//   warps 0-3, 4-7  softmax of tile 0 and 1, one thread per row
+//   warp 8          producer: Q tiles, and K and V tiles into one ring, by TMA; a cache's pages
+//                   are rows of a 4-D map, one box per page (its lanes look up the table)
+//   warps 9, 10     one MMA thread per tile: S_g = Q_g Kᵀ, then O_g += P_g V; the two tiles
+//                   alternate on the tensor core, each tile's MMAs run under the other's softmax
+//   warp 11         the walk over the work (descriptors in a ring), and every V tile's release:
+//                   rows that no query of the item sees are cleared in the item's last tile
+//                   (whatever lies behind a sequence, NaN included, must not reach 0·V)
+// Tensor memory (512 columns): S_0, S_1 (128 each, P in place of S as packed pairs), O_0, O_1.
+//
+// A value of V that is not finite and that only some rows of the item see (a later token of
+// the same tile) is taken out of the tile and added back to the rows that see it at the end.
+#include "evo_seq_internal.h"
+#include "evo_seq_sched.cuh"
+
+namespace evo {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kWalkWarp = 11;
+constexpr uint32_t kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
+static_assert(128 * kRegsOther + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split exceeds the launch");
+constexpr float kMoveLog2 = 8.0f;  // the reference moves only past this margin
+constexpr int kDescs = 4, kReady = 8, kMaxSlots = 10;
+static_assert(kReady >= kMaxSlots / 2 + 1, "a V tile's release must not lap the MMA threads");
+
+struct Bars {
+  uint64_t desc_full[kDescs], desc_empty[kDescs];
+  uint64_t q_full, q_empty;
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t v_ready[kReady];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], drain[2];
+  Work work[kDescs];
+  int dirty[kDescs];  // a V tile of the item held values that were taken out
+  uint32_t tmem_slot;
+  int abort;
+};
+
+template <int DP>
+struct Layout {
+  static constexpr uint32_t kHalf = kTile * 128u;            // 64 features of 128 rows
+  static constexpr uint32_t kTB = kTile * DP * 2u;           // one tile
+  static constexpr int kSlots = DP == 128 ? 5 : 10;          // K and V tiles in flight: 160 KB
+  static constexpr uint32_t q = 0, ring = 2 * kTB, bars = ring + kSlots * kTB;
+  static constexpr uint32_t total = bars + ((sizeof(Bars) + 127) & ~127u);
+};
+static_assert(Layout<128>::total + 1024 <= 232448, "shared memory");
+
+__device__ __forceinline__ uint32_t col_s(uint32_t g) { return g * 128u; }
+__device__ __forceinline__ uint32_t col_o(uint32_t g) { return 256u + g * 128u; }
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const SeqFwdArgs& a) {
+  volatile int never = 0;
+  WaitGuard g{a.wait_ns, a.s.status, &never};
+  mbar_wait_inl(bar, parity, g);
+}
+
+// The next descriptor, read by every lane of a warp (or by one thread alone).
+template <bool WARP>
+__device__ __forceinline__ bool take(Bars* bars, uint32_t it, const WaitGuard& g, Work& w) {
+  const uint32_t s = it % kDescs;
+  const bool ok = WARP ? mbar_wait_warp_inl(smem_u32(&bars->desc_full[s]), (it / kDescs) & 1, g)
+                       : mbar_wait_inl(smem_u32(&bars->desc_full[s]), (it / kDescs) & 1, g);
+  if (!ok) return false;
+  w = bars->work[s];
+  return !w.stop;
+}
+__device__ __forceinline__ void give_back(Bars* bars, uint32_t it) {
+  mbar_arrive(smem_u32(&bars->desc_empty[it % kDescs]));
+}
+// Key tiles of tile g of the item: none when it has no token.
+__device__ __forceinline__ int tiles_of(const Work& w, int g, int TQ) {
+  if (g == 0 && w.nt > TQ) {
+    const int end = w.pos + TQ;
+    return end > 0 ? (end + kTile - 1) / kTile : 1;
+  }
+  return g * TQ < w.nt ? w.kt : 0;
+}
+
+// ------------------------------------------------------------ producer (one warp)
+template <int DP>
+__device__ __forceinline__ void producer(const SeqFwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
+  using L = Layout<DP>;
+  const SeqDesc& s = a.s;
+  const bool paged = s.table != nullptr;
+  const int box = paged ? (s.page < kTile ? s.page : kTile) : kTile;  // rows per copy
+  const int boxes = kTile / box;
+  const uint32_t qbytes = static_cast<uint32_t>(a.TQ * s.group) * 128u * (DP / 64);
+  uint32_t use = 0, it = 0, queries = 0;
+  Work w;
+  for (; take<true>(bars, it, g, w); ++it) {
+    __syncwarp();
+    if (lane == 0) give_back(bars, it);
+    if (!mbar_wait_warp_inl(smem_u32(&bars->q_empty), (it & 1) ^ 1, g)) break;
+    if (lane == 0) {
+      const uint32_t full = smem_u32(&bars->q_full);
+      const int tiles = w.nt > a.TQ ? 2 : 1;
+      mbar_arrive_expect_tx(full, tiles * qbytes);
+      for (int t = 0; t < tiles; ++t)
+        for (int h = 0; h < DP / 64; ++h)
+          tma_load_4d(smem_u32(base + L::q + t * L::kTB + h * L::kHalf), &a.tq, full, h * 64, 0, w.kvh,
+                      w.row0 + w.t0 + t * a.TQ);
+    }
+    ++queries;
+    // this lane's page of a tile (a page past the keys, or a bad one, reads as zeros)
+    auto page = [&](int j) -> int {
+      const int key = j * kTile + lane * box;
+      if (lane >= boxes || key >= w.kv_end) return s.num_pages;
+      const int p = page_of(s, w.b, key);
+      return p < 0 ? s.num_pages : p;
+    };
+    int mine = paged ? page(w.j0) : 0;
+    bool ok = true;
+    for (int j = w.j0; j < w.j1; ++j) {
+      const int cur = mine;
+      if (paged && j + 1 < w.j1) mine = page(j + 1);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv, ++use) {
+        const uint32_t slot = use % L::kSlots;
+        if (!mbar_wait_warp_inl(smem_u32(&bars->empty[slot]), ((use / L::kSlots) & 1) ^ 1, g)) { ok = false; break; }
+        const uint32_t full = smem_u32(&bars->full[slot]), dst = smem_u32(base + L::ring + slot * L::kTB);
+        if (lane == 0) mbar_arrive_expect_tx(full, L::kTB);
+        __syncwarp();
+        const CUtensorMap* m = kv ? &a.tv : &a.tk;
+        if (paged) {
+          if (lane < boxes)
+            for (int h = 0; h < DP / 64; ++h)
+              tma_load_4d(dst + h * L::kHalf + lane * box * 128, m, full, h * 64, w.kvh, (j * kTile) % s.page * (boxes == 1),
+                          cur);
+        } else if (lane < DP / 64) {
+          tma_load_3d(dst + lane * L::kHalf, m, full, lane * 64, w.kvh, w.row0 + j * kTile);
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok) break;
+  }
+  // every copy this warp started has landed before the CTA may exit
+  __syncwarp();
+  for (uint32_t x = use > L::kSlots ? use - L::kSlots : 0; x < use; ++x)
+    drain_wait(smem_u32(&bars->full[x % L::kSlots]), (x / L::kSlots) & 1, a);
+  if (queries > 0) drain_wait(smem_u32(&bars->q_full), (queries - 1) & 1, a);
+}
+
+// ------------------------------------------------------------ MMA (one thread per tile)
+template <int DP, bool BF16>
+__device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* bars, uint32_t tmem, uint32_t gq,
+                                    const WaitGuard& g) {
+  using L = Layout<DP>;
+  const int steps = (a.s.D + 15) / 16;  // of 16 features
+  const uint32_t id_s = idesc_f16(128, 128, BF16, false, false);
+  const uint32_t id_o = idesc_f16(128, steps * 16, BF16, false, true);
+  const uint64_t qd = smem_desc(smem_u32(base + L::q + gq * L::kTB), 16, 1024, kSwizzle128B);
+  uint32_t n = 0, u = 0, it = 0, own = 0;
+  bool ok = true;
+  Work w;
+  for (; ok && take<false>(bars, it, g, w); ++it) {
+    give_back(bars, it);
+    int mine = tiles_of(w, static_cast<int>(gq), a.TQ);
+    if (mine > w.j1) mine = w.j1;
+    if (!mbar_wait_inl(smem_u32(&bars->q_full), it & 1, g)) break;
+    tc_fence_after();
+    if (mine <= w.j0) mbar_arrive(smem_u32(&bars->q_empty));
+    for (int j = w.j0; j < w.j1; ++j, ++n) {
+      const uint32_t uk = 2 * n, uv = 2 * n + 1, ks = uk % L::kSlots, vs = uv % L::kSlots;
+      if (!mbar_wait_inl(smem_u32(&bars->full[ks]), (uk / L::kSlots) & 1, g)) { ok = false; break; }
+      if (j >= mine) {  // the other tile's
+        mbar_arrive(smem_u32(&bars->empty[ks]));
+        if (!mbar_wait_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
+        mbar_arrive(smem_u32(&bars->empty[vs]));
+        continue;
+      }
+      // S takes the place of the previous P, which its P·V must have read
+      if (u > 0 && !mbar_wait_inl(smem_u32(&bars->pv_done[gq]), (u - 1) & 1, g)) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t kd = smem_desc(smem_u32(base + L::ring + ks * L::kTB), 16, 1024, kSwizzle128B);
+      for (int k = 0; k < steps; ++k) {
+        const uint64_t o = (k & 3) * 2 + (k >> 2) * (L::kHalf / 16);
+        umma_ss(tmem + col_s(gq), qd + o, kd + o, id_s, k > 0);
+      }
+      umma_commit(smem_u32(&bars->s_full[gq]));
+      umma_commit(smem_u32(&bars->empty[ks]));
+      if (j == mine - 1) umma_commit(smem_u32(&bars->q_empty));
+      if (!mbar_wait_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
+      if (!mbar_wait_inl(smem_u32(&bars->full[vs]), (uv / L::kSlots) & 1, g)) { ok = false; break; }
+      if (!mbar_wait_inl(smem_u32(&bars->p_full[gq]), u & 1, g)) { ok = false; break; }
+      if (j == w.j0 && !mbar_wait_inl(smem_u32(&bars->o_free[gq]), (own & 1) ^ 1, g)) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t vd = smem_desc(smem_u32(base + L::ring + vs * L::kTB), L::kHalf, 1024, kSwizzle128B);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)  // 128 keys in steps of 16 (8 columns of packed pairs)
+        umma_ts(tmem + col_o(gq), tmem + col_s(gq) + k * 8, vd + k * (2048 / 16), id_o, (j > w.j0 || k > 0) ? 1u : 0u);
+      umma_commit(smem_u32(&bars->pv_done[gq]));
+      umma_commit(smem_u32(&bars->empty[vs]));
+      ++u;
+    }
+    if (mine > w.j0) ++own;
+  }
+  umma_commit(smem_u32(&bars->drain[gq]));
+  drain_wait(smem_u32(&bars->drain[gq]), 0, a);
+}
+
+// ------------------------------------------------------------ the walk, and V's release (one warp)
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_finite2(uint32_t x) {  // a mask of the halves that are not finite
+  constexpr uint32_t e = BF16 ? 0x7F80u : 0x7C00u;
+  return ((x & e) == e ? 0xffffu : 0u) | ((x & (e << 16)) == (e << 16) ? 0xffff0000u : 0u);
+}
+
+// Rows [from, to) of a V tile: values that are not finite become 0; true if there were any.
+template <int DP, bool BF16>
+__device__ __forceinline__ bool take_out(uint8_t* tile, int from, int to, int lane) {
+  constexpr int per = DP / 8;  // 16-byte chunks a row
+  bool found = false;
+#pragma unroll 4
+  for (int i = from * per + lane; i < to * per; i += 32) {
+    const int r = i / per, c = i % per;
+    uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * Layout<DP>::kHalf + r * 128 + (c & 7) * 16);
+    // (the swizzle permutes the chunks of a row among themselves: any order covers them)
+    uint4 x = *p;
+    const uint32_t m0 = not_finite2<BF16>(x.x), m1 = not_finite2<BF16>(x.y), m2 = not_finite2<BF16>(x.z),
+                   m3 = not_finite2<BF16>(x.w);
+    if (m0 | m1 | m2 | m3) {
+      x.x &= ~m0, x.y &= ~m1, x.z &= ~m2, x.w &= ~m3;
+      *p = x;
+      found = true;
+    }
+  }
+  return found;
+}
+
+template <int DP, bool BF16>
+__device__ __forceinline__ void walk(const SeqFwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
+  using L = Layout<DP>;
+  Walk walk;
+  walk.init(a.s, a.W, blockIdx.x, gridDim.x);
+  PieceRecord* rec = a.records + 2 * blockIdx.x;
+  if (lane < 2) rec[lane].used = 0;
+  __syncwarp();
+  Work ring[2];  // published, V tiles not yet released: the current item and the one after it
+  uint32_t pub = 0, n = 0;
+  bool more = true;
+  auto publish = [&](Work& w) -> bool {
+    w = walk.next();
+    const uint32_t s = pub % kDescs;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->desc_empty[s]), ((pub / kDescs) & 1) ^ 1, g)) return false;
+    if (lane == 0) {
+      bars->work[s] = w;
+      bars->dirty[s] = 0;
+      if (!w.stop && w.slot >= 0) rec[w.slot] = PieceRecord{1, w.j1 == w.kt, w.b, w.kvh, w.row0, w.t0, w.nt, 0};
+      mbar_arrive(smem_u32(&bars->desc_full[s]));
+    }
+    ++pub;
+    more = !w.stop;
+    return true;
+  };
+  if (!publish(ring[0])) return;
+  for (uint32_t it = 0; !ring[0].stop; ++it) {
+    ring[1].stop = 1;
+    if (more && !publish(ring[1])) return;
+    const Work w = ring[0];
+    for (int j = w.j0; j < w.j1; ++j, ++n) {
+      const uint32_t uv = 2 * n + 1, slot = uv % L::kSlots;
+      if (!mbar_wait_warp_inl(smem_u32(&bars->full[slot]), (uv / L::kSlots) & 1, g)) return;
+      const int last = w.kv_end - j * kTile;      // rows of the tile that some query sees
+      const int all = w.pos + 1 - j * kTile;      // ... that every query sees
+      if (last < kTile || all < last) {
+        uint8_t* tile = base + L::ring + slot * L::kTB;
+        if (all < (last < kTile ? last : kTile)) {
+          const bool found = take_out<DP, BF16>(tile, all > 0 ? all : 0, last < kTile ? last : kTile, lane);
+          if (__any_sync(0xffffffffu, found) && lane == 0) bars->dirty[it % kDescs] = 1;
+        }
+        for (int i = (last > 0 ? last : 0) * (DP / 8) + lane; i < kTile * (DP / 8); i += 32) {
+          const int r = i / (DP / 8), c = i % (DP / 8);
+          *reinterpret_cast<uint4*>(tile + (c >> 3) * L::kHalf + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(smem_u32(&bars->v_ready[n % kReady]));
+    }
+    ring[0] = ring[1];
+  }
+}
+
+// ------------------------------------------------------------ softmax (warps 0..7)
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+// Max of 32 scores (columns c0..), those past column `lim` taken out when MASK.
+template <bool MASK>
+__device__ __forceinline__ void chunk_max(uint32_t (&y)[32], int lim, float& mt) {
+  float mx[4] = {mt, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) {
+    if (MASK) {
+      if (x > lim) y[x] = 0xff800000u;
+      if (x + 1 > lim) y[x + 1] = 0xff800000u;
+    }
+    mx[(x >> 1) & 3] = max3(mx[(x >> 1) & 3], __uint_as_float(y[x]), __uint_as_float(y[x + 1]));
+  }
+  mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+// P = 2^(y·s - m) of 32 scores, packed, and their sum.
+template <bool BF16>
+__device__ __forceinline__ void chunk_exp(const uint32_t (&y)[32], float2 sl2, float2 nm2, uint32_t (&pp)[16], float2& rs) {
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) {
+    const float2 t = fma2(make_float2(__uint_as_float(y[x]), __uint_as_float(y[x + 1])), sl2, nm2);
+    const float p0 = ex2(t.x), p1 = ex2(t.y);
+    rs = add2(rs, make_float2(p0, p1));
+    pp[x >> 1] = pack2<BF16>(p0, p1);
+  }
+}
+
+// The values of V that were taken out of the item's tiles, added to a row that sees them
+// (features c0 .. c0 + 31 of the unscaled O; what is added is an infinity or a NaN).
+template <bool BF16>
+__device__ __forceinline__ void add_back(const SeqFwdArgs& a, const Work& w, int pos, int c0, uint32_t (&out)[32]) {
+  uint32_t x[32];  // indexed by a run-time column: kept apart from the caller's registers
+#pragma unroll
+  for (int c = 0; c < 32; ++c) x[c] = out[c];
+  const SeqDesc& s = a.s;
+  int from = w.pos + 1 > w.j0 * kTile ? w.pos + 1 : w.j0 * kTile;
+  if (from < 0) from = 0;
+  const int to = pos + 1 < w.j1 * kTile ? pos + 1 : w.j1 * kTile;
+  for (int j = from; j < to; ++j) {
+    const uint16_t* row;
+    if (s.table) {
+      const int p = page_of(s, w.b, j);
+      if (p < 0) continue;
+      row = a.v + p * a.v_page + (static_cast<long long>(j % s.page) * s.kv_heads + w.kvh) * s.D;
+    } else {
+      row = a.v + static_cast<long long>(w.row0 + j) * a.v_stride + static_cast<long long>(w.kvh) * s.D;
+    }
+#pragma unroll 1
+    for (int c = 0; c < 32 && c0 + c < s.D; ++c) {
+      const uint16_t v = row[c0 + c];
+      if (not_finite2<BF16>(v) & 0xffffu) x[c] = __float_as_uint(__uint_as_float(x[c]) + to_f32<BF16>(v));
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 32; ++c) out[c] = x[c];
+}
+
+template <int DP, bool BF16>
+__device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars* bars, uint32_t tmem,
+                                        const WaitGuard& g) {
+  const SeqDesc& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gq = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
+  const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+  const uint32_t scol = trow + col_s(gq), ocol = trow + col_o(gq);
+  const int dt = r / s.group, head = r % s.group;  // token within the tile, head within the group
+  const float scale_log2 = a.scale_log2;
+  const float2 sl2 = make_float2(scale_log2, scale_log2);
+  uint32_t u = 0, it = 0;
+  bool ok = true;
+  Work w;
+  for (; ok && take<true>(bars, it, g, w); ++it) {
+    int mine = tiles_of(w, gq, a.TQ);
+    if (mine > w.j1) mine = w.j1;
+    const int tok = gq * a.TQ + dt;              // token within the block
+    const bool live = dt < a.TQ && tok < w.nt;
+    const int pos = w.pos + tok;
+    float m = 0.0f, l = 0.0f;
+    bool have = false;
+    for (int j = w.j0; j < mine; ++j) {
+      if (!mbar_wait_warp_inl(smem_u32(&bars->s_full[gq]), u & 1, g)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t ya[64], yb[64];
+      uint32_t(&y0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[0]);
+      uint32_t(&y1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[32]);
+      uint32_t(&y2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&yb[0]);
+      uint32_t(&y3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&yb[32]);
+      float mt = -INFINITY;
+      tmem_ld64(scol, ya);
+      tmem_wait_ld(ya);
+      tmem_ld64(scol + 64, yb);
+      // the tile's first token sees the whole key tile: no row needs its mask
+      if (w.pos + gq * a.TQ >= j * kTile + kTile - 1) {
+        chunk_max<false>(y0, 0, mt);
+        chunk_max<false>(y1, 0, mt);
+        tmem_wait_ld(yb);
+        chunk_max<false>(y2, 0, mt);
+        chunk_max<false>(y3, 0, mt);
+      } else {
+        const int lim = pos - j * kTile;
+        chunk_max<true>(y0, lim, mt);
+        chunk_max<true>(y1, lim - 32, mt);
+        tmem_wait_ld(yb);
+        chunk_max<true>(y2, lim - 64, mt);
+        chunk_max<true>(y3, lim - 96, mt);
+      }
+      mt *= scale_log2;  // (a positive factor keeps the max)
+      bool moved = false;
+      float alpha = 1.0f;
+      if (mt != -INFINITY && (!have || mt > m + kMoveLog2)) {
+        moved = have;
+        alpha = have ? ex2(m - mt) : 1.0f;
+        m = mt;
+        have = true;
+      }
+      const float2 nm2 = make_float2(-m, -m);
+      float2 rs = make_float2(0.0f, 0.0f);
+      {
+        uint32_t pp[32];
+        uint32_t(&p0)[16] = *reinterpret_cast<uint32_t(*)[16]>(&pp[0]);
+        uint32_t(&p1)[16] = *reinterpret_cast<uint32_t(*)[16]>(&pp[16]);
+        chunk_exp<BF16>(y0, sl2, nm2, p0, rs);
+        chunk_exp<BF16>(y1, sl2, nm2, p1, rs);
+        tmem_st32(scol, pp);
+        chunk_exp<BF16>(y2, sl2, nm2, p0, rs);
+        chunk_exp<BF16>(y3, sl2, nm2, p1, rs);
+        tmem_st32(scol + 32, pp);
+      }
+      // O so far is complete: this tile's S was issued behind the previous P·V
+      if (j > w.j0 && __any_sync(0xffffffffu, moved)) {
+#pragma unroll 1
+        for (int c = 0; c < DP / 16; ++c) {
+          uint32_t x[16];
+          tmem_ld16(ocol + c * 16, x);
+          tmem_wait_ld(x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+          tmem_st16(ocol + c * 16, x);
+        }
+        l *= alpha;
+      }
+      l += rs.x + rs.y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[gq]));
+      ++u;
+    }
+    if (!ok) break;
+    const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * 256 + gq * 128 + r;
+    if (mine > w.j0) {
+      if (!mbar_wait_warp_inl(smem_u32(&bars->pv_done[gq]), (u - 1) & 1, g)) break;
+      tc_fence_after();
+      const bool dirty = bars->dirty[it % kDescs] != 0;
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const size_t row = static_cast<size_t>(w.row0) + w.t0 + tok;
+      const int h = w.kvh * s.group + head;
+      uint16_t* out = a.out + row * a.out_stride + static_cast<size_t>(h) * s.D;
+      float* part = a.part_o + prow * DP;
+#pragma unroll 1
+      for (int c = 0; c < s.D; c += 32) {
+        uint32_t x[32];
+        tmem_ld32(ocol + c, x);
+        tmem_wait_ld(x);
+        if (live) {
+          if (dirty) add_back<BF16>(a, w, pos, c, x);
+          if (w.slot < 0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float lo = __uint_as_float(x[e + 2 * i]) * inv, hi = __uint_as_float(x[e + 2 * i + 1]) * inv;
+                o[i] = l == 0.0f ? 0u : pack2<BF16>(lo, hi);
+              }
+              if (a.out32) {
+                if (c + e < s.D) st_global_32(out + c + e, o);
+              } else {
+                if (c + e < s.D) *reinterpret_cast<uint4*>(out + c + e) = make_uint4(o[0], o[1], o[2], o[3]);
+                if (c + e + 8 < s.D) *reinterpret_cast<uint4*>(out + c + e + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              const uint32_t(&o)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&x[e]);
+              st_global_32(part + c + e, o);
+            }
+          }
+        }
+        __syncwarp();  // the loads above are the whole warp's
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->o_free[gq]));
+      if (live && w.slot < 0)
+        a.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (m + lg2(l)) * kSeqLn2;
+    }
+    if (w.slot >= 0) a.part_ml[prow] = make_float2(m, l);
+    __syncwarp();
+    if (lane == 0) give_back(bars, it);
+  }
+}
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_constant__ SeqFwdArgs a) {
+  using L = Layout<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(base + L::bars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    bars->abort = 0;
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(smem_u32(&bars->desc_full[i]), 1);
+      mbar_init(smem_u32(&bars->desc_empty[i]), 11);  // producer, two MMA threads, eight softmax warps
+    }
+    mbar_init(smem_u32(&bars->q_full), 1);
+    mbar_init(smem_u32(&bars->q_empty), 2);
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(smem_u32(&bars->full[i]), 1);
+      mbar_init(smem_u32(&bars->empty[i]), 2);  // both MMA threads
+    }
+    for (int i = 0; i < kReady; ++i) mbar_init(smem_u32(&bars->v_ready[i]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars->s_full[i]), 1);
+      mbar_init(smem_u32(&bars->p_full[i]), 4);
+      mbar_init(smem_u32(&bars->pv_done[i]), 1);
+      mbar_init(smem_u32(&bars->o_free[i]), 4);
+      mbar_init(smem_u32(&bars->drain[i]), 1);
+    }
+    fence_barrier_init();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    tma_prefetch_desc(&a.tq);
+    tma_prefetch_desc(&a.tk);
+    tma_prefetch_desc(&a.tv);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&bars->tmem_slot), 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_slot;
+  const WaitGuard g{a.wait_ns, a.s.status, &bars->abort};
+  if (warp >= kProducerWarp) {
+    setmaxnreg_dec<kRegsOther>();
+    if (warp == kProducerWarp) {
+      producer<DP>(a, base, bars, g, lane);
+    } else if (warp == kWalkWarp) {
+      walk<DP, BF16>(a, base, bars, g, lane);
+    } else {
+      if (lane == 0) mma<DP, BF16>(a, base, bars, tmem, static_cast<uint32_t>(warp - kMmaWarp), g);
+      __syncwarp();
+    }
+  } else {
+    setmaxnreg_inc<kRegsSoftmax>();
+    softmax<DP, BF16>(a, base, bars, tmem, g);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ join
+// The pieces of an item that the borders between CTAs cut: the one that begins it (slot 1 of
+// CTA c), then slot 0 of c + 1, c + 2, ... up to its end, joined in that order.  One warp per row:
+// M = max m, l = Σ l 2^(m - M), O = Σ O 2^(m - M).
+constexpr int kJoinRows = 8;
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kJoinRows * 32) evo_seq_join_kernel(const __grid_constant__ SeqFwdArgs a, int ctas) {
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const PieceRecord first = a.records[2 * c0 + 1];
+  if (!first.used) return;
+  const SeqDesc& s = a.s;
+  int pieces = 1;
+  while (c0 + pieces < ctas) {
+    const PieceRecord p = a.records[2 * (c0 + pieces)];
+    if (!p.used) break;
+    ++pieces;
+    if (p.ends) break;
+  }
+  for (int i = blockIdx.y * kJoinRows + (threadIdx.x >> 5); i < 256; i += gridDim.y * kJoinRows) {
+    const int gq = i >> 7, r = i & 127, dt = r / s.group, tok = gq * a.TQ + dt;
+    if (dt >= a.TQ || tok >= first.nt) continue;
+    auto at = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * 256 + i; };
+    float big = -INFINITY;
+    for (int p = 0; p < pieces; ++p) {
+      const float2 ml = a.part_ml[at(p)];
+      if (ml.y != 0.0f) big = fmaxf(big, ml.x);
+    }
+    float o[DP / 32] = {};
+    float l = 0.0f;
+    for (int p = 0; p < pieces; ++p) {
+      const float2 ml = a.part_ml[at(p)];
+      if (ml.y == 0.0f) continue;
+      const float f = ex2(ml.x - big);
+      l += ml.y * f;
+      const float* x = a.part_o + at(p) * DP;
+#pragma unroll
+      for (int e = 0; e < DP / 32; ++e) {
+        const int d = lane + 32 * e;
+        if (d < s.D) o[e] = fmaf(x[d], f, o[e]);
+      }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const size_t row = static_cast<size_t>(first.row0) + first.t0 + tok;
+    const int h = first.kvh * s.group + r % s.group;
+    uint16_t* out = a.out + row * a.out_stride + static_cast<size_t>(h) * s.D;
+#pragma unroll
+    for (int e = 0; e < DP / 32; ++e) {
+      const int d = lane + 32 * e;
+      if (d < s.D) out[d] = l == 0.0f ? 0 : static_cast<uint16_t>(pack2<BF16>(o[e] * inv, 0.0f) & 0xffffu);
+    }
+    if (lane == 0) a.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
+  }
+}
+
+template <int DP, bool BF16>
+cudaError_t launch_t(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
+  auto kern = evo_seq_fwd_kernel<DP, BF16>;
+  static bool limit_set[64] = {};
+  cudaError_t e = ensure_smem_limit(kern, 232448, limit_set);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, kThreads, Layout<DP>::total + 1024, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  evo_seq_join_kernel<DP, BF16><<<dim3(ctas, 4), kJoinRows * 32, 0, st>>>(a, ctas);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws) {
+  const int DP = D <= 64 ? 64 : 128;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = ws ? ws + off : nullptr;
+    off += (bytes + 255) & ~size_t(255);
+    return p;
+  };
+  uint8_t* rec = take(size_t(ctas) * 2 * sizeof(PieceRecord));
+  uint8_t* ml = take(size_t(ctas) * 2 * 256 * sizeof(float2));
+  uint8_t* po = take(size_t(ctas) * 2 * 256 * DP * sizeof(float));
+  if (a) {
+    a->records = reinterpret_cast<PieceRecord*>(rec);
+    a->part_ml = reinterpret_cast<float2*>(ml);
+    a->part_o = reinterpret_cast<float*>(po);
+  }
+  return off;
+}
+
+cudaError_t launch_seq_fwd(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st) {
+  if (a.s.D <= 64) return bf16 ? launch_t<64, true>(a, ctas, st) : launch_t<64, false>(a, ctas, st);
+  return bf16 ? launch_t<128, true>(a, ctas, st) : launch_t<128, false>(a, ctas, st);
+}
+
+}  // namespace evo

@@ -136,8 +136,59 @@ SeqDesc desc(const evo_seq_shape_t& s, const int32_t* cu, const int32_t* lens, c
   return d;
 }
 
+// Tensor maps of the forward.
+bool encode16(CUtensorMap* m, const void* base, bool bf16, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box, int64_t D) {
+  // a head's row of more than 64 features is two boxes next to each other: one 256-byte line request
+  return host_encode(m, base, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, dims,
+                     strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                     D > 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+}
+// [tokens, kv_heads * group, D] as (D, group, kv_heads, tokens), box (64, group, 1, TQ).
+bool map_q(CUtensorMap* m, const void* p, bool bf16, const evo_seq_shape_t& s, int64_t stride, int TQ) {
+  const int64_t G = s.q_heads / s.kv_heads;
+  cuuint64_t dims[4] = {cuuint64_t(s.head_dim), cuuint64_t(G), cuuint64_t(s.kv_heads), cuuint64_t(s.tokens)};
+  cuuint64_t st[3] = {cuuint64_t(s.head_dim * 2), cuuint64_t(G * s.head_dim * 2), cuuint64_t(stride * 2)};
+  cuuint32_t box[4] = {64, cuuint32_t(G), 1, cuuint32_t(TQ)};
+  return encode16(m, p, bf16, 4, dims, st, box, s.head_dim);
+}
+// [tokens, kv_heads, D] as (D, kv_heads, tokens), box (64, 1, 128).
+bool map_rows(CUtensorMap* m, const void* p, bool bf16, const evo_seq_shape_t& s, int64_t stride) {
+  cuuint64_t dims[3] = {cuuint64_t(s.head_dim), cuuint64_t(s.kv_heads), cuuint64_t(s.tokens)};
+  cuuint64_t st[2] = {cuuint64_t(s.head_dim * 2), cuuint64_t(stride * 2)};
+  cuuint32_t box[3] = {64, 1, kTile};
+  return encode16(m, p, bf16, 3, dims, st, box, s.head_dim);
+}
+// [num_pages, page, kv_heads, D] as (D, kv_heads, page, num_pages), box (64, 1, min(page, 128), 1).
+bool map_pages(CUtensorMap* m, const void* p, bool bf16, const evo_seq_shape_t& s, const evo_cache_shape_t& c,
+               int64_t stride) {
+  cuuint64_t dims[4] = {cuuint64_t(s.head_dim), cuuint64_t(s.kv_heads), cuuint64_t(c.page_size), cuuint64_t(c.num_pages)};
+  cuuint64_t st[3] = {cuuint64_t(s.head_dim * 2), cuuint64_t(s.kv_heads * s.head_dim * 2), cuuint64_t(stride * 2)};
+  cuuint32_t box[4] = {64, 1, cuuint32_t(c.page_size < kTile ? c.page_size : kTile), 1};
+  return encode16(m, p, bf16, 4, dims, st, box, s.head_dim);
+}
+
 float scale_of(const Opts& o, const evo_seq_shape_t& s) {
   return o.scale != 0.0f ? o.scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(s.head_dim)));
+}
+
+// Fills what both forwards share and launches; K and V maps are the caller's.
+evo_status_t run_fwd(SeqFwdArgs& a, const void* q, const void* v, void* out, float* lse, void* workspace, int sms,
+                     const evo_seq_shape_t& s, bool bf16, const Strides& t, const Opts& o, cudaStream_t st) {
+  const int G = static_cast<int>(s.q_heads / s.kv_heads);
+  a.TQ = kTile / G;
+  a.W = 2 * a.TQ;
+  if (!map_q(&a.tq, q, bf16, s, t.q, a.TQ)) return EVO_ERR_CUDA;
+  a.out32 = aligned(out, 32) && t.out % 16 == 0 && s.head_dim % 16 == 0;
+  a.scale_log2 = scale_of(o, s) * kSeqLog2e;
+  a.v = static_cast<const uint16_t*>(v);
+  a.out = static_cast<uint16_t*>(out);
+  a.out_stride = t.out;
+  a.lse = lse;
+  a.wait_ns = o.wait_ns;
+  seq_fwd_workspace(sms, static_cast<int>(s.head_dim), &a, static_cast<uint8_t*>(workspace));
+  const cudaError_t e = launch_seq_fwd(a, sms, bf16, st);
+  return e == cudaSuccess ? EVO_OK : cuda_fail("sequence forward launch", e);
 }
 
 }  // namespace
@@ -149,7 +200,7 @@ extern "C" {
 
 size_t evo_prompt_fwd_workspace_bytes(evo_seq_shape_t shape) {
   if (check_seq_shape(shape, true) != EVO_OK) return 0;
-  return 256;
+  return seq_fwd_workspace(num_sms(), static_cast<int>(shape.head_dim), nullptr, nullptr);
 }
 
 size_t evo_prompt_bwd_workspace_bytes(evo_seq_shape_t shape) {
@@ -160,7 +211,7 @@ size_t evo_prompt_bwd_workspace_bytes(evo_seq_shape_t shape) {
 size_t evo_paged_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache_shape_t cache) {
   int64_t a, b;
   if (check_seq_shape(shape, true) != EVO_OK || check_cache(cache, shape, &a, &b) != EVO_OK) return 0;
-  return 256;
+  return seq_fwd_workspace(num_sms(), static_cast<int>(shape.head_dim), nullptr, nullptr);
 }
 
 evo_status_t evo_prompt_fwd(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, void* out,
@@ -189,18 +240,12 @@ evo_status_t evo_prompt_fwd(const void* q, const void* k, const void* v, const i
   int sms = 0;
   int* fallback = nullptr;
   if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
-  SeqAttnArgs a{};
+  SeqFwdArgs a{};
   a.s = desc(shape, cu_seqlens, nullptr, nullptr, nullptr, -1, o.status ? o.status : fallback);
-  a.q = static_cast<const uint16_t*>(q);
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
-  a.out = static_cast<uint16_t*>(out);
-  a.lse = lse;
-  a.q_stride = t.q, a.k_stride = t.k, a.v_stride = t.v, a.out_stride = t.out;
-  a.scale = scale_of(o, shape);
-  a.wait_ns = o.wait_ns;
-  const cudaError_t e = launch_seq_fwd(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? EVO_OK : cuda_fail("prompt forward launch", e);
+  const bool bf16 = dtype == EVO_BF16;
+  if (!map_rows(&a.tk, k, bf16, shape, t.k) || !map_rows(&a.tv, v, bf16, shape, t.v)) return EVO_ERR_CUDA;
+  a.v_stride = t.v;
+  return run_fwd(a, q, v, out, lse, workspace, sms, shape, bf16, t, o, static_cast<cudaStream_t>(stream));
 }
 
 evo_status_t evo_prompt_bwd(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, const void* out,
@@ -335,22 +380,26 @@ evo_status_t evo_paged_fwd(const void* q, const void* k_pages, const void* v_pag
   int sms = 0;
   int* fallback = nullptr;
   if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
-  SeqAttnArgs a{};
+  SeqFwdArgs a{};
   a.s = desc(shape, cu_seqlens, seq_lens, block_table, &cache, weights ? weights_len : -1,
              o.status ? o.status : fallback);
-  a.q = static_cast<const uint16_t*>(q);
-  a.k = static_cast<const uint16_t*>(k_pages);
-  a.v = static_cast<const uint16_t*>(v_pages);
-  a.out = static_cast<uint16_t*>(out);
-  a.lse = lse;
-  a.weights = weights;
-  a.weights_len = weights_len;
-  a.q_stride = t.q, a.out_stride = t.out, a.k_page = kp, a.v_page = vp;
-  a.scale = scale_of(o, shape);
-  a.wait_ns = o.wait_ns;
-  cudaError_t e = launch_seq_fwd(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess && weights) e = launch_seq_weights(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? EVO_OK : cuda_fail("paged forward launch", e);
+  const bool bf16 = dtype == EVO_BF16;
+  if (!map_pages(&a.tk, k_pages, bf16, shape, cache, kp) || !map_pages(&a.tv, v_pages, bf16, shape, cache, vp))
+    return EVO_ERR_CUDA;
+  a.v_page = vp;
+  st = run_fwd(a, q, v_pages, out, lse, workspace, sms, shape, bf16, t, o, static_cast<cudaStream_t>(stream));
+  if (st != EVO_OK || !weights) return st;
+  SeqAttnArgs w{};
+  w.s = a.s;
+  w.q = static_cast<const uint16_t*>(q);
+  w.k = static_cast<const uint16_t*>(k_pages);
+  w.lse = lse;
+  w.weights = weights;
+  w.weights_len = weights_len;
+  w.q_stride = t.q, w.k_page = kp;
+  w.scale = scale_of(o, shape);
+  const cudaError_t e = launch_seq_weights(w, bf16, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EVO_OK : cuda_fail("weight sums launch", e);
 }
 
 evo_status_t evo_cache_evict(void* k_pages, void* v_pages, const int32_t* block_table, int32_t* seq_lens,

@@ -103,9 +103,33 @@ struct SeqAttnArgs {
   uint64_t wait_ns;
 };
 
+struct PieceRecord;
+
+// The forward on the tensor cores.
+struct SeqFwdArgs {
+  CUtensorMap tq;       // q as (D, group, kv_heads, tokens), box (64, group, 1, TQ)
+  CUtensorMap tk, tv;   // prompt: (D, kv_heads, tokens), box (64, 1, 128); cache: (D, kv_heads, page, num_pages),
+                        // box (64, 1, min(page, 128), 1); 128-byte swizzle, zeros outside
+  SeqDesc s;
+  int TQ, W;            // tokens of a query tile (floor(128 / group)) and of an item (two tiles)
+  int out32;            // rows of out start at multiples of 32 bytes
+  float scale_log2;     // scale · log2 e
+  const uint16_t* v;    // plain pointer and strides of V, for what add_back reads
+  long long v_stride, v_page;
+  uint16_t* out;
+  long long out_stride;
+  float* lse;
+  PieceRecord* records;  // workspace: two per CTA
+  float2* part_ml;       // ... [ctas][2][256] (m, l)
+  float* part_o;         // ... [ctas][2][256][DP], not yet divided by l
+  uint64_t wait_ns;
+};
+// Bytes of the workspace for `ctas` CTAs; with a and ws, a's pointers into it.
+size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws);
+
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
-cudaError_t launch_seq_fwd(const SeqAttnArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_seq_fwd(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 cudaError_t launch_seq_weights(const SeqAttnArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_prompt_bwd(const SeqAttnArgs& a, bool bf16, cudaStream_t st);
 

@@ -54,39 +54,6 @@ __device__ __forceinline__ void load_key(const SeqAttnArgs& a, const uint16_t* b
     for (int e = 0; e < kMaxPerLane; ++e) x[e] = 0.0f;
 }
 
-template <bool BF16>
-__global__ void seq_fwd_simple(const SeqAttnArgs a) {
-  const SeqDesc& s = a.s;
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(s);
-  const int lane = threadIdx.x & 31, h = blockIdx.y;
-  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= s.tokens) return;
-  const int b = find_seq(s, t);
-  if (b < 0) return;
-  const Seq q = load_seq(s, b);
-  if (t < q.row0 || t >= q.row0 + q.n) return;
-  const int pos = q.pos0 + (t - q.row0), hk = h / s.group;
-  float qr[kMaxPerLane], kr[kMaxPerLane], o[kMaxPerLane] = {};
-  load_row<BF16>(a.q + t * a.q_stride + h * s.D, s.D, lane, qr);
-  float m = -INFINITY, l = 0.0f;
-  for (int j = 0; j <= pos; ++j) {
-    load_key<BF16>(a, a.k, a.k_stride, a.k_page, q, b, j, hk, lane, kr);
-    const float x = dot(qr, kr) * a.scale;
-    const float mn = fmaxf(m, x);
-    const float up = mn == -INFINITY ? 1.0f : expf(m - mn), p = mn == -INFINITY ? 0.0f : expf(x - mn);
-    load_key<BF16>(a, a.v, a.v_stride, a.v_page, q, b, j, hk, lane, kr);
-#pragma unroll
-    for (int e = 0; e < kMaxPerLane; ++e) o[e] = o[e] * up + p * kr[e];
-    l = l * up + p;
-    m = mn;
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int e = 0; e < kMaxPerLane; ++e) o[e] = l == 0.0f ? 0.0f : o[e] * inv;
-  store_row<BF16>(a.out + t * a.out_stride + h * s.D, s.D, lane, o);
-  if (lane == 0) a.lse[static_cast<size_t>(h) * s.tokens + t] = l == 0.0f ? -INFINITY : m + logf(l);
-}
-
 // weights[b][h][j] += Σ P: one warp per (b, h, j), rows in order.
 template <bool BF16>
 __global__ void seq_weights_simple(const SeqAttnArgs a) {
@@ -188,14 +155,6 @@ constexpr int kWarps = 8;
 dim3 rows_grid(const SeqDesc& s, int heads) { return dim3((s.tokens + kWarps - 1) / kWarps, heads); }
 
 }  // namespace
-
-cudaError_t launch_seq_fwd(const SeqAttnArgs& a, bool bf16, cudaStream_t st) {
-  if (bf16)
-    seq_fwd_simple<true><<<rows_grid(a.s, a.s.q_heads), kWarps * 32, 0, st>>>(a);
-  else
-    seq_fwd_simple<false><<<rows_grid(a.s, a.s.q_heads), kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_seq_weights(const SeqAttnArgs& a, bool bf16, cudaStream_t st) {
   const dim3 grid(256, a.s.kv_heads, a.s.seqs);
