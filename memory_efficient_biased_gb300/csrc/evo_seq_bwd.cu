@@ -1,0 +1,783 @@
+// evo_seq_bwd.cu — gradients of causal attention over packed prompts
+// (include/evo_seq.h) on the tensor cores.
+//
+// With P = 2^(s·log2e·S - log2e·lse) rebuilt from the saved lse, dP = dO·vᵀ,
+// dS = P∘(dP - delta) and delta = dO·O:
+//     dV = Σ Pᵀ dO     dK = s Σ dSᵀ q     dQ = s Σ dS k.
+// Five products per pair of tiles would do; here it is seven in two kernels, since dQ
+// gathers over key tiles what dK and dV gather over query tiles: in one kernel either its
+// sums (64 KB of fp32 per pair of tiles) go through L2 by atomics whose order changes the
+// result, or wait for one another.  Two kernels keep every sum in tensor memory, in a
+// fixed order, and P and dS (the MMAs' A operands) in tensor memory too.
+//
+//   evo_seq_rows_kernel  (lse·log2e, delta) per row, [tokens][q_heads]
+//   evo_seq_dkv_kernel   items: 128 keys of a kv head, over the tiles of queries that see
+//                        them (TQ tokens x the heads of the group, as in the forward, which sums
+//                        dK and dV over a group's heads for nothing); Sᵀ = K Qᵀ, dPᵀ = V dOᵀ, a
+//                        thread per key and half of the rows; dV += Pᵀ dO, dK += dSᵀ Q
+//   evo_seq_dq_kernel    items: one tile of queries over its key tiles; S = Q Kᵀ, dP = dO Vᵀ, a
+//                        thread per row and half of the keys; dQ += dS K
+// Work is shared out and cut items joined as in the forward (evo_seq_sched.cuh); pieces are
+// fp32 sums, added in order.
+//
+// Rounded to the input type: P and dS as MMA operands, and the results.
+#include "evo_seq_internal.h"
+#include "evo_seq_sched.cuh"
+
+#include <type_traits>
+
+namespace evo {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kRowsWarp = 10;  // and 11: the walk
+constexpr uint32_t kRegsLaunch = 168, kRegsCompute = 200, kRegsOther = 104;
+static_assert(128 * kRegsOther + 256 * kRegsCompute <= kThreads * kRegsLaunch, "register split exceeds the launch");
+constexpr int kDescs = 4, kReady = 4;
+// The streamed tiles: the one that is read twice (Q for dK, K for dQ: first by the scores, then by
+// the gradient) has three buffers, the other (dO, V) two: 160 KB with head_dim 128, and the
+// item's own two tiles 64 KB.
+constexpr int kASlots = 3, kBSlots = 2;
+
+struct Bars {
+  uint64_t desc_full[kDescs], desc_empty[kDescs];
+  uint64_t own_full, own_empty;                      // the item's own two tiles
+  uint64_t a_full[kASlots], a_empty[kASlots];        // streamed: Q or K
+  uint64_t b_full[kBSlots], b_empty[kBSlots];        // streamed: dO or V
+  uint64_t ready[kReady];                            // a pair of streamed tiles, cleaned
+  uint64_t rows_full[2], rows_empty[2];              // dK/dV: (lse, delta) of a tile of queries
+  uint64_t s_full[2], dp_full, p_ready, ds_ready;
+  uint64_t first_done, second_done;                  // P·dO has read P; dS·(Q or K) has read dS
+  uint64_t acc_full, acc_free, drain;
+  Work work[kDescs];
+  uint32_t tmem_slot;
+  int abort;
+};
+
+template <int DP>
+struct Layout {
+  static constexpr uint32_t kHalf = kTile * 128u;
+  static constexpr uint32_t kTB = kTile * DP * 2u;
+  static constexpr uint32_t own = 0, a = 2 * kTB, b = a + kASlots * kTB, rows = b + kBSlots * kTB,
+                            bars = rows + 2 * kTile * 8u;
+  static constexpr uint32_t total = bars + ((sizeof(Bars) + 127) & ~127u);
+};
+static_assert(Layout<128>::total <= 232448, "shared memory");
+
+// Tensor memory columns.  P and dS, as packed pairs, take the place of the scores they were
+// made from, each warpgroup's in its own half.
+constexpr uint32_t kColS = 0, kColDp = 128, kColV = 256, kColK = 384;   // dK/dV
+constexpr uint32_t kColDp2 = 256, kColQ = 384;                          // dQ: S in 0 and 128 by turns
+__device__ __forceinline__ uint32_t packed_col(int k) {  // 16 rows or keys from 16·k on
+  return k < 4 ? k * 8 : 64 + (k - 4) * 8;
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const SeqBwdArgs& a) {
+  volatile int never = 0;
+  WaitGuard g{a.wait_ns, a.s.status, &never};
+  mbar_wait_inl(bar, parity, g);
+}
+template <bool WARP>
+__device__ __forceinline__ bool take(Bars* bars, uint32_t it, const WaitGuard& g, Work& w) {
+  const uint32_t s = it % kDescs;
+  const bool ok = WARP ? mbar_wait_warp_inl(smem_u32(&bars->desc_full[s]), (it / kDescs) & 1, g)
+                       : mbar_wait_inl(smem_u32(&bars->desc_full[s]), (it / kDescs) & 1, g);
+  if (!ok) return false;
+  w = bars->work[s];
+  return !w.stop;
+}
+__device__ __forceinline__ void give_back(Bars* bars, uint32_t it) {
+  mbar_arrive(smem_u32(&bars->desc_empty[it % kDescs]));
+}
+
+// ------------------------------------------------------------ producer (one thread)
+template <int DP, bool DKV>
+__device__ __forceinline__ void producer(const SeqBwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g) {
+  using L = Layout<DP>;
+  constexpr int kHalves = DP / 64;
+  const uint32_t qbytes = static_cast<uint32_t>(a.TQ * a.s.group) * 128u * kHalves;
+  uint32_t n = 0, it = 0, own = 0, na = 0, nb = 0;
+  auto queries = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, const Work& w, int token) {
+    for (int h = 0; h < kHalves; ++h) tma_load_4d(dst + h * L::kHalf, m, bar, h * 64, 0, w.kvh, w.row0 + token);
+  };
+  auto keys = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, const Work& w, int token) {
+    for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * L::kHalf, m, bar, h * 64, w.kvh, w.row0 + token);
+  };
+  Work w;
+  bool ok = true;
+  for (; ok && take<false>(bars, it, g, w); ++it) {
+    give_back(bars, it);
+    for (int j = w.j0; j < w.j1; ++j, ++n) {
+      const uint32_t as = n % kASlots, bs = n % kBSlots;
+      if (!mbar_wait_inl(smem_u32(&bars->a_empty[as]), ((n / kASlots) & 1) ^ 1, g)) { ok = false; break; }
+      uint32_t bar = smem_u32(&bars->a_full[as]), dst = smem_u32(base + L::a + as * L::kTB);
+      mbar_arrive_expect_tx(bar, DKV ? qbytes : L::kTB);
+      if (DKV)
+        queries(dst, &a.tq, bar, w, j * a.TQ);
+      else
+        keys(dst, &a.tk, bar, w, j * kTile);
+      ++na;
+      if (j == w.j0) {  // the item's own tiles, behind the first streamed one
+        if (!mbar_wait_inl(smem_u32(&bars->own_empty), (it & 1) ^ 1, g)) { ok = false; break; }
+        bar = smem_u32(&bars->own_full), dst = smem_u32(base + L::own);
+        mbar_arrive_expect_tx(bar, 2 * (DKV ? L::kTB : qbytes));
+        if (DKV) {
+          keys(dst, &a.tk, bar, w, w.t0);
+          keys(dst + L::kTB, &a.tv, bar, w, w.t0);
+        } else {
+          queries(dst, &a.tq, bar, w, w.t0);
+          queries(dst + L::kTB, &a.tdo, bar, w, w.t0);
+        }
+        ++own;
+      }
+      if (!mbar_wait_inl(smem_u32(&bars->b_empty[bs]), ((n / kBSlots) & 1) ^ 1, g)) { ok = false; break; }
+      bar = smem_u32(&bars->b_full[bs]), dst = smem_u32(base + L::b + bs * L::kTB);
+      mbar_arrive_expect_tx(bar, DKV ? qbytes : L::kTB);
+      if (DKV)
+        queries(dst, &a.tdo, bar, w, j * a.TQ);
+      else
+        keys(dst, &a.tv, bar, w, j * kTile);
+      ++nb;
+    }
+  }
+  // every copy has landed before the CTA may exit
+  for (uint32_t x = na > kASlots ? na - kASlots : 0; x < na; ++x)
+    drain_wait(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, a);
+  for (uint32_t x = nb > kBSlots ? nb - kBSlots : 0; x < nb; ++x)
+    drain_wait(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, a);
+  if (own > 0) drain_wait(smem_u32(&bars->own_full), (own - 1) & 1, a);
+}
+
+// ------------------------------------------------------------ the walk, and the streamed tiles' release
+// Rows of a streamed tile that belong to no token of the sequence are cleared: they are
+// multiplied by P or dS of 0, and 0 times a NaN of a neighbouring sequence would spread.
+template <int DP, bool DKV>
+__device__ __forceinline__ void walk(const SeqBwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
+  using L = Layout<DP>;
+  using Blocks = typename std::conditional<DKV, KeyBlocks, QueryBlocks>::type;
+  Walk<Blocks> walk;
+  walk.init(a.s, Blocks{a.TQ}, blockIdx.x, gridDim.x);
+  PieceRecord* rec = a.records + 2 * blockIdx.x;
+  if (lane < 2) rec[lane].used = 0;
+  __syncwarp();
+  Work cur, ahead;
+  uint32_t pub = 0, n = 0;
+  bool more = true;
+  auto publish = [&](Work& w) -> bool {
+    w = walk.next();
+    const uint32_t s = pub % kDescs;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->desc_empty[s]), ((pub / kDescs) & 1) ^ 1, g)) return false;
+    if (lane == 0) {
+      bars->work[s] = w;
+      if (!w.stop && w.slot >= 0) rec[w.slot] = PieceRecord{1, w.j1 == w.kt, w.b, w.kvh, w.row0, w.t0, w.nt, 0};
+      mbar_arrive(smem_u32(&bars->desc_full[s]));
+    }
+    ++pub;
+    more = !w.stop;
+    return true;
+  };
+  auto clear = [&](uint8_t* tile, int from) {
+    for (int i = from * (DP / 8) + lane; i < kTile * (DP / 8); i += 32) {
+      const int r = i / (DP / 8), c = i % (DP / 8);
+      *reinterpret_cast<uint4*>(tile + (c >> 3) * L::kHalf + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  if (!publish(cur)) return;
+  while (!cur.stop) {
+    ahead.stop = 1;
+    if (more && !publish(ahead)) return;
+    for (int j = cur.j0; j < cur.j1; ++j, ++n) {
+      const uint32_t as = n % kASlots, bs = n % kBSlots;
+      if (!mbar_wait_warp_inl(smem_u32(&bars->a_full[as]), (n / kASlots) & 1, g)) return;
+      if (!mbar_wait_warp_inl(smem_u32(&bars->b_full[bs]), (n / kBSlots) & 1, g)) return;
+      const int last = DKV ? (cur.kv_end - j * a.TQ) * a.s.group : cur.kv_end - j * kTile;  // rows in the sequence
+      if (last < (DKV ? a.TQ * a.s.group : kTile)) {
+        clear(base + L::a + as * L::kTB, last);
+        if (DKV) clear(base + L::b + bs * L::kTB, last);  // (V's rows only reach masked entries of dP)
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(smem_u32(&bars->ready[n % kReady]));
+    }
+    cur = ahead;
+  }
+}
+
+// ------------------------------------------------------------ dK, dV: (lse, delta) of each tile of queries
+__device__ __forceinline__ void rows(const SeqBwdArgs& a, float2* buf, Bars* bars, const WaitGuard& g, int lane) {
+  const SeqDesc& s = a.s;
+  int dt[4], head[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dt[e] = (lane + 32 * e) / s.group, head[e] = (lane + 32 * e) % s.group;
+  uint32_t n = 0;
+  Work w;
+  for (uint32_t it = 0; take<true>(bars, it, g, w); ++it) {
+    __syncwarp();
+    if (lane == 0) give_back(bars, it);
+    for (int j = w.j0; j < w.j1; ++j, ++n) {
+      float2 x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = j * a.TQ + dt[e];
+        x[e] = make_float2(INFINITY, 0.0f);  // P = 0
+        if (dt[e] < a.TQ && t < w.kv_end)
+          x[e] = a.rows[static_cast<size_t>(w.row0 + t) * s.q_heads + w.kvh * s.group + head[e]];
+      }
+      const uint32_t st = n & 1;
+      if (!mbar_wait_warp_inl(smem_u32(&bars->rows_empty[st]), ((n >> 1) & 1) ^ 1, g)) return;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) buf[st * kTile + lane + 32 * e] = x[e];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->rows_full[st]));
+    }
+  }
+}
+
+// ------------------------------------------------------------ MMA (one thread)
+template <int DP>
+__device__ __forceinline__ uint64_t k_step(int k) {  // 16 features further in a tile, in descriptor units
+  return (k & 3) * 2 + (k >> 2) * (Layout<DP>::kHalf / 16);
+}
+// D = A Bᵀ over the features: two tiles of 128 rows.
+template <int DP>
+__device__ __forceinline__ void scores(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t id) {
+  const uint64_t ad = smem_desc(a, 16, 1024, kSwizzle128B), bd = smem_desc(b, 16, 1024, kSwizzle128B);
+  for (int k = 0; k < steps; ++k) umma_ss(d, ad + k_step<DP>(k), bd + k_step<DP>(k), id, k > 0);
+}
+// D (+)= A B over 128 rows or keys, A packed in tensor memory, B a tile (features along N).
+template <int DP>
+__device__ __forceinline__ void gather(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool add) {
+  const uint64_t bd = smem_desc(b, Layout<DP>::kHalf, 1024, kSwizzle128B);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) umma_ts(d, a + packed_col(k), bd + k * (2048 / 16), id, (add || k > 0) ? 1u : 0u);
+}
+
+template <int DP, bool BF16>
+__device__ __forceinline__ void mma_dkv(const SeqBwdArgs& a, uint8_t* base, Bars* bars, uint32_t tmem, const WaitGuard& g) {
+  using L = Layout<DP>;
+  const int steps = (a.s.D + 15) / 16;
+  const uint32_t id_s = idesc_f16(128, 128, BF16, false, false), id_g = idesc_f16(128, steps * 16, BF16, false, true);
+  const uint32_t ks = smem_u32(base + L::own), vs = ks + L::kTB;
+  uint32_t n = 0, it = 0;
+  bool ok = true;
+  // Sᵀ of streamed tile x, and dPᵀ
+  auto issue_s = [&](uint32_t x) -> bool {
+    if (!mbar_wait_inl(smem_u32(&bars->ready[x % kReady]), (x / kReady) & 1, g)) return false;
+    if (!mbar_wait_inl(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, g)) return false;
+    if (x > 0 && !mbar_wait_inl(smem_u32(&bars->first_done), (x - 1) & 1, g)) return false;  // P read
+    tc_fence_after();
+    scores<DP>(tmem + kColS, ks, smem_u32(base + L::a + (x % kASlots) * L::kTB), steps, id_s);
+    umma_commit(smem_u32(&bars->s_full[0]));
+    return true;
+  };
+  auto issue_dp = [&](uint32_t x) -> bool {
+    if (!mbar_wait_inl(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g)) return false;
+    if (x > 0 && !mbar_wait_inl(smem_u32(&bars->second_done), (x - 1) & 1, g)) return false;  // dS read
+    tc_fence_after();
+    scores<DP>(tmem + kColDp, vs, smem_u32(base + L::b + (x % kBSlots) * L::kTB), steps, id_s);
+    umma_commit(smem_u32(&bars->dp_full));
+    return true;
+  };
+  Work w;
+  for (; ok && take<false>(bars, it, g, w); ++it) {
+    give_back(bars, it);
+    if (!mbar_wait_inl(smem_u32(&bars->own_full), it & 1, g)) break;
+    if (!issue_s(n) || !issue_dp(n)) break;
+    for (int j = w.j0; j < w.j1; ++j, ++n) {
+      const uint32_t as = n % kASlots, bs = n % kBSlots;
+      if (!mbar_wait_inl(smem_u32(&bars->p_ready), n & 1, g)) { ok = false; break; }
+      if (j == w.j0 && !mbar_wait_inl(smem_u32(&bars->acc_free), (it & 1) ^ 1, g)) { ok = false; break; }
+      tc_fence_after();
+      gather<DP>(tmem + kColV, tmem + kColS, smem_u32(base + L::b + bs * L::kTB), id_g, j > w.j0);
+      umma_commit(smem_u32(&bars->first_done));
+      umma_commit(smem_u32(&bars->b_empty[bs]));
+      if (j + 1 < w.j1 && !issue_s(n + 1)) { ok = false; break; }
+      if (!mbar_wait_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
+      tc_fence_after();
+      gather<DP>(tmem + kColK, tmem + kColDp, smem_u32(base + L::a + as * L::kTB), id_g, j > w.j0);
+      umma_commit(smem_u32(&bars->second_done));
+      umma_commit(smem_u32(&bars->a_empty[as]));
+      if (j + 1 < w.j1 && !issue_dp(n + 1)) { ok = false; break; }
+    }
+    umma_commit(smem_u32(&bars->own_empty));
+    umma_commit(smem_u32(&bars->acc_full));
+  }
+  umma_commit(smem_u32(&bars->drain));
+  drain_wait(smem_u32(&bars->drain), 0, a);
+}
+
+template <int DP, bool BF16>
+__device__ __forceinline__ void mma_dq(const SeqBwdArgs& a, uint8_t* base, Bars* bars, uint32_t tmem, const WaitGuard& g) {
+  using L = Layout<DP>;
+  const int steps = (a.s.D + 15) / 16;
+  const uint32_t id_s = idesc_f16(128, 128, BF16, false, false), id_g = idesc_f16(128, steps * 16, BF16, false, true);
+  const uint32_t qs = smem_u32(base + L::own), dos = qs + L::kTB;
+  uint32_t n = 0, it = 0;
+  bool ok = true;
+  uint32_t gathers = 0;  // issued
+  auto issue_s = [&](uint32_t x) -> bool {
+    if (!mbar_wait_inl(smem_u32(&bars->ready[x % kReady]), (x / kReady) & 1, g)) return false;
+    if (!mbar_wait_inl(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, g)) return false;
+    // its buffer held dS of tile x - 2.  The wait is for the newest gather issued (a parity
+    // says nothing about an older phase): x - 2's within an item, x - 1's at an item's start
+    if (gathers > 0 && !mbar_wait_inl(smem_u32(&bars->second_done), (gathers - 1) & 1, g)) return false;
+    tc_fence_after();
+    scores<DP>(tmem + (x & 1) * 128, qs, smem_u32(base + L::a + (x % kASlots) * L::kTB), steps, id_s);
+    umma_commit(smem_u32(&bars->s_full[x & 1]));
+    return true;
+  };
+  auto issue_dp = [&](uint32_t x) -> bool {  // (dP of tile x - 1 was read before its dS was ready)
+    if (!mbar_wait_inl(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g)) return false;
+    tc_fence_after();
+    scores<DP>(tmem + kColDp2, dos, smem_u32(base + L::b + (x % kBSlots) * L::kTB), steps, id_s);
+    umma_commit(smem_u32(&bars->dp_full));
+    umma_commit(smem_u32(&bars->b_empty[x % kBSlots]));
+    return true;
+  };
+  Work w;
+  for (; ok && take<false>(bars, it, g, w); ++it) {
+    give_back(bars, it);
+    if (!mbar_wait_inl(smem_u32(&bars->own_full), it & 1, g)) break;
+    if (!issue_s(n) || !issue_dp(n)) break;
+    for (int j = w.j0; j < w.j1; ++j, ++n) {
+      const uint32_t as = n % kASlots;
+      if (j + 1 < w.j1 && !issue_s(n + 1)) { ok = false; break; }
+      if (!mbar_wait_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
+      if (j == w.j0 && !mbar_wait_inl(smem_u32(&bars->acc_free), (it & 1) ^ 1, g)) { ok = false; break; }
+      tc_fence_after();
+      gather<DP>(tmem + kColQ, tmem + (n & 1) * 128, smem_u32(base + L::a + as * L::kTB), id_g, j > w.j0);
+      ++gathers;
+      umma_commit(smem_u32(&bars->second_done));
+      umma_commit(smem_u32(&bars->a_empty[as]));
+      if (j + 1 < w.j1 && !issue_dp(n + 1)) { ok = false; break; }
+    }
+    umma_commit(smem_u32(&bars->own_empty));
+    umma_commit(smem_u32(&bars->acc_full));
+  }
+  umma_commit(smem_u32(&bars->drain));
+  drain_wait(smem_u32(&bars->drain), 0, a);
+}
+
+// ------------------------------------------------------------ compute (warps 0..7)
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+// Columns [c0, c1) (multiples of 32; stops at D) of this thread's row of an accumulator: times f in the
+// result's type at `out`, or as they are at `part`.  Warp-collective.
+template <bool BF16>
+__device__ __forceinline__ void write_row(uint32_t col, int c0, int c1, int D, bool live, bool piece, float f, uint16_t* out,
+                                          bool out32, float* part) {
+#pragma unroll 1
+  for (int c = c0; c < c1 && c < D; c += 32) {
+    uint32_t x[32];
+    tmem_ld32(col + c, x);
+    tmem_wait_ld(x);
+    if (live) {
+      if (piece) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          const uint32_t(&o)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&x[e]);
+          st_global_32(part + c + e, o);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e += 16) {
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            o[i] = pack2<BF16>(__uint_as_float(x[e + 2 * i]) * f, __uint_as_float(x[e + 2 * i + 1]) * f);
+          if (out32) {
+            if (c + e < D) st_global_32(out + c + e, o);
+          } else {
+            if (c + e < D) *reinterpret_cast<uint4*>(out + c + e) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (c + e + 8 < D) *reinterpret_cast<uint4*>(out + c + e + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// dK, dV.  Thread: key r of the tile, rows 64·grp .. 64·grp + 63 of each tile of queries.
+template <int DP, bool BF16>
+__device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float2* rowbuf, Bars* bars, uint32_t tmem,
+                                            const WaitGuard& g) {
+  const SeqDesc& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
+  const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  const uint32_t scol = trow + kColS + grp * 64, dcol = trow + kColDp + grp * 64;
+  const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
+  uint32_t n = 0, it = 0;
+  bool ok = true;
+  Work w;
+  for (; ok && take<true>(bars, it, g, w); ++it) {
+    __syncwarp();
+    if (lane == 0) give_back(bars, it);
+    const int key = w.t0 + r;
+    for (int j = w.j0; j < w.j1; ++j, ++n) {
+      const uint32_t st = n & 1;
+      const float4* rb = reinterpret_cast<const float4*>(rowbuf + st * kTile + grp * 64);
+      // rows below `from` belong to tokens in front of the key; none does once the tile lies behind the keys
+      const bool mask = j * a.TQ < w.t0 + kTile - 1;
+      const int from = (key - j * a.TQ) * s.group - grp * 64;
+      uint32_t p[64];
+      if (!mbar_wait_warp_inl(smem_u32(&bars->rows_full[st]), (n >> 1) & 1, g)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->s_full[0]), n & 1, g)) { ok = false; break; }
+      tc_fence_after();
+      tmem_ld64(scol, p);
+      tmem_wait_ld(p);
+      {
+        uint32_t pp[32];
+#pragma unroll
+        for (int x = 0; x < 64; x += 2) {
+          const float4 z = rb[x >> 1];  // (lse, delta) of two rows
+          const float2 t = fma2(make_float2(__uint_as_float(p[x]), __uint_as_float(p[x + 1])), sl2, make_float2(-z.x, -z.z));
+          float p0 = ex2(t.x), p1 = ex2(t.y);
+          if (mask) {
+            if (x < from) p0 = 0.0f;
+            if (x + 1 < from) p1 = 0.0f;
+          }
+          p[x] = __float_as_uint(p0);
+          p[x + 1] = __float_as_uint(p1);
+          pp[x >> 1] = pack2<BF16>(p0, p1);
+        }
+        tmem_st32(scol, pp);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->p_ready));
+      if (!mbar_wait_warp_inl(smem_u32(&bars->dp_full), n & 1, g)) { ok = false; break; }
+      tc_fence_after();
+      {
+        uint32_t pp[32];
+#pragma unroll
+        for (int h = 0; h < 64; h += 32) {
+          uint32_t d[32];
+          tmem_ld32(dcol + h, d);
+          tmem_wait_ld(d);
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const float4 z = rb[(h + x) >> 1];
+            const float2 t = add2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), make_float2(-z.y, -z.w));
+            float2 ds = mul2(t, make_float2(__uint_as_float(p[h + x]), __uint_as_float(p[h + x + 1])));
+            if (mask) {
+              if (h + x < from) ds.x = 0.0f;
+              if (h + x + 1 < from) ds.y = 0.0f;
+            }
+            pp[(h + x) >> 1] = pack2<BF16>(ds.x, ds.y);
+          }
+        }
+        tmem_st32(dcol, pp);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&bars->ds_ready));
+        mbar_arrive(smem_u32(&bars->rows_empty[st]));
+      }
+    }
+    if (!ok || !mbar_wait_warp_inl(smem_u32(&bars->acc_full), it & 1, g)) break;
+    tc_fence_after();
+    const bool live = r < w.nt;
+    const size_t row = static_cast<size_t>(w.row0) + key;
+    uint16_t* out = (grp ? a.dk + row * a.dk_stride : a.dv + row * a.dv_stride) + static_cast<size_t>(w.kvh) * s.D;
+    float* part = a.part + (((static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * 2 + grp) * kTile + r) * DP;
+    write_row<BF16>(trow + (grp ? kColK : kColV), 0, DP, s.D, live, w.slot >= 0, grp ? a.scale : 1.0f, out,
+                    grp ? a.dk32 : a.dv32, part);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->acc_free));
+  }
+}
+
+// dQ.  Thread: row r of the tile, keys 64·grp .. 64·grp + 63 of each key tile.
+template <int DP, bool BF16>
+__device__ __forceinline__ void compute_dq(const SeqBwdArgs& a, Bars* bars, uint32_t tmem, const WaitGuard& g) {
+  const SeqDesc& s = a.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
+  const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  const uint32_t dcol = trow + kColDp2 + grp * 64;
+  const int dt = r / s.group, head = r % s.group;
+  const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
+  uint32_t n = 0, it = 0;
+  bool ok = true;
+  Work w;
+  for (; ok && take<true>(bars, it, g, w); ++it) {
+    __syncwarp();
+    if (lane == 0) give_back(bars, it);
+    const bool live = dt < a.TQ && dt < w.nt;
+    const size_t row = static_cast<size_t>(w.row0) + w.t0 + dt;
+    const int h = w.kvh * s.group + head;
+    float2 z = make_float2(INFINITY, 0.0f);
+    if (live) z = a.rows[row * s.q_heads + h];
+    const float2 nl = make_float2(-z.x, -z.x), nd = make_float2(-z.y, -z.y);
+    for (int j = w.j0; j < w.j1; ++j, ++n) {
+      const uint32_t scol = trow + (n & 1) * 128 + grp * 64;
+      const bool mask = w.pos < j * kTile + kTile - 1;
+      const int lim = w.pos + dt - j * kTile - grp * 64;  // keys past it are not seen
+      uint32_t p[64];
+      if (!mbar_wait_warp_inl(smem_u32(&bars->s_full[n & 1]), (n >> 1) & 1, g)) { ok = false; break; }
+      tc_fence_after();
+      tmem_ld64(scol, p);
+      tmem_wait_ld(p);
+#pragma unroll
+      for (int x = 0; x < 64; x += 2) {
+        const float2 t = fma2(make_float2(__uint_as_float(p[x]), __uint_as_float(p[x + 1])), sl2, nl);
+        p[x] = __float_as_uint(ex2(t.x));
+        p[x + 1] = __float_as_uint(ex2(t.y));
+      }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->dp_full), n & 1, g)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t pp[32];
+#pragma unroll
+      for (int q = 0; q < 64; q += 32) {
+        uint32_t d[32];
+        tmem_ld32(dcol + q, d);
+        tmem_wait_ld(d);
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const float2 t = add2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), nd);
+          float2 ds = mul2(t, make_float2(__uint_as_float(p[q + x]), __uint_as_float(p[q + x + 1])));
+          if (mask) {
+            if (q + x > lim) ds.x = 0.0f;
+            if (q + x + 1 > lim) ds.y = 0.0f;
+          }
+          pp[(q + x) >> 1] = pack2<BF16>(ds.x, ds.y);
+        }
+      }
+      tmem_st32(scol, pp);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->ds_ready));
+    }
+    if (!ok || !mbar_wait_warp_inl(smem_u32(&bars->acc_full), it & 1, g)) break;
+    tc_fence_after();
+    uint16_t* out = a.dq + row * a.dq_stride + static_cast<size_t>(h) * s.D;
+    float* part = a.part + ((static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * kTile + r) * DP;
+    write_row<BF16>(trow + kColQ, grp * (DP / 2), (grp + 1) * (DP / 2), s.D, live, w.slot >= 0, a.scale, out, a.dq32, part);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->acc_free));
+  }
+}
+
+template <int DP, bool BF16, bool DKV>
+__global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_constant__ SeqBwdArgs a) {
+  using L = Layout<DP>;
+  extern __shared__ __align__(1024) uint8_t base[];
+  Bars* bars = reinterpret_cast<Bars*>(base + L::bars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (smem_u32(base) & 1023u) {  // the tiles' swizzle counts from 1 KB borders
+    if (threadIdx.x == 0) atomicExch(a.s.status, kStatusTimeout);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    bars->abort = 0;
+    for (int i = 0; i < kDescs; ++i) {
+      mbar_init(smem_u32(&bars->desc_full[i]), 1);
+      mbar_init(smem_u32(&bars->desc_empty[i]), DKV ? 11 : 10);  // producer, MMA, compute warps; rows
+    }
+    mbar_init(smem_u32(&bars->own_full), 1);
+    mbar_init(smem_u32(&bars->own_empty), 1);
+    for (int i = 0; i < kASlots; ++i) {
+      mbar_init(smem_u32(&bars->a_full[i]), 1);
+      mbar_init(smem_u32(&bars->a_empty[i]), 1);
+    }
+    for (int i = 0; i < kBSlots; ++i) {
+      mbar_init(smem_u32(&bars->b_full[i]), 1);
+      mbar_init(smem_u32(&bars->b_empty[i]), 1);
+    }
+    for (int i = 0; i < kReady; ++i) mbar_init(smem_u32(&bars->ready[i]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars->rows_full[i]), 1);
+      mbar_init(smem_u32(&bars->rows_empty[i]), 8);
+      mbar_init(smem_u32(&bars->s_full[i]), 1);
+    }
+    mbar_init(smem_u32(&bars->dp_full), 1);
+    mbar_init(smem_u32(&bars->p_ready), 8);
+    mbar_init(smem_u32(&bars->ds_ready), 8);
+    mbar_init(smem_u32(&bars->first_done), 1);
+    mbar_init(smem_u32(&bars->second_done), 1);
+    mbar_init(smem_u32(&bars->acc_full), 1);
+    mbar_init(smem_u32(&bars->acc_free), 8);
+    mbar_init(smem_u32(&bars->drain), 1);
+    fence_barrier_init();
+  }
+  if (warp == kProducerWarp && lane == 0) {
+    tma_prefetch_desc(&a.tq);
+    tma_prefetch_desc(&a.tk);
+    tma_prefetch_desc(&a.tv);
+    tma_prefetch_desc(&a.tdo);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&bars->tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (DKV && a.TQ * a.s.group < kTile) {
+    // rows that no query tile fills are read by the gradient MMAs (against P = dS = 0)
+    for (uint32_t i = threadIdx.x; i < (kASlots + kBSlots) * L::kTB / 16; i += kThreads)
+      reinterpret_cast<uint4*>(base + L::a)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_slot;
+  const WaitGuard g{a.wait_ns, a.s.status, &bars->abort};
+  float2* rowbuf = reinterpret_cast<float2*>(base + L::rows);
+  if (warp >= kProducerWarp) {
+    setmaxnreg_dec<kRegsOther>();
+    if (warp == kProducerWarp) {
+      if (lane == 0) producer<DP, DKV>(a, base, bars, g);
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) {
+        if (DKV)
+          mma_dkv<DP, BF16>(a, base, bars, tmem, g);
+        else
+          mma_dq<DP, BF16>(a, base, bars, tmem, g);
+      }
+      __syncwarp();
+    } else if (warp == kRowsWarp) {
+      if (DKV) rows(a, rowbuf, bars, g, lane);
+    } else {
+      walk<DP, DKV>(a, base, bars, g, lane);
+    }
+  } else {
+    setmaxnreg_inc<kRegsCompute>();
+    if (DKV)
+      compute_dkv<DP, BF16>(a, rowbuf, bars, tmem, g);
+    else
+      compute_dq<DP, BF16>(a, bars, tmem, g);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------ pieces, summed in order
+template <int DP, bool BF16, bool DKV>
+__global__ void __launch_bounds__(256) evo_seq_bwd_join_kernel(const __grid_constant__ SeqBwdArgs a, int ctas) {
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const PieceRecord first = a.records[2 * c0 + 1];
+  if (!first.used) return;
+  const SeqDesc& s = a.s;
+  int pieces = 1;
+  while (c0 + pieces < ctas) {
+    const PieceRecord p = a.records[2 * (c0 + pieces)];
+    if (!p.used) break;
+    ++pieces;
+    if (p.ends) break;
+  }
+  constexpr int kParts = DKV ? 2 : 1;
+  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < kParts * kTile; i += gridDim.y * 8) {
+    const int part = i / kTile, r = i % kTile;
+    const int tok = DKV ? r : r / s.group;
+    if (tok >= first.nt || (!DKV && tok >= a.TQ)) continue;
+    float x[DP / 32] = {};
+    for (int p = 0; p < pieces; ++p) {
+      const float* y = a.part + (((static_cast<size_t>(c0 + p) * 2 + (p == 0)) * kParts + part) * kTile + r) * DP;
+#pragma unroll
+      for (int e = 0; e < DP / 32; ++e)
+        if (lane + 32 * e < s.D) x[e] += y[lane + 32 * e];
+    }
+    const size_t row = static_cast<size_t>(first.row0) + first.t0 + tok;
+    uint16_t* out = DKV ? (part ? a.dk + row * a.dk_stride : a.dv + row * a.dv_stride) + static_cast<size_t>(first.kvh) * s.D
+                        : a.dq + row * a.dq_stride + static_cast<size_t>(first.kvh * s.group + r % s.group) * s.D;
+    const float f = DKV && part == 0 ? 1.0f : a.scale;
+#pragma unroll
+    for (int e = 0; e < DP / 32; ++e)
+      if (lane + 32 * e < s.D) out[lane + 32 * e] = static_cast<uint16_t>(pack2<BF16>(x[e] * f, 0.0f) & 0xffffu);
+  }
+}
+
+// ------------------------------------------------------------ lse and delta
+// 16 threads per (row, head), 16 bytes of O and of dO each.  Bound by those bytes.
+template <bool BF16>
+__global__ void __launch_bounds__(256) evo_seq_rows_kernel(const __grid_constant__ SeqBwdArgs a) {
+  const SeqDesc& s = a.s;
+  const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 4;
+  const int c = threadIdx.x & 15;
+  float d = 0.0f;
+  const bool in = i < static_cast<long long>(s.tokens) * s.q_heads;
+  const int t = in ? static_cast<int>(i / s.q_heads) : 0, h = in ? static_cast<int>(i % s.q_heads) : 0;
+  if (in && c * 8 < s.D) {
+    const uint4 x = *reinterpret_cast<const uint4*>(a.out + t * a.out_stride + static_cast<long long>(h) * s.D + c * 8);
+    const uint4 y = *reinterpret_cast<const uint4*>(a.dout + t * a.dout_stride + static_cast<long long>(h) * s.D + c * 8);
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 u = unpack2<BF16>(xs[e]), v = unpack2<BF16>(ys[e]);
+      d = fmaf(u.x, v.x, d);
+      d = fmaf(u.y, v.y, d);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if (in && c == 0) {
+    const float z = a.lse[static_cast<size_t>(h) * s.tokens + t];
+    a.rows[i] = make_float2(z == -INFINITY ? INFINITY : z * kSeqLog2e, d);
+  }
+}
+
+template <int DP, bool BF16, bool DKV>
+cudaError_t launch_k(const SeqBwdArgs& a, int ctas, cudaStream_t st) {
+  auto kern = evo_seq_bwd_kernel<DP, BF16, DKV>;
+  static bool limit_set[64] = {};
+  cudaError_t e = ensure_smem_limit(kern, 232448, limit_set);
+  if (e != cudaSuccess) return e;
+  // more than half of an SM's shared memory: each CTA allocates all of tensor memory
+  const size_t smem = Layout<DP>::total > 118784 ? Layout<DP>::total : 118784;
+  kern<<<ctas, kThreads, smem, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  evo_seq_bwd_join_kernel<DP, BF16, DKV><<<dim3(ctas, 4), 256, 0, st>>>(a, ctas);
+  return cudaGetLastError();
+}
+template <int DP, bool BF16>
+cudaError_t launch_t(const SeqBwdArgs& a, int ctas, cudaStream_t st) {
+  const long long n = static_cast<long long>(a.s.tokens) * a.s.q_heads;
+  evo_seq_rows_kernel<BF16><<<static_cast<unsigned>((n + 15) / 16), 256, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_k<DP, BF16, true>(a, ctas, st);
+  if (e == cudaSuccess) e = launch_k<DP, BF16, false>(a, ctas, st);
+  return e;
+}
+
+}  // namespace
+
+size_t prompt_bwd_workspace(int ctas, const SeqDesc& s, SeqBwdArgs* a, uint8_t* ws) {
+  const int DP = s.D <= 64 ? 64 : 128;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = ws ? ws + off : nullptr;
+    off += (bytes + 255) & ~size_t(255);
+    return p;
+  };
+  uint8_t* rec = take(size_t(ctas) * 2 * sizeof(PieceRecord));
+  uint8_t* rows = take(size_t(s.tokens) * s.q_heads * sizeof(float2));
+  uint8_t* part = take(size_t(ctas) * 2 * 2 * kTile * DP * sizeof(float));  // dK and dV's; dQ's afterwards
+  if (a) {
+    a->records = reinterpret_cast<PieceRecord*>(rec);
+    a->rows = reinterpret_cast<float2*>(rows);
+    a->part = reinterpret_cast<float*>(part);
+  }
+  return off;
+}
+
+cudaError_t launch_prompt_bwd(const SeqBwdArgs& a, int ctas, bool bf16, cudaStream_t st) {
+  if (a.s.D <= 64) return bf16 ? launch_t<64, true>(a, ctas, st) : launch_t<64, false>(a, ctas, st);
+  return bf16 ? launch_t<128, true>(a, ctas, st) : launch_t<128, false>(a, ctas, st);
+}
+
+}  // namespace evo

@@ -247,8 +247,8 @@ __device__ __forceinline__ bool take_out(uint8_t* tile, int from, int to, int la
 template <int DP, bool BF16>
 __device__ __forceinline__ void walk(const SeqFwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
   using L = Layout<DP>;
-  Walk walk;
-  walk.init(a.s, a.W, blockIdx.x, gridDim.x);
+  Walk<QueryBlocks> walk;
+  walk.init(a.s, QueryBlocks{a.W}, blockIdx.x, gridDim.x);
   PieceRecord* rec = a.records + 2 * blockIdx.x;
   if (lane < 2) rec[lane].used = 0;
   __syncwarp();

@@ -15,8 +15,6 @@ constexpr int64_t kMaxStride = int64_t(1) << 36;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
-
 struct Opts {
   float scale = 0.0f;
   uint64_t wait_ns = kDefaultWaitNs;
@@ -205,7 +203,7 @@ size_t evo_prompt_fwd_workspace_bytes(evo_seq_shape_t shape) {
 
 size_t evo_prompt_bwd_workspace_bytes(evo_seq_shape_t shape) {
   if (check_seq_shape(shape, true) != EVO_OK) return 0;
-  return 256 + round256(size_t(shape.tokens) * shape.q_heads * 4);
+  return prompt_bwd_workspace(num_sms(), desc(shape, nullptr, nullptr, nullptr, nullptr, -1, nullptr), nullptr, nullptr);
 }
 
 size_t evo_paged_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache_shape_t cache) {
@@ -279,23 +277,27 @@ evo_status_t evo_prompt_bwd(const void* q, const void* k, const void* v, const i
   int sms = 0;
   int* fallback = nullptr;
   if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
-  SeqAttnArgs a{};
+  SeqBwdArgs a{};
   a.s = desc(shape, cu_seqlens, nullptr, nullptr, nullptr, -1, o.status ? o.status : fallback);
-  a.q = static_cast<const uint16_t*>(q);
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
-  a.out = static_cast<uint16_t*>(const_cast<void*>(out));
-  a.lse = const_cast<float*>(lse);
+  a.TQ = kTile / a.s.group;
+  const bool bf16 = dtype == EVO_BF16;
+  if (!map_q(&a.tq, q, bf16, shape, t.q, a.TQ) || !map_q(&a.tdo, dout, bf16, shape, t.dout, a.TQ) ||
+      !map_rows(&a.tk, k, bf16, shape, t.k) || !map_rows(&a.tv, v, bf16, shape, t.v))
+    return EVO_ERR_CUDA;
+  auto wide = [&](const void* p, long long stride) { return aligned(p, 32) && stride % 16 == 0 && shape.head_dim % 16 == 0; };
+  a.dq32 = wide(dq, t.dq), a.dk32 = wide(dk, t.dk), a.dv32 = wide(dv, t.dv);
+  a.scale = scale_of(o, shape);
+  a.scale_log2 = a.scale * kSeqLog2e;
+  a.out = static_cast<const uint16_t*>(out);
   a.dout = static_cast<const uint16_t*>(dout);
+  a.lse = lse;
   a.dq = static_cast<uint16_t*>(dq);
   a.dk = static_cast<uint16_t*>(dk);
   a.dv = static_cast<uint16_t*>(dv);
-  a.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
-  a.q_stride = t.q, a.k_stride = t.k, a.v_stride = t.v, a.out_stride = t.out, a.dout_stride = t.dout;
-  a.dq_stride = t.dq, a.dk_stride = t.dk, a.dv_stride = t.dv;
-  a.scale = scale_of(o, shape);
+  a.out_stride = t.out, a.dout_stride = t.dout, a.dq_stride = t.dq, a.dk_stride = t.dk, a.dv_stride = t.dv;
   a.wait_ns = o.wait_ns;
-  const cudaError_t e = launch_prompt_bwd(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
+  prompt_bwd_workspace(sms, a.s, &a, static_cast<uint8_t*>(workspace));
+  const cudaError_t e = launch_prompt_bwd(a, sms, bf16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? EVO_OK : cuda_fail("prompt backward launch", e);
 }
 

@@ -127,10 +127,28 @@ struct SeqFwdArgs {
 // Bytes of the workspace for `ctas` CTAs; with a and ws, a's pointers into it.
 size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws);
 
+// The prompt's backward on the tensor cores (tk, tv as the prompt forward's).
+struct SeqBwdArgs {
+  CUtensorMap tq, tdo, tk, tv;
+  SeqDesc s;
+  int TQ;
+  int dq32, dk32, dv32;  // rows of the gradients start at multiples of 32 bytes
+  float scale, scale_log2;
+  const uint16_t *out, *dout;
+  const float* lse;
+  uint16_t *dq, *dk, *dv;
+  long long out_stride, dout_stride, dq_stride, dk_stride, dv_stride;
+  PieceRecord* records;  // workspace: two per CTA
+  float2* rows;          // ... [tokens][q_heads] (lse·log2 e, delta)
+  float* part;           // ... [ctas][2][dV, dK][128][DP], then [ctas][2][128][DP]
+  uint64_t wait_ns;
+};
+size_t prompt_bwd_workspace(int ctas, const SeqDesc& s, SeqBwdArgs* a, uint8_t* ws);
+
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_seq_fwd(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 cudaError_t launch_seq_weights(const SeqAttnArgs& a, bool bf16, cudaStream_t st);
-cudaError_t launch_prompt_bwd(const SeqAttnArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_prompt_bwd(const SeqBwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 
 }  // namespace evo

@@ -1,12 +1,12 @@
 // evo_seq_sched.cuh — how the attention of include/evo_seq.h is shared out over the CTAs
 // of one launch, all of it on the device (the lengths are device data).
 //
-// A work item is a block of W query tokens of one sequence with all the heads of one
-// group, over the keys it sees; items are laid out one behind the other (sequence, kv head,
-// block), and each counts as many units as it has keys, plus kItemCost for what every item
-// costs.  CTA c takes the units [c·share, (c+1)·share): every CTA has the same amount of
-// work whatever the lengths are, and an item that a border cuts (at a multiple of 128 keys)
-// is computed in pieces, whose results are joined in a fixed order by a second kernel.
+// A work item is a block of one sequence's tokens with all the heads of one group, over
+// what its tokens see (or, for a block of keys, are seen by); items are laid out one behind
+// the other (sequence, kv head, block), and each counts as many units as it has tokens to
+// walk over, plus kItemCost for what every item costs.  CTA c takes the units [c·share, (c+1)·share): every CTA has the same amount of
+// work whatever the lengths are, and an item that a border cuts (between two tiles) is
+// computed in pieces, whose results are joined in a fixed order by a second kernel.
 #pragma once
 
 #include "evo_seq_internal.h"
@@ -35,54 +35,83 @@ struct PieceRecord {
   int b, kvh, row0, t0, nt, pad;
 };
 
-// Units of block p (of P blocks of W tokens) of a sequence, and of all blocks before p.
-struct BlockUnits {
-  long long pos0c;  // position of its first new token, at least 0
-  int n, W, P;
-  __device__ __forceinline__ BlockUnits(const Seq& q, int w)
-      : pos0c(q.pos0 > 0 ? q.pos0 : 0), n(q.n), W(w), P((q.n + w - 1) / w) {}
-  __device__ __forceinline__ long long of(int p) const {
+// How a sequence's items are laid out and cut.  Both kinds count an item's units as what it
+// walks over (keys, or query tokens) plus kItemCost.
+//
+// Blocks of W query tokens over the key tiles they see (forward, dQ).
+struct QueryBlocks {
+  int W;
+  __device__ __forceinline__ int count(const Seq& q) const { return (q.n + W - 1) / W; }
+  // a position below 0 (more new tokens than the length) counts as 0
+  __device__ __forceinline__ long long of(const Seq& q, int p) const {
     const long long end = static_cast<long long>(p + 1) * W;
-    return pos0c + (end < n ? end : n) + kItemCost;
+    return (q.pos0 > 0 ? q.pos0 : 0) + (end < q.n ? end : q.n) + kItemCost;
   }
-  __device__ __forceinline__ long long before(int p) const {  // p < P
-    return p * (pos0c + kItemCost) + static_cast<long long>(W) * p * (p + 1) / 2;
+  __device__ __forceinline__ long long before(const Seq& q, int p) const {  // p < count
+    return p * static_cast<long long>((q.pos0 > 0 ? q.pos0 : 0) + kItemCost) + static_cast<long long>(W) * p * (p + 1) / 2;
   }
-  __device__ __forceinline__ long long total() const { return P > 0 ? before(P - 1) + of(P - 1) : 0; }
-  // the block that holds unit x < total()
-  __device__ __forceinline__ int find(long long x) const {
-    const float c = static_cast<float>(pos0c + kItemCost) + 0.5f * W;
-    int p = static_cast<int>((sqrtf(c * c + 2.0f * W * static_cast<float>(x)) - c) / W);
-    p = p < 0 ? 0 : (p > P - 1 ? P - 1 : p);
-    while (p > 0 && before(p) > x) --p;
-    while (p + 1 < P && before(p + 1) <= x) ++p;
-    return p;
+  __device__ __forceinline__ void place(Work& w, const Seq& q, int p) const {
+    w.t0 = p * W;
+    w.nt = q.n - w.t0 < W ? q.n - w.t0 : W;
+    w.pos = q.pos0 + w.t0;
+    w.kv_end = w.pos + w.nt > 0 ? w.pos + w.nt : 0;
+    w.kt = w.kv_end > 0 ? (w.kv_end + kTile - 1) / kTile : 1;
+  }
+  __device__ __forceinline__ int first(const Work&) const { return 0; }
+  __device__ __forceinline__ int tile(const Work&, long long keys) const { return static_cast<int>(keys / kTile); }
+};
+
+// Tiles of 128 keys under the tiles of TQ query tokens that see them (dK and dV of a prompt).
+// Work: t0, nt the keys; j0, j1, kt tiles of queries.
+struct KeyBlocks {
+  int TQ;
+  __device__ __forceinline__ int count(const Seq& q) const { return (q.n + kTile - 1) / kTile; }
+  __device__ __forceinline__ long long of(const Seq& q, int p) const { return q.n - p * kTile + kItemCost; }
+  __device__ __forceinline__ long long before(const Seq& q, int p) const {
+    return p * static_cast<long long>(q.n + kItemCost) - static_cast<long long>(kTile / 2) * p * (p - 1);
+  }
+  __device__ __forceinline__ void place(Work& w, const Seq& q, int p) const {
+    w.t0 = p * kTile;
+    w.nt = q.n - w.t0 < kTile ? q.n - w.t0 : kTile;
+    w.pos = w.t0;
+    w.kv_end = q.n;
+    w.kt = (q.n + TQ - 1) / TQ;
+  }
+  __device__ __forceinline__ int first(const Work& w) const { return w.t0 / TQ; }
+  __device__ __forceinline__ int tile(const Work& w, long long tokens) const {
+    return static_cast<int>((w.t0 + tokens) / TQ);
   }
 };
 
 // The walk of one CTA over its share; run by one whole warp (every lane holds the state).
+template <class Blocks>
 struct Walk {
   const SeqDesc* d;
-  int W, b, kvh, p;
+  Blocks k;
+  int b, kvh, p, P;
   Seq q;
   long long off, left;  // units of the current item already passed; units of the share left
-  int end_b;
 
-  __device__ __forceinline__ void init(const SeqDesc& desc, int w, int cta, int ctas) {
+  __device__ __forceinline__ long long total(const Seq& s) const {
+    const int n = k.count(s);
+    return n > 0 ? k.before(s, n - 1) + k.of(s, n - 1) : 0;
+  }
+
+  __device__ __forceinline__ void init(const SeqDesc& desc, const Blocks& blocks, int cta, int ctas) {
     d = &desc;
-    W = w;
+    k = blocks;
     const int lane = threadIdx.x & 31;
-    long long total = 0;
+    long long all = 0;
     for (int base = 0; base < desc.seqs; base += 32) {
       const int i = base + lane;
-      if (i < desc.seqs) total += BlockUnits(load_seq(desc, i), w).total() * desc.kv_heads;
+      if (i < desc.seqs) all += total(load_seq(desc, i)) * desc.kv_heads;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    long long share = (total + ctas - 1) / ctas;
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    long long share = (all + ctas - 1) / ctas;
     if (share < kItemCost + 128) share = kItemCost + 128;
     const long long x0 = share * cta;
-    left = total - x0 < share ? total - x0 : share;
+    left = all - x0 < share ? all - x0 : share;
     b = desc.seqs;
     if (left <= 0) {
       left = 0;
@@ -91,65 +120,70 @@ struct Walk {
     long long passed = 0;  // units of the sequences before `base`
     for (int base = 0; base < desc.seqs; base += 32) {
       const int i = base + lane;
-      const long long mine = i < desc.seqs ? BlockUnits(load_seq(desc, i), w).total() * desc.kv_heads : 0;
+      const long long mine = i < desc.seqs ? total(load_seq(desc, i)) * desc.kv_heads : 0;
       long long run = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, run, o);
         if (lane >= o) run += y;
       }
-      const bool here = x0 < passed + run;
-      const uint32_t any = __ballot_sync(0xffffffffu, here);
+      const uint32_t any = __ballot_sync(0xffffffffu, x0 < passed + run);
       if (any) {
         const int first = __ffs(any) - 1;
         const long long begin = __shfl_sync(0xffffffffu, passed + run - mine, first);
         b = base + first;
         q = load_seq(desc, b);
-        const BlockUnits u(q, w);
+        P = k.count(q);
+        const long long per = total(q);
         long long x = x0 - begin;
-        kvh = static_cast<int>(x / u.total());
-        x -= kvh * u.total();
-        p = u.find(x);
-        off = x - u.before(p);
+        kvh = static_cast<int>(x / per);
+        x -= kvh * per;
+        int lo = 0, hi = P - 1;  // the block that holds unit x
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (k.before(q, mid) <= x)
+            lo = mid;
+          else
+            hi = mid - 1;
+        }
+        p = lo;
+        off = x - k.before(q, p);
         return;
       }
       passed += __shfl_sync(0xffffffffu, run, 31);
     }
+    left = 0;
   }
 
-  // The next piece with at least one key tile, or stop.
+  // The next piece with at least one tile, or stop.
   __device__ __forceinline__ Work next() {
     Work w{};
     while (left > 0) {
-      const BlockUnits u(q, W);
-      const long long units = u.of(p), to = off + left < units ? off + left : units;
+      const long long units = k.of(q, p), to = off + left < units ? off + left : units;
       w.b = b, w.kvh = kvh, w.row0 = q.row0;
-      w.t0 = p * W;
-      w.nt = q.n - w.t0 < W ? q.n - w.t0 : W;
-      w.pos = q.pos0 + w.t0;
-      w.kv_end = w.pos + w.nt > 0 ? w.pos + w.nt : 0;
-      w.kt = w.kv_end > 0 ? (w.kv_end + kTile - 1) / kTile : 1;
+      k.place(w, q, p);
+      const int begin = k.first(w);
       auto tile = [&](long long x) {
-        const long long t = x > kItemCost ? (x - kItemCost) / kTile : 0;
-        return t < w.kt ? static_cast<int>(t) : w.kt;
+        const int t = x > kItemCost ? k.tile(w, x - kItemCost) : begin;
+        return t < w.kt ? t : w.kt;
       };
       w.j0 = tile(off);
       w.j1 = to == units ? w.kt : tile(to);
-      w.slot = w.j0 > 0 ? 0 : (w.j1 < w.kt ? 1 : -1);
+      w.slot = w.j0 > begin ? 0 : (w.j1 < w.kt ? 1 : -1);
       left -= to - off;
       off = 0;
-      if (to == units && ++p == u.P) {
+      if (to == units && ++p == P) {
         p = 0;
         if (++kvh == d->kv_heads) {
           kvh = 0;
           do {
-            ++b;
-            if (b >= d->seqs) {
+            if (++b >= d->seqs) {
               left = 0;
               break;
             }
             q = load_seq(*d, b);
-          } while (q.n == 0);
+            P = k.count(q);
+          } while (P == 0);
         }
       }
       if (w.j0 < w.j1) return w;

@@ -76,83 +76,7 @@ __global__ void seq_weights_simple(const SeqAttnArgs a) {
   }
 }
 
-template <bool BF16>
-__global__ void prompt_delta_simple(const SeqAttnArgs a) {
-  const SeqDesc& s = a.s;
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(s);
-  const int lane = threadIdx.x & 31, h = blockIdx.y;
-  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= s.tokens) return;
-  float x[kMaxPerLane], y[kMaxPerLane];
-  load_row<BF16>(a.out + t * a.out_stride + h * s.D, s.D, lane, x);
-  load_row<BF16>(a.dout + t * a.dout_stride + h * s.D, s.D, lane, y);
-  const float d = dot(x, y);
-  if (lane == 0) a.delta[static_cast<size_t>(h) * s.tokens + t] = d;
-}
-
-template <bool BF16>
-__global__ void prompt_dq_simple(const SeqAttnArgs a) {
-  const SeqDesc& s = a.s;
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(s);
-  const int lane = threadIdx.x & 31, h = blockIdx.y;
-  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= s.tokens) return;
-  const int b = find_seq(s, t);
-  if (b < 0) return;
-  const Seq q = load_seq(s, b);
-  if (t < q.row0 || t >= q.row0 + q.n) return;
-  const int hk = h / s.group;
-  float qr[kMaxPerLane], dor[kMaxPerLane], kr[kMaxPerLane], vr[kMaxPerLane], g[kMaxPerLane] = {};
-  load_row<BF16>(a.q + t * a.q_stride + h * s.D, s.D, lane, qr);
-  load_row<BF16>(a.dout + t * a.dout_stride + h * s.D, s.D, lane, dor);
-  const size_t at = static_cast<size_t>(h) * s.tokens + t;
-  const float z = a.lse[at], delta = a.delta[at];
-  for (int j = 0; j <= t - q.row0; ++j) {
-    load_key<BF16>(a, a.k, a.k_stride, a.k_page, q, b, j, hk, lane, kr);
-    load_key<BF16>(a, a.v, a.v_stride, a.v_page, q, b, j, hk, lane, vr);
-    const float p = z == -INFINITY ? 0.0f : expf(dot(qr, kr) * a.scale - z);
-    const float ds = p * (dot(dor, vr) - delta) * a.scale;
-#pragma unroll
-    for (int e = 0; e < kMaxPerLane; ++e) g[e] = fmaf(ds, kr[e], g[e]);
-  }
-  store_row<BF16>(a.dq + t * a.dq_stride + h * s.D, s.D, lane, g);
-}
-
-template <bool BF16>
-__global__ void prompt_dkv_simple(const SeqAttnArgs a) {
-  const SeqDesc& s = a.s;
-  const int lane = threadIdx.x & 31, hk = blockIdx.y;
-  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= s.tokens) return;
-  const int b = find_seq(s, t);
-  if (b < 0) return;
-  const Seq q = load_seq(s, b);
-  if (t < q.row0 || t >= q.row0 + q.n) return;
-  float qr[kMaxPerLane], dor[kMaxPerLane], kr[kMaxPerLane], vr[kMaxPerLane], gk[kMaxPerLane] = {}, gv[kMaxPerLane] = {};
-  load_row<BF16>(a.k + t * a.k_stride + hk * s.D, s.D, lane, kr);
-  load_row<BF16>(a.v + t * a.v_stride + hk * s.D, s.D, lane, vr);
-  for (int i = t; i < q.row0 + q.n; ++i) {
-    for (int g = 0; g < s.group; ++g) {
-      const int h = hk * s.group + g;
-      load_row<BF16>(a.q + i * a.q_stride + h * s.D, s.D, lane, qr);
-      load_row<BF16>(a.dout + i * a.dout_stride + h * s.D, s.D, lane, dor);
-      const size_t at = static_cast<size_t>(h) * s.tokens + i;
-      const float z = a.lse[at], delta = a.delta[at];
-      const float p = z == -INFINITY ? 0.0f : expf(dot(qr, kr) * a.scale - z);
-      const float ds = p * (dot(dor, vr) - delta) * a.scale;
-#pragma unroll
-      for (int e = 0; e < kMaxPerLane; ++e) {
-        gk[e] = fmaf(ds, qr[e], gk[e]);
-        gv[e] = fmaf(p, dor[e], gv[e]);
-      }
-    }
-  }
-  store_row<BF16>(a.dk + t * a.dk_stride + hk * s.D, s.D, lane, gk);
-  store_row<BF16>(a.dv + t * a.dv_stride + hk * s.D, s.D, lane, gv);
-}
-
 constexpr int kWarps = 8;
-dim3 rows_grid(const SeqDesc& s, int heads) { return dim3((s.tokens + kWarps - 1) / kWarps, heads); }
 
 }  // namespace
 
@@ -163,17 +87,6 @@ cudaError_t launch_seq_weights(const SeqAttnArgs& a, bool bf16, cudaStream_t st)
   else
     seq_weights_simple<false><<<grid, kWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
-}
-
-template <bool BF16>
-static cudaError_t bwd_t(const SeqAttnArgs& a, cudaStream_t st) {
-  prompt_delta_simple<BF16><<<rows_grid(a.s, a.s.q_heads), kWarps * 32, 0, st>>>(a);
-  prompt_dq_simple<BF16><<<rows_grid(a.s, a.s.q_heads), kWarps * 32, 0, st>>>(a);
-  prompt_dkv_simple<BF16><<<rows_grid(a.s, a.s.kv_heads), kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
-}
-cudaError_t launch_prompt_bwd(const SeqAttnArgs& a, bool bf16, cudaStream_t st) {
-  return bf16 ? bwd_t<true>(a, st) : bwd_t<false>(a, st);
 }
 
 }  // namespace evo
