@@ -115,7 +115,8 @@ typedef struct {
  * shape.  They depend on the shape and on the current device's number of SMs. */
 EVO_API size_t evo_prompt_fwd_workspace_bytes(evo_seq_shape_t shape);
 EVO_API size_t evo_prompt_bwd_workspace_bytes(evo_seq_shape_t shape);
-EVO_API size_t evo_paged_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache_shape_t cache);
+EVO_API size_t evo_paged_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache_shape_t cache,
+                                             int64_t weights_len /* 0: a call without weights */);
 
 /* Attention over whole prompts: out and lse of every row of a sequence. */
 EVO_API evo_status_t evo_prompt_fwd(const void* q, const void* k, const void* v, const int32_t* cu_seqlens,

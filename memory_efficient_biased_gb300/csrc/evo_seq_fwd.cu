@@ -332,6 +332,17 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&y)[32], float2 sl2, f
   }
 }
 
+// 64 scores, times s·log2 e, for the sums of the weights.
+__device__ __forceinline__ void leave_scores(const uint32_t (&y)[64], float scale_log2, float* to) {
+#pragma unroll
+  for (int x = 0; x < 64; x += 8) {
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(y[x + e]) * scale_log2);
+    st_global_32(to + x, o);
+  }
+}
+
 // The values of V that were taken out of the item's tiles, added to a row that sees them
 // (features c0 .. c0 + 31 of the unscaled O; what is added is an infinity or a NaN).
 template <bool BF16>
@@ -411,6 +422,13 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
         chunk_max<true>(y2, lim - 64, mt);
         chunk_max<true>(y3, lim - 96, mt);
       }
+      if (a.scores && live) {
+        float* to = a.scores + ((static_cast<size_t>(w.row0) + w.t0 + tok) * s.q_heads + w.kvh * s.group + head) * a.scores_ld +
+                    static_cast<size_t>(j) * kTile;
+        leave_scores(ya, scale_log2, to);
+        leave_scores(yb, scale_log2, to + 64);
+      }
+      __syncwarp();
       mt *= scale_log2;  // (a positive factor keeps the max)
       bool moved = false;
       float alpha = 1.0f;

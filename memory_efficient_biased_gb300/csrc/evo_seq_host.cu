@@ -134,6 +134,21 @@ SeqDesc desc(const evo_seq_shape_t& s, const int32_t* cu, const int32_t* lens, c
   return d;
 }
 
+// Scores left behind by the forward for the weights (0: they are formed again).  A row's score is
+// written and read once, 8 bytes a key; forming it again reads 2 head_dim bytes a key, whatever
+// the number of rows.  So: up to 16 rows a key on the average, and only while the
+// scores, sized by the longest length the table can hold, stay below a quarter of the cache.
+long long scores_row(const evo_cache_shape_t& c, int64_t weights_len) {
+  const int64_t most = c.page_size * c.pages_per_seq < weights_len ? c.page_size * c.pages_per_seq : weights_len;
+  return (most + kTile - 1) / kTile * kTile;
+}
+size_t scores_bytes(const evo_seq_shape_t& s, const evo_cache_shape_t& c, int64_t weights_len) {
+  if (weights_len <= 0 || s.tokens * (s.q_heads / s.kv_heads) > 16 * s.seqs) return 0;
+  const double bytes = 4.0 * double(s.tokens) * double(s.q_heads) * double(scores_row(c, weights_len));
+  const double cache = 4.0 * double(c.num_pages) * double(c.page_size) * double(s.kv_heads) * double(s.head_dim);
+  return bytes <= cache / 4 ? (static_cast<size_t>(bytes) + 255) & ~size_t(255) : 0;
+}
+
 // Tensor maps of the forward.
 bool encode16(CUtensorMap* m, const void* base, bool bf16, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
               const cuuint32_t* box, int64_t D) {
@@ -206,10 +221,11 @@ size_t evo_prompt_bwd_workspace_bytes(evo_seq_shape_t shape) {
   return prompt_bwd_workspace(num_sms(), desc(shape, nullptr, nullptr, nullptr, nullptr, -1, nullptr), nullptr, nullptr);
 }
 
-size_t evo_paged_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache_shape_t cache) {
+size_t evo_paged_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache_shape_t cache, int64_t weights_len) {
   int64_t a, b;
-  if (check_seq_shape(shape, true) != EVO_OK || check_cache(cache, shape, &a, &b) != EVO_OK) return 0;
-  return seq_fwd_workspace(num_sms(), static_cast<int>(shape.head_dim), nullptr, nullptr);
+  if (check_seq_shape(shape, true) != EVO_OK || check_cache(cache, shape, &a, &b) != EVO_OK || weights_len < 0) return 0;
+  return seq_fwd_workspace(num_sms(), static_cast<int>(shape.head_dim), nullptr, nullptr) +
+         scores_bytes(shape, cache, weights_len);
 }
 
 evo_status_t evo_prompt_fwd(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, void* out,
@@ -367,7 +383,7 @@ evo_status_t evo_paged_fwd(const void* q, const void* k_pages, const void* v_pag
       !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(lse, 4) ||
       !aligned(weights, 4) || !aligned(workspace, 256) || !aligned(o.status, 4))
     return EVO_ERR_MISALIGNED;
-  if (workspace_bytes < evo_paged_fwd_workspace_bytes(shape, cache)) return EVO_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < evo_paged_fwd_workspace_bytes(shape, cache, weights ? weights_len : 0)) return EVO_ERR_WORKSPACE_TOO_SMALL;
   const int64_t T = shape.tokens, nq = shape.q_heads * shape.head_dim;
   const Span in[] = {strided(q, T, t.q, nq),
                      pages(k_pages, cache, shape, kp),
@@ -389,18 +405,27 @@ evo_status_t evo_paged_fwd(const void* q, const void* k_pages, const void* v_pag
   if (!map_pages(&a.tk, k_pages, bf16, shape, cache, kp) || !map_pages(&a.tv, v_pages, bf16, shape, cache, vp))
     return EVO_ERR_CUDA;
   a.v_page = vp;
+  if (weights && scores_bytes(shape, cache, weights_len)) {
+    a.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                        seq_fwd_workspace(sms, static_cast<int>(shape.head_dim), nullptr, nullptr));
+    a.scores_ld = scores_row(cache, weights_len);
+  }
   st = run_fwd(a, q, v_pages, out, lse, workspace, sms, shape, bf16, t, o, static_cast<cudaStream_t>(stream));
   if (st != EVO_OK || !weights) return st;
-  SeqAttnArgs w{};
+  SeqWeightsArgs w{};
+  w.tq = a.tq, w.tk = a.tk;
   w.s = a.s;
-  w.q = static_cast<const uint16_t*>(q);
-  w.k = static_cast<const uint16_t*>(k_pages);
+  w.TQ = a.TQ;
+  w.scale_log2 = a.scale_log2;
   w.lse = lse;
   w.weights = weights;
   w.weights_len = weights_len;
-  w.q_stride = t.q, w.k_page = kp;
-  w.scale = scale_of(o, shape);
-  const cudaError_t e = launch_seq_weights(w, bf16, static_cast<cudaStream_t>(stream));
+  w.scores = a.scores;
+  w.scores_ld = a.scores_ld;
+  w.records = a.records;
+  w.part = a.part_o;
+  w.wait_ns = o.wait_ns;
+  const cudaError_t e = launch_seq_weights(w, sms, bf16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? EVO_OK : cuda_fail("weight sums launch", e);
 }
 

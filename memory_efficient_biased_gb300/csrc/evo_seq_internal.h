@@ -87,22 +87,6 @@ struct EvictArgs {
   int budget, recent;
 };
 
-// Plain pointers of one attention call; keys and values are token rows or pages.
-struct SeqAttnArgs {
-  SeqDesc s;
-  const uint16_t *q, *k, *v;
-  const uint16_t* dout;
-  uint16_t *out, *dq, *dk, *dv;
-  float* lse;
-  float* delta;
-  float* weights;
-  long long weights_len;
-  long long q_stride, k_stride, v_stride, out_stride, dout_stride, dq_stride, dk_stride, dv_stride;
-  long long k_page, v_page;
-  float scale;
-  uint64_t wait_ns;
-};
-
 struct PieceRecord;
 
 // The forward on the tensor cores.
@@ -122,6 +106,24 @@ struct SeqFwdArgs {
   PieceRecord* records;  // workspace: two per CTA
   float2* part_ml;       // ... [ctas][2][256] (m, l)
   float* part_o;         // ... [ctas][2][256][DP], not yet divided by l
+  float* scores;         // nullable: s·log2e·S left behind for the weights, [tokens][q_heads][scores_ld]
+  long long scores_ld;   // max_kv rounded up to whole tiles
+  uint64_t wait_ns;
+};
+// The sums of the attention weights: from the forward's scores where it left them (scores), else
+// formed again (tq, tk as the forward's).
+struct SeqWeightsArgs {
+  CUtensorMap tq, tk;
+  SeqDesc s;
+  int TQ;
+  float scale_log2;
+  const float* lse;
+  float* weights;
+  long long weights_len;
+  const float* scores;
+  long long scores_ld;
+  PieceRecord* records;  // workspace of the forward, which is done with it
+  float* part;           // ... [ctas][2][128]
   uint64_t wait_ns;
 };
 // Bytes of the workspace for `ctas` CTAs; with a and ws, a's pointers into it.
@@ -148,7 +150,7 @@ size_t prompt_bwd_workspace(int ctas, const SeqDesc& s, SeqBwdArgs* a, uint8_t* 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_seq_fwd(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st);
-cudaError_t launch_seq_weights(const SeqAttnArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_seq_weights(const SeqWeightsArgs& a, int ctas, bool bf16, cudaStream_t st);
 cudaError_t launch_prompt_bwd(const SeqBwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 
 }  // namespace evo

@@ -60,7 +60,7 @@ def load():
     for name, res, args in (
             ("evo_prompt_fwd_workspace_bytes", sz, [SeqShape]),
             ("evo_prompt_bwd_workspace_bytes", sz, [SeqShape]),
-            ("evo_paged_fwd_workspace_bytes", sz, [SeqShape, CacheShape]),
+            ("evo_paged_fwd_workspace_bytes", sz, [SeqShape, CacheShape, i64]),
             ("evo_prompt_fwd", i32, [vp] * 7 + [sz, SeqShape] + tail),
             ("evo_prompt_bwd", i32, [vp] * 11 + [sz, SeqShape] + tail),
             ("evo_cache_append", i32, [vp] * 7 + [SeqShape, CacheShape] + tail),
@@ -268,9 +268,10 @@ def evo_cache_append(k, v, cu_seqlens, seq_lens, k_pages, v_pages, block_table, 
 
 
 def evo_paged_fwd_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim, num_pages, page_size,
-                                  pages_per_seq) -> int:
+                                  pages_per_seq, weights_len=0) -> int:
     return int(load().evo_paged_fwd_workspace_bytes(SeqShape(tokens, seqs, q_heads, kv_heads, head_dim),
-                                                    CacheShape(num_pages, page_size, pages_per_seq, 0, 0)))
+                                                    CacheShape(num_pages, page_size, pages_per_seq, 0, 0),
+                                                    weights_len))
 
 
 def evo_paged_fwd(q, k_pages, v_pages, cu_seqlens, seq_lens, block_table, out=None, lse=None, weights=None,
@@ -304,7 +305,7 @@ def evo_paged_fwd(q, k_pages, v_pages, cu_seqlens, seq_lens, block_table, out=No
             out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
         if lse is None:
             lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-        ws = _workspace(workspace, lib.evo_paged_fwd_workspace_bytes(shape, cache), q.device)
+        ws = _workspace(workspace, lib.evo_paged_fwd_workspace_bytes(shape, cache, wlen), q.device)
     strides = SeqStrides(q=sq, out=_rows(out, "out", q.shape, dt))
     _check(lse, "lse", (Hq, T), torch.float32)
     _done(lib.evo_paged_fwd(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(cu_seqlens), _ptr(seq_lens),

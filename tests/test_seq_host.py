@@ -71,7 +71,7 @@ def paged(lib, s=None, c=None, dt=1, strides=None, o=None, ws_bytes=None, w=None
     s, c = s or shape(), c or cache()
     a = dict(q=A, kp=14 * A, vpg=15 * A, cu=4 * A, lens=12 * A, table=13 * A, out=5 * A, lse=6 * A, ws=7 * A)
     a.update(p)
-    need = lib.evo_paged_fwd_workspace_bytes(s, c) if ws_bytes is None else ws_bytes
+    need = lib.evo_paged_fwd_workspace_bytes(s, c, wlen if w else 0) if ws_bytes is None else ws_bytes
     return lib.evo_paged_fwd(*(vp(a[n]) for n in ("q", "kp", "vpg", "cu", "lens", "table", "out", "lse")), vp(w), wlen,
                              vp(a["ws"]), need, s, c, dt, ref(strides), o, None)
 
@@ -178,8 +178,17 @@ def test_workspace_bytes(lib):
     assert lib.evo_prompt_fwd_workspace_bytes(shape(D=12)) == 0
     assert lib.evo_prompt_bwd_workspace_bytes(shape(Hq=3)) == 0
     assert lib.evo_prompt_bwd_workspace_bytes(shape()) >= 64 * 8 * 4  # delta
-    assert lib.evo_paged_fwd_workspace_bytes(shape(), cache(page=24)) == 0
-    assert lib.evo_paged_fwd_workspace_bytes(shape(), cache()) > 0
+    assert lib.evo_paged_fwd_workspace_bytes(shape(), cache(page=24), 0) == 0
+    assert lib.evo_paged_fwd_workspace_bytes(shape(), cache(), -1) == 0
+    plain = lib.evo_paged_fwd_workspace_bytes(shape(), cache(), 0)
+    assert plain > 0
+    # single tokens: room for the scores ([tokens][q_heads][length, in whole tiles] fp32) with weights ...
+    one, c = shape(T=2), cache(P=40, cols=16)
+    assert lib.evo_paged_fwd_workspace_bytes(one, c, 200) == \
+        lib.evo_paged_fwd_workspace_bytes(one, c, 0) + 2 * 8 * 256 * 4
+    # ... unless they would be large beside the cache, or there are many rows a key
+    assert lib.evo_paged_fwd_workspace_bytes(one, cache(P=2, cols=16), 256) == plain
+    assert lib.evo_paged_fwd_workspace_bytes(shape(T=16), c, 256) == plain
 
 
 def test_binding_refuses_host_tensors_and_shapes():
