@@ -10,7 +10,7 @@
 // result, or wait for one another.  Two kernels keep every sum in tensor memory, in a
 // fixed order, and P and dS (the MMAs' A operands) in tensor memory too.
 //
-//   evo_seq_rows_kernel  (lse·log2e, delta) per row, [tokens][q_heads]
+//   evo_seq_rows_kernel  (-lse·log2e, -delta) per row, [tokens][q_heads]
 //   evo_seq_dkv_kernel   items: 128 keys of a kv head, over the tiles of queries that see
 //                        them (TQ tokens x the heads of the group, as in the forward, which sums
 //                        dK and dV over a group's heads for nothing); Sᵀ = K Qᵀ, dPᵀ = V dOᵀ, a
@@ -204,7 +204,8 @@ __device__ __forceinline__ void walk(const SeqBwdArgs& a, uint8_t* base, Bars* b
 }
 
 // ------------------------------------------------------------ dK, dV: (lse, delta) of each tile of queries
-__device__ __forceinline__ void rows(const SeqBwdArgs& a, float2* buf, Bars* bars, const WaitGuard& g, int lane) {
+// (per stage 128 of -lse·log2 e, then 128 of -delta)
+__device__ __forceinline__ void rows(const SeqBwdArgs& a, float* buf, Bars* bars, const WaitGuard& g, int lane) {
   const SeqDesc& s = a.s;
   int dt[4], head[4];
 #pragma unroll
@@ -219,21 +220,24 @@ __device__ __forceinline__ void rows(const SeqBwdArgs& a, float2* buf, Bars* bar
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = j * a.TQ + dt[e];
-        x[e] = make_float2(INFINITY, 0.0f);  // P = 0
+        x[e] = make_float2(-INFINITY, 0.0f);  // P = 0
         if (dt[e] < a.TQ && t < w.kv_end)
           x[e] = a.rows[static_cast<size_t>(w.row0 + t) * s.q_heads + w.kvh * s.group + head[e]];
       }
       const uint32_t st = n & 1;
       if (!mbar_wait_warp_inl(smem_u32(&bars->rows_empty[st]), ((n >> 1) & 1) ^ 1, g)) return;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) buf[st * kTile + lane + 32 * e] = x[e];
+      for (int e = 0; e < 4; ++e) {
+        buf[st * 2 * kTile + lane + 32 * e] = x[e].x;
+        buf[st * 2 * kTile + kTile + lane + 32 * e] = x[e].y;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->rows_full[st]));
     }
   }
 }
 
-// ------------------------------------------------------------ MMA (one thread)
+// ------------------------------------------------------------ MMA (one warp, one of its threads issuing)
 template <int DP>
 __device__ __forceinline__ uint64_t k_step(int k) {  // 16 features further in a tile, in descriptor units
   return (k & 3) * 2 + (k >> 2) * (Layout<DP>::kHalf / 16);
@@ -242,7 +246,9 @@ __device__ __forceinline__ uint64_t k_step(int k) {  // 16 features further in a
 template <int DP>
 __device__ __forceinline__ void scores(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t id) {
   const uint64_t ad = smem_desc(a, 16, 1024, kSwizzle128B), bd = smem_desc(b, 16, 1024, kSwizzle128B);
-  for (int k = 0; k < steps; ++k) umma_ss(d, ad + k_step<DP>(k), bd + k_step<DP>(k), id, k > 0);
+#pragma unroll
+  for (int k = 0; k < DP / 16; ++k)
+    if (k < steps) umma_ss(d, ad + k_step<DP>(k), bd + k_step<DP>(k), id, k > 0);
 }
 // D (+)= A B over 128 rows or keys, A packed in tensor memory, B a tile (features along N).
 template <int DP>
@@ -262,47 +268,65 @@ __device__ __forceinline__ void mma_dkv(const SeqBwdArgs& a, uint8_t* base, Bars
   bool ok = true;
   // Sᵀ of streamed tile x, and dPᵀ
   auto issue_s = [&](uint32_t x) -> bool {
-    if (!mbar_wait_inl(smem_u32(&bars->ready[x % kReady]), (x / kReady) & 1, g)) return false;
-    if (!mbar_wait_inl(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, g)) return false;
-    if (x > 0 && !mbar_wait_inl(smem_u32(&bars->first_done), (x - 1) & 1, g)) return false;  // P read
+    if (!mbar_wait_warp_inl(smem_u32(&bars->ready[x % kReady]), (x / kReady) & 1, g)) return false;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, g)) return false;
+    if (x > 0 && !mbar_wait_warp_inl(smem_u32(&bars->first_done), (x - 1) & 1, g)) return false;  // P read
     tc_fence_after();
-    scores<DP>(tmem + kColS, ks, smem_u32(base + L::a + (x % kASlots) * L::kTB), steps, id_s);
-    umma_commit(smem_u32(&bars->s_full[0]));
+    if (elect_one()) {
+      scores<DP>(tmem + kColS, ks, smem_u32(base + L::a + (x % kASlots) * L::kTB), steps, id_s);
+      umma_commit(smem_u32(&bars->s_full[0]));
+    }
+    __syncwarp();
     return true;
   };
   auto issue_dp = [&](uint32_t x) -> bool {
-    if (!mbar_wait_inl(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g)) return false;
-    if (x > 0 && !mbar_wait_inl(smem_u32(&bars->second_done), (x - 1) & 1, g)) return false;  // dS read
+    if (!mbar_wait_warp_inl(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g)) return false;
+    if (x > 0 && !mbar_wait_warp_inl(smem_u32(&bars->second_done), (x - 1) & 1, g)) return false;  // dS read
     tc_fence_after();
-    scores<DP>(tmem + kColDp, vs, smem_u32(base + L::b + (x % kBSlots) * L::kTB), steps, id_s);
-    umma_commit(smem_u32(&bars->dp_full));
+    if (elect_one()) {
+      scores<DP>(tmem + kColDp, vs, smem_u32(base + L::b + (x % kBSlots) * L::kTB), steps, id_s);
+      umma_commit(smem_u32(&bars->dp_full));
+    }
+    __syncwarp();
     return true;
   };
   Work w;
-  for (; ok && take<false>(bars, it, g, w); ++it) {
-    give_back(bars, it);
-    if (!mbar_wait_inl(smem_u32(&bars->own_full), it & 1, g)) break;
+  for (; ok && take<true>(bars, it, g, w); ++it) {
+    __syncwarp();
+    if (elect_one()) give_back(bars, it);
+    const int j0 = uniform(w.j0), j1 = uniform(w.j1);
+    if (!mbar_wait_warp_inl(smem_u32(&bars->own_full), it & 1, g)) break;
     if (!issue_s(n) || !issue_dp(n)) break;
-    for (int j = w.j0; j < w.j1; ++j, ++n) {
+    for (int j = j0; j < j1; ++j, ++n) {
       const uint32_t as = n % kASlots, bs = n % kBSlots;
-      if (!mbar_wait_inl(smem_u32(&bars->p_ready), n & 1, g)) { ok = false; break; }
-      if (j == w.j0 && !mbar_wait_inl(smem_u32(&bars->acc_free), (it & 1) ^ 1, g)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->p_ready), n & 1, g)) { ok = false; break; }
+      if (j == j0 && !mbar_wait_warp_inl(smem_u32(&bars->acc_free), (it & 1) ^ 1, g)) { ok = false; break; }
       tc_fence_after();
-      gather<DP>(tmem + kColV, tmem + kColS, smem_u32(base + L::b + bs * L::kTB), id_g, j > w.j0);
-      umma_commit(smem_u32(&bars->first_done));
-      umma_commit(smem_u32(&bars->b_empty[bs]));
-      if (j + 1 < w.j1 && !issue_s(n + 1)) { ok = false; break; }
-      if (!mbar_wait_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
+      if (elect_one()) {
+        gather<DP>(tmem + kColV, tmem + kColS, smem_u32(base + L::b + bs * L::kTB), id_g, j > j0);
+        umma_commit(smem_u32(&bars->first_done));
+        umma_commit(smem_u32(&bars->b_empty[bs]));
+      }
+      __syncwarp();
+      if (j + 1 < j1 && !issue_s(n + 1)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
       tc_fence_after();
-      gather<DP>(tmem + kColK, tmem + kColDp, smem_u32(base + L::a + as * L::kTB), id_g, j > w.j0);
-      umma_commit(smem_u32(&bars->second_done));
-      umma_commit(smem_u32(&bars->a_empty[as]));
-      if (j + 1 < w.j1 && !issue_dp(n + 1)) { ok = false; break; }
+      if (elect_one()) {
+        gather<DP>(tmem + kColK, tmem + kColDp, smem_u32(base + L::a + as * L::kTB), id_g, j > j0);
+        umma_commit(smem_u32(&bars->second_done));
+        umma_commit(smem_u32(&bars->a_empty[as]));
+      }
+      __syncwarp();
+      if (j + 1 < j1 && !issue_dp(n + 1)) { ok = false; break; }
     }
-    umma_commit(smem_u32(&bars->own_empty));
-    umma_commit(smem_u32(&bars->acc_full));
+    if (elect_one()) {
+      umma_commit(smem_u32(&bars->own_empty));
+      umma_commit(smem_u32(&bars->acc_full));
+    }
+    __syncwarp();
   }
-  umma_commit(smem_u32(&bars->drain));
+  __syncwarp();
+  if (elect_one()) umma_commit(smem_u32(&bars->drain));
   drain_wait(smem_u32(&bars->drain), 0, a);
 }
 
@@ -316,45 +340,60 @@ __device__ __forceinline__ void mma_dq(const SeqBwdArgs& a, uint8_t* base, Bars*
   bool ok = true;
   uint32_t gathers = 0;  // issued
   auto issue_s = [&](uint32_t x) -> bool {
-    if (!mbar_wait_inl(smem_u32(&bars->ready[x % kReady]), (x / kReady) & 1, g)) return false;
-    if (!mbar_wait_inl(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, g)) return false;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->ready[x % kReady]), (x / kReady) & 1, g)) return false;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, g)) return false;
     // its buffer held dS of tile x - 2.  The wait is for the newest gather issued (a parity
     // says nothing about an older phase): x - 2's within an item, x - 1's at an item's start
-    if (gathers > 0 && !mbar_wait_inl(smem_u32(&bars->second_done), (gathers - 1) & 1, g)) return false;
+    if (gathers > 0 && !mbar_wait_warp_inl(smem_u32(&bars->second_done), (gathers - 1) & 1, g)) return false;
     tc_fence_after();
-    scores<DP>(tmem + (x & 1) * 128, qs, smem_u32(base + L::a + (x % kASlots) * L::kTB), steps, id_s);
-    umma_commit(smem_u32(&bars->s_full[x & 1]));
+    if (elect_one()) {
+      scores<DP>(tmem + (x & 1) * 128, qs, smem_u32(base + L::a + (x % kASlots) * L::kTB), steps, id_s);
+      umma_commit(smem_u32(&bars->s_full[x & 1]));
+    }
+    __syncwarp();
     return true;
   };
   auto issue_dp = [&](uint32_t x) -> bool {  // (dP of tile x - 1 was read before its dS was ready)
-    if (!mbar_wait_inl(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g)) return false;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g)) return false;
     tc_fence_after();
-    scores<DP>(tmem + kColDp2, dos, smem_u32(base + L::b + (x % kBSlots) * L::kTB), steps, id_s);
-    umma_commit(smem_u32(&bars->dp_full));
-    umma_commit(smem_u32(&bars->b_empty[x % kBSlots]));
+    if (elect_one()) {
+      scores<DP>(tmem + kColDp2, dos, smem_u32(base + L::b + (x % kBSlots) * L::kTB), steps, id_s);
+      umma_commit(smem_u32(&bars->dp_full));
+      umma_commit(smem_u32(&bars->b_empty[x % kBSlots]));
+    }
+    __syncwarp();
     return true;
   };
   Work w;
-  for (; ok && take<false>(bars, it, g, w); ++it) {
-    give_back(bars, it);
-    if (!mbar_wait_inl(smem_u32(&bars->own_full), it & 1, g)) break;
+  for (; ok && take<true>(bars, it, g, w); ++it) {
+    __syncwarp();
+    if (elect_one()) give_back(bars, it);
+    const int j0 = uniform(w.j0), j1 = uniform(w.j1);
+    if (!mbar_wait_warp_inl(smem_u32(&bars->own_full), it & 1, g)) break;
     if (!issue_s(n) || !issue_dp(n)) break;
-    for (int j = w.j0; j < w.j1; ++j, ++n) {
+    for (int j = j0; j < j1; ++j, ++n) {
       const uint32_t as = n % kASlots;
-      if (j + 1 < w.j1 && !issue_s(n + 1)) { ok = false; break; }
-      if (!mbar_wait_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
-      if (j == w.j0 && !mbar_wait_inl(smem_u32(&bars->acc_free), (it & 1) ^ 1, g)) { ok = false; break; }
+      if (j + 1 < j1 && !issue_s(n + 1)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
+      if (j == j0 && !mbar_wait_warp_inl(smem_u32(&bars->acc_free), (it & 1) ^ 1, g)) { ok = false; break; }
       tc_fence_after();
-      gather<DP>(tmem + kColQ, tmem + (n & 1) * 128, smem_u32(base + L::a + as * L::kTB), id_g, j > w.j0);
+      if (elect_one()) {
+        gather<DP>(tmem + kColQ, tmem + (n & 1) * 128, smem_u32(base + L::a + as * L::kTB), id_g, j > j0);
+        umma_commit(smem_u32(&bars->second_done));
+        umma_commit(smem_u32(&bars->a_empty[as]));
+      }
+      __syncwarp();
       ++gathers;
-      umma_commit(smem_u32(&bars->second_done));
-      umma_commit(smem_u32(&bars->a_empty[as]));
-      if (j + 1 < w.j1 && !issue_dp(n + 1)) { ok = false; break; }
+      if (j + 1 < j1 && !issue_dp(n + 1)) { ok = false; break; }
     }
-    umma_commit(smem_u32(&bars->own_empty));
-    umma_commit(smem_u32(&bars->acc_full));
+    if (elect_one()) {
+      umma_commit(smem_u32(&bars->own_empty));
+      umma_commit(smem_u32(&bars->acc_full));
+    }
+    __syncwarp();
   }
-  umma_commit(smem_u32(&bars->drain));
+  __syncwarp();
+  if (elect_one()) umma_commit(smem_u32(&bars->drain));
   drain_wait(smem_u32(&bars->drain), 0, a);
 }
 
@@ -402,9 +441,63 @@ __device__ __forceinline__ void write_row(uint32_t col, int c0, int c1, int D, b
   }
 }
 
+// P = 2^(S·s + nl) of 64 scores in place, nl (-lse·log2 e) per column, and packed; columns below
+// `from` do not see the key.
+template <bool BF16, bool MASK>
+__device__ __forceinline__ void probs(uint32_t (&p)[64], uint32_t (&pp)[32], float2 sl2, const float4* nl, int from) {
+#pragma unroll
+  for (int x = 0; x < 64; x += 4) {
+    const float4 z = nl[x >> 2];
+    const float2 t0 = fma2(make_float2(__uint_as_float(p[x]), __uint_as_float(p[x + 1])), sl2, make_float2(z.x, z.y));
+    const float2 t1 = fma2(make_float2(__uint_as_float(p[x + 2]), __uint_as_float(p[x + 3])), sl2, make_float2(z.z, z.w));
+    float e[4] = {ex2(t0.x), ex2(t0.y), ex2(t1.x), ex2(t1.y)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (MASK && x + i < from) e[i] = 0.0f;
+      p[x + i] = __float_as_uint(e[i]);
+    }
+    pp[x >> 1] = pack2<BF16>(e[0], e[1]);
+    pp[(x >> 1) + 1] = pack2<BF16>(e[2], e[3]);
+  }
+}
+// dS = P (dP + nd) of 32 columns, packed; nd (-delta) per column.
+template <bool BF16, bool MASK>
+__device__ __forceinline__ void dscores(const uint32_t (&d)[32], const uint32_t* p, uint32_t* pp, const float4* nd, int from) {
+#pragma unroll
+  for (int x = 0; x < 32; x += 4) {
+    const float4 z = nd[x >> 2];
+    float2 s0 = mul2(add2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), make_float2(z.x, z.y)),
+                     make_float2(__uint_as_float(p[x]), __uint_as_float(p[x + 1])));
+    float2 s1 = mul2(add2(make_float2(__uint_as_float(d[x + 2]), __uint_as_float(d[x + 3])), make_float2(z.z, z.w)),
+                     make_float2(__uint_as_float(p[x + 2]), __uint_as_float(p[x + 3])));
+    if (MASK) {
+      if (x < from) s0.x = 0.0f;
+      if (x + 1 < from) s0.y = 0.0f;
+      if (x + 2 < from) s1.x = 0.0f;
+      if (x + 3 < from) s1.y = 0.0f;
+    }
+    pp[x >> 1] = pack2<BF16>(s0.x, s0.y);
+    pp[(x >> 1) + 1] = pack2<BF16>(s1.x, s1.y);
+  }
+}
+// The same with one row's delta; columns past `lim` are not seen.
+template <bool BF16, bool MASK>
+__device__ __forceinline__ void dscores_row(const uint32_t (&d)[32], const uint32_t* p, uint32_t* pp, float2 nd, int lim) {
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) {
+    float2 ds = mul2(add2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), nd),
+                     make_float2(__uint_as_float(p[x]), __uint_as_float(p[x + 1])));
+    if (MASK) {
+      if (x > lim) ds.x = 0.0f;
+      if (x + 1 > lim) ds.y = 0.0f;
+    }
+    pp[x >> 1] = pack2<BF16>(ds.x, ds.y);
+  }
+}
+
 // dK, dV.  Thread: key r of the tile, rows 64·grp .. 64·grp + 63 of each tile of queries.
 template <int DP, bool BF16>
-__device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float2* rowbuf, Bars* bars, uint32_t tmem,
+__device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float* rowbuf, Bars* bars, uint32_t tmem,
                                             const WaitGuard& g) {
   const SeqDesc& s = a.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -421,7 +514,8 @@ __device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float2* r
     const int key = w.t0 + r;
     for (int j = w.j0; j < w.j1; ++j, ++n) {
       const uint32_t st = n & 1;
-      const float4* rb = reinterpret_cast<const float4*>(rowbuf + st * kTile + grp * 64);
+      const float4* nl = reinterpret_cast<const float4*>(rowbuf + st * 2 * kTile + grp * 64);
+      const float4* nd = reinterpret_cast<const float4*>(rowbuf + st * 2 * kTile + kTile + grp * 64);
       // rows below `from` belong to tokens in front of the key; none does once the tile lies behind the keys
       const bool mask = j * a.TQ < w.t0 + kTile - 1;
       const int from = (key - j * a.TQ) * s.group - grp * 64;
@@ -433,19 +527,10 @@ __device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float2* r
       tmem_wait_ld(p);
       {
         uint32_t pp[32];
-#pragma unroll
-        for (int x = 0; x < 64; x += 2) {
-          const float4 z = rb[x >> 1];  // (lse, delta) of two rows
-          const float2 t = fma2(make_float2(__uint_as_float(p[x]), __uint_as_float(p[x + 1])), sl2, make_float2(-z.x, -z.z));
-          float p0 = ex2(t.x), p1 = ex2(t.y);
-          if (mask) {
-            if (x < from) p0 = 0.0f;
-            if (x + 1 < from) p1 = 0.0f;
-          }
-          p[x] = __float_as_uint(p0);
-          p[x + 1] = __float_as_uint(p1);
-          pp[x >> 1] = pack2<BF16>(p0, p1);
-        }
+        if (mask)
+          probs<BF16, true>(p, pp, sl2, nl, from);
+        else
+          probs<BF16, false>(p, pp, sl2, nl, 0);
         tmem_st32(scol, pp);
       }
       tmem_wait_st();
@@ -461,17 +546,10 @@ __device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float2* r
           uint32_t d[32];
           tmem_ld32(dcol + h, d);
           tmem_wait_ld(d);
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const float4 z = rb[(h + x) >> 1];
-            const float2 t = add2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), make_float2(-z.y, -z.w));
-            float2 ds = mul2(t, make_float2(__uint_as_float(p[h + x]), __uint_as_float(p[h + x + 1])));
-            if (mask) {
-              if (h + x < from) ds.x = 0.0f;
-              if (h + x + 1 < from) ds.y = 0.0f;
-            }
-            pp[(h + x) >> 1] = pack2<BF16>(ds.x, ds.y);
-          }
+          if (mask)
+            dscores<BF16, true>(d, p + h, pp + h / 2, nd + h / 4, from - h);
+          else
+            dscores<BF16, false>(d, p + h, pp + h / 2, nd + h / 4, 0);
         }
         tmem_st32(dcol, pp);
       }
@@ -516,9 +594,9 @@ __device__ __forceinline__ void compute_dq(const SeqBwdArgs& a, Bars* bars, uint
     const bool live = dt < a.TQ && dt < w.nt;
     const size_t row = static_cast<size_t>(w.row0) + w.t0 + dt;
     const int h = w.kvh * s.group + head;
-    float2 z = make_float2(INFINITY, 0.0f);
+    float2 z = make_float2(-INFINITY, 0.0f);
     if (live) z = a.rows[row * s.q_heads + h];
-    const float2 nl = make_float2(-z.x, -z.x), nd = make_float2(-z.y, -z.y);
+    const float2 nl = make_float2(z.x, z.x), nd = make_float2(z.y, z.y);
     for (int j = w.j0; j < w.j1; ++j, ++n) {
       const uint32_t scol = trow + (n & 1) * 128 + grp * 64;
       const bool mask = w.pos < j * kTile + kTile - 1;
@@ -542,16 +620,10 @@ __device__ __forceinline__ void compute_dq(const SeqBwdArgs& a, Bars* bars, uint
         uint32_t d[32];
         tmem_ld32(dcol + q, d);
         tmem_wait_ld(d);
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          const float2 t = add2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), nd);
-          float2 ds = mul2(t, make_float2(__uint_as_float(p[q + x]), __uint_as_float(p[q + x + 1])));
-          if (mask) {
-            if (q + x > lim) ds.x = 0.0f;
-            if (q + x + 1 > lim) ds.y = 0.0f;
-          }
-          pp[(q + x) >> 1] = pack2<BF16>(ds.x, ds.y);
-        }
+        if (mask)
+          dscores_row<BF16, true>(d, p + q, pp + q / 2, nd, lim - q);
+        else
+          dscores_row<BF16, false>(d, p + q, pp + q / 2, nd, 0);
       }
       tmem_st32(scol, pp);
       tmem_wait_st();
@@ -632,20 +704,17 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
   const WaitGuard g{a.wait_ns, a.s.status, &bars->abort};
-  float2* rowbuf = reinterpret_cast<float2*>(base + L::rows);
+  float* rowbuf = reinterpret_cast<float*>(base + L::rows);
   if (warp >= kProducerWarp) {
     setmaxnreg_dec<kRegsOther>();
     if (warp == kProducerWarp) {
       if (lane == 0) producer<DP, DKV>(a, base, bars, g);
       __syncwarp();
     } else if (warp == kMmaWarp) {
-      if (lane == 0) {
-        if (DKV)
-          mma_dkv<DP, BF16>(a, base, bars, tmem, g);
-        else
-          mma_dq<DP, BF16>(a, base, bars, tmem, g);
-      }
-      __syncwarp();
+      if (DKV)
+        mma_dkv<DP, BF16>(a, base, bars, tmem, g);
+      else
+        mma_dq<DP, BF16>(a, base, bars, tmem, g);
     } else if (warp == kRowsWarp) {
       if (DKV) rows(a, rowbuf, bars, g, lane);
     } else {
@@ -681,10 +750,11 @@ __global__ void __launch_bounds__(256) evo_seq_bwd_join_kernel(const __grid_cons
     if (p.ends) break;
   }
   constexpr int kParts = DKV ? 2 : 1;
-  for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < kParts * kTile; i += gridDim.y * 8) {
+  {
+    const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int part = i / kTile, r = i % kTile;
     const int tok = DKV ? r : r / s.group;
-    if (tok >= first.nt || (!DKV && tok >= a.TQ)) continue;
+    if (tok >= first.nt || (!DKV && tok >= a.TQ)) return;
     float x[DP / 32] = {};
     for (int p = 0; p < pieces; ++p) {
       const float* y = a.part + (((static_cast<size_t>(c0 + p) * 2 + (p == 0)) * kParts + part) * kTile + r) * DP;
@@ -727,7 +797,7 @@ __global__ void __launch_bounds__(256) evo_seq_rows_kernel(const __grid_constant
   for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   if (in && c == 0) {
     const float z = a.lse[static_cast<size_t>(h) * s.tokens + t];
-    a.rows[i] = make_float2(z == -INFINITY ? INFINITY : z * kSeqLog2e, d);
+    a.rows[i] = make_float2(z == -INFINITY ? -INFINITY : -z * kSeqLog2e, -d);
   }
 }
 
@@ -741,7 +811,7 @@ cudaError_t launch_k(const SeqBwdArgs& a, int ctas, cudaStream_t st) {
   const size_t smem = Layout<DP>::total > 118784 ? Layout<DP>::total : 118784;
   kern<<<ctas, kThreads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  evo_seq_bwd_join_kernel<DP, BF16, DKV><<<dim3(ctas, 4), 256, 0, st>>>(a, ctas);
+  evo_seq_bwd_join_kernel<DP, BF16, DKV><<<dim3(ctas, (DKV ? 2 : 1) * kTile / 8), 256, 0, st>>>(a, ctas);
   return cudaGetLastError();
 }
 template <int DP, bool BF16>

@@ -44,7 +44,7 @@ struct Bars {
   uint64_t q_full, q_empty;
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t v_ready[kReady];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], drain[2];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], drain[2], turn[2];
   Work work[kDescs];
   int dirty[kDescs];  // a V tile of the item held values that were taken out
   uint32_t tmem_slot;
@@ -157,7 +157,7 @@ __device__ __forceinline__ void producer(const SeqFwdArgs& a, uint8_t* base, Bar
   if (queries > 0) drain_wait(smem_u32(&bars->q_full), (queries - 1) & 1, a);
 }
 
-// ------------------------------------------------------------ MMA (one thread per tile)
+// ------------------------------------------------------------ MMA (one warp per tile, one of its threads issuing)
 template <int DP, bool BF16>
 __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* bars, uint32_t tmem, uint32_t gq,
                                     const WaitGuard& g) {
@@ -169,49 +169,61 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
   uint32_t n = 0, u = 0, it = 0, own = 0;
   bool ok = true;
   Work w;
-  for (; ok && take<false>(bars, it, g, w); ++it) {
-    give_back(bars, it);
-    int mine = tiles_of(w, static_cast<int>(gq), a.TQ);
-    if (mine > w.j1) mine = w.j1;
-    if (!mbar_wait_inl(smem_u32(&bars->q_full), it & 1, g)) break;
+  for (; ok && take<true>(bars, it, g, w); ++it) {
+    __syncwarp();
+    if (elect_one()) give_back(bars, it);
+    const int j0 = uniform(w.j0), j1 = uniform(w.j1);
+    int mine = uniform(tiles_of(w, static_cast<int>(gq), a.TQ));
+    if (mine > j1) mine = j1;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->q_full), it & 1, g)) break;
     tc_fence_after();
-    if (mine <= w.j0) mbar_arrive(smem_u32(&bars->q_empty));
-    for (int j = w.j0; j < w.j1; ++j, ++n) {
+    if (mine <= j0 && elect_one()) mbar_arrive(smem_u32(&bars->q_empty));
+    __syncwarp();
+    for (int j = j0; j < j1; ++j, ++n) {
       const uint32_t uk = 2 * n, uv = 2 * n + 1, ks = uk % L::kSlots, vs = uv % L::kSlots;
-      if (!mbar_wait_inl(smem_u32(&bars->full[ks]), (uk / L::kSlots) & 1, g)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->full[ks]), (uk / L::kSlots) & 1, g)) { ok = false; break; }
       if (j >= mine) {  // the other tile's
-        mbar_arrive(smem_u32(&bars->empty[ks]));
-        if (!mbar_wait_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
-        mbar_arrive(smem_u32(&bars->empty[vs]));
+        if (elect_one()) mbar_arrive(smem_u32(&bars->empty[ks]));
+        if (!mbar_wait_warp_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
+        if (elect_one()) mbar_arrive(smem_u32(&bars->empty[vs]));
+        __syncwarp();
         continue;
       }
       // S takes the place of the previous P, which its P·V must have read
-      if (u > 0 && !mbar_wait_inl(smem_u32(&bars->pv_done[gq]), (u - 1) & 1, g)) { ok = false; break; }
+      if (u > 0 && !mbar_wait_warp_inl(smem_u32(&bars->pv_done[gq]), (u - 1) & 1, g)) { ok = false; break; }
       tc_fence_after();
       const uint64_t kd = smem_desc(smem_u32(base + L::ring + ks * L::kTB), 16, 1024, kSwizzle128B);
-      for (int k = 0; k < steps; ++k) {
-        const uint64_t o = (k & 3) * 2 + (k >> 2) * (L::kHalf / 16);
-        umma_ss(tmem + col_s(gq), qd + o, kd + o, id_s, k > 0);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint64_t o = (k & 3) * 2 + (k >> 2) * (L::kHalf / 16);
+          if (k < steps) umma_ss(tmem + col_s(gq), qd + o, kd + o, id_s, k > 0);
+        }
+        umma_commit(smem_u32(&bars->s_full[gq]));
+        umma_commit(smem_u32(&bars->empty[ks]));
+        if (j == mine - 1) umma_commit(smem_u32(&bars->q_empty));
       }
-      umma_commit(smem_u32(&bars->s_full[gq]));
-      umma_commit(smem_u32(&bars->empty[ks]));
-      if (j == mine - 1) umma_commit(smem_u32(&bars->q_empty));
-      if (!mbar_wait_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
-      if (!mbar_wait_inl(smem_u32(&bars->full[vs]), (uv / L::kSlots) & 1, g)) { ok = false; break; }
-      if (!mbar_wait_inl(smem_u32(&bars->p_full[gq]), u & 1, g)) { ok = false; break; }
-      if (j == w.j0 && !mbar_wait_inl(smem_u32(&bars->o_free[gq]), (own & 1) ^ 1, g)) { ok = false; break; }
+      __syncwarp();
+      if (!mbar_wait_warp_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->full[vs]), (uv / L::kSlots) & 1, g)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->p_full[gq]), u & 1, g)) { ok = false; break; }
+      if (j == j0 && !mbar_wait_warp_inl(smem_u32(&bars->o_free[gq]), (own & 1) ^ 1, g)) { ok = false; break; }
       tc_fence_after();
       const uint64_t vd = smem_desc(smem_u32(base + L::ring + vs * L::kTB), L::kHalf, 1024, kSwizzle128B);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)  // 128 keys in steps of 16 (8 columns of packed pairs)
-        umma_ts(tmem + col_o(gq), tmem + col_s(gq) + k * 8, vd + k * (2048 / 16), id_o, (j > w.j0 || k > 0) ? 1u : 0u);
-      umma_commit(smem_u32(&bars->pv_done[gq]));
-      umma_commit(smem_u32(&bars->empty[vs]));
+        for (int k = 0; k < 8; ++k)  // 128 keys in steps of 16 (8 columns of packed pairs)
+          umma_ts(tmem + col_o(gq), tmem + col_s(gq) + k * 8, vd + k * (2048 / 16), id_o, (j > j0 || k > 0) ? 1u : 0u);
+        umma_commit(smem_u32(&bars->pv_done[gq]));
+        umma_commit(smem_u32(&bars->empty[vs]));
+      }
+      __syncwarp();
       ++u;
     }
-    if (mine > w.j0) ++own;
+    if (mine > j0) ++own;
   }
-  umma_commit(smem_u32(&bars->drain[gq]));
+  __syncwarp();
+  if (elect_one()) umma_commit(smem_u32(&bars->drain[gq]));
   drain_wait(smem_u32(&bars->drain[gq]), 0, a);
 }
 
@@ -275,7 +287,10 @@ __device__ __forceinline__ void walk(const SeqFwdArgs& a, uint8_t* base, Bars* b
     if (more && !publish(ring[1])) return;
     const Work w = ring[0];
     for (int j = w.j0; j < w.j1; ++j, ++n) {
-      const uint32_t uv = 2 * n + 1, slot = uv % L::kSlots;
+      // (K's arrival too: keys and values take turns in a slot, and a wait by parity has to
+      // follow every phase of its barrier)
+      const uint32_t uk = 2 * n, uv = 2 * n + 1, slot = uv % L::kSlots;
+      if (!mbar_wait_warp_inl(smem_u32(&bars->full[uk % L::kSlots]), (uk / L::kSlots) & 1, g)) return;
       if (!mbar_wait_warp_inl(smem_u32(&bars->full[slot]), (uv / L::kSlots) & 1, g)) return;
       const int last = w.kv_end - j * kTile;      // rows of the tile that some query sees
       const int all = w.pos + 1 - j * kTile;      // ... that every query sees
@@ -384,11 +399,11 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
   const int dt = r / s.group, head = r % s.group;  // token within the tile, head within the group
   const float scale_log2 = a.scale_log2;
   const float2 sl2 = make_float2(scale_log2, scale_log2);
-  uint32_t u = 0, it = 0;
+  uint32_t u = 0, it = 0, turns = 0;
   bool ok = true;
   Work w;
   for (; ok && take<true>(bars, it, g, w); ++it) {
-    int mine = tiles_of(w, gq, a.TQ);
+    int mine = tiles_of(w, gq, a.TQ), other = tiles_of(w, gq ^ 1, a.TQ);
     if (mine > w.j1) mine = w.j1;
     const int tok = gq * a.TQ + dt;              // token within the block
     const bool live = dt < a.TQ && tok < w.nt;
@@ -440,6 +455,10 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
       }
       const float2 nm2 = make_float2(-m, -m);
       float2 rs = make_float2(0.0f, 0.0f);
+      // The two tiles take turns for the exponentials, tile 0 first: without that their phases
+      // fall into step, and the tensor core idles while both compute.
+      const bool both = j < other;
+      if (both && !mbar_wait_warp_inl(smem_u32(&bars->turn[gq]), (turns & 1) ^ (gq ^ 1), g)) { ok = false; break; }
       {
         uint32_t pp[32];
         uint32_t(&p0)[16] = *reinterpret_cast<uint32_t(*)[16]>(&pp[0]);
@@ -448,6 +467,11 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
         chunk_exp<BF16>(y1, sl2, nm2, p1, rs);
         tmem_st32(scol, pp);
         chunk_exp<BF16>(y2, sl2, nm2, p0, rs);
+        if (both) {  // handed over a little early
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->turn[gq ^ 1]));
+          ++turns;
+        }
         chunk_exp<BF16>(y3, sl2, nm2, p1, rs);
         tmem_st32(scol + 32, pp);
       }
@@ -553,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_c
       mbar_init(smem_u32(&bars->pv_done[i]), 1);
       mbar_init(smem_u32(&bars->o_free[i]), 4);
       mbar_init(smem_u32(&bars->drain[i]), 1);
+      mbar_init(smem_u32(&bars->turn[i]), 4);
     }
     fence_barrier_init();
   }
@@ -576,8 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_c
     } else if (warp == kWalkWarp) {
       walk<DP, BF16>(a, base, bars, g, lane);
     } else {
-      if (lane == 0) mma<DP, BF16>(a, base, bars, tmem, static_cast<uint32_t>(warp - kMmaWarp), g);
-      __syncwarp();
+      mma<DP, BF16>(a, base, bars, tmem, static_cast<uint32_t>(uniform(warp) - kMmaWarp), g);
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
@@ -609,9 +633,10 @@ __global__ void __launch_bounds__(kJoinRows * 32) evo_seq_join_kernel(const __gr
     ++pieces;
     if (p.ends) break;
   }
-  for (int i = blockIdx.y * kJoinRows + (threadIdx.x >> 5); i < 256; i += gridDim.y * kJoinRows) {
+  {
+    const int i = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
     const int gq = i >> 7, r = i & 127, dt = r / s.group, tok = gq * a.TQ + dt;
-    if (dt >= a.TQ || tok >= first.nt) continue;
+    if (dt >= a.TQ || tok >= first.nt) return;
     auto at = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * 256 + i; };
     float big = -INFINITY;
     for (int p = 0; p < pieces; ++p) {
@@ -654,7 +679,7 @@ cudaError_t launch_t(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
   kern<<<ctas, kThreads, Layout<DP>::total + 1024, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  evo_seq_join_kernel<DP, BF16><<<dim3(ctas, 4), kJoinRows * 32, 0, st>>>(a, ctas);
+  evo_seq_join_kernel<DP, BF16><<<dim3(ctas, 256 / kJoinRows), kJoinRows * 32, 0, st>>>(a, ctas);
   return cudaGetLastError();
 }
 

@@ -141,7 +141,7 @@ struct SeqBwdArgs {
   uint16_t *dq, *dk, *dv;
   long long out_stride, dout_stride, dq_stride, dk_stride, dv_stride;
   PieceRecord* records;  // workspace: two per CTA
-  float2* rows;          // ... [tokens][q_heads] (lse·log2 e, delta)
+  float2* rows;          // ... [tokens][q_heads] (-lse·log2 e, -delta)
   float* part;           // ... [ctas][2][dV, dK][128][DP], then [ctas][2][128][DP]
   uint64_t wait_ns;
 };

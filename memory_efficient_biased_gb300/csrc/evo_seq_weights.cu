@@ -138,31 +138,39 @@ __device__ __forceinline__ void mma(const SeqWeightsArgs& a, uint8_t* base, Bars
   uint32_t n = 0, it = 0;
   bool ok = true;
   Work w;
-  for (; ok && take<false>(bars, it, g, w); ++it) {
-    give_back(bars, it);
+  for (; ok && take<true>(bars, it, g, w); ++it) {
+    __syncwarp();
+    if (elect_one()) give_back(bars, it);
+    const int j0 = uniform(w.j0), j1 = uniform(w.j1);
     const uint32_t ks = it & 1;
-    if (!mbar_wait_inl(smem_u32(&bars->k_full[ks]), (it >> 1) & 1, g)) break;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->k_full[ks]), (it >> 1) & 1, g)) break;
     const uint64_t kd = smem_desc(smem_u32(base + L::k + ks * L::kTB), 16, 1024, kSwizzle128B);
-    for (int j = w.j0; j < w.j1; ++j, ++n) {
+    for (int j = j0; j < j1; ++j, ++n) {
       const uint32_t st = n % kSlots;
-      if (!mbar_wait_inl(smem_u32(&bars->q_full[st]), (n / kSlots) & 1, g)) { ok = false; break; }
-      if (!mbar_wait_inl(smem_u32(&bars->s_free[n & 1]), ((n >> 1) & 1) ^ 1, g)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->q_full[st]), (n / kSlots) & 1, g)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->s_free[n & 1]), ((n >> 1) & 1) ^ 1, g)) { ok = false; break; }
       tc_fence_after();
       const uint64_t qd = smem_desc(smem_u32(base + L::q + st * L::kTB), 16, 1024, kSwizzle128B);
-      for (int k = 0; k < steps; ++k) {
-        const uint64_t o = (k & 3) * 2 + (k >> 2) * (L::kHalf / 16);
-        umma_ss(tmem + (n & 1) * 128, kd + o, qd + o, id, k > 0);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint64_t o = (k & 3) * 2 + (k >> 2) * (L::kHalf / 16);
+          if (k < steps) umma_ss(tmem + (n & 1) * 128, kd + o, qd + o, id, k > 0);
+        }
+        umma_commit(smem_u32(&bars->s_full[n & 1]));
+        umma_commit(smem_u32(&bars->q_empty[st]));
       }
-      umma_commit(smem_u32(&bars->s_full[n & 1]));
-      umma_commit(smem_u32(&bars->q_empty[st]));
+      __syncwarp();
     }
-    umma_commit(smem_u32(&bars->k_empty[ks]));
+    __syncwarp();
+    if (elect_one()) umma_commit(smem_u32(&bars->k_empty[ks]));
   }
-  umma_commit(smem_u32(&bars->drain));
+  __syncwarp();
+  if (elect_one()) umma_commit(smem_u32(&bars->drain));
   drain_wait(smem_u32(&bars->drain), 0, a);
 }
 
-// log2e·lse of each tile of queries; +inf (P = 0) for a row that saw nothing.
+// -log2e·lse of each tile of queries; -inf (P = 0) for a row that saw nothing.
 __device__ __forceinline__ void rows(const SeqWeightsArgs& a, float* buf, Bars* bars, const WaitGuard& g, int lane) {
   const SeqDesc& s = a.s;
   int dt[4], head[4];
@@ -178,10 +186,10 @@ __device__ __forceinline__ void rows(const SeqWeightsArgs& a, float* buf, Bars* 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = j * a.TQ + dt[e];
-        x[e] = INFINITY;
+        x[e] = -INFINITY;
         if (dt[e] < a.TQ && t < w.kv_end) {
           const float z = a.lse[static_cast<size_t>(w.kvh * s.group + head[e]) * s.tokens + w.row0 + t];
-          if (z != -INFINITY) x[e] = z * kSeqLog2e;
+          if (z != -INFINITY) x[e] = -z * kSeqLog2e;
         }
       }
       const uint32_t st = n & 1;
@@ -210,6 +218,27 @@ __device__ __forceinline__ void walk(const SeqWeightsArgs& a, Bars* bars, const 
       mbar_arrive(smem_u32(&bars->desc_full[s]));
     }
     if (w.stop) return;
+  }
+}
+
+// Σ 2^(S·s + nl) over 64 columns, nl (-lse·log2 e) per column, of those in [from, to).
+template <bool MASK>
+__device__ __forceinline__ void add_probs(const uint32_t (&y)[64], float2 sl2, const float4* nl, int from, int to,
+                                          float2 (&acc)[2]) {
+#pragma unroll
+  for (int x = 0; x < 64; x += 4) {
+    const float4 z = nl[x >> 2];
+    const float2 t0 = fma2(make_float2(__uint_as_float(y[x]), __uint_as_float(y[x + 1])), sl2, make_float2(z.x, z.y));
+    const float2 t1 = fma2(make_float2(__uint_as_float(y[x + 2]), __uint_as_float(y[x + 3])), sl2, make_float2(z.z, z.w));
+    float2 p0 = make_float2(ex2(t0.x), ex2(t0.y)), p1 = make_float2(ex2(t1.x), ex2(t1.y));
+    if (MASK) {
+      if (x < from || x >= to) p0.x = 0.0f;
+      if (x + 1 < from || x + 1 >= to) p0.y = 0.0f;
+      if (x + 2 < from || x + 2 >= to) p1.x = 0.0f;
+      if (x + 3 < from || x + 3 >= to) p1.y = 0.0f;
+    }
+    acc[0] = add2(acc[0], p0);
+    acc[1] = add2(acc[1], p1);
   }
 }
 
@@ -246,21 +275,10 @@ __device__ __forceinline__ void compute(const SeqWeightsArgs& a, const float* ro
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[st]));
       float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-      for (int x = 0; x < 64; x += 4) {
-        const float4 z = rb[x >> 2];
-        const float2 t0 = fma2(make_float2(__uint_as_float(y[x]), __uint_as_float(y[x + 1])), sl2, make_float2(-z.x, -z.y));
-        const float2 t1 = fma2(make_float2(__uint_as_float(y[x + 2]), __uint_as_float(y[x + 3])), sl2, make_float2(-z.z, -z.w));
-        float2 p0 = make_float2(ex2(t0.x), ex2(t0.y)), p1 = make_float2(ex2(t1.x), ex2(t1.y));
-        if (mask) {
-          if (x < from || x >= to) p0.x = 0.0f;
-          if (x + 1 < from || x + 1 >= to) p0.y = 0.0f;
-          if (x + 2 < from || x + 2 >= to) p1.x = 0.0f;
-          if (x + 3 < from || x + 3 >= to) p1.y = 0.0f;
-        }
-        acc[0] = add2(acc[0], p0);
-        acc[1] = add2(acc[1], p1);
-      }
+      if (mask)
+        add_probs<true>(y, sl2, rb, from, to, acc);
+      else
+        add_probs<false>(y, sl2, rb, 0, 0, acc);
       sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->rows_empty[st]));
@@ -332,8 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_weights_kernel(const __gr
   if (warp == kProducerWarp) {
     producer<DP>(a, base, bars, g, lane);
   } else if (warp == kMmaWarp) {
-    if (lane == 0) mma<DP, BF16>(a, base, bars, tmem, g);
-    __syncwarp();
+    mma<DP, BF16>(a, base, bars, tmem, g);
   } else if (warp == kRowsWarp) {
     rows(a, rowbuf, bars, g, lane);
   } else if (warp > kRowsWarp) {
