@@ -46,8 +46,8 @@ struct Bars {
   uint64_t b_full[kBSlots], b_empty[kBSlots];        // streamed: dO or V
   uint64_t ready[kReady];                            // a pair of streamed tiles, cleaned
   uint64_t rows_full[2], rows_empty[2];              // dK/dV: (lse, delta) of a tile of queries
-  uint64_t s_full[2], dp_full, p_ready, ds_ready;
-  uint64_t first_done, second_done;                  // P·dO has read P; dS·(Q or K) has read dS
+  uint64_t s_full[2], dp_full, p_ready, dp_free, ds_ready;
+  uint64_t second_done;                              // dS·(Q or K), and all before it, is done
   uint64_t acc_full, acc_free, drain;
   Work work[kDescs];
   uint32_t tmem_slot;
@@ -64,10 +64,14 @@ struct Layout {
 };
 static_assert(Layout<128>::total <= 232448, "shared memory");
 
-// Tensor memory columns.  P and dS, as packed pairs, take the place of the scores they were
-// made from, each warpgroup's in its own half.
-constexpr uint32_t kColS = 0, kColDp = 128, kColV = 256, kColK = 384;   // dK/dV
-constexpr uint32_t kColDp2 = 256, kColQ = 384;                          // dQ: S in 0 and 128 by turns
+// Tensor memory columns.  P and dS, as packed pairs, take the place of the scores that they were
+// made from, each warpgroup's in its own half (P its first, dS its second 32 columns).
+//   dK/dV  two regions of 128 by turns: tile x has Sᵀ, then P and dS, in region x & 1, and dPᵀ in the
+//          other, so Sᵀ of x + 1 (where dPᵀ of x was) waits only for dPᵀ to be loaded, and
+//          dPᵀ of x + 1 for the gradients of x
+//   dQ     S, then dS, in region x & 1; dP in a third
+constexpr uint32_t kColV = 256, kColK = 384;    // dK/dV
+constexpr uint32_t kColDp2 = 256, kColQ = 384;  // dQ
 __device__ __forceinline__ uint32_t packed_col(int k) {  // 16 rows or keys from 16·k on
   return k < 4 ? k * 8 : 64 + (k - 4) * 8;
 }
@@ -270,10 +274,10 @@ __device__ __forceinline__ void mma_dkv(const SeqBwdArgs& a, uint8_t* base, Bars
   auto issue_s = [&](uint32_t x) -> bool {
     if (!mbar_wait_warp_inl(smem_u32(&bars->ready[x % kReady]), (x / kReady) & 1, g)) return false;
     if (!mbar_wait_warp_inl(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, g)) return false;
-    if (x > 0 && !mbar_wait_warp_inl(smem_u32(&bars->first_done), (x - 1) & 1, g)) return false;  // P read
+    if (x > 0 && !mbar_wait_warp_inl(smem_u32(&bars->dp_free), (x - 1) & 1, g)) return false;
     tc_fence_after();
     if (elect_one()) {
-      scores<DP>(tmem + kColS, ks, smem_u32(base + L::a + (x % kASlots) * L::kTB), steps, id_s);
+      scores<DP>(tmem + (x & 1) * 128, ks, smem_u32(base + L::a + (x % kASlots) * L::kTB), steps, id_s);
       umma_commit(smem_u32(&bars->s_full[0]));
     }
     __syncwarp();
@@ -281,10 +285,10 @@ __device__ __forceinline__ void mma_dkv(const SeqBwdArgs& a, uint8_t* base, Bars
   };
   auto issue_dp = [&](uint32_t x) -> bool {
     if (!mbar_wait_warp_inl(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g)) return false;
-    if (x > 0 && !mbar_wait_warp_inl(smem_u32(&bars->second_done), (x - 1) & 1, g)) return false;  // dS read
+    if (x > 0 && !mbar_wait_warp_inl(smem_u32(&bars->second_done), (x - 1) & 1, g)) return false;
     tc_fence_after();
     if (elect_one()) {
-      scores<DP>(tmem + kColDp, vs, smem_u32(base + L::b + (x % kBSlots) * L::kTB), steps, id_s);
+      scores<DP>(tmem + (~x & 1) * 128, vs, smem_u32(base + L::b + (x % kBSlots) * L::kTB), steps, id_s);
       umma_commit(smem_u32(&bars->dp_full));
     }
     __syncwarp();
@@ -303,8 +307,7 @@ __device__ __forceinline__ void mma_dkv(const SeqBwdArgs& a, uint8_t* base, Bars
       if (j == j0 && !mbar_wait_warp_inl(smem_u32(&bars->acc_free), (it & 1) ^ 1, g)) { ok = false; break; }
       tc_fence_after();
       if (elect_one()) {
-        gather<DP>(tmem + kColV, tmem + kColS, smem_u32(base + L::b + bs * L::kTB), id_g, j > j0);
-        umma_commit(smem_u32(&bars->first_done));
+        gather<DP>(tmem + kColV, tmem + (n & 1) * 128, smem_u32(base + L::b + bs * L::kTB), id_g, j > j0);
         umma_commit(smem_u32(&bars->b_empty[bs]));
       }
       __syncwarp();
@@ -312,7 +315,7 @@ __device__ __forceinline__ void mma_dkv(const SeqBwdArgs& a, uint8_t* base, Bars
       if (!mbar_wait_warp_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
       tc_fence_after();
       if (elect_one()) {
-        gather<DP>(tmem + kColK, tmem + kColDp, smem_u32(base + L::a + as * L::kTB), id_g, j > j0);
+        gather<DP>(tmem + kColK, tmem + (n & 1) * 128 + 32, smem_u32(base + L::a + as * L::kTB), id_g, j > j0);
         umma_commit(smem_u32(&bars->second_done));
         umma_commit(smem_u32(&bars->a_empty[as]));
       }
@@ -353,8 +356,9 @@ __device__ __forceinline__ void mma_dq(const SeqBwdArgs& a, uint8_t* base, Bars*
     __syncwarp();
     return true;
   };
-  auto issue_dp = [&](uint32_t x) -> bool {  // (dP of tile x - 1 was read before its dS was ready)
+  auto issue_dp = [&](uint32_t x) -> bool {
     if (!mbar_wait_warp_inl(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g)) return false;
+    if (x > 0 && !mbar_wait_warp_inl(smem_u32(&bars->dp_free), (x - 1) & 1, g)) return false;
     tc_fence_after();
     if (elect_one()) {
       scores<DP>(tmem + kColDp2, dos, smem_u32(base + L::b + (x % kBSlots) * L::kTB), steps, id_s);
@@ -373,7 +377,7 @@ __device__ __forceinline__ void mma_dq(const SeqBwdArgs& a, uint8_t* base, Bars*
     if (!issue_s(n) || !issue_dp(n)) break;
     for (int j = j0; j < j1; ++j, ++n) {
       const uint32_t as = n % kASlots;
-      if (j + 1 < j1 && !issue_s(n + 1)) { ok = false; break; }
+      if (j + 1 < j1 && (!issue_s(n + 1) || !issue_dp(n + 1))) { ok = false; break; }
       if (!mbar_wait_warp_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
       if (j == j0 && !mbar_wait_warp_inl(smem_u32(&bars->acc_free), (it & 1) ^ 1, g)) { ok = false; break; }
       tc_fence_after();
@@ -384,7 +388,6 @@ __device__ __forceinline__ void mma_dq(const SeqBwdArgs& a, uint8_t* base, Bars*
       }
       __syncwarp();
       ++gathers;
-      if (j + 1 < j1 && !issue_dp(n + 1)) { ok = false; break; }
     }
     if (elect_one()) {
       umma_commit(smem_u32(&bars->own_empty));
@@ -460,11 +463,12 @@ __device__ __forceinline__ void probs(uint32_t (&p)[64], uint32_t (&pp)[32], flo
     pp[(x >> 1) + 1] = pack2<BF16>(e[2], e[3]);
   }
 }
-// dS = P (dP + nd) of 32 columns, packed; nd (-delta) per column.
+// dS = P (dP + nd) of 64 columns, packed; nd (-delta) per column.
 template <bool BF16, bool MASK>
-__device__ __forceinline__ void dscores(const uint32_t (&d)[32], const uint32_t* p, uint32_t* pp, const float4* nd, int from) {
+__device__ __forceinline__ void dscores(const uint32_t (&d)[64], const uint32_t (&p)[64], uint32_t (&pp)[32], const float4* nd,
+                                        int from) {
 #pragma unroll
-  for (int x = 0; x < 32; x += 4) {
+  for (int x = 0; x < 64; x += 4) {
     const float4 z = nd[x >> 2];
     float2 s0 = mul2(add2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), make_float2(z.x, z.y)),
                      make_float2(__uint_as_float(p[x]), __uint_as_float(p[x + 1])));
@@ -482,9 +486,10 @@ __device__ __forceinline__ void dscores(const uint32_t (&d)[32], const uint32_t*
 }
 // The same with one row's delta; columns past `lim` are not seen.
 template <bool BF16, bool MASK>
-__device__ __forceinline__ void dscores_row(const uint32_t (&d)[32], const uint32_t* p, uint32_t* pp, float2 nd, int lim) {
+__device__ __forceinline__ void dscores_row(const uint32_t (&d)[64], const uint32_t (&p)[64], uint32_t (&pp)[32], float2 nd,
+                                            int lim) {
 #pragma unroll
-  for (int x = 0; x < 32; x += 2) {
+  for (int x = 0; x < 64; x += 2) {
     float2 ds = mul2(add2(make_float2(__uint_as_float(d[x]), __uint_as_float(d[x + 1])), nd),
                      make_float2(__uint_as_float(p[x]), __uint_as_float(p[x + 1])));
     if (MASK) {
@@ -503,7 +508,6 @@ __device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float* ro
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
   const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-  const uint32_t scol = trow + kColS + grp * 64, dcol = trow + kColDp + grp * 64;
   const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
   uint32_t n = 0, it = 0;
   bool ok = true;
@@ -513,7 +517,7 @@ __device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float* ro
     if (lane == 0) give_back(bars, it);
     const int key = w.t0 + r;
     for (int j = w.j0; j < w.j1; ++j, ++n) {
-      const uint32_t st = n & 1;
+      const uint32_t st = n & 1, scol = trow + st * 128 + grp * 64, dcol = trow + (st ^ 1) * 128 + grp * 64;
       const float4* nl = reinterpret_cast<const float4*>(rowbuf + st * 2 * kTile + grp * 64);
       const float4* nd = reinterpret_cast<const float4*>(rowbuf + st * 2 * kTile + kTile + grp * 64);
       // rows below `from` belong to tokens in front of the key; none does once the tile lies behind the keys
@@ -540,18 +544,17 @@ __device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float* ro
       if (!mbar_wait_warp_inl(smem_u32(&bars->dp_full), n & 1, g)) { ok = false; break; }
       tc_fence_after();
       {
-        uint32_t pp[32];
-#pragma unroll
-        for (int h = 0; h < 64; h += 32) {
-          uint32_t d[32];
-          tmem_ld32(dcol + h, d);
-          tmem_wait_ld(d);
-          if (mask)
-            dscores<BF16, true>(d, p + h, pp + h / 2, nd + h / 4, from - h);
-          else
-            dscores<BF16, false>(d, p + h, pp + h / 2, nd + h / 4, 0);
-        }
-        tmem_st32(dcol, pp);
+        uint32_t d[64], pp[32];
+        tmem_ld64(dcol, d);
+        tmem_wait_ld(d);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->dp_free));
+        if (mask)
+          dscores<BF16, true>(d, p, pp, nd, from);
+        else
+          dscores<BF16, false>(d, p, pp, nd, 0);
+        tmem_st32(scol + 32, pp);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -614,17 +617,16 @@ __device__ __forceinline__ void compute_dq(const SeqBwdArgs& a, Bars* bars, uint
       }
       if (!mbar_wait_warp_inl(smem_u32(&bars->dp_full), n & 1, g)) { ok = false; break; }
       tc_fence_after();
-      uint32_t pp[32];
-#pragma unroll
-      for (int q = 0; q < 64; q += 32) {
-        uint32_t d[32];
-        tmem_ld32(dcol + q, d);
-        tmem_wait_ld(d);
-        if (mask)
-          dscores_row<BF16, true>(d, p + q, pp + q / 2, nd, lim - q);
-        else
-          dscores_row<BF16, false>(d, p + q, pp + q / 2, nd, 0);
-      }
+      uint32_t d[64], pp[32];
+      tmem_ld64(dcol, d);
+      tmem_wait_ld(d);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->dp_free));
+      if (mask)
+        dscores_row<BF16, true>(d, p, pp, nd, lim);
+      else
+        dscores_row<BF16, false>(d, p, pp, nd, 0);
       tmem_st32(scol, pp);
       tmem_wait_st();
       tc_fence_before();
@@ -677,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_c
     mbar_init(smem_u32(&bars->dp_full), 1);
     mbar_init(smem_u32(&bars->p_ready), 8);
     mbar_init(smem_u32(&bars->ds_ready), 8);
-    mbar_init(smem_u32(&bars->first_done), 1);
+    mbar_init(smem_u32(&bars->dp_free), 8);
     mbar_init(smem_u32(&bars->second_done), 1);
     mbar_init(smem_u32(&bars->acc_full), 1);
     mbar_init(smem_u32(&bars->acc_free), 8);

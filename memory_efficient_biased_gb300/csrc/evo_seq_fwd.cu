@@ -44,7 +44,7 @@ struct Bars {
   uint64_t q_full, q_empty;
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t v_ready[kReady];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2], drain[2], turn[2];
+  uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], drain[2], turn[2];
   Work work[kDescs];
   int dirty[kDescs];  // a V tile of the item held values that were taken out
   uint32_t tmem_slot;
@@ -206,14 +206,23 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
       __syncwarp();
       if (!mbar_wait_warp_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
       if (!mbar_wait_warp_inl(smem_u32(&bars->full[vs]), (uv / L::kSlots) & 1, g)) { ok = false; break; }
-      if (!mbar_wait_warp_inl(smem_u32(&bars->p_full[gq]), u & 1, g)) { ok = false; break; }
       if (j == j0 && !mbar_wait_warp_inl(smem_u32(&bars->o_free[gq]), (own & 1) ^ 1, g)) { ok = false; break; }
-      tc_fence_after();
       const uint64_t vd = smem_desc(smem_u32(base + L::ring + vs * L::kTB), L::kHalf, 1024, kSwizzle128B);
+      // the first 64 keys while the softmax works on the others
+      if (!mbar_wait_warp_inl(smem_u32(&bars->p_half[gq]), u & 1, g)) { ok = false; break; }
+      tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)  // 128 keys in steps of 16 (8 columns of packed pairs)
+        for (int k = 0; k < 4; ++k)  // steps of 16 keys (8 columns of packed pairs)
           umma_ts(tmem + col_o(gq), tmem + col_s(gq) + k * 8, vd + k * (2048 / 16), id_o, (j > j0 || k > 0) ? 1u : 0u);
+      }
+      __syncwarp();
+      if (!mbar_wait_warp_inl(smem_u32(&bars->p_full[gq]), u & 1, g)) { ok = false; break; }
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 4; k < 8; ++k)
+          umma_ts(tmem + col_o(gq), tmem + col_s(gq) + k * 8, vd + k * (2048 / 16), id_o, 1u);
         umma_commit(smem_u32(&bars->pv_done[gq]));
         umma_commit(smem_u32(&bars->empty[vs]));
       }
@@ -453,6 +462,19 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
         m = mt;
         have = true;
       }
+      // O so far is complete: this tile's S was issued behind the previous P·V
+      if (j > w.j0 && __any_sync(0xffffffffu, moved)) {
+#pragma unroll 1
+        for (int c = 0; c < DP / 16; ++c) {
+          uint32_t x[16];
+          tmem_ld16(ocol + c * 16, x);
+          tmem_wait_ld(x);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+          tmem_st16(ocol + c * 16, x);
+        }
+        l *= alpha;
+      }
       const float2 nm2 = make_float2(-m, -m);
       float2 rs = make_float2(0.0f, 0.0f);
       // The two tiles take turns for the exponentials, tile 0 first: without that their phases
@@ -466,6 +488,10 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
         chunk_exp<BF16>(y0, sl2, nm2, p0, rs);
         chunk_exp<BF16>(y1, sl2, nm2, p1, rs);
         tmem_st32(scol, pp);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->p_half[gq]));
         chunk_exp<BF16>(y2, sl2, nm2, p0, rs);
         if (both) {  // handed over a little early
           __syncwarp();
@@ -474,19 +500,6 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
         }
         chunk_exp<BF16>(y3, sl2, nm2, p1, rs);
         tmem_st32(scol + 32, pp);
-      }
-      // O so far is complete: this tile's S was issued behind the previous P·V
-      if (j > w.j0 && __any_sync(0xffffffffu, moved)) {
-#pragma unroll 1
-        for (int c = 0; c < DP / 16; ++c) {
-          uint32_t x[16];
-          tmem_ld16(ocol + c * 16, x);
-          tmem_wait_ld(x);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-          tmem_st16(ocol + c * 16, x);
-        }
-        l *= alpha;
       }
       l += rs.x + rs.y;
       tmem_wait_st();
@@ -573,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_c
     for (int i = 0; i < kReady; ++i) mbar_init(smem_u32(&bars->v_ready[i]), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->s_full[i]), 1);
+      mbar_init(smem_u32(&bars->p_half[i]), 4);
       mbar_init(smem_u32(&bars->p_full[i]), 4);
       mbar_init(smem_u32(&bars->pv_done[i]), 1);
       mbar_init(smem_u32(&bars->o_free[i]), 4);
