@@ -44,8 +44,9 @@ struct Bars {
   uint64_t q_full, q_empty;
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t v_ready[kReady];
-  uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], drain[2], turn[2];
+  uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], drain[2], turn[2], merge_full;
   Work work[kDescs];
+  float2 merge[kTile];  // (m, l) of the second warpgroup's share of a single tile
   int dirty[kDescs];  // a V tile of the item held values that were taken out
   uint32_t tmem_slot;
   int abort;
@@ -83,13 +84,20 @@ __device__ __forceinline__ bool take(Bars* bars, uint32_t it, const WaitGuard& g
 __device__ __forceinline__ void give_back(Bars* bars, uint32_t it) {
   mbar_arrive(smem_u32(&bars->desc_empty[it % kDescs]));
 }
-// Key tiles of tile g of the item: none when it has no token.
-__device__ __forceinline__ int tiles_of(const Work& w, int g, int TQ) {
-  if (g == 0 && w.nt > TQ) {
+// One tile of queries: its key tiles alternate between the warpgroups.
+__device__ __forceinline__ bool single(const Work& w, int TQ) { return w.nt <= TQ; }
+// The key tiles of this piece that warpgroup g works on: from, from + step, ... below to.
+struct Share {
+  int from, to, step;
+};
+__device__ __forceinline__ Share share_of(const Work& w, int g, int TQ) {
+  if (single(w, TQ)) return Share{w.j0 + g, w.j1, 2};
+  int kt = w.kt;
+  if (g == 0) {
     const int end = w.pos + TQ;
-    return end > 0 ? (end + kTile - 1) / kTile : 1;
+    kt = end > 0 ? (end + kTile - 1) / kTile : 1;
   }
-  return g * TQ < w.nt ? w.kt : 0;
+  return Share{w.j0, kt < w.j1 ? kt : w.j1, 1};
 }
 
 // ------------------------------------------------------------ producer (one warp)
@@ -165,7 +173,6 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
   const int steps = (a.s.D + 15) / 16;  // of 16 features
   const uint32_t id_s = idesc_f16(128, 128, BF16, false, false);
   const uint32_t id_o = idesc_f16(128, steps * 16, BF16, false, true);
-  const uint64_t qd = smem_desc(smem_u32(base + L::q + gq * L::kTB), 16, 1024, kSwizzle128B);
   uint32_t n = 0, u = 0, it = 0, own = 0;
   bool ok = true;
   Work w;
@@ -173,22 +180,26 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
     __syncwarp();
     if (elect_one()) give_back(bars, it);
     const int j0 = uniform(w.j0), j1 = uniform(w.j1);
-    int mine = uniform(tiles_of(w, static_cast<int>(gq), a.TQ));
-    if (mine > j1) mine = j1;
+    const bool one = uniform(single(w, a.TQ)) != 0;
+    const Share sh = share_of(w, static_cast<int>(gq), a.TQ);
+    const int from = uniform(sh.from), to = uniform(sh.to), step = one ? 2 : 1;
+    const uint64_t qd = smem_desc(smem_u32(base + L::q + (one ? 0 : gq * L::kTB)), 16, 1024, kSwizzle128B);
     if (!mbar_wait_warp_inl(smem_u32(&bars->q_full), it & 1, g)) break;
     tc_fence_after();
-    if (mine <= j0 && elect_one()) mbar_arrive(smem_u32(&bars->q_empty));
+    if (from >= to && elect_one()) mbar_arrive(smem_u32(&bars->q_empty));
     __syncwarp();
+    int next = from;  // this warpgroup's next key tile
     for (int j = j0; j < j1; ++j, ++n) {
       const uint32_t uk = 2 * n, uv = 2 * n + 1, ks = uk % L::kSlots, vs = uv % L::kSlots;
       if (!mbar_wait_warp_inl(smem_u32(&bars->full[ks]), (uk / L::kSlots) & 1, g)) { ok = false; break; }
-      if (j >= mine) {  // the other tile's
+      if (j != next || j >= to) {  // the other warpgroup's
         if (elect_one()) mbar_arrive(smem_u32(&bars->empty[ks]));
         if (!mbar_wait_warp_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
         if (elect_one()) mbar_arrive(smem_u32(&bars->empty[vs]));
         __syncwarp();
         continue;
       }
+      next += step;
       // S takes the place of the previous P, which its P·V must have read
       if (u > 0 && !mbar_wait_warp_inl(smem_u32(&bars->pv_done[gq]), (u - 1) & 1, g)) { ok = false; break; }
       tc_fence_after();
@@ -201,12 +212,12 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
         }
         umma_commit(smem_u32(&bars->s_full[gq]));
         umma_commit(smem_u32(&bars->empty[ks]));
-        if (j == mine - 1) umma_commit(smem_u32(&bars->q_empty));
+        if (next >= to) umma_commit(smem_u32(&bars->q_empty));
       }
       __syncwarp();
       if (!mbar_wait_warp_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
       if (!mbar_wait_warp_inl(smem_u32(&bars->full[vs]), (uv / L::kSlots) & 1, g)) { ok = false; break; }
-      if (j == j0 && !mbar_wait_warp_inl(smem_u32(&bars->o_free[gq]), (own & 1) ^ 1, g)) { ok = false; break; }
+      if (j == from && !mbar_wait_warp_inl(smem_u32(&bars->o_free[gq]), (own & 1) ^ 1, g)) { ok = false; break; }
       const uint64_t vd = smem_desc(smem_u32(base + L::ring + vs * L::kTB), L::kHalf, 1024, kSwizzle128B);
       // the first 64 keys while the softmax works on the others
       if (!mbar_wait_warp_inl(smem_u32(&bars->p_half[gq]), u & 1, g)) { ok = false; break; }
@@ -214,7 +225,7 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // steps of 16 keys (8 columns of packed pairs)
-          umma_ts(tmem + col_o(gq), tmem + col_s(gq) + k * 8, vd + k * (2048 / 16), id_o, (j > j0 || k > 0) ? 1u : 0u);
+          umma_ts(tmem + col_o(gq), tmem + col_s(gq) + k * 8, vd + k * (2048 / 16), id_o, (j > from || k > 0) ? 1u : 0u);
       }
       __syncwarp();
       if (!mbar_wait_warp_inl(smem_u32(&bars->p_full[gq]), u & 1, g)) { ok = false; break; }
@@ -229,7 +240,7 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
       __syncwarp();
       ++u;
     }
-    if (mine > j0) ++own;
+    if (from < to) ++own;
   }
   __syncwarp();
   if (elect_one()) umma_commit(smem_u32(&bars->drain[gq]));
@@ -356,6 +367,21 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&y)[32], float2 sl2, f
   }
 }
 
+// This thread's row of an accumulator times alpha.  Warp-collective.
+template <int DP>
+__device__ __forceinline__ void rescale(uint32_t ocol, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < DP / 16; ++c) {
+    uint32_t x[16];
+    tmem_ld16(ocol + c * 16, x);
+    tmem_wait_ld(x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+    tmem_st16(ocol + c * 16, x);
+  }
+  tmem_wait_st();
+}
+
 // 64 scores, times s·log2 e, for the sums of the weights.
 __device__ __forceinline__ void leave_scores(const uint32_t (&y)[64], float scale_log2, float* to) {
 #pragma unroll
@@ -397,7 +423,9 @@ __device__ __forceinline__ void add_back(const SeqFwdArgs& a, const Work& w, int
   for (int c = 0; c < 32; ++c) out[c] = x[c];
 }
 
-template <int DP, bool BF16>
+// SCORES: leave the scores behind for the sums of the weights (a kernel of its own: as a branch in
+// the loop it cost prompts 3 %).
+template <int DP, bool BF16, bool SCORES>
 __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars* bars, uint32_t tmem,
                                         const WaitGuard& g) {
   const SeqDesc& s = a.s;
@@ -408,80 +436,90 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
   const int dt = r / s.group, head = r % s.group;  // token within the tile, head within the group
   const float scale_log2 = a.scale_log2;
   const float2 sl2 = make_float2(scale_log2, scale_log2);
-  uint32_t u = 0, it = 0, turns = 0;
+  uint32_t u = 0, it = 0, merges = 0, turns = 0;
   bool ok = true;
   Work w;
   for (; ok && take<true>(bars, it, g, w); ++it) {
-    int mine = tiles_of(w, gq, a.TQ), other = tiles_of(w, gq ^ 1, a.TQ);
-    if (mine > w.j1) mine = w.j1;
-    const int tok = gq * a.TQ + dt;              // token within the block
+    const bool one = single(w, a.TQ);
+    const Share sh = share_of(w, gq, a.TQ);
+    const int both = one ? 0 : share_of(w, gq ^ 1, a.TQ).to;  // below it the other tile works too
+    const int first = one ? 0 : gq * a.TQ;       // the tile's first token within the block
+    const int tok = first + dt;
     const bool live = dt < a.TQ && tok < w.nt;
+    const bool any = __any_sync(0xffffffffu, live);
     const int pos = w.pos + tok;
     float m = 0.0f, l = 0.0f;
     bool have = false;
-    for (int j = w.j0; j < mine; ++j) {
-      if (!mbar_wait_warp_inl(smem_u32(&bars->s_full[gq]), u & 1, g)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t ya[64], yb[64];
-      uint32_t(&y0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[0]);
-      uint32_t(&y1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[32]);
-      uint32_t(&y2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&yb[0]);
-      uint32_t(&y3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&yb[32]);
-      float mt = -INFINITY;
-      tmem_ld64(scol, ya);
-      tmem_wait_ld(ya);
-      tmem_ld64(scol + 64, yb);
-      // the tile's first token sees the whole key tile: no row needs its mask
-      if (w.pos + gq * a.TQ >= j * kTile + kTile - 1) {
-        chunk_max<false>(y0, 0, mt);
-        chunk_max<false>(y1, 0, mt);
-        tmem_wait_ld(yb);
-        chunk_max<false>(y2, 0, mt);
-        chunk_max<false>(y3, 0, mt);
-      } else {
-        const int lim = pos - j * kTile;
-        chunk_max<true>(y0, lim, mt);
-        chunk_max<true>(y1, lim - 32, mt);
-        tmem_wait_ld(yb);
-        chunk_max<true>(y2, lim - 64, mt);
-        chunk_max<true>(y3, lim - 96, mt);
-      }
-      if (a.scores && live) {
-        float* to = a.scores + ((static_cast<size_t>(w.row0) + w.t0 + tok) * s.q_heads + w.kvh * s.group + head) * a.scores_ld +
-                    static_cast<size_t>(j) * kTile;
-        leave_scores(ya, scale_log2, to);
-        leave_scores(yb, scale_log2, to + 64);
-      }
-      __syncwarp();
-      mt *= scale_log2;  // (a positive factor keeps the max)
-      bool moved = false;
-      float alpha = 1.0f;
-      if (mt != -INFINITY && (!have || mt > m + kMoveLog2)) {
-        moved = have;
-        alpha = have ? ex2(m - mt) : 1.0f;
-        m = mt;
-        have = true;
-      }
-      // O so far is complete: this tile's S was issued behind the previous P·V
-      if (j > w.j0 && __any_sync(0xffffffffu, moved)) {
-#pragma unroll 1
-        for (int c = 0; c < DP / 16; ++c) {
-          uint32_t x[16];
-          tmem_ld16(ocol + c * 16, x);
-          tmem_wait_ld(x);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-          tmem_st16(ocol + c * 16, x);
+    if (!any) {  // no row of this warp is anybody's: P may be what it is
+      for (int j = sh.from; j < sh.to; j += sh.step, ++u) {
+        if (!mbar_wait_warp_inl(smem_u32(&bars->s_full[gq]), u & 1, g)) { ok = false; break; }
+        if (j < both) {
+          if (!mbar_wait_warp_inl(smem_u32(&bars->turn[gq]), (turns & 1) ^ (gq ^ 1), g)) { ok = false; break; }
+          ++turns;
+          if (lane == 0) mbar_arrive(smem_u32(&bars->turn[gq ^ 1]));
         }
-        l *= alpha;
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->p_half[gq]));
+          mbar_arrive(smem_u32(&bars->p_full[gq]));
+        }
       }
-      const float2 nm2 = make_float2(-m, -m);
-      float2 rs = make_float2(0.0f, 0.0f);
-      // The two tiles take turns for the exponentials, tile 0 first: without that their phases
-      // fall into step, and the tensor core idles while both compute.
-      const bool both = j < other;
-      if (both && !mbar_wait_warp_inl(smem_u32(&bars->turn[gq]), (turns & 1) ^ (gq ^ 1), g)) { ok = false; break; }
-      {
+    } else {
+      for (int j = sh.from; j < sh.to; j += sh.step) {
+        if (!mbar_wait_warp_inl(smem_u32(&bars->s_full[gq]), u & 1, g)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t ya[64], yb[64];
+        uint32_t(&y0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[0]);
+        uint32_t(&y1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[32]);
+        uint32_t(&y2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&yb[0]);
+        uint32_t(&y3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&yb[32]);
+        float mt = -INFINITY;
+        tmem_ld64(scol, ya);
+        tmem_wait_ld(ya);
+        tmem_ld64(scol + 64, yb);
+        if (w.pos + first >= j * kTile + kTile - 1) {
+          // the tile's first token sees the whole key tile: no row needs its mask
+          chunk_max<false>(y0, 0, mt);
+          chunk_max<false>(y1, 0, mt);
+          tmem_wait_ld(yb);
+          chunk_max<false>(y2, 0, mt);
+          chunk_max<false>(y3, 0, mt);
+        } else {
+          const int lim = pos - j * kTile;
+          chunk_max<true>(y0, lim, mt);
+          chunk_max<true>(y1, lim - 32, mt);
+          tmem_wait_ld(yb);
+          chunk_max<true>(y2, lim - 64, mt);
+          chunk_max<true>(y3, lim - 96, mt);
+        }
+        if constexpr (SCORES) {
+          if (live) {
+            const size_t at = (static_cast<size_t>(w.row0) + w.t0 + tok) * s.q_heads + w.kvh * s.group + head;
+            float* to = a.scores + at * a.scores_ld + static_cast<size_t>(j) * kTile;
+            leave_scores(ya, scale_log2, to);
+            leave_scores(yb, scale_log2, to + 64);
+          }
+          __syncwarp();
+        }
+        mt *= scale_log2;  // (a positive factor keeps the max)
+        bool moved = false;
+        float alpha = 1.0f;
+        if (mt != -INFINITY && (!have || mt > m + kMoveLog2)) {
+          moved = have;
+          alpha = have ? ex2(m - mt) : 1.0f;
+          m = mt;
+          have = true;
+        }
+        // O so far is complete: this tile's S was issued behind the previous P·V
+        if (__any_sync(0xffffffffu, moved)) {
+          rescale<DP>(ocol, alpha);
+          l *= alpha;
+        }
+        const float2 nm2 = make_float2(-m, -m);
+        float2 rs = make_float2(0.0f, 0.0f);
+        // Two tiles take turns for the exponentials, tile 0 first: without that their phases fall into
+        // step, and the tensor core idles while both compute (16384 tokens, 16 heads of 128: 1085 us
+        // without turns, 891 with).
+        if (j < both && !mbar_wait_warp_inl(smem_u32(&bars->turn[gq]), (turns & 1) ^ (gq ^ 1), g)) { ok = false; break; }
         uint32_t pp[32];
         uint32_t(&p0)[16] = *reinterpret_cast<uint32_t(*)[16]>(&pp[0]);
         uint32_t(&p1)[16] = *reinterpret_cast<uint32_t(*)[16]>(&pp[16]);
@@ -491,80 +529,120 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->p_half[gq]));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->p_half[gq]));
+        }
         chunk_exp<BF16>(y2, sl2, nm2, p0, rs);
-        if (both) {  // handed over a little early
+        if (j < both) {  // handed over a little early
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars->turn[gq ^ 1]));
-          ++turns;
         }
         chunk_exp<BF16>(y3, sl2, nm2, p1, rs);
+        if (j < both) ++turns;
         tmem_st32(scol + 32, pp);
+        l += rs.x + rs.y;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars->p_full[gq]));
+        }
+        ++u;
       }
-      l += rs.x + rs.y;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[gq]));
-      ++u;
     }
     if (!ok) break;
-    const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * 256 + gq * 128 + r;
-    if (mine > w.j0) {
-      if (!mbar_wait_warp_inl(smem_u32(&bars->pv_done[gq]), (u - 1) & 1, g)) break;
-      tc_fence_after();
-      const bool dirty = bars->dirty[it % kDescs] != 0;
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const size_t row = static_cast<size_t>(w.row0) + w.t0 + tok;
-      const int h = w.kvh * s.group + head;
-      uint16_t* out = a.out + row * a.out_stride + static_cast<size_t>(h) * s.D;
-      float* part = a.part_o + prow * DP;
+    const bool worked = sh.from < sh.to;
+    if (worked && !mbar_wait_warp_inl(smem_u32(&bars->pv_done[gq]), (u - 1) & 1, g)) break;
+    tc_fence_after();
+    const size_t row = static_cast<size_t>(w.row0) + w.t0 + tok;
+    const int h = w.kvh * s.group + head;
+    const bool two = one && w.j1 - w.j0 > 1;  // the second warpgroup has a share to add
+    if (gq == 1 && one) {
+      if (two) {
+        bars->merge[r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->merge_full));
+      }
+    } else {
+      float f0 = 1.0f, f1 = 0.0f;
+      if (two) {
+        if (!mbar_wait_warp_inl(smem_u32(&bars->merge_full), merges & 1, g)) break;
+        ++merges;
+        tc_fence_after();
+        const float2 o = bars->merge[r];
+        const float big = l == 0.0f ? o.x : (o.y == 0.0f ? m : fmaxf(m, o.x));
+        f0 = l == 0.0f ? 0.0f : ex2(m - big);
+        f1 = o.y == 0.0f ? 0.0f : ex2(o.x - big);
+        l = l * f0 + o.y * f1;
+        m = big;
+      }
+      if (worked && any) {
+        const bool dirty = bars->dirty[it % kDescs] != 0;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* out = a.out + row * a.out_stride + static_cast<size_t>(h) * s.D;
+        const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * 256 + gq * 128 + r;
+        float* part = a.part_o + prow * DP;
 #pragma unroll 1
-      for (int c = 0; c < s.D; c += 32) {
-        uint32_t x[32];
-        tmem_ld32(ocol + c, x);
-        tmem_wait_ld(x);
-        if (live) {
-          if (dirty) add_back<BF16>(a, w, pos, c, x);
-          if (w.slot < 0) {
+        for (int c = 0; c < s.D; c += 32) {
+          uint32_t x[32];
+          tmem_ld32(ocol + c, x);
+          tmem_wait_ld(x);
+          if (two) {
+            uint32_t y[32];
+            tmem_ld32(trow + col_o(1) + c, y);
+            tmem_wait_ld(y);
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              uint32_t o[8];
+            for (int e = 0; e < 32; ++e)
+              x[e] = __float_as_uint(__uint_as_float(x[e]) * f0 + __uint_as_float(y[e]) * f1);
+          }
+          if (live) {
+            if (dirty) add_back<BF16>(a, w, pos, c, x);
+            if (w.slot < 0) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float lo = __uint_as_float(x[e + 2 * i]) * inv, hi = __uint_as_float(x[e + 2 * i + 1]) * inv;
-                o[i] = l == 0.0f ? 0u : pack2<BF16>(lo, hi);
+              for (int e = 0; e < 32; e += 16) {
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float lo = __uint_as_float(x[e + 2 * i]) * inv, hi = __uint_as_float(x[e + 2 * i + 1]) * inv;
+                  o[i] = l == 0.0f ? 0u : pack2<BF16>(lo, hi);
+                }
+                if (a.out32) {
+                  if (c + e < s.D) st_global_32(out + c + e, o);
+                } else {
+                  if (c + e < s.D) *reinterpret_cast<uint4*>(out + c + e) = make_uint4(o[0], o[1], o[2], o[3]);
+                  if (c + e + 8 < s.D) *reinterpret_cast<uint4*>(out + c + e + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
               }
-              if (a.out32) {
-                if (c + e < s.D) st_global_32(out + c + e, o);
-              } else {
-                if (c + e < s.D) *reinterpret_cast<uint4*>(out + c + e) = make_uint4(o[0], o[1], o[2], o[3]);
-                if (c + e + 8 < s.D) *reinterpret_cast<uint4*>(out + c + e + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-              }
-            }
-          } else {
+            } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              const uint32_t(&o)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&x[e]);
-              st_global_32(part + c + e, o);
+              for (int e = 0; e < 32; e += 8) {
+                const uint32_t(&o)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&x[e]);
+                st_global_32(part + c + e, o);
+              }
             }
           }
+          __syncwarp();  // the loads above are the whole warp's
         }
-        __syncwarp();  // the loads above are the whole warp's
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->o_free[gq]));
-      if (live && w.slot < 0)
-        a.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (m + lg2(l)) * kSeqLn2;
+      if (lane == 0) {
+        if (worked) mbar_arrive(smem_u32(&bars->o_free[gq]));
+        if (two) mbar_arrive(smem_u32(&bars->o_free[1]));
+      }
+      if (live) {
+        if (w.slot < 0)
+          a.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (m + lg2(l)) * kSeqLn2;
+        else
+          a.part_ml[(static_cast<size_t>(blockIdx.x) * 2 + w.slot) * 256 + gq * 128 + r] = make_float2(m, l);
+      }
     }
-    if (w.slot >= 0) a.part_ml[prow] = make_float2(m, l);
     __syncwarp();
     if (lane == 0) give_back(bars, it);
   }
 }
 
-template <int DP, bool BF16>
+template <int DP, bool BF16, bool SCORES>
 __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_constant__ SeqFwdArgs a) {
   using L = Layout<DP>;
   extern __shared__ uint8_t smem_raw[];
@@ -584,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_c
       mbar_init(smem_u32(&bars->empty[i]), 2);  // both MMA threads
     }
     for (int i = 0; i < kReady; ++i) mbar_init(smem_u32(&bars->v_ready[i]), 1);
+    mbar_init(smem_u32(&bars->merge_full), 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->s_full[i]), 1);
       mbar_init(smem_u32(&bars->p_half[i]), 4);
@@ -619,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_c
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
-    softmax<DP, BF16>(a, base, bars, tmem, g);
+    softmax<DP, BF16, SCORES>(a, base, bars, tmem, g);
   }
   tc_fence_before();
   __syncthreads();
@@ -631,15 +710,18 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_c
 
 // ------------------------------------------------------------ join
 // The pieces of an item that the borders between CTAs cut: the one that begins it (slot 1 of
-// CTA c), then slot 0 of c + 1, c + 2, ... up to its end, joined in that order.  One warp per row:
-// M = max m, l = Σ l 2^(m - M), O = Σ O 2^(m - M).
-constexpr int kJoinRows = 8;
+// CTA c), then slot 0 of c + 1, c + 2, ... up to its end, joined in that order.  Eight threads a row:
+// M = max m, l = Σ l 2^(m - M), O = Σ O 2^(m - M).  Latency is what it costs (the records, then the
+// (m, l), then O): 32 rows a block, so that every block of a launch is resident at once.
+constexpr int kJoinRows = 32;
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(kJoinRows * 32) evo_seq_join_kernel(const __grid_constant__ SeqFwdArgs a, int ctas) {
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(256) evo_seq_join_kernel(const __grid_constant__ SeqFwdArgs a, int ctas) {
+  const int c0 = blockIdx.x, i = blockIdx.y * kJoinRows + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (DP / 8);
   const PieceRecord first = a.records[2 * c0 + 1];
   if (!first.used) return;
   const SeqDesc& s = a.s;
+  const int gq = i >> 7, r = i & 127, dt = r / s.group, tok = gq * a.TQ + dt;
+  if (dt >= a.TQ || tok >= first.nt) return;
   int pieces = 1;
   while (c0 + pieces < ctas) {
     const PieceRecord p = a.records[2 * (c0 + pieces)];
@@ -647,53 +729,57 @@ __global__ void __launch_bounds__(kJoinRows * 32) evo_seq_join_kernel(const __gr
     ++pieces;
     if (p.ends) break;
   }
-  {
-    const int i = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
-    const int gq = i >> 7, r = i & 127, dt = r / s.group, tok = gq * a.TQ + dt;
-    if (dt >= a.TQ || tok >= first.nt) return;
-    auto at = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * 256 + i; };
-    float big = -INFINITY;
-    for (int p = 0; p < pieces; ++p) {
-      const float2 ml = a.part_ml[at(p)];
-      if (ml.y != 0.0f) big = fmaxf(big, ml.x);
-    }
-    float o[DP / 32] = {};
-    float l = 0.0f;
-    for (int p = 0; p < pieces; ++p) {
-      const float2 ml = a.part_ml[at(p)];
-      if (ml.y == 0.0f) continue;
-      const float f = ex2(ml.x - big);
-      l += ml.y * f;
-      const float* x = a.part_o + at(p) * DP;
-#pragma unroll
-      for (int e = 0; e < DP / 32; ++e) {
-        const int d = lane + 32 * e;
-        if (d < s.D) o[e] = fmaf(x[d], f, o[e]);
-      }
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const size_t row = static_cast<size_t>(first.row0) + first.t0 + tok;
-    const int h = first.kvh * s.group + r % s.group;
-    uint16_t* out = a.out + row * a.out_stride + static_cast<size_t>(h) * s.D;
+  auto at = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * 256 + i; };
+  float big = -INFINITY;
+  for (int p = 0; p < pieces; ++p) {
+    const float2 ml = a.part_ml[at(p)];
+    if (ml.y != 0.0f) big = fmaxf(big, ml.x);
+  }
+  float o[DP / 8] = {};
+  float l = 0.0f;
+  for (int p = 0; p < pieces; ++p) {
+    const float2 ml = a.part_ml[at(p)];
+    if (ml.y == 0.0f) continue;
+    const float f = ex2(ml.x - big);
+    l += ml.y * f;
+    const float4* x = reinterpret_cast<const float4*>(a.part_o + at(p) * DP + d0);
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e) {
-      const int d = lane + 32 * e;
-      if (d < s.D) out[d] = l == 0.0f ? 0 : static_cast<uint16_t>(pack2<BF16>(o[e] * inv, 0.0f) & 0xffffu);
+      const float4 v = x[e];
+      o[4 * e] = fmaf(v.x, f, o[4 * e]);
+      o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
+      o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
+      o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
     }
-    if (lane == 0) a.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
   }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const size_t row = static_cast<size_t>(first.row0) + first.t0 + tok;
+  const int h = first.kvh * s.group + r % s.group;
+  uint16_t* out = a.out + row * a.out_stride + static_cast<size_t>(h) * s.D + d0;
+#pragma unroll
+  for (int e = 0; e < DP / 8; e += 8) {  // (columns past D hold nothing and are not written)
+    uint32_t v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = l == 0.0f ? 0u : pack2<BF16>(o[e + 2 * q] * inv, o[e + 2 * q + 1] * inv);
+    if (d0 + e < s.D) *reinterpret_cast<uint4*>(out + e) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  if (d0 == 0) a.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
 }
 
-template <int DP, bool BF16>
-cudaError_t launch_t(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
-  auto kern = evo_seq_fwd_kernel<DP, BF16>;
+template <int DP, bool BF16, bool SCORES>
+cudaError_t launch_k(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
+  auto kern = evo_seq_fwd_kernel<DP, BF16, SCORES>;
   static bool limit_set[64] = {};
   cudaError_t e = ensure_smem_limit(kern, 232448, limit_set);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kThreads, Layout<DP>::total + 1024, st>>>(a);
-  e = cudaGetLastError();
+  return cudaGetLastError();
+}
+template <int DP, bool BF16>
+cudaError_t launch_t(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
+  const cudaError_t e = a.scores ? launch_k<DP, BF16, true>(a, ctas, st) : launch_k<DP, BF16, false>(a, ctas, st);
   if (e != cudaSuccess) return e;
-  evo_seq_join_kernel<DP, BF16><<<dim3(ctas, 256 / kJoinRows), kJoinRows * 32, 0, st>>>(a, ctas);
+  evo_seq_join_kernel<DP, BF16><<<dim3(ctas, 256 / kJoinRows), 256, 0, st>>>(a, ctas);
   return cudaGetLastError();
 }
 

@@ -16,13 +16,14 @@ with ValueError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
 import torch
 
 from . import evo_attn as E
-from .evo_attn import EVO_OK, EvoAttnError, _DTYPE_CODE, _check, _on_current_device, _ptr, _stream_ptr
+from .evo_attn import EVO_OK, EvoAttnError, _DTYPE_CODE, _stream_ptr
 
 STRIDE_FIELDS = ("q", "k", "v", "out", "dout", "dq", "dk", "dv")
 
@@ -72,11 +73,13 @@ def load():
     return lib
 
 
-def _options(scale, wait_limit_ns, status):
+# The checks of a call run on every one of its tensors, in front of kernels of a few microseconds:
+# the current device is asked for once, and tensors are looked at through their own methods.
+def _options(scale, wait_limit_ns, status, dev):
     if scale is None and not wait_limit_ns and status is None:
         return None
     if status is not None:
-        _check(status, "status", dtype=torch.int32)
+        _flat(status, "status", None, torch.int32, dev)
         if status.numel() < 1:
             raise ValueError("status must have an element")
     if scale is not None and not (0.0 < scale < float("inf")):
@@ -86,19 +89,35 @@ def _options(scale, wait_limit_ns, status):
     return ctypes.byref(o)
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
-    """Checks a [tokens, heads, head_dim] tensor; its token stride (0 = packed)."""
+def _placed(t, name: str, dtype, dev: int):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a tensor")
-    _on_current_device(t, name)
+    if t.get_device() != dev:
+        E._on_current_device(t, name)
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+def _flat(t, name: str, shape, dtype, dev: int):
+    """Checks a contiguous tensor."""
+    _placed(t, name, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(t, name: str, shape, dtype, dev: int) -> int:
+    """Checks a [tokens, heads, head_dim] tensor; its token stride (0 = packed)."""
+    _placed(t, name, dtype, dev)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.is_contiguous():
+        return 0
     tokens, heads, d = shape
-    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+    stride, head, one = t.stride()
+    if (d > 1 and one != 1) or (heads > 1 and head != d):
         raise ValueError(f"{name} must have packed (heads, head_dim) dimensions")
-    stride = t.stride(0)
     if tokens <= 1 or stride == heads * d:
         return 0
     if stride < heads * d or stride % 8:
@@ -106,67 +125,75 @@ def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
     return stride
 
 
-def _ints(t: torch.Tensor, name: str, shape):
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
-    _check(t, name, shape, torch.int32)
-
-
-def _heads(q: torch.Tensor, k_heads: int, d: int, name: str = "q"):
-    if q.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+def _queries(q, k_heads: int, d: int, keys: str):
+    """Shape of q [T, Hq, D] beside keys with k_heads heads of d."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [tokens, heads, head_dim]")
     if q.dtype not in _DTYPE_CODE:
         raise ValueError("inputs must be float16 or bfloat16")
-    if q.shape[2] != d or k_heads < 1 or q.shape[1] % k_heads:
-        raise ValueError(f"{name} has {q.shape[1]} heads of {q.shape[2]}, the keys {k_heads} of {d}")
+    T, Hq, D = q.shape
+    if D != d or k_heads < 1 or Hq % k_heads:
+        raise ValueError(f"q has {Hq} heads of {D}, {keys} {k_heads} of {d}")
+    return T, Hq, D
 
 
-def _offsets(cu: torch.Tensor) -> int:
+def _offsets(cu, dev: int) -> int:
     if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError("cu_seqlens must be a tensor [seqs + 1]")
-    _ints(cu, "cu_seqlens", cu.shape)
+    _flat(cu, "cu_seqlens", None, torch.int32, dev)
     return cu.shape[0] - 1
 
 
-def _cache(k_pages, v_pages, block_table, dtype) -> CacheShape:
+def _pages(k_pages):
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or k_pages.dtype not in _DTYPE_CODE:
+        raise ValueError("k_pages must be a float16 or bfloat16 tensor [num_pages, page_size, kv_heads, head_dim]")
+    return k_pages.shape
+
+
+def _cache(k_pages, v_pages, block_table, seqs, dtype, dev: int) -> CacheShape:
+    strides = []
     for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise ValueError(f"{n} must be [num_pages, page_size, kv_heads, head_dim]")
-        _on_current_device(t, n)
-        if t.dtype != dtype:
-            raise ValueError(f"{n} has dtype {t.dtype}, expected {dtype}")
+        _placed(t, n, dtype, dev)
         if t.shape != k_pages.shape:
             raise ValueError(f"{n} has shape {tuple(t.shape)}, expected {tuple(k_pages.shape)}")
+        if t.is_contiguous():
+            strides.append(0)
+            continue
         if t.numel() and not t[0].is_contiguous():
             raise ValueError(f"{n} must have contiguous pages")
+        strides.append(t.stride(0) if t.shape[0] > 1 else 0)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor [seqs, pages_per_seq]")
-    _ints(block_table, "block_table", block_table.shape)
+    _flat(block_table, "block_table", None, torch.int32, dev)
+    if seqs is not None and block_table.shape[0] != seqs:
+        raise ValueError(f"block_table has {block_table.shape[0]} rows, expected {seqs}")
     pages, page = k_pages.shape[:2]
-    strides = [t.stride(0) if pages > 1 else 0 for t in (k_pages, v_pages)]
     return CacheShape(pages, page, block_table.shape[1], *strides)
 
 
-class _On:
+def _device_and_stream(t, stream):
+    """The current device, which t must be on, and the handle of the stream to launch on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("inputs must be CUDA tensors")
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, _stream_ptr(stream).value or 0
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
     """Allocations of a call go to the stream it runs on."""
-
-    def __init__(self, stream):
-        self.ctx = torch.cuda.stream(stream) if stream is not None else None
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
-def _workspace(workspace, need, device):
+def _workspace(workspace, need, like, dev):
     if workspace is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-    _check(workspace, "workspace")
-    return workspace
+        return like.new_empty(need, dtype=torch.uint8), need
+    _flat(workspace, "workspace", None, None, dev)
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _done(st: int, where: str):
@@ -174,8 +201,8 @@ def _done(st: int, where: str):
         raise EvoAttnError(st, where)
 
 
-def _nbytes(t):
-    return t.numel() * t.element_size()
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
 def evo_prompt_fwd_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim) -> int:
@@ -190,26 +217,30 @@ def evo_prompt_fwd(q, k, v, cu_seqlens, out=None, lse=None, workspace=None, stre
                    scale: Optional[float] = None, wait_limit_ns: int = 0, status: Optional[torch.Tensor] = None):
     """Causal attention within each of the packed sequences; (out [T,Hq,D], lse [Hq,T] fp32).
     Rows in no sequence keep what out and lse held (new ones are uninitialised there)."""
-    if k.dim() != 3:
-        raise ValueError("k must be [tokens, heads, head_dim]")
-    _heads(q, k.shape[1], k.shape[2])
-    T, Hq, D = q.shape
-    Hk, dt = k.shape[1], q.dtype
-    B = _offsets(cu_seqlens)
-    sq, sk, sv = _rows(q, "q", q.shape, dt), _rows(k, "k", (T, Hk, D), dt), _rows(v, "v", (T, Hk, D), dt)
-    shape, lib = SeqShape(T, B, Hq, Hk, D), load()
-    sp = _stream_ptr(stream)
-    opts = _options(scale, wait_limit_ns, status)
-    with _On(stream):
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a tensor [tokens, heads, head_dim]")
+    Hk = k.shape[1]
+    T, Hq, D = _queries(q, Hk, k.shape[2], "k")
+    dev, sp = _device_and_stream(q, stream)
+    dt, rows, keys = q.dtype, q.shape, (T, Hk, D)
+    B = _offsets(cu_seqlens, dev)
+    sq, sk, sv = _rows(q, "q", rows, dt, dev), _rows(k, "k", keys, dt, dev), _rows(v, "v", keys, dt, dev)
+    opts = _options(scale, wait_limit_ns, status, dev)
+    shape, lib, so = SeqShape(T, B, Hq, Hk, D), load(), 0
+    with _on(stream):
         if out is None:
-            out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+            out = q.new_empty(rows)
+        else:
+            so = _rows(out, "out", rows, dt, dev)
         if lse is None:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-        ws = _workspace(workspace, lib.evo_prompt_fwd_workspace_bytes(shape), q.device)
-    strides = SeqStrides(q=sq, k=sk, v=sv, out=_rows(out, "out", q.shape, dt))
-    _check(lse, "lse", (Hq, T), torch.float32)
-    _done(lib.evo_prompt_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws),
-                             shape, _DTYPE_CODE[dt], ctypes.byref(strides), opts, sp), "evo_prompt_fwd")
+            lse = q.new_empty((Hq, T), dtype=torch.float32)
+        else:
+            _flat(lse, "lse", (Hq, T), torch.float32, dev)
+        ws, size = _workspace(workspace, lib.evo_prompt_fwd_workspace_bytes(shape), q, dev)
+    strides = SeqStrides(sq, sk, sv, so) if sq or sk or sv or so else None
+    _done(lib.evo_prompt_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(),
+                             lse.data_ptr(), ws.data_ptr(), size, shape, _DTYPE_CODE[dt], strides, opts, sp),
+          "evo_prompt_fwd")
     return out, lse
 
 
@@ -217,32 +248,36 @@ def evo_prompt_bwd(q, k, v, cu_seqlens, out, lse, dout, dq=None, dk=None, dv=Non
                    scale: Optional[float] = None, wait_limit_ns: int = 0, status: Optional[torch.Tensor] = None):
     """Gradients of evo_prompt_fwd from its inputs and outputs; (dq, dk, dv).  Rows in no
     sequence keep what dq, dk and dv held (new ones are uninitialised there)."""
-    if k.dim() != 3:
-        raise ValueError("k must be [tokens, heads, head_dim]")
-    _heads(q, k.shape[1], k.shape[2])
-    T, Hq, D = q.shape
-    Hk, dt = k.shape[1], q.dtype
-    B = _offsets(cu_seqlens)
-    keys = torch.Size((T, Hk, D))
-    strides = SeqStrides(q=_rows(q, "q", q.shape, dt), k=_rows(k, "k", keys, dt), v=_rows(v, "v", keys, dt),
-                         out=_rows(out, "out", q.shape, dt), dout=_rows(dout, "dout", q.shape, dt))
-    _check(lse, "lse", (Hq, T), torch.float32)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a tensor [tokens, heads, head_dim]")
+    Hk = k.shape[1]
+    T, Hq, D = _queries(q, Hk, k.shape[2], "k")
+    dev, sp = _device_and_stream(q, stream)
+    dt, rows, keys = q.dtype, q.shape, (T, Hk, D)
+    B = _offsets(cu_seqlens, dev)
+    given = [_rows(q, "q", rows, dt, dev), _rows(k, "k", keys, dt, dev), _rows(v, "v", keys, dt, dev),
+             _rows(out, "out", rows, dt, dev), _rows(dout, "dout", rows, dt, dev), 0, 0, 0]
+    _flat(lse, "lse", (Hq, T), torch.float32, dev)
+    opts = _options(scale, wait_limit_ns, status, dev)
     shape, lib = SeqShape(T, B, Hq, Hk, D), load()
-    sp = _stream_ptr(stream)
-    opts = _options(scale, wait_limit_ns, status)
-    with _On(stream):
+    with _on(stream):
         if dq is None:
-            dq = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+            dq = q.new_empty(rows)
+        else:
+            given[5] = _rows(dq, "dq", rows, dt, dev)
         if dk is None:
-            dk = torch.empty(keys, dtype=dt, device=q.device)
+            dk = q.new_empty(keys)
+        else:
+            given[6] = _rows(dk, "dk", keys, dt, dev)
         if dv is None:
-            dv = torch.empty(keys, dtype=dt, device=q.device)
-        ws = _workspace(workspace, lib.evo_prompt_bwd_workspace_bytes(shape), q.device)
-    strides.dq, strides.dk, strides.dv = (_rows(dq, "dq", q.shape, dt), _rows(dk, "dk", keys, dt),
-                                          _rows(dv, "dv", keys, dt))
-    _done(lib.evo_prompt_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
-                             _ptr(dk), _ptr(dv), _ptr(ws), _nbytes(ws), shape, _DTYPE_CODE[dt], ctypes.byref(strides),
-                             opts, sp), "evo_prompt_bwd")
+            dv = q.new_empty(keys)
+        else:
+            given[7] = _rows(dv, "dv", keys, dt, dev)
+        ws, size = _workspace(workspace, lib.evo_prompt_bwd_workspace_bytes(shape), q, dev)
+    strides = SeqStrides(*given) if any(given) else None
+    _done(lib.evo_prompt_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(),
+                             lse.data_ptr(), dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                             ws.data_ptr(), size, shape, _DTYPE_CODE[dt], strides, opts, sp), "evo_prompt_bwd")
     return dq, dk, dv
 
 
@@ -250,21 +285,21 @@ def evo_cache_append(k, v, cu_seqlens, seq_lens, k_pages, v_pages, block_table, 
                      status: Optional[torch.Tensor] = None):
     """Writes the new tokens' rows k, v [T,Hkv,D] into the cache: sequence b's are the last
     of its seq_lens[b] (which counts them already)."""
-    if k.dim() != 3 or k.dtype not in _DTYPE_CODE:
+    if not isinstance(k, torch.Tensor) or k.dim() != 3 or k.dtype not in _DTYPE_CODE:
         raise ValueError("k must be a float16 or bfloat16 tensor [tokens, heads, head_dim]")
-    T, Hk, D = k.shape
-    dt, B = k.dtype, _offsets(cu_seqlens)
-    cache = _cache(k_pages, v_pages, block_table, dt)
-    if tuple(k_pages.shape[2:]) != (Hk, D):
+    dev, sp = _device_and_stream(k, stream)
+    T, Hk, D = keys = k.shape
+    dt, B = k.dtype, _offsets(cu_seqlens, dev)
+    if tuple(_pages(k_pages)[2:]) != (Hk, D):
         raise ValueError(f"k has {Hk} heads of {D}, the cache {tuple(k_pages.shape[2:])}")
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows, expected {B}")
-    _ints(seq_lens, "seq_lens", (B,))
-    strides = SeqStrides(k=_rows(k, "k", k.shape, dt), v=_rows(v, "v", k.shape, dt))
-    sp = _stream_ptr(stream)
-    _done(load().evo_cache_append(_ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(seq_lens), _ptr(block_table), _ptr(k_pages),
-                                  _ptr(v_pages), SeqShape(T, B, Hk, Hk, D), cache, _DTYPE_CODE[dt],
-                                  ctypes.byref(strides), _options(None, 0, status), sp), "evo_cache_append")
+    cache = _cache(k_pages, v_pages, block_table, B, dt, dev)
+    _flat(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    sk, sv = _rows(k, "k", keys, dt, dev), _rows(v, "v", keys, dt, dev)
+    strides = SeqStrides(0, sk, sv) if sk or sv else None
+    _done(load().evo_cache_append(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(),
+                                  block_table.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                  SeqShape(T, B, Hk, Hk, D), cache, _DTYPE_CODE[dt], strides,
+                                  _options(None, 0, status, dev), sp), "evo_cache_append")
 
 
 def evo_paged_fwd_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim, num_pages, page_size,
@@ -280,37 +315,36 @@ def evo_paged_fwd(q, k_pages, v_pages, cu_seqlens, seq_lens, block_table, out=No
     """Attention of the new tokens q [T,Hq,D] over the cache that already holds them;
     (out, lse [Hq,T] fp32).  ``weights`` [B,Hkv,n] fp32, where given, gains for every key the
     attention weight that this call's rows gave it."""
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
-        raise ValueError("k_pages must be [num_pages, page_size, kv_heads, head_dim]")
-    Hk = k_pages.shape[2]
-    _heads(q, Hk, k_pages.shape[3])
-    T, Hq, D = q.shape
-    dt, B = q.dtype, _offsets(cu_seqlens)
-    cache = _cache(k_pages, v_pages, block_table, dt)
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows, expected {B}")
-    _ints(seq_lens, "seq_lens", (B,))
-    sq = _rows(q, "q", q.shape, dt)
-    wlen = 0
+    _, _, Hk, d = _pages(k_pages)
+    T, Hq, D = _queries(q, Hk, d, "the cache")
+    dev, sp = _device_and_stream(q, stream)
+    dt, rows = q.dtype, q.shape
+    B = _offsets(cu_seqlens, dev)
+    cache = _cache(k_pages, v_pages, block_table, B, dt, dev)
+    _flat(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    sq, so, wlen = _rows(q, "q", rows, dt, dev), 0, 0
     if weights is not None:
-        if weights.dim() != 3:
-            raise ValueError("weights must be [seqs, kv_heads, n]")
+        if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
+            raise ValueError("weights must be a tensor [seqs, kv_heads, n]")
         wlen = weights.shape[2]
-        _check(weights, "weights", (B, Hk, wlen), torch.float32)
+        _flat(weights, "weights", (B, Hk, wlen), torch.float32, dev)
+    opts = _options(scale, wait_limit_ns, status, dev)
     shape, lib = SeqShape(T, B, Hq, Hk, D), load()
-    sp = _stream_ptr(stream)
-    opts = _options(scale, wait_limit_ns, status)
-    with _On(stream):
+    with _on(stream):
         if out is None:
-            out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+            out = q.new_empty(rows)
+        else:
+            so = _rows(out, "out", rows, dt, dev)
         if lse is None:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-        ws = _workspace(workspace, lib.evo_paged_fwd_workspace_bytes(shape, cache, wlen), q.device)
-    strides = SeqStrides(q=sq, out=_rows(out, "out", q.shape, dt))
-    _check(lse, "lse", (Hq, T), torch.float32)
-    _done(lib.evo_paged_fwd(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(cu_seqlens), _ptr(seq_lens),
-                            _ptr(block_table), _ptr(out), _ptr(lse), _ptr(weights), wlen, _ptr(ws), _nbytes(ws), shape,
-                            cache, _DTYPE_CODE[dt], ctypes.byref(strides), opts, sp), "evo_paged_fwd")
+            lse = q.new_empty((Hq, T), dtype=torch.float32)
+        else:
+            _flat(lse, "lse", (Hq, T), torch.float32, dev)
+        ws, size = _workspace(workspace, lib.evo_paged_fwd_workspace_bytes(shape, cache, wlen), q, dev)
+    strides = SeqStrides(sq, 0, 0, so) if sq or so else None
+    _done(lib.evo_paged_fwd(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), cu_seqlens.data_ptr(),
+                            seq_lens.data_ptr(), block_table.data_ptr(), out.data_ptr(), lse.data_ptr(), _p(weights),
+                            wlen, ws.data_ptr(), size, shape, cache, _DTYPE_CODE[dt], strides, opts, sp),
+          "evo_paged_fwd")
     return out, lse
 
 
@@ -319,24 +353,25 @@ def evo_cache_evict(k_pages, v_pages, block_table, seq_lens, weights, budget: in
     """Cuts every sequence longer than ``budget`` down to it, in place and per key/value head:
     its ``recent`` newest tokens and the others of the largest ``weights`` [B,Hkv,n]; returns
     kept [B,Hkv,budget] int32, the place every row came from (-1 behind the last)."""
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4 or k_pages.dtype not in _DTYPE_CODE:
-        raise ValueError("k_pages must be a float16 or bfloat16 tensor [num_pages, page_size, kv_heads, head_dim]")
-    dt, (Hk, D) = k_pages.dtype, k_pages.shape[2:]
-    cache = _cache(k_pages, v_pages, block_table, dt)
+    _, _, Hk, D = _pages(k_pages)
+    dev, sp = _device_and_stream(k_pages, stream)
+    dt = k_pages.dtype
+    cache = _cache(k_pages, v_pages, block_table, None, dt, dev)
     B = block_table.shape[0]
-    _ints(seq_lens, "seq_lens", (B,))
+    _flat(seq_lens, "seq_lens", (B,), torch.int32, dev)
     if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
         raise ValueError("weights must be a tensor [seqs, kv_heads, n]")
-    _check(weights, "weights", (B, Hk, weights.shape[2]), torch.float32)
+    n = weights.shape[2]
+    _flat(weights, "weights", (B, Hk, n), torch.float32, dev)
     budget, recent = int(budget), int(recent)
     if budget < 1 or not 0 <= recent <= budget:
         raise ValueError(f"1 <= budget and 0 <= recent <= budget are needed, got budget {budget}, recent {recent}")
-    sp = _stream_ptr(stream)
-    with _On(stream):
-        if kept is None:
-            kept = torch.empty((B, Hk, budget), dtype=torch.int32, device=k_pages.device)
-    _ints(kept, "kept", (B, Hk, budget))
-    _done(load().evo_cache_evict(_ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(weights),
-                                 weights.shape[2], _ptr(kept), budget, recent, SeqShape(0, B, Hk, Hk, D), cache,
-                                 _DTYPE_CODE[dt], _options(None, 0, status), sp), "evo_cache_evict")
+    if kept is None:
+        with _on(stream):
+            kept = seq_lens.new_empty((B, Hk, budget))
+    else:
+        _flat(kept, "kept", (B, Hk, budget), torch.int32, dev)
+    _done(load().evo_cache_evict(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                                 weights.data_ptr(), n, kept.data_ptr(), budget, recent, SeqShape(0, B, Hk, Hk, D),
+                                 cache, _DTYPE_CODE[dt], _options(None, 0, status, dev), sp), "evo_cache_evict")
     return kept
