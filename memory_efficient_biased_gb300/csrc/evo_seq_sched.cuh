@@ -4,7 +4,7 @@
 // A work item is a block of one sequence's tokens with all the heads of one group, over
 // what its tokens see (or, for a block of keys, are seen by); items are laid out one behind
 // the other (sequence, kv head, block), and each counts as many units as it has tokens to
-// walk over, plus kItemCost for what every item costs.  CTA c takes the units [c·share, (c+1)·share): every CTA has the same amount of
+// walk over, plus cost() for what every item costs (its own loads, the first scores, the output).  CTA c takes the units [c·share, (c+1)·share): every CTA has the same amount of
 // work whatever the lengths are, and an item that a border cuts (between two tiles) is
 // computed in pieces, whose results are joined in a fixed order by a second kernel.
 #pragma once
@@ -12,9 +12,6 @@
 #include "evo_seq_internal.h"
 
 namespace evo {
-
-// An item's fixed cost (its query load, first scores and output) in keys.
-constexpr int kItemCost = 128;
 
 // One item or a piece of one, as the roles of a CTA see it.
 struct Work {
@@ -35,20 +32,23 @@ struct PieceRecord {
   int b, kvh, row0, t0, nt, pad;
 };
 
-// How a sequence's items are laid out and cut.  Both kinds count an item's units as what it
-// walks over (keys, or query tokens) plus kItemCost.
+// How a sequence's items are laid out and cut.  An item's units are what it walks over (keys, or
+// query tokens) plus cost(), about two tiles: measured on the forward, an item takes 3.4 us and a
+// key tile 1.85 us (with half that cost, CTAs that held 25 to 40 short items ended up to a third
+// later than the others).
 //
 // Blocks of W query tokens over the key tiles they see (forward, dQ).
 struct QueryBlocks {
   int W;
+  __device__ __forceinline__ int cost() const { return 2 * kTile; }
   __device__ __forceinline__ int count(const Seq& q) const { return (q.n + W - 1) / W; }
   // a position below 0 (more new tokens than the length) counts as 0
   __device__ __forceinline__ long long of(const Seq& q, int p) const {
     const long long end = static_cast<long long>(p + 1) * W;
-    return (q.pos0 > 0 ? q.pos0 : 0) + (end < q.n ? end : q.n) + kItemCost;
+    return (q.pos0 > 0 ? q.pos0 : 0) + (end < q.n ? end : q.n) + cost();
   }
   __device__ __forceinline__ long long before(const Seq& q, int p) const {  // p < count
-    return p * static_cast<long long>((q.pos0 > 0 ? q.pos0 : 0) + kItemCost) + static_cast<long long>(W) * p * (p + 1) / 2;
+    return p * static_cast<long long>((q.pos0 > 0 ? q.pos0 : 0) + cost()) + static_cast<long long>(W) * p * (p + 1) / 2;
   }
   __device__ __forceinline__ void place(Work& w, const Seq& q, int p) const {
     w.t0 = p * W;
@@ -65,10 +65,11 @@ struct QueryBlocks {
 // Work: t0, nt the keys; j0, j1, kt tiles of queries.
 struct KeyBlocks {
   int TQ;
+  __device__ __forceinline__ int cost() const { return 2 * TQ; }
   __device__ __forceinline__ int count(const Seq& q) const { return (q.n + kTile - 1) / kTile; }
-  __device__ __forceinline__ long long of(const Seq& q, int p) const { return q.n - p * kTile + kItemCost; }
+  __device__ __forceinline__ long long of(const Seq& q, int p) const { return q.n - p * kTile + cost(); }
   __device__ __forceinline__ long long before(const Seq& q, int p) const {
-    return p * static_cast<long long>(q.n + kItemCost) - static_cast<long long>(kTile / 2) * p * (p - 1);
+    return p * static_cast<long long>(q.n + cost()) - static_cast<long long>(kTile / 2) * p * (p - 1);
   }
   __device__ __forceinline__ void place(Work& w, const Seq& q, int p) const {
     w.t0 = p * kTile;
@@ -101,15 +102,20 @@ struct Walk {
     d = &desc;
     k = blocks;
     const int lane = threadIdx.x & 31;
-    long long all = 0;
-    for (int base = 0; base < desc.seqs; base += 32) {
+    // the first 32 sequences stay in the lanes' registers: for most calls that is all of them,
+    // and every look at device memory more costs the launch most of a microsecond
+    const Seq none{0, 0, 0, 0};
+    const Seq early = lane < desc.seqs ? load_seq(desc, lane) : none;
+    const long long units = total(early) * desc.kv_heads;
+    long long all = units;
+    for (int base = 32; base < desc.seqs; base += 32) {
       const int i = base + lane;
       if (i < desc.seqs) all += total(load_seq(desc, i)) * desc.kv_heads;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     long long share = (all + ctas - 1) / ctas;
-    if (share < kItemCost + 128) share = kItemCost + 128;
+    if (share < kTile) share = kTile;
     const long long x0 = share * cta;
     left = all - x0 < share ? all - x0 : share;
     b = desc.seqs;
@@ -120,7 +126,8 @@ struct Walk {
     long long passed = 0;  // units of the sequences before `base`
     for (int base = 0; base < desc.seqs; base += 32) {
       const int i = base + lane;
-      const long long mine = i < desc.seqs ? total(load_seq(desc, i)) * desc.kv_heads : 0;
+      const Seq mine_q = base == 0 ? early : (i < desc.seqs ? load_seq(desc, i) : none);
+      const long long mine = base == 0 ? units : total(mine_q) * desc.kv_heads;
       long long run = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -132,7 +139,10 @@ struct Walk {
         const int first = __ffs(any) - 1;
         const long long begin = __shfl_sync(0xffffffffu, passed + run - mine, first);
         b = base + first;
-        q = load_seq(desc, b);
+        q.row0 = __shfl_sync(0xffffffffu, mine_q.row0, first);
+        q.n = __shfl_sync(0xffffffffu, mine_q.n, first);
+        q.kv = __shfl_sync(0xffffffffu, mine_q.kv, first);
+        q.pos0 = __shfl_sync(0xffffffffu, mine_q.pos0, first);
         P = k.count(q);
         const long long per = total(q);
         long long x = x0 - begin;
@@ -164,7 +174,7 @@ struct Walk {
       k.place(w, q, p);
       const int begin = k.first(w);
       auto tile = [&](long long x) {
-        const int t = x > kItemCost ? k.tile(w, x - kItemCost) : begin;
+        const int t = x > k.cost() ? k.tile(w, x - k.cost()) : begin;
         return t < w.kt ? t : w.kt;
       };
       w.j0 = tile(off);

@@ -44,16 +44,17 @@ struct Layout {
 // Work: t0, nt the keys; pos the first new token's position; kv_end the new tokens.
 struct CachedKeyBlocks {
   int TQ;
+  __device__ __forceinline__ int cost() const { return 2 * TQ; }
   __device__ __forceinline__ int count(const Seq& q) const { return q.n > 0 ? (q.kv + kTile - 1) / kTile : 0; }
   __device__ __forceinline__ int unseen(const Seq& q, int p) const {  // new tokens in front of the keys
     return p * kTile > q.pos0 ? p * kTile - q.pos0 : 0;
   }
-  __device__ __forceinline__ long long of(const Seq& q, int p) const { return q.n - unseen(q, p) + kItemCost; }
+  __device__ __forceinline__ long long of(const Seq& q, int p) const { return q.n - unseen(q, p) + cost(); }
   __device__ __forceinline__ long long before(const Seq& q, int p) const {
     const long long whole = q.pos0 >= 0 ? q.pos0 / kTile + 1 : 0;  // blocks that every new token sees
     const long long x = p;
-    if (x <= whole) return x * (q.n + kItemCost);
-    return x * kItemCost + whole * q.n + (x - whole) * q.kv - (kTile / 2) * (x * (x - 1) - whole * (whole - 1));
+    if (x <= whole) return x * (q.n + cost());
+    return x * cost() + whole * q.n + (x - whole) * q.kv - (kTile / 2) * (x * (x - 1) - whole * (whole - 1));
   }
   __device__ __forceinline__ void place(Work& w, const Seq& q, int p) const {
     w.t0 = p * kTile;
