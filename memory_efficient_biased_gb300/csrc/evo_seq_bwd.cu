@@ -407,26 +407,30 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8]) {
                : "memory");
 }
 
-// Columns [c0, c1) (multiples of 32; stops at D) of this thread's row of an accumulator: times f in the
+// Columns [c0, c1) (N at a time; stops at D) of this thread's row of an accumulator: times f in the
 // result's type at `out`, or as they are at `part`.  Warp-collective.
-template <bool BF16>
+template <int N, bool BF16>
 __device__ __forceinline__ void write_row(uint32_t col, int c0, int c1, int D, bool live, bool piece, float f, uint16_t* out,
                                           bool out32, float* part) {
 #pragma unroll 1
-  for (int c = c0; c < c1 && c < D; c += 32) {
-    uint32_t x[32];
-    tmem_ld32(col + c, x);
+  for (int c = c0; c < c1 && c < D; c += N) {
+    uint32_t x[N];
+    if constexpr (N == 64) {
+      tmem_ld64(col + c, x);
+    } else {
+      tmem_ld32(col + c, x);
+    }
     tmem_wait_ld(x);
     if (live) {
       if (piece) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
+        for (int e = 0; e < N; e += 8) {
           const uint32_t(&o)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&x[e]);
           st_global_32(part + c + e, o);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 32; e += 16) {
+        for (int e = 0; e < N; e += 16) {
           uint32_t o[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -570,7 +574,7 @@ __device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float* ro
     const size_t row = static_cast<size_t>(w.row0) + key;
     uint16_t* out = (grp ? a.dk + row * a.dk_stride : a.dv + row * a.dv_stride) + static_cast<size_t>(w.kvh) * s.D;
     float* part = a.part + (((static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * 2 + grp) * kTile + r) * DP;
-    write_row<BF16>(trow + (grp ? kColK : kColV), 0, DP, s.D, live, w.slot >= 0, grp ? a.scale : 1.0f, out,
+    write_row<64, BF16>(trow + (grp ? kColK : kColV), 0, DP, s.D, live, w.slot >= 0, grp ? a.scale : 1.0f, out,
                     grp ? a.dk32 : a.dv32, part);
     tc_fence_before();
     __syncwarp();
@@ -637,7 +641,7 @@ __device__ __forceinline__ void compute_dq(const SeqBwdArgs& a, Bars* bars, uint
     tc_fence_after();
     uint16_t* out = a.dq + row * a.dq_stride + static_cast<size_t>(h) * s.D;
     float* part = a.part + ((static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * kTile + r) * DP;
-    write_row<BF16>(trow + kColQ, grp * (DP / 2), (grp + 1) * (DP / 2), s.D, live, w.slot >= 0, a.scale, out, a.dq32, part);
+    write_row<DP / 2, BF16>(trow + kColQ, grp * (DP / 2), (grp + 1) * (DP / 2), s.D, live, w.slot >= 0, a.scale, out, a.dq32, part);
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->acc_free));
@@ -738,39 +742,38 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------ pieces, summed in order
+// Eight threads a row, 32 rows a block.
 template <int DP, bool BF16, bool DKV>
 __global__ void __launch_bounds__(256) evo_seq_bwd_join_kernel(const __grid_constant__ SeqBwdArgs a, int ctas) {
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  constexpr int kParts = DKV ? 2 : 1;
+  const int c0 = blockIdx.x, i = blockIdx.y * 32 + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (DP / 8);
   const PieceRecord first = a.records[2 * c0 + 1];
   if (!first.used) return;
+  const int pieces = count_pieces(a.records, c0, ctas);
   const SeqDesc& s = a.s;
-  int pieces = 1;
-  while (c0 + pieces < ctas) {
-    const PieceRecord p = a.records[2 * (c0 + pieces)];
-    if (!p.used) break;
-    ++pieces;
-    if (p.ends) break;
-  }
-  constexpr int kParts = DKV ? 2 : 1;
-  {
-    const int i = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int part = i / kTile, r = i % kTile;
-    const int tok = DKV ? r : r / s.group;
-    if (tok >= first.nt || (!DKV && tok >= a.TQ)) return;
-    float x[DP / 32] = {};
-    for (int p = 0; p < pieces; ++p) {
-      const float* y = a.part + (((static_cast<size_t>(c0 + p) * 2 + (p == 0)) * kParts + part) * kTile + r) * DP;
+  const int part = i / kTile, r = i % kTile;
+  const int tok = DKV ? r : r / s.group;
+  if (tok >= first.nt || (!DKV && tok >= a.TQ)) return;
+  float x[DP / 8] = {};
+  for (int p = 0; p < pieces; ++p) {
+    const float4* y = reinterpret_cast<const float4*>(
+        a.part + (((static_cast<size_t>(c0 + p) * 2 + (p == 0)) * kParts + part) * kTile + r) * DP + d0);
 #pragma unroll
-      for (int e = 0; e < DP / 32; ++e)
-        if (lane + 32 * e < s.D) x[e] += y[lane + 32 * e];
+    for (int e = 0; e < DP / 32; ++e) {
+      const float4 v = y[e];
+      x[4 * e] += v.x, x[4 * e + 1] += v.y, x[4 * e + 2] += v.z, x[4 * e + 3] += v.w;
     }
-    const size_t row = static_cast<size_t>(first.row0) + first.t0 + tok;
-    uint16_t* out = DKV ? (part ? a.dk + row * a.dk_stride : a.dv + row * a.dv_stride) + static_cast<size_t>(first.kvh) * s.D
-                        : a.dq + row * a.dq_stride + static_cast<size_t>(first.kvh * s.group + r % s.group) * s.D;
-    const float f = DKV && part == 0 ? 1.0f : a.scale;
+  }
+  const size_t row = static_cast<size_t>(first.row0) + first.t0 + tok;
+  uint16_t* out = DKV ? (part ? a.dk + row * a.dk_stride : a.dv + row * a.dv_stride) + static_cast<size_t>(first.kvh) * s.D
+                      : a.dq + row * a.dq_stride + static_cast<size_t>(first.kvh * s.group + r % s.group) * s.D;
+  const float f = DKV && part == 0 ? 1.0f : a.scale;
 #pragma unroll
-    for (int e = 0; e < DP / 32; ++e)
-      if (lane + 32 * e < s.D) out[lane + 32 * e] = static_cast<uint16_t>(pack2<BF16>(x[e] * f, 0.0f) & 0xffffu);
+  for (int e = 0; e < DP / 8; e += 8) {  // (columns past D hold nothing and are not written)
+    uint32_t v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = pack2<BF16>(x[e + 2 * q] * f, x[e + 2 * q + 1] * f);
+    if (d0 + e < s.D) *reinterpret_cast<uint4*>(out + d0 + e) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -813,7 +816,7 @@ cudaError_t launch_k(const SeqBwdArgs& a, int ctas, cudaStream_t st) {
   const size_t smem = Layout<DP>::total > 118784 ? Layout<DP>::total : 118784;
   kern<<<ctas, kThreads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  evo_seq_bwd_join_kernel<DP, BF16, DKV><<<dim3(ctas, (DKV ? 2 : 1) * kTile / 8), 256, 0, st>>>(a, ctas);
+  evo_seq_bwd_join_kernel<DP, BF16, DKV><<<dim3(ctas, (DKV ? 2 : 1) * kTile / 32), 256, 0, st>>>(a, ctas);
   return cudaGetLastError();
 }
 template <int DP, bool BF16>

@@ -394,12 +394,12 @@ __device__ __forceinline__ void leave_scores(const uint32_t (&y)[64], float scal
 }
 
 // The values of V that were taken out of the item's tiles, added to a row that sees them
-// (features c0 .. c0 + 31 of the unscaled O; what is added is an infinity or a NaN).
+// (features c0 .. c0 + 63 of the unscaled O; what is added is an infinity or a NaN).
 template <bool BF16>
-__device__ __forceinline__ void add_back(const SeqFwdArgs& a, const Work& w, int pos, int c0, uint32_t (&out)[32]) {
-  uint32_t x[32];  // indexed by a run-time column: kept apart from the caller's registers
+__device__ __forceinline__ void add_back(const SeqFwdArgs& a, const Work& w, int pos, int c0, uint32_t (&out)[64]) {
+  uint32_t x[64];  // indexed by a run-time column: kept apart from the caller's registers
 #pragma unroll
-  for (int c = 0; c < 32; ++c) x[c] = out[c];
+  for (int c = 0; c < 64; ++c) x[c] = out[c];
   const SeqDesc& s = a.s;
   int from = w.pos + 1 > w.j0 * kTile ? w.pos + 1 : w.j0 * kTile;
   if (from < 0) from = 0;
@@ -414,13 +414,13 @@ __device__ __forceinline__ void add_back(const SeqFwdArgs& a, const Work& w, int
       row = a.v + static_cast<long long>(w.row0 + j) * a.v_stride + static_cast<long long>(w.kvh) * s.D;
     }
 #pragma unroll 1
-    for (int c = 0; c < 32 && c0 + c < s.D; ++c) {
+    for (int c = 0; c < 64 && c0 + c < s.D; ++c) {
       const uint16_t v = row[c0 + c];
       if (not_finite2<BF16>(v) & 0xffffu) x[c] = __float_as_uint(__uint_as_float(x[c]) + to_f32<BF16>(v));
     }
   }
 #pragma unroll
-  for (int c = 0; c < 32; ++c) out[c] = x[c];
+  for (int c = 0; c < 64; ++c) out[c] = x[c];
 }
 
 // SCORES: leave the scores behind for the sums of the weights (a kernel of its own: as a branch in
@@ -583,23 +583,24 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
         const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * 256 + gq * 128 + r;
         float* part = a.part_o + prow * DP;
 #pragma unroll 1
-        for (int c = 0; c < s.D; c += 32) {
-          uint32_t x[32];
-          tmem_ld32(ocol + c, x);
-          tmem_wait_ld(x);
+        for (int c = 0; c < s.D; c += 64) {
+          uint32_t x[64];
+          tmem_ld64(ocol + c, x);
           if (two) {
-            uint32_t y[32];
-            tmem_ld32(trow + col_o(1) + c, y);
+            uint32_t y[64];
+            tmem_ld64(trow + col_o(1) + c, y);
             tmem_wait_ld(y);
+            tmem_wait_ld(x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 64; ++e)
               x[e] = __float_as_uint(__uint_as_float(x[e]) * f0 + __uint_as_float(y[e]) * f1);
           }
+          tmem_wait_ld(x);
           if (live) {
             if (dirty) add_back<BF16>(a, w, pos, c, x);
             if (w.slot < 0) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 16) {
+              for (int e = 0; e < 64; e += 16) {
                 uint32_t o[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -615,7 +616,7 @@ __device__ __forceinline__ void softmax(const SeqFwdArgs& a, uint8_t* base, Bars
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
+              for (int e = 0; e < 64; e += 8) {
                 const uint32_t(&o)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&x[e]);
                 st_global_32(part + c + e, o);
               }
@@ -719,16 +720,10 @@ __global__ void __launch_bounds__(256) evo_seq_join_kernel(const __grid_constant
   const int c0 = blockIdx.x, i = blockIdx.y * kJoinRows + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (DP / 8);
   const PieceRecord first = a.records[2 * c0 + 1];
   if (!first.used) return;
+  const int pieces = count_pieces(a.records, c0, ctas);
   const SeqDesc& s = a.s;
   const int gq = i >> 7, r = i & 127, dt = r / s.group, tok = gq * a.TQ + dt;
   if (dt >= a.TQ || tok >= first.nt) return;
-  int pieces = 1;
-  while (c0 + pieces < ctas) {
-    const PieceRecord p = a.records[2 * (c0 + pieces)];
-    if (!p.used) break;
-    ++pieces;
-    if (p.ends) break;
-  }
   auto at = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * 256 + i; };
   float big = -INFINITY;
   for (int p = 0; p < pieces; ++p) {

@@ -32,6 +32,24 @@ struct PieceRecord {
   int b, kvh, row0, t0, nt, pad;
 };
 
+// How many pieces the item has that begins in slot 1 of CTA c0: it goes on in slot 0 of the next
+// CTAs up to the one that ends it.  Whole warps; the records are read 32 at a time.
+__device__ __forceinline__ int count_pieces(const PieceRecord* records, int c0, int ctas) {
+  const int lane = threadIdx.x & 31;
+  for (int base = c0 + 1; base < ctas; base += 32) {
+    int used = 0, ends = 0;
+    if (base + lane < ctas) {
+      used = records[2 * (base + lane)].used;
+      ends = records[2 * (base + lane)].ends;
+    }
+    const uint32_t gap = __ballot_sync(0xffffffffu, !used), last = __ballot_sync(0xffffffffu, used && ends);
+    const int g = gap ? __ffs(gap) - 1 : 32, e = last ? __ffs(last) - 1 : 32;
+    if (e < g) return base - c0 + e + 1;
+    if (g < 32) return base - c0 + g;
+  }
+  return ctas - c0;
+}
+
 // How a sequence's items are laid out and cut.  An item's units are what it walks over (keys, or
 // query tokens) plus cost(), about two tiles: measured on the forward, an item takes 3.4 us and a
 // key tile 1.85 us (with half that cost, CTAs that held 25 to 40 short items ended up to a third

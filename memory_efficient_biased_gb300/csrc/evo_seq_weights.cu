@@ -371,14 +371,11 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_weights_kernel(const __gr
 __global__ void __launch_bounds__(kTile) evo_seq_weights_join_kernel(const __grid_constant__ SeqWeightsArgs a, int ctas) {
   const int c0 = blockIdx.x, r = threadIdx.x;
   const PieceRecord first = a.records[2 * c0 + 1];
-  if (!first.used || r >= first.nt) return;
+  if (!first.used) return;
+  const int pieces = count_pieces(a.records, c0, ctas);
+  if (r >= first.nt) return;
   float sum = a.part[(static_cast<size_t>(c0) * 2 + 1) * kTile + r];
-  for (int p = 1; c0 + p < ctas; ++p) {
-    const PieceRecord rec = a.records[2 * (c0 + p)];
-    if (!rec.used) break;
-    sum += a.part[static_cast<size_t>(c0 + p) * 2 * kTile + r];
-    if (rec.ends) break;
-  }
+  for (int p = 1; p < pieces; ++p) sum += a.part[static_cast<size_t>(c0 + p) * 2 * kTile + r];
   a.weights[(static_cast<size_t>(first.b) * a.s.kv_heads + first.kvh) * a.weights_len + first.t0 + r] += sum;
 }
 
