@@ -816,6 +816,7 @@ cudaError_t launch_k(const SeqBwdArgs& a, int ctas, cudaStream_t st) {
   const size_t smem = Layout<DP>::total > 118784 ? Layout<DP>::total : 118784;
   kern<<<ctas, kThreads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.s.tokens <= (DKV ? a.TQ : kTile)) return e;  // items of one tile: nothing is cut
   evo_seq_bwd_join_kernel<DP, BF16, DKV><<<dim3(ctas, (DKV ? 2 : 1) * kTile / 32), 256, 0, st>>>(a, ctas);
   return cudaGetLastError();
 }

@@ -160,52 +160,79 @@ __global__ void __launch_bounds__(kSelThreads) evo_evict_select_kernel(const Evi
 }
 
 // ------------------------------------------------------------------ eviction: moves
-constexpr int kMoveThreads = 256, kMoveDeep = 8;
+constexpr int kMoveThreads = 256, kMoveDeep = 4, kMoveTable = 4096;
 
 // One CTA per 64-byte slice of the rows of one (sequence, kv head) of keys or values.
 // Row i moves from place kept[i] >= i: no row that is still to be read lies at or below a
 // place already written, so batches in order need only all of a batch's reads to be done
 // before its writes (one barrier), and the next batch's reads may be under way meanwhile.
 // Bound by the bytes: a row read and written once.  64-byte slices rather than whole rows
-// give four times the CTAs at head_dim 128 and keep whole sectors.
+// give four times the CTAs at head_dim 128 and keep whole sectors.  The places of a batch are
+// read two batches ahead and the sequence's pages are looked up in shared memory, so that
+// only the rows themselves are waited for.
 __global__ void __launch_bounds__(kMoveThreads) evo_evict_move_kernel(const EvictArgs a, int slices) {
+  __shared__ int table[kMoveTable];
   const SeqDesc& s = a.s;
   const int slice = blockIdx.x % slices, kv = blockIdx.x / slices, h = blockIdx.y, b = blockIdx.z;
+  const int* kept = a.kept + (static_cast<long long>(b) * s.kv_heads + h) * a.budget;
+  const int len = kept[a.budget - 1] < 0 ? 0 : kept[a.budget - 1] + 1;  // the last row kept is the newest
+  const int entries = len / s.page + 1;
+  for (int i = threadIdx.x; i < entries && i < s.pages_per_seq && i < kMoveTable; i += kMoveThreads)
+    table[i] = s.table[static_cast<size_t>(b) * s.pages_per_seq + i];
+  __syncthreads();
   uint16_t* pages = kv ? a.v_pages : a.k_pages;
   const long long page_stride = kv ? a.v_page : a.k_page;
-  const int* kept = a.kept + (static_cast<long long>(b) * s.kv_heads + h) * a.budget;
   const int chunk = slice * 4 + (threadIdx.x & 3);  // 16 bytes
   const bool live = chunk * 8 < s.D;
   constexpr int kRows = kMoveThreads / 4 * kMoveDeep;
   const int r0 = threadIdx.x >> 2;
+  const int row = s.kv_heads * s.D;
+  pages += static_cast<long long>(h) * s.D + chunk * 8;
   auto place = [&](int j) -> uint16_t* {
-    const int p = page_of(s, b, j);
-    if (p < 0) return nullptr;
-    return pages + p * page_stride + (static_cast<long long>(j % s.page) * s.kv_heads + h) * s.D + chunk * 8;
+    const int e = j / s.page;
+    int p;
+    if (e < kMoveTable) {
+      p = table[e];
+      if (p < 0 || p >= s.num_pages) {
+        report_bad_index(s.status);
+        return nullptr;
+      }
+    } else {
+      p = page_of(s, b, j);
+      if (p < 0) return nullptr;
+    }
+    return pages + p * page_stride + static_cast<long long>(j - e * s.page) * row;
   };
-  uint4 now[kMoveDeep], ahead[kMoveDeep];
-  uint32_t has_now = 0, has_ahead = 0;
-  auto load = [&](int base, uint4 (&x)[kMoveDeep], uint32_t& has) {
-    has = 0;
-    int from[kMoveDeep];
+  auto places = [&](int base, int (&from)[kMoveDeep]) {
 #pragma unroll
     for (int e = 0; e < kMoveDeep; ++e) {
       const int i = base + e * (kMoveThreads / 4) + r0;
       from[e] = i < a.budget && live ? kept[i] : -1;
-      if (from[e] == i) from[e] = -1;  // stays where it is
     }
+  };
+  auto load = [&](int base, const int (&from)[kMoveDeep], uint4 (&x)[kMoveDeep]) -> uint32_t {
+    uint32_t has = 0;
 #pragma unroll
     for (int e = 0; e < kMoveDeep; ++e) {
-      if (from[e] < 0) continue;
+      // (a row that stays where it is is left alone)
+      if (from[e] < 0 || from[e] == base + e * (kMoveThreads / 4) + r0) continue;
       const uint16_t* p = place(from[e]);
       if (!p) continue;
       x[e] = __ldcg(reinterpret_cast<const uint4*>(p));
       has |= 1u << e;
     }
+    return has;
   };
-  load(0, now, has_now);
+  uint4 now[kMoveDeep], ahead[kMoveDeep];
+  int from[kMoveDeep], next[kMoveDeep];
+  places(0, from);
+  places(kRows, next);
+  uint32_t has_now = load(0, from, now), has_ahead = 0;
   for (int base = 0; base < a.budget; base += kRows) {
-    load(base + kRows, ahead, has_ahead);
+#pragma unroll
+    for (int e = 0; e < kMoveDeep; ++e) from[e] = next[e];
+    places(base + 2 * kRows, next);
+    has_ahead = load(base + kRows, from, ahead);
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < kMoveDeep; ++e) {
@@ -219,8 +246,8 @@ __global__ void __launch_bounds__(kMoveThreads) evo_evict_move_kernel(const Evic
   }
   // the only reader and writer of this length in this launch
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0) {
-    const int len = a.seq_lens[b];
-    if (len > a.budget && len <= s.max_kv) a.seq_lens[b] = a.budget;
+    const int n = a.seq_lens[b];
+    if (n > a.budget && n <= s.max_kv) a.seq_lens[b] = a.budget;
   }
 }
 

@@ -773,7 +773,7 @@ cudaError_t launch_k(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
 template <int DP, bool BF16>
 cudaError_t launch_t(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
   const cudaError_t e = a.scores ? launch_k<DP, BF16, true>(a, ctas, st) : launch_k<DP, BF16, false>(a, ctas, st);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.s.max_kv <= kTile) return e;  // one key tile: nothing is cut
   evo_seq_join_kernel<DP, BF16><<<dim3(ctas, 256 / kJoinRows), 256, 0, st>>>(a, ctas);
   return cudaGetLastError();
 }
