@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kSelThreads) evo_evict_select_kernel(const Evi
 }
 
 // ------------------------------------------------------------------ eviction: moves
-constexpr int kMoveThreads = 256, kMoveDeep = 4, kMoveTable = 4096;
+constexpr int kMoveThreads = 512, kMoveDeep = 4, kMoveTable = 4096;
 
 // One CTA per 64-byte slice of the rows of one (sequence, kv head) of keys or values.
 // Row i moves from place kept[i] >= i: no row that is still to be read lies at or below a
@@ -169,13 +169,14 @@ constexpr int kMoveThreads = 256, kMoveDeep = 4, kMoveTable = 4096;
 // Bound by the bytes: a row read and written once.  64-byte slices rather than whole rows
 // give four times the CTAs at head_dim 128 and keep whole sectors.  The places of a batch are
 // read two batches ahead and the sequence's pages are looked up in shared memory, so that
-// only the rows themselves are waited for.
+// only the rows themselves are waited for.  (16 sequences, 8 heads of 128, 4096 rows kept: 512 threads
+// with four rows each in flight 96 us, 5.6 TB/s; 256 threads 102, eight rows each 134, 128-byte slices 112.)
 __global__ void __launch_bounds__(kMoveThreads) evo_evict_move_kernel(const EvictArgs a, int slices) {
   __shared__ int table[kMoveTable];
   const SeqDesc& s = a.s;
   const int slice = blockIdx.x % slices, kv = blockIdx.x / slices, h = blockIdx.y, b = blockIdx.z;
   const int* kept = a.kept + (static_cast<long long>(b) * s.kv_heads + h) * a.budget;
-  const int len = kept[a.budget - 1] < 0 ? 0 : kept[a.budget - 1] + 1;  // the last row kept is the newest
+  const int len = kept[a.budget - 1] + 1;  // places read are below it (0: the sequence is not cut)
   const int entries = len / s.page + 1;
   for (int i = threadIdx.x; i < entries && i < s.pages_per_seq && i < kMoveTable; i += kMoveThreads)
     table[i] = s.table[static_cast<size_t>(b) * s.pages_per_seq + i];
