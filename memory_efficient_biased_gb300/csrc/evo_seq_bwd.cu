@@ -158,9 +158,11 @@ __device__ __forceinline__ void producer(const SeqBwdArgs& a, uint8_t* base, Bar
 template <int DP, bool DKV>
 __device__ __forceinline__ void walk(const SeqBwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
   using L = Layout<DP>;
-  using Blocks = typename std::conditional<DKV, KeyBlocks, QueryBlocks>::type;
-  Walk<Blocks> walk;
-  walk.init(a.s, Blocks{a.TQ}, blockIdx.x, gridDim.x);
+  Walk<typename std::conditional<DKV, KeyBlocks, QueryBlocks>::type> walk;
+  if constexpr (DKV)
+    walk.init(a.s, KeyBlocks{a.TQ}, blockIdx.x, gridDim.x);
+  else
+    walk.init(a.s, QueryBlocks{a.TQ}, blockIdx.x, gridDim.x);
   PieceRecord* rec = a.records + 2 * blockIdx.x;
   if (lane < 2) rec[lane].used = 0;
   __syncwarp();
@@ -778,31 +780,44 @@ __global__ void __launch_bounds__(256) evo_seq_bwd_join_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------ lse and delta
-// 16 threads per (row, head), 16 bytes of O and of dO each.  Bound by those bytes.
+// 16 threads per (row, head), 16 bytes of O and of dO each, four (row, head)s one behind the other
+// so that eight loads are under way.  Bound by those bytes.
+constexpr int kRowsPer = 4;
 template <bool BF16>
 __global__ void __launch_bounds__(256) evo_seq_rows_kernel(const __grid_constant__ SeqBwdArgs a) {
   const SeqDesc& s = a.s;
-  const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) >> 4;
   const int c = threadIdx.x & 15;
-  float d = 0.0f;
-  const bool in = i < static_cast<long long>(s.tokens) * s.q_heads;
-  const int t = in ? static_cast<int>(i / s.q_heads) : 0, h = in ? static_cast<int>(i % s.q_heads) : 0;
-  if (in && c * 8 < s.D) {
-    const uint4 x = *reinterpret_cast<const uint4*>(a.out + t * a.out_stride + static_cast<long long>(h) * s.D + c * 8);
-    const uint4 y = *reinterpret_cast<const uint4*>(a.dout + t * a.dout_stride + static_cast<long long>(h) * s.D + c * 8);
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  const long long first = static_cast<long long>(blockIdx.x) * (16 * kRowsPer) + (threadIdx.x >> 4);
+  const long long end = static_cast<long long>(s.tokens) * s.q_heads;
+  uint4 x[kRowsPer], y[kRowsPer];
+  float z[kRowsPer];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 u = unpack2<BF16>(xs[e]), v = unpack2<BF16>(ys[e]);
+  for (int e = 0; e < kRowsPer; ++e) {
+    const long long i = first + 16 * e;
+    x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
+    z[e] = 0.0f;
+    if (i >= end) continue;
+    const int t = static_cast<int>(i / s.q_heads), h = static_cast<int>(i % s.q_heads);
+    if (c * 8 < s.D) {
+      x[e] = *reinterpret_cast<const uint4*>(a.out + t * a.out_stride + static_cast<long long>(h) * s.D + c * 8);
+      y[e] = *reinterpret_cast<const uint4*>(a.dout + t * a.dout_stride + static_cast<long long>(h) * s.D + c * 8);
+    }
+    if (c == 0) z[e] = a.lse[static_cast<size_t>(h) * s.tokens + t];
+  }
+#pragma unroll
+  for (int e = 0; e < kRowsPer; ++e) {
+    const uint32_t xs[4] = {x[e].x, x[e].y, x[e].z, x[e].w}, ys[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+    float d = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 u = unpack2<BF16>(xs[q]), v = unpack2<BF16>(ys[q]);
       d = fmaf(u.x, v.x, d);
       d = fmaf(u.y, v.y, d);
     }
-  }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if (in && c == 0) {
-    const float z = a.lse[static_cast<size_t>(h) * s.tokens + t];
-    a.rows[i] = make_float2(z == -INFINITY ? -INFINITY : -z * kSeqLog2e, -d);
+    for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    const long long i = first + 16 * e;
+    if (i < end && c == 0) a.rows[i] = make_float2(z[e] == -INFINITY ? -INFINITY : -z[e] * kSeqLog2e, -d);
   }
 }
 
@@ -823,7 +838,7 @@ cudaError_t launch_k(const SeqBwdArgs& a, int ctas, cudaStream_t st) {
 template <int DP, bool BF16>
 cudaError_t launch_t(const SeqBwdArgs& a, int ctas, cudaStream_t st) {
   const long long n = static_cast<long long>(a.s.tokens) * a.s.q_heads;
-  evo_seq_rows_kernel<BF16><<<static_cast<unsigned>((n + 15) / 16), 256, 0, st>>>(a);
+  evo_seq_rows_kernel<BF16><<<static_cast<unsigned>((n + 16 * kRowsPer - 1) / (16 * kRowsPer)), 256, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) e = launch_k<DP, BF16, true>(a, ctas, st);
   if (e == cudaSuccess) e = launch_k<DP, BF16, false>(a, ctas, st);

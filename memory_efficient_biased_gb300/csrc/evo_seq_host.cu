@@ -134,6 +134,19 @@ SeqDesc desc(const evo_seq_shape_t& s, const int32_t* cu, const int32_t* lens, c
   return d;
 }
 
+// CTAs of a launch: one per SM, or as many shares of a tile as the work can fill, whatever the
+// lengths turn out to be (blocks: items per kv head; most: units of one).
+int fwd_ctas(int sms, const evo_seq_shape_t& s, int64_t max_kv) {
+  const double W = 2 * (kTile / (s.q_heads / s.kv_heads));
+  const double units = (double(s.tokens) / W + double(s.seqs)) * (double(max_kv) + 2 * kTile) * double(s.kv_heads);
+  return units < double(sms) * kTile ? static_cast<int>(units / kTile) + 1 : sms;
+}
+int bwd_ctas(int sms, const evo_seq_shape_t& s) {
+  const double TQ = kTile / (s.q_heads / s.kv_heads), T = double(s.tokens);
+  const double units = (T / TQ + double(s.seqs)) * (T + 3 * kTile) * double(s.kv_heads);  // dQ's, the more
+  return units < double(sms) * kTile ? static_cast<int>(units / kTile) + 1 : sms;
+}
+
 // Scores left behind by the forward for the weights (0: they are formed again).  A row's score is
 // written and read once, 8 bytes a key; forming it again reads 2 head_dim bytes a key, whatever
 // the number of rows.  So: up to 16 rows a key on the average, and only while the
@@ -186,7 +199,7 @@ float scale_of(const Opts& o, const evo_seq_shape_t& s) {
 }
 
 // Fills what both forwards share and launches; K and V maps are the caller's.
-evo_status_t run_fwd(SeqFwdArgs& a, const void* q, const void* v, void* out, float* lse, void* workspace, int sms,
+evo_status_t run_fwd(SeqFwdArgs& a, const void* q, const void* v, void* out, float* lse, void* workspace, int ctas,
                      const evo_seq_shape_t& s, bool bf16, const Strides& t, const Opts& o, cudaStream_t st) {
   const int G = static_cast<int>(s.q_heads / s.kv_heads);
   a.TQ = kTile / G;
@@ -199,8 +212,8 @@ evo_status_t run_fwd(SeqFwdArgs& a, const void* q, const void* v, void* out, flo
   a.out_stride = t.out;
   a.lse = lse;
   a.wait_ns = o.wait_ns;
-  seq_fwd_workspace(sms, static_cast<int>(s.head_dim), &a, static_cast<uint8_t*>(workspace));
-  const cudaError_t e = launch_seq_fwd(a, sms, bf16, st);
+  seq_fwd_workspace(ctas, static_cast<int>(s.head_dim), &a, static_cast<uint8_t*>(workspace));
+  const cudaError_t e = launch_seq_fwd(a, ctas, bf16, st);
   return e == cudaSuccess ? EVO_OK : cuda_fail("sequence forward launch", e);
 }
 
@@ -213,18 +226,20 @@ extern "C" {
 
 size_t evo_prompt_fwd_workspace_bytes(evo_seq_shape_t shape) {
   if (check_seq_shape(shape, true) != EVO_OK) return 0;
-  return seq_fwd_workspace(num_sms(), static_cast<int>(shape.head_dim), nullptr, nullptr);
+  return seq_fwd_workspace(fwd_ctas(num_sms(), shape, shape.tokens), static_cast<int>(shape.head_dim), nullptr, nullptr);
 }
 
 size_t evo_prompt_bwd_workspace_bytes(evo_seq_shape_t shape) {
   if (check_seq_shape(shape, true) != EVO_OK) return 0;
-  return prompt_bwd_workspace(num_sms(), desc(shape, nullptr, nullptr, nullptr, nullptr, -1, nullptr), nullptr, nullptr);
+  return prompt_bwd_workspace(bwd_ctas(num_sms(), shape), desc(shape, nullptr, nullptr, nullptr, nullptr, -1, nullptr),
+                              nullptr, nullptr);
 }
 
 size_t evo_paged_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache_shape_t cache, int64_t weights_len) {
   int64_t a, b;
   if (check_seq_shape(shape, true) != EVO_OK || check_cache(cache, shape, &a, &b) != EVO_OK || weights_len < 0) return 0;
-  return seq_fwd_workspace(num_sms(), static_cast<int>(shape.head_dim), nullptr, nullptr) +
+  return seq_fwd_workspace(fwd_ctas(num_sms(), shape, cache.page_size * cache.pages_per_seq),
+                           static_cast<int>(shape.head_dim), nullptr, nullptr) +
          scores_bytes(shape, cache, weights_len);
 }
 
@@ -259,7 +274,8 @@ evo_status_t evo_prompt_fwd(const void* q, const void* k, const void* v, const i
   const bool bf16 = dtype == EVO_BF16;
   if (!map_rows(&a.tk, k, bf16, shape, t.k) || !map_rows(&a.tv, v, bf16, shape, t.v)) return EVO_ERR_CUDA;
   a.v_stride = t.v;
-  return run_fwd(a, q, v, out, lse, workspace, sms, shape, bf16, t, o, static_cast<cudaStream_t>(stream));
+  return run_fwd(a, q, v, out, lse, workspace, fwd_ctas(sms, shape, shape.tokens), shape, bf16, t, o,
+                 static_cast<cudaStream_t>(stream));
 }
 
 evo_status_t evo_prompt_bwd(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, const void* out,
@@ -312,8 +328,9 @@ evo_status_t evo_prompt_bwd(const void* q, const void* k, const void* v, const i
   a.dv = static_cast<uint16_t*>(dv);
   a.out_stride = t.out, a.dout_stride = t.dout, a.dq_stride = t.dq, a.dk_stride = t.dk, a.dv_stride = t.dv;
   a.wait_ns = o.wait_ns;
-  prompt_bwd_workspace(sms, a.s, &a, static_cast<uint8_t*>(workspace));
-  const cudaError_t e = launch_prompt_bwd(a, sms, bf16, static_cast<cudaStream_t>(stream));
+  const int ctas = bwd_ctas(sms, shape);
+  prompt_bwd_workspace(ctas, a.s, &a, static_cast<uint8_t*>(workspace));
+  const cudaError_t e = launch_prompt_bwd(a, ctas, bf16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? EVO_OK : cuda_fail("prompt backward launch", e);
 }
 
@@ -405,12 +422,13 @@ evo_status_t evo_paged_fwd(const void* q, const void* k_pages, const void* v_pag
   if (!map_pages(&a.tk, k_pages, bf16, shape, cache, kp) || !map_pages(&a.tv, v_pages, bf16, shape, cache, vp))
     return EVO_ERR_CUDA;
   a.v_page = vp;
+  const int ctas = fwd_ctas(sms, shape, cache.page_size * cache.pages_per_seq);
   if (weights && scores_bytes(shape, cache, weights_len)) {
     a.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                        seq_fwd_workspace(sms, static_cast<int>(shape.head_dim), nullptr, nullptr));
+                                        seq_fwd_workspace(ctas, static_cast<int>(shape.head_dim), nullptr, nullptr));
     a.scores_ld = scores_row(cache, weights_len);
   }
-  st = run_fwd(a, q, v_pages, out, lse, workspace, sms, shape, bf16, t, o, static_cast<cudaStream_t>(stream));
+  st = run_fwd(a, q, v_pages, out, lse, workspace, ctas, shape, bf16, t, o, static_cast<cudaStream_t>(stream));
   if (st != EVO_OK || !weights) return st;
   SeqWeightsArgs w{};
   w.tq = a.tq, w.tk = a.tk;
@@ -425,7 +443,7 @@ evo_status_t evo_paged_fwd(const void* q, const void* k_pages, const void* v_pag
   w.records = a.records;
   w.part = a.part_o;
   w.wait_ns = o.wait_ns;
-  const cudaError_t e = launch_seq_weights(w, sms, bf16, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_seq_weights(w, ctas, bf16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? EVO_OK : cuda_fail("weight sums launch", e);
 }
 

@@ -51,9 +51,11 @@ __device__ __forceinline__ int count_pieces(const PieceRecord* records, int c0, 
 }
 
 // How a sequence's items are laid out and cut.  An item's units are what it walks over (keys, or
-// query tokens) plus cost(), about two tiles: measured on the forward, an item takes 3.4 us and a
-// key tile 1.85 us (with half that cost, CTAs that held 25 to 40 short items ended up to a third
-// later than the others).
+// query tokens) plus cost(), in tiles: an item of the forward takes 3.4 us and a tile 1.85, of dK/dV
+// 5.8 and 1.9 (its keys are loaded when the last item is done with them).  With one tile in the
+// forward, CTAs that held 25 to 40 short items ended up to a third later than the others; 1, 2 and
+// 3 tiles for dK/dV gave 471, 465 and 458 us at 4096 + 1031 + 2500 + 565 tokens (forward included),
+// 1.25, 2 and 3 for dQ 479, 465 and 469.
 //
 // Blocks of W query tokens over the key tiles they see (forward, dQ).
 struct QueryBlocks {
@@ -83,7 +85,7 @@ struct QueryBlocks {
 // Work: t0, nt the keys; j0, j1, kt tiles of queries.
 struct KeyBlocks {
   int TQ;
-  __device__ __forceinline__ int cost() const { return 2 * TQ; }
+  __device__ __forceinline__ int cost() const { return 3 * TQ; }
   __device__ __forceinline__ int count(const Seq& q) const { return (q.n + kTile - 1) / kTile; }
   __device__ __forceinline__ long long of(const Seq& q, int p) const { return q.n - p * kTile + cost(); }
   __device__ __forceinline__ long long before(const Seq& q, int p) const {

@@ -180,15 +180,18 @@ def test_workspace_bytes(lib):
     assert lib.evo_prompt_bwd_workspace_bytes(shape()) >= 64 * 8 * 4  # delta
     assert lib.evo_paged_fwd_workspace_bytes(shape(), cache(page=24), 0) == 0
     assert lib.evo_paged_fwd_workspace_bytes(shape(), cache(), -1) == 0
-    plain = lib.evo_paged_fwd_workspace_bytes(shape(), cache(), 0)
-    assert plain > 0
+    need = lambda sh, c, w: lib.evo_paged_fwd_workspace_bytes(sh, c, w)
+    assert need(shape(), cache(), 0) > 0
     # single tokens: room for the scores ([tokens][q_heads][length, in whole tiles] fp32) with weights ...
     one, c = shape(T=2), cache(P=40, cols=16)
-    assert lib.evo_paged_fwd_workspace_bytes(one, c, 200) == \
-        lib.evo_paged_fwd_workspace_bytes(one, c, 0) + 2 * 8 * 256 * 4
+    assert need(one, c, 200) == need(one, c, 0) + 2 * 8 * 256 * 4
     # ... unless they would be large beside the cache, or there are many rows a key
-    assert lib.evo_paged_fwd_workspace_bytes(one, cache(P=2, cols=16), 256) == plain
-    assert lib.evo_paged_fwd_workspace_bytes(shape(T=16), c, 256) == plain
+    small, many = cache(P=2, cols=16), shape(T=16)
+    assert need(one, small, 256) == need(one, small, 0)
+    assert need(many, c, 256) == need(many, c, 0)
+    # little work needs few CTAs' worth of partial results
+    assert need(shape(T=1, B=1), cache(), 0) < need(shape(T=4096, B=8), cache(P=4096, cols=1024), 0)
+    assert lib.evo_prompt_fwd_workspace_bytes(shape(T=8)) < lib.evo_prompt_fwd_workspace_bytes(shape(T=8192))
 
 
 def test_binding_refuses_host_tensors_and_shapes():
