@@ -41,7 +41,7 @@ static_assert(kReady >= kMaxSlots / 2 + 1, "a V tile's release must not lap the 
 
 struct Bars {
   uint64_t desc_full[kDescs], desc_empty[kDescs];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t v_ready[kReady];
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], drain[2], turn[2], merge_full;
@@ -109,22 +109,29 @@ __device__ __forceinline__ void producer(const SeqFwdArgs& a, uint8_t* base, Bar
   const int box = paged ? (s.page < kTile ? s.page : kTile) : kTile;  // rows per copy
   const int boxes = kTile / box;
   const uint32_t qbytes = static_cast<uint32_t>(a.TQ * s.group) * 128u * (DP / 64);
-  uint32_t use = 0, it = 0, queries = 0;
+  uint32_t use = 0, it = 0, queries[2] = {0, 0};
   Work w;
+  // Two tiles of queries take a buffer each; a single one takes the buffers by turns (w.q), so that the
+  // next one's load does not wait for this one's last scores.
+  auto load_queries = [&]() -> bool {
+    const bool one = single(w, a.TQ);
+    for (int t = 0; t < (one ? 1 : 2); ++t) {
+      const int b = one ? w.q : t;
+      if (!mbar_wait_warp_inl(smem_u32(&bars->q_empty[b]), (queries[b] & 1) ^ 1, g)) return false;
+      if (lane == 0) {
+        const uint32_t full = smem_u32(&bars->q_full[b]);
+        mbar_arrive_expect_tx(full, qbytes);
+        for (int h = 0; h < DP / 64; ++h)
+          tma_load_4d(smem_u32(base + L::q + b * L::kTB + h * L::kHalf), &a.tq, full, h * 64, 0, w.kvh,
+                      w.row0 + w.t0 + t * a.TQ);
+      }
+      ++queries[b];
+    }
+    return true;
+  };
   for (; take<true>(bars, it, g, w); ++it) {
     __syncwarp();
     if (lane == 0) give_back(bars, it);
-    if (!mbar_wait_warp_inl(smem_u32(&bars->q_empty), (it & 1) ^ 1, g)) break;
-    if (lane == 0) {
-      const uint32_t full = smem_u32(&bars->q_full);
-      const int tiles = w.nt > a.TQ ? 2 : 1;
-      mbar_arrive_expect_tx(full, tiles * qbytes);
-      for (int t = 0; t < tiles; ++t)
-        for (int h = 0; h < DP / 64; ++h)
-          tma_load_4d(smem_u32(base + L::q + t * L::kTB + h * L::kHalf), &a.tq, full, h * 64, 0, w.kvh,
-                      w.row0 + w.t0 + t * a.TQ);
-    }
-    ++queries;
     // this lane's page of a tile (a page past the keys, or a bad one, reads as zeros)
     auto page = [&](int j) -> int {
       const int key = j * kTile + lane * box;
@@ -133,8 +140,8 @@ __device__ __forceinline__ void producer(const SeqFwdArgs& a, uint8_t* base, Bar
       return p < 0 ? s.num_pages : p;
     };
     int mine = paged ? page(w.j0) : 0;
-    bool ok = true;
-    for (int j = w.j0; j < w.j1; ++j) {
+    bool ok = load_queries();
+    for (int j = w.j0; ok && j < w.j1; ++j) {
       const int cur = mine;
       if (paged && j + 1 < w.j1) mine = page(j + 1);
 #pragma unroll
@@ -154,7 +161,6 @@ __device__ __forceinline__ void producer(const SeqFwdArgs& a, uint8_t* base, Bar
           tma_load_3d(dst + lane * L::kHalf, m, full, lane * 64, w.kvh, w.row0 + j * kTile);
         }
       }
-      if (!ok) break;
     }
     if (!ok) break;
   }
@@ -162,7 +168,8 @@ __device__ __forceinline__ void producer(const SeqFwdArgs& a, uint8_t* base, Bar
   __syncwarp();
   for (uint32_t x = use > L::kSlots ? use - L::kSlots : 0; x < use; ++x)
     drain_wait(smem_u32(&bars->full[x % L::kSlots]), (x / L::kSlots) & 1, a);
-  if (queries > 0) drain_wait(smem_u32(&bars->q_full), (queries - 1) & 1, a);
+  for (int b = 0; b < 2; ++b)
+    if (queries[b] > 0) drain_wait(smem_u32(&bars->q_full[b]), (queries[b] - 1) & 1, a);
 }
 
 // ------------------------------------------------------------ MMA (one warp per tile, one of its threads issuing)
@@ -173,7 +180,7 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
   const int steps = (a.s.D + 15) / 16;  // of 16 features
   const uint32_t id_s = idesc_f16(128, 128, BF16, false, false);
   const uint32_t id_o = idesc_f16(128, steps * 16, BF16, false, true);
-  uint32_t n = 0, u = 0, it = 0, own = 0;
+  uint32_t n = 0, u = 0, it = 0, own = 0, queries[2] = {0, 0};
   bool ok = true;
   Work w;
   for (; ok && take<true>(bars, it, g, w); ++it) {
@@ -183,10 +190,20 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
     const bool one = uniform(single(w, a.TQ)) != 0;
     const Share sh = share_of(w, static_cast<int>(gq), a.TQ);
     const int from = uniform(sh.from), to = uniform(sh.to), step = one ? 2 : 1;
-    const uint64_t qd = smem_desc(smem_u32(base + L::q + (one ? 0 : gq * L::kTB)), 16, 1024, kSwizzle128B);
-    if (!mbar_wait_warp_inl(smem_u32(&bars->q_full), it & 1, g)) break;
+    const uint32_t qb = one ? static_cast<uint32_t>(uniform(w.q)) : gq;
+    const uint64_t qd = smem_desc(smem_u32(base + L::q + qb * L::kTB), 16, 1024, kSwizzle128B);
+    // (the other tile's buffer too: it is released by both)
+    for (uint32_t b = 0; b < 2; ++b)
+      if (!one || b == qb) {
+        if (!mbar_wait_warp_inl(smem_u32(&bars->q_full[b]), queries[b] & 1, g)) ok = false;
+        ++queries[b];
+      }
+    if (!ok) break;
     tc_fence_after();
-    if (from >= to && elect_one()) mbar_arrive(smem_u32(&bars->q_empty));
+    if (elect_one()) {
+      if (!one) mbar_arrive(smem_u32(&bars->q_empty[gq ^ 1]));
+      if (from >= to) mbar_arrive(smem_u32(&bars->q_empty[qb]));
+    }
     __syncwarp();
     int next = from;  // this warpgroup's next key tile
     for (int j = j0; j < j1; ++j, ++n) {
@@ -212,7 +229,7 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
         }
         umma_commit(smem_u32(&bars->s_full[gq]));
         umma_commit(smem_u32(&bars->empty[ks]));
-        if (next >= to) umma_commit(smem_u32(&bars->q_empty));
+        if (next >= to) umma_commit(smem_u32(&bars->q_empty[qb]));
       }
       __syncwarp();
       if (!mbar_wait_warp_inl(smem_u32(&bars->v_ready[n % kReady]), (n / kReady) & 1, g)) { ok = false; break; }
@@ -287,8 +304,13 @@ __device__ __forceinline__ void walk(const SeqFwdArgs& a, uint8_t* base, Bars* b
   Work ring[2];  // published, V tiles not yet released: the current item and the one after it
   uint32_t pub = 0, n = 0;
   bool more = true;
+  int turn = 0;  // buffer of the next single tile of queries
   auto publish = [&](Work& w) -> bool {
     w = walk.next();
+    if (!w.stop && single(w, a.TQ)) {
+      w.q = turn;
+      turn ^= 1;
+    }
     const uint32_t s = pub % kDescs;
     if (!mbar_wait_warp_inl(smem_u32(&bars->desc_empty[s]), ((pub / kDescs) & 1) ^ 1, g)) return false;
     if (lane == 0) {
@@ -656,8 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_c
       mbar_init(smem_u32(&bars->desc_full[i]), 1);
       mbar_init(smem_u32(&bars->desc_empty[i]), 11);  // producer, two MMA threads, eight softmax warps
     }
-    mbar_init(smem_u32(&bars->q_full), 1);
-    mbar_init(smem_u32(&bars->q_empty), 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars->q_full[i]), 1);
+      mbar_init(smem_u32(&bars->q_empty[i]), 2);  // both MMA warps
+    }
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 1);
       mbar_init(smem_u32(&bars->empty[i]), 2);  // both MMA threads

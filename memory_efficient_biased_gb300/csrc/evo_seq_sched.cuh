@@ -23,6 +23,7 @@ struct Work {
   int j0, j1;    // key tiles of this piece
   int kt;        // key tiles of the item (at least one, so that empty rows are written)
   int slot;      // -1: the whole item; 0 / 1: a piece, kept in this CTA's slot 0 / 1
+  int q;         // forward, one tile of queries: its buffer
   int stop;      // no more work
 };
 
