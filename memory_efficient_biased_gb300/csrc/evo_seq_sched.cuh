@@ -186,6 +186,28 @@ struct Walk {
     left = 0;
   }
 
+  // The next sequence with an item, looked for 32 at a time.
+  __device__ __forceinline__ void next_sequence() {
+    const int lane = threadIdx.x & 31;
+    for (int base = b + 1; base < d->seqs; base += 32) {
+      Seq mine{0, 0, 0, 0};
+      if (base + lane < d->seqs) mine = load_seq(*d, base + lane);
+      const uint32_t any = __ballot_sync(0xffffffffu, k.count(mine) > 0);
+      if (any) {
+        const int first = __ffs(any) - 1;
+        b = base + first;
+        q.row0 = __shfl_sync(0xffffffffu, mine.row0, first);
+        q.n = __shfl_sync(0xffffffffu, mine.n, first);
+        q.kv = __shfl_sync(0xffffffffu, mine.kv, first);
+        q.pos0 = __shfl_sync(0xffffffffu, mine.pos0, first);
+        P = k.count(q);
+        return;
+      }
+    }
+    b = d->seqs;
+    left = 0;
+  }
+
   // The next piece with at least one tile, or stop.
   __device__ __forceinline__ Work next() {
     Work w{};
@@ -207,14 +229,7 @@ struct Walk {
         p = 0;
         if (++kvh == d->kv_heads) {
           kvh = 0;
-          do {
-            if (++b >= d->seqs) {
-              left = 0;
-              break;
-            }
-            q = load_seq(*d, b);
-            P = k.count(q);
-          } while (P == 0);
+          next_sequence();
         }
       }
       if (w.j0 < w.j1) return w;

@@ -620,3 +620,136 @@ def test_binding_refusals_on_device():
         Q.evo_prompt_fwd(q, k, v, cu, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert E.evo_attn_device_status() == 0
+
+
+# ------------------------------------------------------------------------------ at the edges
+def test_cache_offsets_past_32_bits():
+    """Pages whose elements lie past 2^32: append, attention with weights, eviction."""
+    Hk, D, page, pages, dtype = 8, 128, 64, 70000, BF
+    kp = torch.empty(pages, page, Hk, D, dtype=dtype, device="cuda")
+    vp = torch.empty_like(kp)
+    assert kp.numel() > 2 ** 32
+    rng = np.random.default_rng(31)
+    table = torch.tensor([[69999, 65537, 69000], [66001, 68999, 69998]], dtype=torch.int32)
+    lens, chunks = [150, 130], [150, 130]
+    k, v = S.normal(rng, 280, Hk, D, dtype=dtype), S.normal(rng, 280, Hk, D, dtype=dtype)
+    q = S.normal(rng, 280, 16, D, dtype=dtype)
+    cu, size, td = S.offsets(chunks).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda()
+    Q.evo_cache_append(k.cuda(), v.cuda(), cu, size, kp, vp, td)
+    w = torch.zeros(2, Hk, 192, device="cuda")
+    out, lse = Q.evo_paged_fwd(q.cuda(), kp, vp, cu, size, td, weights=w)
+    ref, ref_lse = Q.evo_prompt_fwd(q.cuda(), k.cuda(), v.cuda(), cu)
+    a = 0
+    for b, n in enumerate(lens):
+        r = slice(a, a + n)
+        a += n
+        (_, _, wo, p), rp = S.check_forward(S.f64(q[r]), S.f64(k[r]), S.f64(v[r]), S.f64(out[r]), S.f64(lse[:, r]),
+                                            D ** -0.5, dtype)
+        S.assert_close(S.f64(w[b, :, :n]), wo, S.weight_bound(p, rp, 2) + 2.0 ** -23 * wo, "weights")
+        kept = [O.choose(S.f64(w[b, h]), n, 100, 10) for h in range(Hk)]
+        rows = [k[r][kept[h], h] for h in range(Hk)]
+        if b == 0:
+            want = rows
+    Q.evo_cache_evict(kp, vp, td, size, w, 100, 10)
+    got = kp[td[0].long()].view(-1, Hk, D)[:100]
+    assert torch.equal(got.cpu(), torch.stack(want, 1))
+    assert size.tolist() == [100, 100] and E.evo_attn_device_status() == 0
+
+
+def test_rows_past_32_bits():
+    """Token rows a long way apart."""
+    T, Hq, Hk, D, stride = 300, 2, 1, 64, 1 << 24
+    big = torch.empty(T * stride, dtype=BF, device="cuda")
+    q = big.as_strided((T, Hq, D), (stride, D, 1))
+    rng = np.random.default_rng(32)
+    qh, k, v, do = (S.normal(rng, T, h, D, dtype=BF) for h in (Hq, Hk, Hk, Hq))
+    q.copy_(qh)
+    cu = S.offsets([T]).cuda()
+    out = big[Hq * D:].as_strided((T, Hq, D), (stride, D, 1))
+    kd, vd, dod = k.cuda(), v.cuda(), do.cuda()
+    Q.evo_prompt_fwd(q, kd, vd, cu, out=out)
+    o2, lse = Q.evo_prompt_fwd(qh.cuda(), kd, vd, cu)
+    assert torch.equal(out, o2)
+    dq = big[2 * Hq * D:].as_strided((T, Hq, D), (stride, D, 1))
+    Q.evo_prompt_bwd(q, kd, vd, cu, out, lse, dod, dq)
+    g = Q.evo_prompt_bwd(qh.cuda(), kd, vd, cu, o2, lse, dod)
+    assert torch.equal(dq, g[0])
+
+
+def test_shared_pages():
+    """Two sequences that share the pages of a common beginning."""
+    rng = np.random.default_rng(33)
+    Hq, Hk, D, page = 4, 2, 64, 32
+    kp, vp, table = S.make_cache(rng, [200, 200], page, Hk, D, BF)
+    common = S.normal(rng, 96, 2 * Hk, D, dtype=BF)
+    table[1, :3] = table[0, :3]
+    ks, vs = [], []
+    for b, n in enumerate((150, 170)):
+        own = S.normal(rng, n - 96, 2 * Hk, D, dtype=BF)
+        rows = torch.cat([common, own])
+        ks.append(rows[:, :Hk].contiguous())
+        vs.append(rows[:, Hk:].contiguous())
+        S.fill_cache(kp, vp, table, b, ks[b], vs[b])
+    q = S.normal(rng, 3, Hq, D, dtype=BF)
+    cu, lens = S.offsets([1, 2]), torch.tensor([150, 170], dtype=torch.int32)
+    w = torch.zeros(2, Hk, 200, device="cuda")
+    out, lse = Q.evo_paged_fwd(q.cuda(), kp.cuda(), vp.cuda(), cu.cuda(), lens.cuda(), table.cuda(), weights=w)
+    check_paged((q, kp, vp, table, cu, lens, ks, vs), [1, 2], [150, 170], out, lse, D ** -0.5, BF, torch.zeros(2, Hk, 200), w)
+
+
+def test_many_empty_sequences():
+    """Thousands of sequences, nearly all of them empty or done."""
+    rng = np.random.default_rng(34)
+    B, Hq, Hk, D, page = 5000, 2, 1, 64, 16
+    chunks = np.zeros(B, dtype=np.int64)
+    chunks[[0, 1234, 1235, 4999]] = [3, 1, 200, 2]
+    ctx = rng.integers(0, 20, B)
+    ctx[[0, 1234, 1235, 4999]] = [3, 60, 230, 17]
+    kp, vp, table = S.make_cache(rng, [240], page, Hk, D, BF)
+    pages = torch.from_numpy(rng.permutation(100).astype(np.int32))
+    kp = torch.full((100, page, Hk, D), float("nan"), dtype=BF)
+    vp = kp.clone()
+    table = torch.zeros(B, 15, dtype=torch.int32)
+    at, ks, vs = 0, {}, {}
+    for b in (0, 1234, 1235, 4999):
+        need = -(-int(ctx[b]) // page)
+        table[b, :need] = pages[at:at + need]
+        at += need
+        ks[b], vs[b] = (S.normal(rng, int(ctx[b]), Hk, D, dtype=BF) for _ in range(2))
+        S.fill_cache(kp, vp, table, b, ks[b], vs[b])
+    q = S.normal(rng, int(chunks.sum()), Hq, D, dtype=BF)
+    cu = S.offsets(chunks)
+    w = torch.zeros(B, Hk, 240, device="cuda")
+    out, lse = Q.evo_paged_fwd(q.cuda(), kp.cuda(), vp.cuda(), cu.cuda(), torch.from_numpy(ctx.astype(np.int32)).cuda(),
+                               table.cuda(), weights=w)
+    assert E.evo_attn_device_status() == 0
+    for b in (0, 1234, 1235, 4999):
+        r = slice(int(cu[b]), int(cu[b + 1]))
+        (_, _, wo, p), rp = S.check_forward(S.f64(q[r]), S.f64(ks[b]), S.f64(vs[b]), S.f64(out[r]), S.f64(lse[:, r]),
+                                            D ** -0.5, BF)
+        S.assert_close(S.f64(w[b, :, :int(ctx[b])]), wo, S.weight_bound(p, rp, 2) + 2.0 ** -23 * wo, "weights")
+    w[[0, 1234, 1235, 4999]] = 0
+    assert torch.all(w == 0)
+
+
+def test_a_wait_limit_and_a_status_word_of_the_callers():
+    q, k, v, do, cu = (x.cuda() for x in prompt_inputs([200, 3], 4, 2, 64, BF))
+    mine = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = Q.evo_prompt_fwd(q, k, v, cu, status=mine, wait_limit_ns=10 ** 9)
+    Q.evo_prompt_bwd(q, k, v, cu, out, lse, do, status=mine, wait_limit_ns=10 ** 9)
+    assert int(mine) == 0 and E.evo_attn_device_status() == 0
+    check_prompt(q.cpu(), k.cpu(), v.cpu(), [200, 3], out, lse, 64 ** -0.5, BF)
+
+
+def test_expanded_key_heads_gather_their_gradient():
+    """Keys given as one head broadcast to two: the gradient is the sum over both."""
+    q, k, v, do, cu = prompt_inputs([77], 4, 1, 64, BF, seed=40)
+    cud = cu.cuda()
+    one_k, one_v = k.cuda().requires_grad_(True), v.cuda().requires_grad_(True)
+    out = prompt_attention(q.cuda(), one_k.expand(77, 2, 64), one_v.expand(77, 2, 64), cud)
+    out.backward(do.cuda())
+    g = Q.evo_prompt_bwd(q.cuda(), k.cuda(), v.cuda(), cud, *Q.evo_prompt_fwd(q.cuda(), k.cuda(), v.cuda(), cud), do.cuda())
+    # two heads' gradients, rounded, then added and rounded: three roundings of at most their sizes
+    for got, want in ((one_k.grad, g[1]), (one_v.grad, g[2])):
+        size = float(want.abs().max())
+        assert float((got.float() - want.float()).abs().max()) <= 6 * 2.0 ** -8 * size
