@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t ordered(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kSelThreads = 1024, kSelPer = 4, kBins = 2048;
+constexpr int kSelThreads = 1024, kSelPer = 4, kSelDeep = 8, kBins = 2048;
 
 // One CTA per (kv head, sequence).  The smallest weight that stays is found by radix
 // selection over the ordered weights (11 + 11 + 10 bits: three histograms in shared
@@ -76,9 +76,15 @@ __global__ void __launch_bounds__(kSelThreads) evo_evict_select_kernel(const Evi
       const uint32_t low = (1u << bits) - 1u;
       for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int j = tid; j < n; j += kSelThreads) {
-        const uint32_t u = ordered(w[j]);
-        if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & low], 1u);
+      for (int base = tid; base < n; base += kSelThreads * kSelDeep) {
+        float x[kSelDeep];  // loads in front of the counting, so that they are under way together
+#pragma unroll
+        for (int e = 0; e < kSelDeep; ++e) x[e] = base + e * kSelThreads < n ? w[base + e * kSelThreads] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < kSelDeep; ++e) {
+          const uint32_t u = ordered(x[e]);
+          if (base + e * kSelThreads < n && (u & mask) == prefix) atomicAdd(&hist[(u >> shift) & low], 1u);
+        }
       }
       __syncthreads();
       // bins from the largest down: thread t holds bins 2047 - 2t and 2046 - 2t
@@ -170,7 +176,8 @@ constexpr int kMoveThreads = 512, kMoveDeep = 4, kMoveTable = 4096;
 // give four times the CTAs at head_dim 128 and keep whole sectors.  The places of a batch are
 // read two batches ahead and the sequence's pages are looked up in shared memory, so that
 // only the rows themselves are waited for.  (16 sequences, 8 heads of 128, 4096 rows kept: 512 threads
-// with four rows each in flight 96 us, 5.6 TB/s; 256 threads 102, eight rows each 134, 128-byte slices 112.)
+// with four rows each in flight 88 us, 6.1 TB/s; 256 threads 6 us more, eight rows each 38, 128-byte
+// slices 16.)
 __global__ void __launch_bounds__(kMoveThreads) evo_evict_move_kernel(const EvictArgs a, int slices) {
   __shared__ int table[kMoveTable];
   const SeqDesc& s = a.s;
@@ -188,9 +195,10 @@ __global__ void __launch_bounds__(kMoveThreads) evo_evict_move_kernel(const Evic
   constexpr int kRows = kMoveThreads / 4 * kMoveDeep;
   const int r0 = threadIdx.x >> 2;
   const int row = s.kv_heads * s.D;
+  const int shift = (s.page & (s.page - 1)) ? -1 : __ffs(s.page) - 1;  // (a division each way was half of the instructions)
   pages += static_cast<long long>(h) * s.D + chunk * 8;
   auto place = [&](int j) -> uint16_t* {
-    const int e = j / s.page;
+    const int e = shift >= 0 ? j >> shift : j / s.page;
     int p;
     if (e < kMoveTable) {
       p = table[e];
