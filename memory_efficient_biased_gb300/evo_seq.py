@@ -191,7 +191,7 @@ def _on(stream):
 
 def _workspace(workspace, need, like, dev):
     if workspace is None:
-        return like.new_empty(need, dtype=torch.uint8), need
+        return torch.empty(need, dtype=torch.uint8, device=like.device), need
     _flat(workspace, "workspace", None, None, dev)
     return workspace, workspace.numel() * workspace.element_size()
 
@@ -229,11 +229,11 @@ def evo_prompt_fwd(q, k, v, cu_seqlens, out=None, lse=None, workspace=None, stre
     shape, lib, so = SeqShape(T, B, Hq, Hk, D), load(), 0
     with _on(stream):
         if out is None:
-            out = q.new_empty(rows)
+            out = torch.empty(rows, dtype=dt, device=q.device)
         else:
             so = _rows(out, "out", rows, dt, dev)
         if lse is None:
-            lse = q.new_empty((Hq, T), dtype=torch.float32)
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
         else:
             _flat(lse, "lse", (Hq, T), torch.float32, dev)
         ws, size = _workspace(workspace, lib.evo_prompt_fwd_workspace_bytes(shape), q, dev)
@@ -262,15 +262,15 @@ def evo_prompt_bwd(q, k, v, cu_seqlens, out, lse, dout, dq=None, dk=None, dv=Non
     shape, lib = SeqShape(T, B, Hq, Hk, D), load()
     with _on(stream):
         if dq is None:
-            dq = q.new_empty(rows)
+            dq = torch.empty(rows, dtype=dt, device=q.device)
         else:
             given[5] = _rows(dq, "dq", rows, dt, dev)
         if dk is None:
-            dk = q.new_empty(keys)
+            dk = torch.empty(keys, dtype=dt, device=q.device)
         else:
             given[6] = _rows(dk, "dk", keys, dt, dev)
         if dv is None:
-            dv = q.new_empty(keys)
+            dv = torch.empty(keys, dtype=dt, device=q.device)
         else:
             given[7] = _rows(dv, "dv", keys, dt, dev)
         ws, size = _workspace(workspace, lib.evo_prompt_bwd_workspace_bytes(shape), q, dev)
@@ -332,11 +332,11 @@ def evo_paged_fwd(q, k_pages, v_pages, cu_seqlens, seq_lens, block_table, out=No
     shape, lib = SeqShape(T, B, Hq, Hk, D), load()
     with _on(stream):
         if out is None:
-            out = q.new_empty(rows)
+            out = torch.empty(rows, dtype=dt, device=q.device)
         else:
             so = _rows(out, "out", rows, dt, dev)
         if lse is None:
-            lse = q.new_empty((Hq, T), dtype=torch.float32)
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
         else:
             _flat(lse, "lse", (Hq, T), torch.float32, dev)
         ws, size = _workspace(workspace, lib.evo_paged_fwd_workspace_bytes(shape, cache, wlen), q, dev)
@@ -368,7 +368,7 @@ def evo_cache_evict(k_pages, v_pages, block_table, seq_lens, weights, budget: in
         raise ValueError(f"1 <= budget and 0 <= recent <= budget are needed, got budget {budget}, recent {recent}")
     if kept is None:
         with _on(stream):
-            kept = seq_lens.new_empty((B, Hk, budget))
+            kept = torch.empty((B, Hk, budget), dtype=torch.int32, device=seq_lens.device)
     else:
         _flat(kept, "kept", (B, Hk, budget), torch.int32, dev)
     _done(load().evo_cache_evict(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
