@@ -161,7 +161,10 @@ def _cache(k_pages, v_pages, block_table, seqs, dtype, dev: int) -> CacheShape:
             continue
         if t.numel() and not t[0].is_contiguous():
             raise ValueError(f"{n} must have contiguous pages")
-        strides.append(t.stride(0) if t.shape[0] > 1 else 0)
+        stride, packed = t.stride(0), t.shape[1] * t.shape[2] * t.shape[3]
+        if t.shape[0] > 1 and (stride < packed or stride % 8):  # (0, an expanded page, would read as packed)
+            raise ValueError(f"{n} has page stride {stride}: at least {packed} and a multiple of 8 is needed")
+        strides.append(stride if t.shape[0] > 1 else 0)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor [seqs, pages_per_seq]")
     _flat(block_table, "block_table", None, torch.int32, dev)

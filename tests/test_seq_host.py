@@ -216,3 +216,17 @@ def test_binding_refuses_host_tensors_and_shapes():
         Q.evo_cache_append(k, k, cu, lens, pages, pages, table)
     with pytest.raises(ValueError):
         Q.evo_cache_evict(pages, pages, table, lens, torch.zeros(1, 2, 32), 8)
+
+
+def test_binding_page_strides():
+    """Pages that overlap (one page expanded to several) are refused: their stride of 0 means packed below."""
+    table, dt = torch.zeros(1, 2, dtype=torch.int32), torch.bfloat16
+    one, many = torch.zeros(1, 16, 2, 64, dtype=dt), torch.zeros(4, 16, 2, 64, dtype=dt)
+    for bad in (one.expand(4, 16, 2, 64), many.as_strided((4, 16, 2, 64), (1024, 128, 64, 1)),
+                many[:, :, :1].expand(4, 16, 2, 64)):
+        for pair in ((bad, many), (many, bad)):
+            with pytest.raises(ValueError):
+                Q._cache(*pair, table, 1, dt, -1)
+    both = torch.zeros(4, 2, 16, 2, 64, dtype=dt)
+    c = Q._cache(both[:, 0], both[:, 1], table, 1, dt, -1)
+    assert (c.num_pages, c.page_size, c.pages_per_seq, c.k_page_stride, c.v_page_stride) == (4, 16, 2, 4096, 4096)
