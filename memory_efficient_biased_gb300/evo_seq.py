@@ -82,8 +82,11 @@ def _options(scale, wait_limit_ns, status, dev):
         _flat(status, "status", None, torch.int32, dev)
         if status.numel() < 1:
             raise ValueError("status must have an element")
-    if scale is not None and not (0.0 < scale < float("inf")):
+    # as the float32 it becomes: a 0 would mean the default
+    if scale is not None and not (0.0 < ctypes.c_float(scale).value < float("inf")):
         raise ValueError(f"scale must be finite and positive, got {scale}")
+    if not 0 <= wait_limit_ns < 1 << 64:
+        raise ValueError(f"wait_limit_ns must be an unsigned 64-bit number, got {wait_limit_ns}")
     o = SeqOptions(ctypes.sizeof(SeqOptions), 0, scale or 0.0, 0, int(wait_limit_ns),
                    None if status is None else status.data_ptr())
     return ctypes.byref(o)

@@ -230,3 +230,15 @@ def test_binding_page_strides():
     both = torch.zeros(4, 2, 16, 2, 64, dtype=dt)
     c = Q._cache(both[:, 0], both[:, 1], table, 1, dt, -1)
     assert (c.num_pages, c.page_size, c.pages_per_seq, c.k_page_stride, c.v_page_stride) == (4, 16, 2, 4096, 4096)
+
+
+def test_binding_options():
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 1e-60, 1e60):
+        with pytest.raises(ValueError):
+            Q._options(scale, 0, None, -1)
+    for wait in (-1, 1 << 64):
+        with pytest.raises(ValueError):
+            Q._options(None, wait, None, -1)
+    assert Q._options(None, 0, None, -1) is None
+    o = Q._options(0.5, 7, None, -1)._obj
+    assert (o.scale, o.wait_limit_ns, o.status) == (0.5, 7, None)
