@@ -17,6 +17,7 @@ returned packed in the shape of q.
 from typing import List, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import evo_attn as E
 from . import evo_seq as Q
@@ -82,7 +83,7 @@ def _packed_rows(t: torch.Tensor) -> torch.Tensor:
     T, H, D = t.shape
     ok = (D == 1 or t.stride(2) == 1) and (H == 1 or t.stride(1) == D) and t.data_ptr() % 16 == 0
     ok = ok and (T <= 1 or (t.stride(0) >= H * D and t.stride(0) % 8 == 0 and t.stride(0) < 1 << 36))
-    return t if ok else t.contiguous()
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 class PromptAttentionFunction(torch.autograd.Function):
@@ -97,6 +98,7 @@ class PromptAttentionFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, cu_seqlens, out, lse = ctx.saved_tensors
         dq, dk, dv = (torch.zeros(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
@@ -110,7 +112,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     k, v [T, Hkv, D] with Hq a multiple of Hkv, cu_seqlens int32 [B + 1] on the device; ``scale``
     defaults to D^-1/2.  Rows in no sequence get zeros, and zero gradients.
 
-    Strided token rows (the parts of one fused projection) are read in place.  To capture the
+    Strided token rows (the parts of one fused projection) are read in place.  The gradients are
+    not differentiable themselves (an error says so).  To capture the
     backward into a CUDA graph, run the forward inside the same capture, on the stream that is
     being captured: PyTorch ties the accumulation of a leaf's gradient to the stream on which
     the leaf was first used, and a capture that meets another stream's work ends with an error."""

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from memory_efficient_biased_gb300 import evo_seq as Q
+from memory_efficient_biased_gb300.autograd import _packed_rows
 
 A = 1 << 32  # fake, well-aligned device addresses far apart: validation never dereferences them
 REACH = (0, 6, 7)  # valid arguments reach the device check
@@ -242,3 +243,16 @@ def test_binding_options():
     assert Q._options(None, 0, None, -1) is None
     o = Q._options(0.5, 7, None, -1)._obj
     assert (o.scale, o.wait_limit_ns, o.status) == (0.5, 7, None)
+
+
+def test_packed_rows():
+    """What the library cannot read in place is copied: a start off 16 bytes too, although contiguous."""
+    for dt in (torch.bfloat16, torch.float16):
+        buf = torch.randn(1 + 5 * 2 * 64).to(dt)
+        odd = buf[1:].view(5, 2, 64)
+        fused = torch.randn(5, 6, 64).to(dt)
+        for t in (odd, fused.transpose(0, 1), fused[:1, :1].expand(5, 2, 64), torch.randn(5, 2, 64).to(dt)[::2, :, :60]):
+            p = _packed_rows(t)
+            assert p.data_ptr() % 16 == 0 and p.is_contiguous() and torch.equal(p, t)
+        for t in (fused, fused[:, 2:4], fused[::2]):
+            assert _packed_rows(t) is t

@@ -753,3 +753,23 @@ def test_expanded_key_heads_gather_their_gradient():
     for got, want in ((one_k.grad, g[1]), (one_v.grad, g[2])):
         size = float(want.abs().max())
         assert float((got.float() - want.float()).abs().max()) <= 6 * 2.0 ** -8 * size
+
+
+def test_autograd_of_odd_gradients():
+    """A gradient that starts off 16 bytes is copied; a second derivative is refused, not dropped."""
+    q, k, v, do, cu = prompt_inputs([40, 9], 4, 2, 64, BF, seed=41)
+    leaves = [x.cuda().requires_grad_(True) for x in (q, k, v)]
+    buf = torch.empty(do.numel() + 1, dtype=BF, device="cuda")
+    odd = buf[1:].view(do.shape)
+    odd.copy_(do)
+    assert odd.data_ptr() % 16
+    grads = []
+    for g in (do.cuda(), odd):
+        out = prompt_attention(*leaves, cu.cuda())
+        grads.append(torch.autograd.grad(out, leaves, g))
+    for x, y in zip(*grads):
+        assert torch.equal(x, y)
+    out = prompt_attention(*leaves, cu.cuda())
+    (dq,) = torch.autograd.grad(out, leaves[:1], do.cuda().requires_grad_(True), create_graph=True)
+    with pytest.raises(RuntimeError):
+        dq.sum().backward()
