@@ -47,7 +47,8 @@
  * Supported: head_dim a multiple of 8 from 8 to 128; q_heads a multiple of
  * kv_heads, at most 128 times it; page_size 16, 32, 64 or a multiple of 128 up
  * to 1024; fp16 or bf16 with fp32 accumulation; tokens and seqs of zero
- * (nothing is then done).
+ * (nothing is then done), up to 2^31 - 1024 tokens and 65535 sequences;
+ * q_heads up to 65535, kv_heads up to 16384.
  *
  * What the device arrays hold is checked on the device: an offset outside
  * [0, tokens] or below its predecessor, a length that is negative or beyond the
@@ -55,6 +56,9 @@
  * a bad offset or length counts as empty; a bad page reads as zeros and is not
  * written.  Either records EVO_ERR_BAD_INDEX in the call's status word (the
  * outputs of that sequence are then undefined, everything else is as usual).
+ * Offsets out of order may give a row to two sequences, and the outputs of both
+ * are undefined then; attention counts every sequence as empty where all of them
+ * together have more rows than tokens.
  *
  * A value that a row does not see does not reach it: what lies behind a
  * sequence's last token, in its last page or in the next sequence, may be

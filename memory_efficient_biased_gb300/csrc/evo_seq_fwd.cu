@@ -310,6 +310,8 @@ __device__ __forceinline__ void walk(const SeqFwdArgs& a, uint8_t* base, Bars* b
   walk.init(a.s, QueryBlocks{a.W}, blockIdx.x, gridDim.x);
   PieceRecord* rec = a.records + 2 * blockIdx.x;
   if (lane < 2) rec[lane].used = 0;
+  // (for the sums of the scores, which do not walk)
+  if (a.scores && blockIdx.x == 0 && lane == 0) a.records[2 * gridDim.x].used = walk.crowded;
   __syncwarp();
   Work ring[2];  // published, V tiles not yet released: the current item and the one after it
   uint32_t pub = 0, n = 0;
@@ -826,7 +828,7 @@ size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws) {
     off += (bytes + 255) & ~size_t(255);
     return p;
   };
-  uint8_t* rec = take(size_t(ctas) * 2 * sizeof(PieceRecord));
+  uint8_t* rec = take((size_t(ctas) * 2 + 1) * sizeof(PieceRecord));
   uint8_t* ml = take(size_t(ctas) * 2 * 256 * sizeof(float2));
   uint8_t* po = take(size_t(ctas) * 2 * 256 * DP * sizeof(float));
   if (a) {

@@ -135,7 +135,7 @@ SeqDesc desc(const evo_seq_shape_t& s, const int32_t* cu, const int32_t* lens, c
 }
 
 // CTAs of a launch: one per SM, or as many shares of a tile as the work can fill, whatever the
-// lengths turn out to be (blocks: items per kv head; most: units of one).
+// lengths turn out to be.
 int fwd_ctas(int sms, const evo_seq_shape_t& s, int64_t max_kv) {
   const double W = 2 * (kTile / (s.q_heads / s.kv_heads));
   const double units = (double(s.tokens) / W + double(s.seqs)) * (double(max_kv) + 2 * kTile) * double(s.kv_heads);

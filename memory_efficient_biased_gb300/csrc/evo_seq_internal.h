@@ -103,7 +103,7 @@ struct SeqFwdArgs {
   uint16_t* out;
   long long out_stride;
   float* lse;
-  PieceRecord* records;  // workspace: two per CTA
+  PieceRecord* records;  // workspace: two per CTA, and one for the sums of the scores
   float2* part_ml;       // ... [ctas][2][256] (m, l)
   float* part_o;         // ... [ctas][2][256][DP], not yet divided by l
   float* scores;         // nullable: s·log2e·S left behind for the weights, [tokens][q_heads][scores_ld]

@@ -4,9 +4,12 @@
 // A work item is a block of one sequence's tokens with all the heads of one group, over
 // what its tokens see (or, for a block of keys, are seen by); items are laid out one behind
 // the other (sequence, kv head, block), and each counts as many units as it has tokens to
-// walk over, plus cost() for what every item costs (its own loads, the first scores, the output).  CTA c takes the units [c·share, (c+1)·share): every CTA has the same amount of
+// walk over, plus cost() for what every item costs (its own loads, the first scores, the
+// output).  CTA c takes the units [c·share, (c+1)·share): every CTA has the same amount of
 // work whatever the lengths are, and an item that a border cuts (between two tiles) is
 // computed in pieces, whose results are joined in a fixed order by a second kernel.
+// Offsets out of order may give one row to many sequences; the work stays that of a call's
+// rows all the same: sequences that together have more rows than the call count as empty.
 #pragma once
 
 #include "evo_seq_internal.h"
@@ -113,6 +116,7 @@ struct Walk {
   int b, kvh, p, P;
   Seq q;
   long long off, left;  // units of the current item already passed; units of the share left
+  bool crowded;         // more rows than the call has
 
   __device__ __forceinline__ long long total(const Seq& s) const {
     const int n = k.count(s);
@@ -128,13 +132,25 @@ struct Walk {
     const Seq none{0, 0, 0, 0};
     const Seq early = lane < desc.seqs ? load_seq(desc, lane) : none;
     const long long units = total(early) * desc.kv_heads;
-    long long all = units;
+    long long all = units, rows = early.n;
     for (int base = 32; base < desc.seqs; base += 32) {
       const int i = base + lane;
-      if (i < desc.seqs) all += total(load_seq(desc, i)) * desc.kv_heads;
+      if (i < desc.seqs) {
+        const Seq one = load_seq(desc, i);
+        all += total(one) * desc.kv_heads;
+        rows += one.n;
+      }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+      rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    }
+    crowded = rows > desc.tokens;
+    if (crowded) {
+      report_bad_index(desc.status);
+      all = 0;
+    }
     long long share = (all + ctas - 1) / ctas;
     if (share < kTile) share = kTile;
     const long long x0 = share * cta;

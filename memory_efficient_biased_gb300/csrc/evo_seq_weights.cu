@@ -381,12 +381,13 @@ __global__ void __launch_bounds__(kTile) evo_seq_weights_join_kernel(const __gri
 
 // From the scores that the forward left behind ([tokens][q_heads][ld], times s·log2 e): four keys a
 // thread, rows in order.
-__global__ void __launch_bounds__(256) evo_scores_sum_kernel(const __grid_constant__ SeqWeightsArgs a) {
+__global__ void __launch_bounds__(256) evo_scores_sum_kernel(const __grid_constant__ SeqWeightsArgs a, int ctas) {
   const SeqDesc& s = a.s;
+  const int crowded = a.records[2 * ctas].used;  // the forward's verdict
   const int hk = blockIdx.y, b = blockIdx.z;
   const Seq q = load_seq(s, b);
   const int key = (blockIdx.x * 256 + threadIdx.x) * 4;
-  if (key >= q.kv || q.n == 0) return;
+  if (key >= q.kv || q.n == 0 || crowded) return;
   float sum[4] = {};
   // (a token at position p sees the keys up to p)
   for (int i = key > q.pos0 ? key - q.pos0 : 0; i < q.n; ++i) {
@@ -426,7 +427,7 @@ cudaError_t launch_t(const SeqWeightsArgs& a, int ctas, cudaStream_t st) {
 cudaError_t launch_seq_weights(const SeqWeightsArgs& a, int ctas, bool bf16, cudaStream_t st) {
   if (a.scores) {
     const dim3 grid((a.s.max_kv + 1023) / 1024, a.s.kv_heads, a.s.seqs);
-    evo_scores_sum_kernel<<<grid, 256, 0, st>>>(a);
+    evo_scores_sum_kernel<<<grid, 256, 0, st>>>(a, ctas);
     return cudaGetLastError();
   }
   if (a.s.D <= 64) return bf16 ? launch_t<64, true>(a, ctas, st) : launch_t<64, false>(a, ctas, st);

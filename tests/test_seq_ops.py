@@ -773,3 +773,27 @@ def test_autograd_of_odd_gradients():
     (dq,) = torch.autograd.grad(out, leaves[:1], do.cuda().requires_grad_(True), create_graph=True)
     with pytest.raises(RuntimeError):
         dq.sum().backward()
+
+
+def test_offsets_that_share_rows():
+    """Sequences with more rows than the call has, by offsets out of order: recorded, and nothing done."""
+    q, k, v, do, _ = prompt_inputs([64], 2, 1, 64, BF, seed=42)
+    d = [x.cuda() for x in (q, k, v)]
+    for cu in ([0, 64, 0, 64], [0, 40, 10, 50], [0, 64] * 50 + [0, 60]):
+        cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        out, lse = torch.full_like(d[0], 7.0), torch.full((2, 64), 7.0, device="cuda")
+        mine = torch.zeros(1, dtype=torch.int32, device="cuda")
+        Q.evo_prompt_fwd(*d, cud, out=out, lse=lse, status=mine)
+        assert int(mine) == 13 and torch.all(out == 7) and torch.all(lse == 7)
+        grads = [torch.full_like(x, 7.0) for x in d]
+        Q.evo_prompt_bwd(*d, cud, out, torch.zeros_like(lse), do.cuda(), *grads)
+        assert E.evo_attn_device_status() == 13 and all(bool(torch.all(x == 7)) for x in grads)
+        # over a cache, the weights from the scores (many sequences) and formed again (few)
+        B = len(cu) - 1
+        pages = torch.zeros(16 * B, 16, 1, 64, dtype=BF, device="cuda")
+        table = torch.arange(16 * B, dtype=torch.int32, device="cuda").view(B, 16)
+        lens = torch.full((B,), 100, dtype=torch.int32, device="cuda")
+        w = torch.full((B, 1, 256), 7.0, device="cuda")
+        Q.evo_paged_fwd(d[0], pages, pages, cud, lens, table, out=out, lse=lse, weights=w)
+        assert E.evo_attn_device_status() == 13
+        assert torch.all(out == 7) and torch.all(lse == 7) and torch.all(w == 7)
