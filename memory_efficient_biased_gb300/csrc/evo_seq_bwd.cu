@@ -4,18 +4,20 @@
 // With P = 2^(s·log2e·S - log2e·lse) rebuilt from the saved lse, dP = dO·vᵀ,
 // dS = P∘(dP - delta) and delta = dO·O:
 //     dV = Σ Pᵀ dO     dK = s Σ dSᵀ q     dQ = s Σ dS k.
-// Five products per pair of tiles would do; here it is seven in two kernels, since dQ
-// gathers over key tiles what dK and dV gather over query tiles: in one kernel either its
+// Five products per pair of tiles would do; here it is seven in two phases, since dQ
+// gathers over key tiles what dK and dV gather over query tiles: in one walk either its
 // sums (64 KB of fp32 per pair of tiles) go through L2 by atomics whose order changes the
-// result, or wait for one another.  Two kernels keep every sum in tensor memory, in a
+// result, or wait for one another.  Two phases keep every sum in tensor memory, in a
 // fixed order, and P and dS (the MMAs' A operands) in tensor memory too.
 //
 //   evo_seq_rows_kernel  (-lse·log2e, -delta) per row, [tokens][q_heads]
-//   evo_seq_dkv_kernel   items: 128 keys of a kv head, over the tiles of queries that see
+//   evo_seq_bwd_kernel   both phases in one launch, one behind the other in each CTA or, for little work,
+//                        side by side (496 tokens of 4 heads of 64, forward included: 35 us, and 45 with a launch and a join for each)
+//     dK, dV             items: 128 keys of a kv head, over the tiles of queries that see
 //                        them (TQ tokens x the heads of the group, as in the forward, which sums
 //                        dK and dV over a group's heads for nothing); Sᵀ = K Qᵀ, dPᵀ = V dOᵀ, a
 //                        thread per key and half of the rows; dV += Pᵀ dO, dK += dSᵀ Q
-//   evo_seq_dq_kernel    items: one tile of queries over its key tiles; S = Q Kᵀ, dP = dO Vᵀ, a
+//     dQ                 items: one tile of queries over its key tiles; S = Q Kᵀ, dP = dO Vᵀ, a
 //                        thread per row and half of the keys; dQ += dS K
 // Work is shared out and cut items joined as in the forward (evo_seq_sched.cuh); pieces are
 // fp32 sums, added in order.
@@ -29,6 +31,7 @@
 #include "evo_seq_internal.h"
 #include "evo_seq_sched.cuh"
 
+#include <cstddef>
 #include <type_traits>
 
 namespace evo {
@@ -168,7 +171,7 @@ __device__ __forceinline__ void walk(const SeqBwdArgs& a, uint8_t* base, Bars* b
     walk.init(a.s, KeyBlocks{a.TQ}, blockIdx.x, gridDim.x);
   else
     walk.init(a.s, QueryBlocks{a.TQ}, blockIdx.x, gridDim.x);
-  PieceRecord* rec = a.records + 2 * blockIdx.x;
+  PieceRecord* rec = a.records + 2 * (blockIdx.x + (DKV ? 0 : gridDim.x));
   if (lane < 2) rec[lane].used = 0;
   __syncwarp();
   Work cur, ahead;
@@ -647,7 +650,7 @@ __device__ __forceinline__ void compute_dq(const SeqBwdArgs& a, Bars* bars, uint
     if (!ok || !mbar_wait_warp_inl(smem_u32(&bars->acc_full), it & 1, g)) break;
     tc_fence_after();
     uint16_t* out = a.dq + row * a.dq_stride + static_cast<size_t>(h) * s.D;
-    float* part = a.part + ((static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * kTile + r) * DP;
+    float* part = a.part_q + ((static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * kTile + r) * DP;
     write_row<DP / 2, BF16>(trow + kColQ, grp * (DP / 2), (grp + 1) * (DP / 2), s.D, live, w.slot >= 0, a.scale, out, a.dq32, part);
     tc_fence_before();
     __syncwarp();
@@ -655,47 +658,86 @@ __device__ __forceinline__ void compute_dq(const SeqBwdArgs& a, Bars* bars, uint
   }
 }
 
+__device__ __forceinline__ void init_bars(Bars* bars, bool dkv) {
+  for (int i = 0; i < kDescs; ++i) {
+    mbar_init(smem_u32(&bars->desc_full[i]), 1);
+    mbar_init(smem_u32(&bars->desc_empty[i]), dkv ? 11 : 10);  // producer, MMA, compute warps; rows
+  }
+  mbar_init(smem_u32(&bars->own_full), 1);
+  mbar_init(smem_u32(&bars->own_empty), 1);
+  for (int i = 0; i < kASlots; ++i) {
+    mbar_init(smem_u32(&bars->a_full[i]), 1);
+    mbar_init(smem_u32(&bars->a_empty[i]), 1);
+  }
+  for (int i = 0; i < kBSlots; ++i) {
+    mbar_init(smem_u32(&bars->b_full[i]), 1);
+    mbar_init(smem_u32(&bars->b_empty[i]), 1);
+  }
+  for (int i = 0; i < kReady; ++i) mbar_init(smem_u32(&bars->ready[i]), 1);
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(smem_u32(&bars->rows_full[i]), 1);
+    mbar_init(smem_u32(&bars->rows_empty[i]), 8);
+    mbar_init(smem_u32(&bars->s_full[i]), 1);
+  }
+  mbar_init(smem_u32(&bars->dp_full), 1);
+  mbar_init(smem_u32(&bars->p_ready), 8);
+  mbar_init(smem_u32(&bars->ds_ready), 8);
+  mbar_init(smem_u32(&bars->dp_free), 8);
+  mbar_init(smem_u32(&bars->second_done), 1);
+  mbar_init(smem_u32(&bars->acc_full), 1);
+  mbar_init(smem_u32(&bars->acc_free), 8);
+  mbar_init(smem_u32(&bars->drain), 1);
+  fence_barrier_init();
+}
+
+// Between dK/dV and dQ, by every thread of the CTA: each warp has waited for the copies and MMAs that it
+// started, so nobody uses a barrier any more, and all of them begin anew.
+__device__ __forceinline__ void turn_over(Bars* bars) {
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint64_t* bar = reinterpret_cast<uint64_t*>(bars);
+    for (uint32_t i = 0; i < offsetof(Bars, work) / 8; ++i) mbar_inval(smem_u32(bar + i));
+    init_bars(bars, false);
+  }
+  __syncthreads();
+  tc_fence_after();
+}
+
 template <int DP, bool BF16, bool DKV>
+__device__ __forceinline__ void other_warps(const SeqBwdArgs& a, uint8_t* base, Bars* bars, uint32_t tmem, const WaitGuard& g,
+                                            float* rowbuf, int warp, int lane) {
+  if (warp == kProducerWarp) {
+    if (lane == 0) producer<DP, DKV>(a, base, bars, g);
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (DKV)
+      mma_dkv<DP, BF16>(a, base, bars, tmem, g);
+    else
+      mma_dq<DP, BF16>(a, base, bars, tmem, g);
+  } else if (warp == kRowsWarp) {
+    if (DKV) rows(a, rowbuf, bars, g, lane);
+  } else {
+    walk<DP, DKV>(a, base, bars, g, lane);
+  }
+}
+
+// With one row of CTAs each does its share of dK/dV and then its share of dQ; with two rows the first
+// does dK/dV and the second dQ at the same time (bwd_rows in evo_seq_host.cu says when).
+template <int DP, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_constant__ SeqBwdArgs a) {
   using L = Layout<DP>;
   extern __shared__ __align__(1024) uint8_t base[];
   Bars* bars = reinterpret_cast<Bars*>(base + L::bars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool both = gridDim.y == 1, dkv = blockIdx.y == 0;
   if (smem_u32(base) & 1023u) {  // the tiles' swizzle counts from 1 KB borders
     if (threadIdx.x == 0) atomicExch(a.s.status, kStatusTimeout);
     return;
   }
   if (threadIdx.x == 0) {
     bars->abort = 0;
-    for (int i = 0; i < kDescs; ++i) {
-      mbar_init(smem_u32(&bars->desc_full[i]), 1);
-      mbar_init(smem_u32(&bars->desc_empty[i]), DKV ? 11 : 10);  // producer, MMA, compute warps; rows
-    }
-    mbar_init(smem_u32(&bars->own_full), 1);
-    mbar_init(smem_u32(&bars->own_empty), 1);
-    for (int i = 0; i < kASlots; ++i) {
-      mbar_init(smem_u32(&bars->a_full[i]), 1);
-      mbar_init(smem_u32(&bars->a_empty[i]), 1);
-    }
-    for (int i = 0; i < kBSlots; ++i) {
-      mbar_init(smem_u32(&bars->b_full[i]), 1);
-      mbar_init(smem_u32(&bars->b_empty[i]), 1);
-    }
-    for (int i = 0; i < kReady; ++i) mbar_init(smem_u32(&bars->ready[i]), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->rows_full[i]), 1);
-      mbar_init(smem_u32(&bars->rows_empty[i]), 8);
-      mbar_init(smem_u32(&bars->s_full[i]), 1);
-    }
-    mbar_init(smem_u32(&bars->dp_full), 1);
-    mbar_init(smem_u32(&bars->p_ready), 8);
-    mbar_init(smem_u32(&bars->ds_ready), 8);
-    mbar_init(smem_u32(&bars->dp_free), 8);
-    mbar_init(smem_u32(&bars->second_done), 1);
-    mbar_init(smem_u32(&bars->acc_full), 1);
-    mbar_init(smem_u32(&bars->acc_free), 8);
-    mbar_init(smem_u32(&bars->drain), 1);
-    fence_barrier_init();
+    init_bars(bars, dkv);
   }
   if (warp == kProducerWarp && lane == 0) {
     tma_prefetch_desc(&a.tq);
@@ -707,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_c
     tmem_alloc(smem_u32(&bars->tmem_slot), 512);
     tmem_relinquish();
   }
-  if (DKV && a.TQ * a.s.group < kTile) {
+  if (dkv && a.TQ * a.s.group < kTile) {
     // rows that no query tile fills are read by the gradient MMAs (against P = dS = 0)
     for (uint32_t i = threadIdx.x; i < (kASlots + kBSlots) * L::kTB / 16; i += kThreads)
       reinterpret_cast<uint4*>(base + L::a)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -720,25 +762,14 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_c
   float* rowbuf = reinterpret_cast<float*>(base + L::rows);
   if (warp >= kProducerWarp) {
     setmaxnreg_dec<kRegsOther>();
-    if (warp == kProducerWarp) {
-      if (lane == 0) producer<DP, DKV>(a, base, bars, g);
-      __syncwarp();
-    } else if (warp == kMmaWarp) {
-      if (DKV)
-        mma_dkv<DP, BF16>(a, base, bars, tmem, g);
-      else
-        mma_dq<DP, BF16>(a, base, bars, tmem, g);
-    } else if (warp == kRowsWarp) {
-      if (DKV) rows(a, rowbuf, bars, g, lane);
-    } else {
-      walk<DP, DKV>(a, base, bars, g, lane);
-    }
+    if (dkv) other_warps<DP, BF16, true>(a, base, bars, tmem, g, rowbuf, warp, lane);
+    if (both) turn_over(bars);
+    if (both || !dkv) other_warps<DP, BF16, false>(a, base, bars, tmem, g, rowbuf, warp, lane);
   } else {
     setmaxnreg_inc<kRegsCompute>();
-    if (DKV)
-      compute_dkv<DP, BF16>(a, rowbuf, bars, tmem, g);
-    else
-      compute_dq<DP, BF16>(a, bars, tmem, g);
+    if (dkv) compute_dkv<DP, BF16>(a, rowbuf, bars, tmem, g);
+    if (both) turn_over(bars);
+    if (both || !dkv) compute_dq<DP, BF16>(a, bars, tmem, g);
   }
   tc_fence_before();
   __syncthreads();
@@ -750,13 +781,15 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_c
 
 // ------------------------------------------------------------ pieces, summed in order
 // Eight threads a row, 32 rows a block.
+constexpr int kJoinRows = 32;
 template <int DP, bool BF16, bool DKV>
-__global__ void __launch_bounds__(256) evo_seq_bwd_join_kernel(const __grid_constant__ SeqBwdArgs a, int ctas) {
+__device__ __forceinline__ void join(const SeqBwdArgs& a, int ctas, int block) {
   constexpr int kParts = DKV ? 2 : 1;
-  const int c0 = blockIdx.x, i = blockIdx.y * 32 + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (DP / 8);
-  const PieceRecord first = a.records[2 * c0 + 1];
+  const int c0 = blockIdx.x, i = block * kJoinRows + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (DP / 8);
+  const PieceRecord* records = a.records + (DKV ? 0 : 2 * ctas);
+  const PieceRecord first = records[2 * c0 + 1];
   if (!first.used) return;
-  const int pieces = count_pieces(a.records, c0, ctas);
+  const int pieces = count_pieces(records, c0, ctas);
   const SeqDesc& s = a.s;
   const int part = i / kTile, r = i % kTile;
   const int tok = DKV ? r : r / s.group;
@@ -764,7 +797,7 @@ __global__ void __launch_bounds__(256) evo_seq_bwd_join_kernel(const __grid_cons
   float x[DP / 8] = {};
   for (int p = 0; p < pieces; ++p) {
     const float4* y = reinterpret_cast<const float4*>(
-        a.part + (((static_cast<size_t>(c0 + p) * 2 + (p == 0)) * kParts + part) * kTile + r) * DP + d0);
+        (DKV ? a.part : a.part_q) + (((static_cast<size_t>(c0 + p) * 2 + (p == 0)) * kParts + part) * kTile + r) * DP + d0);
 #pragma unroll
     for (int e = 0; e < DP / 32; ++e) {
       const float4 v = y[e];
@@ -782,6 +815,15 @@ __global__ void __launch_bounds__(256) evo_seq_bwd_join_kernel(const __grid_cons
     for (int q = 0; q < 4; ++q) v[q] = pack2<BF16>(x[e + 2 * q] * f, x[e + 2 * q + 1] * f);
     if (d0 + e < s.D) *reinterpret_cast<uint4*>(out + d0 + e) = make_uint4(v[0], v[1], v[2], v[3]);
   }
+}
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(256) evo_seq_bwd_join_kernel(const __grid_constant__ SeqBwdArgs a, int ctas) {
+  constexpr int kBlocks = 2 * kTile / kJoinRows;  // dK and dV's
+  if (blockIdx.y < kBlocks)
+    join<DP, BF16, true>(a, ctas, blockIdx.y);
+  else
+    join<DP, BF16, false>(a, ctas, blockIdx.y - kBlocks);
 }
 
 // ------------------------------------------------------------ lse and delta
@@ -826,28 +868,22 @@ __global__ void __launch_bounds__(256) evo_seq_rows_kernel(const __grid_constant
   }
 }
 
-template <int DP, bool BF16, bool DKV>
-cudaError_t launch_k(const SeqBwdArgs& a, int ctas, cudaStream_t st) {
-  auto kern = evo_seq_bwd_kernel<DP, BF16, DKV>;
-  static bool limit_set[64] = {};
-  cudaError_t e = ensure_smem_limit(kern, 232448, limit_set);
-  if (e != cudaSuccess) return e;
-  // more than half of an SM's shared memory: each CTA allocates all of tensor memory
-  const size_t smem = Layout<DP>::total > 118784 ? Layout<DP>::total : 118784;
-  kern<<<ctas, kThreads, smem, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (a.s.tokens <= (DKV ? a.TQ : kTile)) return e;  // items of one tile: nothing is cut
-  evo_seq_bwd_join_kernel<DP, BF16, DKV><<<dim3(ctas, (DKV ? 2 : 1) * kTile / 32), 256, 0, st>>>(a, ctas);
-  return cudaGetLastError();
-}
 template <int DP, bool BF16>
-cudaError_t launch_t(const SeqBwdArgs& a, int ctas, cudaStream_t st) {
+cudaError_t launch_t(const SeqBwdArgs& a, int ctas, int rows, cudaStream_t st) {
   const long long n = static_cast<long long>(a.s.tokens) * a.s.q_heads;
   evo_seq_rows_kernel<BF16><<<static_cast<unsigned>((n + 16 * kRowsPer - 1) / (16 * kRowsPer)), 256, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_k<DP, BF16, true>(a, ctas, st);
-  if (e == cudaSuccess) e = launch_k<DP, BF16, false>(a, ctas, st);
-  return e;
+  if (e != cudaSuccess) return e;
+  auto kern = evo_seq_bwd_kernel<DP, BF16>;
+  static bool limit_set[64] = {};
+  if ((e = ensure_smem_limit(kern, 232448, limit_set)) != cudaSuccess) return e;
+  // more than half of an SM's shared memory: each CTA allocates all of tensor memory
+  const size_t smem = Layout<DP>::total > 118784 ? Layout<DP>::total : 118784;
+  kern<<<dim3(ctas, rows), kThreads, smem, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.s.tokens <= a.TQ) return e;  // items of one tile: nothing is cut
+  evo_seq_bwd_join_kernel<DP, BF16><<<dim3(ctas, 3 * kTile / kJoinRows), 256, 0, st>>>(a, ctas);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -860,20 +896,22 @@ size_t prompt_bwd_workspace(int ctas, const SeqDesc& s, SeqBwdArgs* a, uint8_t* 
     off += (bytes + 255) & ~size_t(255);
     return p;
   };
-  uint8_t* rec = take(size_t(ctas) * 2 * sizeof(PieceRecord));
+  uint8_t* rec = take(size_t(ctas) * 2 * 2 * sizeof(PieceRecord));
   uint8_t* rows = take(size_t(s.tokens) * s.q_heads * sizeof(float2));
-  uint8_t* part = take(size_t(ctas) * 2 * 2 * kTile * DP * sizeof(float));  // dK and dV's; dQ's afterwards
+  uint8_t* part = take(size_t(ctas) * 2 * 2 * kTile * DP * sizeof(float));
+  uint8_t* part_q = take(size_t(ctas) * 2 * kTile * DP * sizeof(float));
   if (a) {
     a->records = reinterpret_cast<PieceRecord*>(rec);
     a->rows = reinterpret_cast<float2*>(rows);
     a->part = reinterpret_cast<float*>(part);
+    a->part_q = reinterpret_cast<float*>(part_q);
   }
   return off;
 }
 
-cudaError_t launch_prompt_bwd(const SeqBwdArgs& a, int ctas, bool bf16, cudaStream_t st) {
-  if (a.s.D <= 64) return bf16 ? launch_t<64, true>(a, ctas, st) : launch_t<64, false>(a, ctas, st);
-  return bf16 ? launch_t<128, true>(a, ctas, st) : launch_t<128, false>(a, ctas, st);
+cudaError_t launch_prompt_bwd(const SeqBwdArgs& a, int ctas, int rows, bool bf16, cudaStream_t st) {
+  if (a.s.D <= 64) return bf16 ? launch_t<64, true>(a, ctas, rows, st) : launch_t<64, false>(a, ctas, rows, st);
+  return bf16 ? launch_t<128, true>(a, ctas, rows, st) : launch_t<128, false>(a, ctas, rows, st);
 }
 
 }  // namespace evo

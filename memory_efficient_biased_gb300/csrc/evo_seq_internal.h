@@ -140,9 +140,10 @@ struct SeqBwdArgs {
   const float* lse;
   uint16_t *dq, *dk, *dv;
   long long out_stride, dout_stride, dq_stride, dk_stride, dv_stride;
-  PieceRecord* records;  // workspace: two per CTA
+  PieceRecord* records;  // workspace: two per CTA for dK and dV, then two for dQ
   float2* rows;          // ... [tokens][q_heads] (-lse·log2 e, -delta)
-  float* part;           // ... [ctas][2][dV, dK][128][DP], then [ctas][2][128][DP]
+  float* part;           // ... [ctas][2][dV, dK][128][DP]
+  float* part_q;         // ... [ctas][2][128][DP]
   uint64_t wait_ns;
 };
 size_t prompt_bwd_workspace(int ctas, const SeqDesc& s, SeqBwdArgs* a, uint8_t* ws);
@@ -151,6 +152,6 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_seq_fwd(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 cudaError_t launch_seq_weights(const SeqWeightsArgs& a, int ctas, bool bf16, cudaStream_t st);
-cudaError_t launch_prompt_bwd(const SeqBwdArgs& a, int ctas, bool bf16, cudaStream_t st);
+cudaError_t launch_prompt_bwd(const SeqBwdArgs& a, int ctas, int rows, bool bf16, cudaStream_t st);
 
 }  // namespace evo

@@ -797,3 +797,21 @@ def test_offsets_that_share_rows():
         Q.evo_paged_fwd(d[0], pages, pages, cud, lens, table, out=out, lse=lse, weights=w)
         assert E.evo_attn_device_status() == 13
         assert torch.all(out == 7) and torch.all(lse == 7) and torch.all(w == 7)
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,dtype", [(4099, 8, 8, 40, BF), (3300, 12, 4, 64, FP)])
+def test_prompt_backward_of_much_work(T, Hq, Hk, D, dtype):
+    """Enough work that every CTA does dK, dV and then dQ; two kv heads against the oracle."""
+    q, k, v, do, cu = prompt_inputs([T], Hq, Hk, D, dtype, seed=43)
+    d = [x.cuda() for x in (q, k, v, cu)]
+    out, lse = Q.evo_prompt_fwd(*d)
+    g = Q.evo_prompt_bwd(*d, out, lse, do.cuda())
+    again = Q.evo_prompt_bwd(*d, out, lse, do.cuda())
+    for x, y in zip(g, again):
+        assert torch.equal(x, y)
+    G = Hq // Hk
+    for h in (0, Hk - 1):
+        hq, hk = slice(h * G, (h + 1) * G), slice(h, h + 1)
+        S.check_gradients(S.f64(q[:, hq]), S.f64(k[:, hk]), S.f64(v[:, hk]), S.f64(do[:, hq]),
+                          [S.f64(g[0][:, hq]), S.f64(g[1][:, hk]), S.f64(g[2][:, hk])], D ** -0.5, dtype)
+    assert E.evo_attn_device_status() == 0
