@@ -753,40 +753,57 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_c
 // The pieces of an item that the borders between CTAs cut: the one that begins it (slot 1 of
 // CTA c), then slot 0 of c + 1, c + 2, ... up to its end, joined in that order.  Eight threads a row:
 // M = max m, l = Σ l 2^(m - M), O = Σ O 2^(m - M).  Latency is what it costs (the records, then the
-// (m, l), then O): 32 rows a block, so that every block of a launch is resident at once.
+// (m, l), then O): 32 rows a block, so that every block of a launch is resident at once, and the
+// pieces of a row read together.
 constexpr int kJoinRows = 32;
 template <int DP, bool BF16>
 __global__ void __launch_bounds__(256) evo_seq_join_kernel(const __grid_constant__ SeqFwdArgs a, int ctas) {
   const int c0 = blockIdx.x, i = blockIdx.y * kJoinRows + (threadIdx.x >> 3), d0 = (threadIdx.x & 7) * (DP / 8);
   const PieceRecord first = a.records[2 * c0 + 1];
+  const int pieces = count_pieces(a.records, c0, ctas);  // (read beside the first record)
   if (!first.used) return;
-  const int pieces = count_pieces(a.records, c0, ctas);
   const SeqDesc& s = a.s;
   const int gq = i >> 7, r = i & 127, dt = r / s.group, tok = gq * a.TQ + dt;
-  if (dt >= a.TQ || tok >= first.nt) return;
+  const bool live = dt < a.TQ && tok < first.nt;
+  if (!__any_sync(0xffffffffu, live)) return;
   auto at = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * 256 + i; };
-  float big = -INFINITY;
-  for (int p = 0; p < pieces; ++p) {
-    const float2 ml = a.part_ml[at(p)];
+  const int sub = threadIdx.x & 7;
+  // (m, l) of eight pieces at a time, one a thread
+  auto load_ml = [&](int base) {
+    return live && base + sub < pieces ? a.part_ml[at(base + sub)] : make_float2(0.0f, 0.0f);
+  };
+  const float2 early = load_ml(0);
+  float big = early.y != 0.0f ? early.x : -INFINITY;
+  for (int base = 8; base < pieces; base += 8) {
+    const float2 ml = load_ml(base);
     if (ml.y != 0.0f) big = fmaxf(big, ml.x);
   }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
   float o[DP / 8] = {};
   float l = 0.0f;
-  for (int p = 0; p < pieces; ++p) {
-    const float2 ml = a.part_ml[at(p)];
-    if (ml.y == 0.0f) continue;
-    const float f = ex2(ml.x - big);
-    l += ml.y * f;
-    const float4* x = reinterpret_cast<const float4*>(a.part_o + at(p) * DP + d0);
+  for (int base = 0; base < pieces; base += 8) {
+    const float2 ml = base == 0 ? early : load_ml(base);
+    const float f_mine = ml.y != 0.0f ? ex2(ml.x - big) : 0.0f;
+    for (int q0 = 0; q0 < 8 && base + q0 < pieces; q0 += 4) {
 #pragma unroll
-    for (int e = 0; e < DP / 32; ++e) {
-      const float4 v = x[e];
-      o[4 * e] = fmaf(v.x, f, o[4 * e]);
-      o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
-      o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
-      o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
+      for (int q = 0; q < 4; ++q) {  // the loads of four pieces under way together
+        const float f = __shfl_sync(0xffffffffu, f_mine, q0 + q, 8), y = __shfl_sync(0xffffffffu, ml.y, q0 + q, 8);
+        const float4* x = reinterpret_cast<const float4*>(a.part_o + at(base + q0 + q) * DP + d0);
+        l += y * f;
+#pragma unroll
+        for (int e = 0; e < DP / 32; ++e) {
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (y != 0.0f) v = x[e];  // (no key, or no piece: nothing is there)
+          o[4 * e] = fmaf(v.x, f, o[4 * e]);
+          o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
+          o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
+          o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
+        }
+      }
     }
   }
+  if (!live) return;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const size_t row = static_cast<size_t>(first.row0) + first.t0 + tok;
   const int h = first.kvh * s.group + r % s.group;

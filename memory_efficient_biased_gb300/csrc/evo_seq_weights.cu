@@ -371,10 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_weights_kernel(const __gr
 __global__ void __launch_bounds__(kTile) evo_seq_weights_join_kernel(const __grid_constant__ SeqWeightsArgs a, int ctas) {
   const int c0 = blockIdx.x, r = threadIdx.x;
   const PieceRecord first = a.records[2 * c0 + 1];
-  if (!first.used) return;
-  const int pieces = count_pieces(a.records, c0, ctas);
-  if (r >= first.nt) return;
+  const int pieces = count_pieces(a.records, c0, ctas);  // (read beside the first record)
+  if (!first.used || r >= first.nt) return;
   float sum = a.part[(static_cast<size_t>(c0) * 2 + 1) * kTile + r];
+#pragma unroll 4
   for (int p = 1; p < pieces; ++p) sum += a.part[static_cast<size_t>(c0 + p) * 2 * kTile + r];
   a.weights[(static_cast<size_t>(first.b) * a.s.kv_heads + first.kvh) * a.weights_len + first.t0 + r] += sum;
 }
