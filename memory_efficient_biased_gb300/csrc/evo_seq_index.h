@@ -1,0 +1,19 @@
+// evo_seq_index.h — index arithmetic of the causal-sequence kernels that has to hold up to the
+// longest sequences (2^31 keys) and the widest groups (128 heads).  Plain C++: compiled for the host
+// too, where no sequence of that length is needed to check it.
+#pragma once
+
+#if defined(__CUDACC__)
+#define EVO_HD __host__ __device__ __forceinline__
+#else
+#define EVO_HD inline
+#endif
+
+namespace evo {
+
+// The first row (token by token, `group` heads each) of a tile of TQ tokens that sees a key
+// `ahead` tokens behind the tile's first one (negative: in front of it, and every row sees it).
+// A key in front of the tile may be 2^31 tokens away: the product is taken of no more than a tile.
+EVO_HD int first_row(int ahead, int TQ, int group) { return (ahead > -TQ ? ahead : -TQ) * group; }
+
+}  // namespace evo

@@ -5,6 +5,7 @@
 
 #include "evo_internal.h"
 #include "evo_ptx.cuh"
+#include "evo_seq_index.h"
 
 namespace evo {
 

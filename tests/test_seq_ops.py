@@ -815,3 +815,51 @@ def test_prompt_backward_of_much_work(T, Hq, Hk, D, dtype):
         S.check_gradients(S.f64(q[:, hq]), S.f64(k[:, hk]), S.f64(v[:, hk]), S.f64(do[:, hq]),
                           [S.f64(g[0][:, hq]), S.f64(g[1][:, hk]), S.f64(g[2][:, hk])], D ** -0.5, dtype)
     assert E.evo_attn_device_status() == 0
+
+
+def long_cache(L, page, D, dtype, seed):
+    """A cache of L places that goes over the same four pages again and again: (k, v [4·page, D] fp64, k_pages,
+    v_pages, table, how often each of the 4·page rows is there)."""
+    rng = np.random.default_rng(seed)
+    k, v = S.normal(rng, 4, page, 1, D, dtype=dtype), S.normal(rng, 4, page, 1, D, dtype=dtype)
+    table = (torch.arange(-(-L // page), dtype=torch.int32) % 4)[None].contiguous()
+    rows = 4 * page
+    times = L // rows + (np.arange(rows) < L % rows)
+    return S.f64(k).reshape(rows, D), S.f64(v).reshape(rows, D), k.cuda(), v.cuda(), table.cuda(), times
+
+
+def check_long(q, k, v, times, L, out, lse, w, scale, dtype):
+    """One token over long_cache's: every place of a row has the row's weight.  Bounds as in seq_util; l, O and
+    the weights are sums of L/128 tiles, one rounding each, in whatever order."""
+    G = q.shape[0]
+    x = scale * (q @ k.T)
+    m = x.max(1, keepdims=True)
+    e = np.exp(x - m)
+    total = (e * times).sum(1)
+    z, p = m[:, 0] + np.log(total), e / total[:, None]
+    es, u = S.score_error(q[None], k[:, None], scale), S.U[dtype]
+    adds = (L / 128 + 256) * 2.0 ** -24
+    S.assert_close(S.f64(lse[:, 0]), z, es + 2.0 ** -19 * (1 + np.abs(z)) + adds, "lse")
+    rp = 2 * es + 2.0 ** -18 * (1 + np.abs(z)) + 2 * adds
+    S.assert_close(S.f64(out[0]), (p * times) @ v, (2 * u + rp[:, None]) * ((p * times) @ np.abs(v)), "out")
+    if w is not None:
+        want, bound = p.sum(0), (p * (rp[:, None] + G * 2.0 ** -24)).sum(0)
+        rows = k.shape[0]
+        got = S.f64(w)
+        for a in range(0, L, 1024 * rows):  # some million places at a time
+            n = min(1024 * rows, L - a)
+            idx = np.arange(n) % rows
+            S.assert_close(got[a:a + n], want[idx], bound[idx], f"weights from {a}")
+        assert np.all(got[L:] == 0)
+
+
+def test_weights_of_a_wide_group_over_millions_of_keys():
+    """(place of the key - place of the row) x heads of the group passes 2^31."""
+    L, G, D, dtype = 23_000_000, 96, 8, BF
+    k, v, kp, vp, table, times = long_cache(L, 1024, D, dtype, 51)
+    q = S.normal(np.random.default_rng(52), 1, G, D, dtype=dtype)
+    w = torch.zeros(1, 1, L + 5, device="cuda")
+    out, lse = Q.evo_paged_fwd(q.cuda(), kp, vp, S.offsets([1]).cuda(), torch.tensor([L], dtype=torch.int32).cuda(), table,
+                               weights=w)
+    assert E.evo_attn_device_status() == 0
+    check_long(S.f64(q[0]), k, v, times, L, out, lse, w[0, 0], D ** -0.5, dtype)
