@@ -204,7 +204,7 @@ __device__ __forceinline__ void walk(const SeqBwdArgs& a, uint8_t* base, Bars* b
       const uint32_t as = n % kASlots, bs = n % kBSlots;
       if (!mbar_wait_warp_inl(smem_u32(&bars->a_full[as]), (n / kASlots) & 1, g)) return;
       if (!mbar_wait_warp_inl(smem_u32(&bars->b_full[bs]), (n / kBSlots) & 1, g)) return;
-      const int last = DKV ? (cur.kv_end - j * a.TQ) * a.s.group : cur.kv_end - j * kTile;  // rows in the sequence
+      const int last = DKV ? tile_rows(cur.kv_end - j * a.TQ, a.TQ, a.s.group) : cur.kv_end - j * kTile;  // rows in the sequence
       if (last < (DKV ? a.TQ * a.s.group : kTile)) {
         clear(base + L::a + as * L::kTB, last);
         if (DKV) clear(base + L::b + bs * L::kTB, last);  // (V's rows only reach masked entries of dP)
@@ -536,7 +536,7 @@ __device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float* ro
       const float4* nd = reinterpret_cast<const float4*>(rowbuf + st * 2 * kTile + kTile + grp * 64);
       // rows below `from` belong to tokens in front of the key; none does once the tile lies behind the keys
       const bool mask = j * a.TQ < w.t0 + kTile - 1;
-      const int from = (key - j * a.TQ) * s.group - grp * 64;
+      const int from = first_row(key - j * a.TQ, a.TQ, s.group) - grp * 64;
       uint32_t p[64];
       if (!mbar_wait_warp_inl(smem_u32(&bars->rows_full[st]), (n >> 1) & 1, g)) { ok = false; break; }
       if (!mbar_wait_warp_inl(smem_u32(&bars->s_full[0]), n & 1, g)) { ok = false; break; }

@@ -16,4 +16,8 @@ namespace evo {
 // A key in front of the tile may be 2^31 tokens away: the product is taken of no more than a tile.
 EVO_HD int first_row(int ahead, int TQ, int group) { return (ahead > -TQ ? ahead : -TQ) * group; }
 
+// Rows of a tile of TQ tokens that hold a token, where the sequence ends `left` tokens behind the
+// tile's first one (up to 2^31: counted within the tile before the product).
+EVO_HD int tile_rows(int left, int TQ, int group) { return (left < TQ ? left : TQ) * group; }
+
 }  // namespace evo

@@ -263,7 +263,7 @@ __device__ __forceinline__ void compute(const SeqWeightsArgs& a, const float* ro
       const uint32_t st = n & 1;
       const float4* rb = reinterpret_cast<const float4*>(rowbuf + st * kTile + grp * 64);
       // rows [from, to) of this half belong to new tokens that see the key
-      const int rows = w.kv_end - j * a.TQ < a.TQ ? (w.kv_end - j * a.TQ) * s.group : a.TQ * s.group;
+      const int rows = tile_rows(w.kv_end - j * a.TQ, a.TQ, s.group);
       const int from = first_row(key - w.pos - j * a.TQ, a.TQ, s.group) - grp * 64, to = rows - grp * 64;
       const bool mask = rows < kTile || w.pos + j * a.TQ < w.t0 + kTile - 1;
       if (!mbar_wait_warp_inl(smem_u32(&bars->rows_full[st]), (n >> 1) & 1, g)) { ok = false; break; }

@@ -10,6 +10,7 @@ from memory_efficient_biased_gb300 import build
 SOURCE = """
 #include "evo_seq_index.h"
 extern "C" int first_row(int ahead, int TQ, int group) { return evo::first_row(ahead, TQ, group); }
+extern "C" int tile_rows(int left, int TQ, int group) { return evo::tile_rows(left, TQ, group); }
 """
 GROUPS = (1, 2, 3, 8, 96, 127, 128)
 
@@ -32,3 +33,12 @@ def test_first_row(lib):
             got = lib.first_row(ahead, TQ, G)
             seen = [r >= got for r in range(TQ * G)]
             assert seen == [r // G >= ahead for r in range(TQ * G)], (G, ahead)
+
+
+def test_tile_rows(lib):
+    """A tile's rows in the sequence, for ends up to 2^31 tokens behind the tile: what lies behind them is
+    cleared, so a count that is too small would clear rows of the sequence or what is not the tile's."""
+    for G in GROUPS:
+        TQ = 128 // G
+        for left in [2 ** 31 - 1025, min(2 ** 31 // G + 1, 2 ** 31 - 1025), 2 ** 25, 2 ** 24 + 1, *range(1, 300)]:
+            assert lib.tile_rows(left, TQ, G) == min(left, TQ) * G, (G, left)
