@@ -67,7 +67,9 @@ __global__ void __launch_bounds__(kSelThreads) evo_evict_select_kernel(const Evi
     return;
   }
   float* w = a.weights + bh * a.weights_len;
-  const int n = len - a.recent, k = a.budget - a.recent;  // k of the n oldest stay
+  // Places are unsigned: the last pass over them may look up to 8192 past 2^31 (and see that nothing is there).
+  const uint32_t size = len, n = len - a.recent;
+  const int k = a.budget - a.recent;  // of the n oldest that stay
   uint32_t prefix = 0, mask = 0, want = k;                // of those matching prefix, `want` stay
   if (k > 0) {
 #pragma unroll 1
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(kSelThreads) evo_evict_select_kernel(const Evi
       const uint32_t low = (1u << bits) - 1u;
       for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
       __syncthreads();
-      for (int base = tid; base < n; base += kSelThreads * kSelDeep) {
+      for (uint32_t base = tid; base < n; base += kSelThreads * kSelDeep) {
         float x[kSelDeep];  // loads in front of the counting, so that they are under way together
 #pragma unroll
         for (int e = 0; e < kSelDeep; ++e) x[e] = base + e * kSelThreads < n ? w[base + e * kSelThreads] : 0.0f;
@@ -114,14 +116,14 @@ __global__ void __launch_bounds__(kSelThreads) evo_evict_select_kernel(const Evi
   }
   // `want` of the weights equal to `prefix` stay (k == 0: none does)
   uint32_t above = 0, equal = 0;  // kept so far: above the threshold (or recent), equal to it
-  for (int base = 0; base < len; base += kSelThreads * kSelPer) {
-    const int j0 = base + tid * kSelPer;
+  for (uint32_t base = 0; base < size; base += kSelThreads * kSelPer) {
+    const uint32_t j0 = base + tid * kSelPer;
     float x[kSelPer];
     uint32_t up = 0, eq = 0;  // bits
 #pragma unroll
     for (int e = 0; e < kSelPer; ++e) {
       x[e] = 0.0f;
-      if (j0 + e < len) {
+      if (j0 + e < size) {
         x[e] = w[j0 + e];
         const uint32_t u = ordered(x[e]);
         if (j0 + e >= n || (k > 0 && u > prefix))
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kSelThreads) evo_evict_select_kernel(const Evi
       const bool is_up = (up >> e) & 1u, is_eq = (eq >> e) & 1u;
       if (is_up || (is_eq && e0 < want)) {
         const uint32_t to = u0 + (e0 < want ? e0 : want);
-        kept[to] = j0 + e;
+        kept[to] = static_cast<int>(j0 + e);
         w[to] = x[e];  // to <= j0 + e: places of this pass, already read, or of an earlier one
       }
       u0 += is_up;
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kSelThreads) evo_evict_select_kernel(const Evi
     equal += total & 0xffffu;
     __syncthreads();  // warp_sums is rewritten by the next pass, and w below it is final
   }
-  for (int j = a.budget + tid; j < len; j += kSelThreads) w[j] = 0.0f;
+  for (uint32_t j = a.budget + tid; j < size; j += kSelThreads) w[j] = 0.0f;
 }
 
 // ------------------------------------------------------------------ eviction: moves

@@ -863,3 +863,37 @@ def test_weights_of_a_wide_group_over_millions_of_keys():
                                weights=w)
     assert E.evo_attn_device_status() == 0
     check_long(S.f64(q[0]), k, v, times, L, out, lse, w[0, 0], D ** -0.5, dtype)
+
+
+def test_evict_the_longest_sequence():
+    """2^31 - 1025 places: the passes over them end past 2^31."""
+    L, page, D, budget, recent = 2 ** 31 - 1025, 1024, 8, 600, 10
+    cols = -(-L // page)
+    gen = torch.Generator(device="cuda").manual_seed(61)
+    kp = torch.empty(cols, page, 1, D, dtype=BF, device="cuda")
+    vp = torch.empty_like(kp)
+    table = torch.randperm(cols, generator=gen, device="cuda").to(torch.int32)[None].contiguous()
+    rng = np.random.default_rng(62)
+    n, old = L - recent, budget - recent
+    # the heaviest places: anywhere, the first, and the last ones of the passes
+    some = sorted({0, 5000, n - 1, n - 2, n - 1024, n - 5000, n - 8192} | {int(x) for x in rng.integers(0, n, old)})
+    drop = rng.permutation(range(1, len(some) - 7))[:len(some) - old]
+    some = [x for i, x in enumerate(some) if i not in set(drop.tolist())]
+    assert len(some) == old
+    places = torch.tensor(some + list(range(n, L)), device="cuda")
+    w = torch.zeros(1, 1, L + 3, device="cuda")
+    w[0, 0, places[:old]] = torch.rand(old, generator=gen, device="cuda") + 0.5
+    w[0, 0, n:L] = 0.25
+    at = table[0].long()[places // page], places % page
+    rows = torch.randn(2, budget, 1, D, generator=gen, device="cuda").to(BF)
+    kp[at], vp[at] = rows[0], rows[1]
+    want_w = w[0, 0, places].clone()
+    size = torch.tensor([L], dtype=torch.int32, device="cuda")
+    kept = Q.evo_cache_evict(kp, vp, table, size, w, budget, recent)
+    assert E.evo_attn_device_status() == 0 and size.tolist() == [budget]
+    assert torch.equal(kept[0, 0].long(), places)
+    to = torch.arange(budget, device="cuda")
+    for pages, want in ((kp, rows[0]), (vp, rows[1])):
+        assert torch.equal(pages[table[0].long()[to // page], to % page], want)
+    assert torch.equal(w[0, 0, :budget], want_w)
+    assert int(torch.count_nonzero(w[0, 0, budget:])) == 0
