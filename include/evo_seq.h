@@ -102,7 +102,8 @@ typedef struct {
 
 /* Per-call options; NULL or all zero (but size) = the defaults.
  *   scale          s above; 0 = head_dim^-1/2, otherwise finite and positive
- *   wait_limit_ns  bound on every device-side wait (0 = 2e9)
+ *   wait_limit_ns  bound on every device-side wait (0 = 2e9, below 1000 = 1000).  A kernel that gave
+ *                  up still waits for its own copies and products, up to 2 s whatever the limit.
  *   status         device int set to EVO_ERR_DEVICE_TIMEOUT or EVO_ERR_BAD_INDEX
  *                  (the caller clears it); NULL = the fallback word, read with
  *                  evo_attn_device_status */

@@ -84,11 +84,6 @@ __device__ __forceinline__ uint32_t packed_col(int k) {  // 16 rows or keys from
   return k < 4 ? k * 8 : 64 + (k - 4) * 8;
 }
 
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const SeqBwdArgs& a) {
-  volatile int never = 0;
-  WaitGuard g{a.wait_ns, a.s.status, &never};
-  mbar_wait_inl(bar, parity, g);
-}
 template <bool WARP>
 __device__ __forceinline__ bool take(Bars* bars, uint32_t it, const WaitGuard& g, Work& w) {
   const uint32_t s = it % kDescs;
@@ -154,10 +149,10 @@ __device__ __forceinline__ void producer(const SeqBwdArgs& a, uint8_t* base, Bar
   }
   // every copy has landed before the CTA may exit
   for (uint32_t x = na > kASlots ? na - kASlots : 0; x < na; ++x)
-    drain_wait(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, a);
+    drain_wait(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, g);
   for (uint32_t x = nb > kBSlots ? nb - kBSlots : 0; x < nb; ++x)
-    drain_wait(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, a);
-  if (own > 0) drain_wait(smem_u32(&bars->own_full), (own - 1) & 1, a);
+    drain_wait(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g);
+  if (own > 0) drain_wait(smem_u32(&bars->own_full), (own - 1) & 1, g);
 }
 
 // ------------------------------------------------------------ the walk, and the streamed tiles' release
@@ -172,8 +167,6 @@ __device__ __forceinline__ void walk(const SeqBwdArgs& a, uint8_t* base, Bars* b
   else
     walk.init(a.s, QueryBlocks{a.TQ}, blockIdx.x, gridDim.x);
   PieceRecord* rec = a.records + 2 * (blockIdx.x + (DKV ? 0 : gridDim.x));
-  if (lane < 2) rec[lane].used = 0;
-  __syncwarp();
   Work cur, ahead;
   uint32_t pub = 0, n = 0;
   bool more = true;
@@ -340,7 +333,7 @@ __device__ __forceinline__ void mma_dkv(const SeqBwdArgs& a, uint8_t* base, Bars
   }
   __syncwarp();
   if (elect_one()) umma_commit(smem_u32(&bars->drain));
-  drain_wait(smem_u32(&bars->drain), 0, a);
+  drain_wait(smem_u32(&bars->drain), 0, g);
 }
 
 template <int DP, bool BF16>
@@ -407,7 +400,7 @@ __device__ __forceinline__ void mma_dq(const SeqBwdArgs& a, uint8_t* base, Bars*
   }
   __syncwarp();
   if (elect_one()) umma_commit(smem_u32(&bars->drain));
-  drain_wait(smem_u32(&bars->drain), 0, a);
+  drain_wait(smem_u32(&bars->drain), 0, g);
 }
 
 // ------------------------------------------------------------ compute (warps 0..7)
@@ -691,17 +684,20 @@ __device__ __forceinline__ void init_bars(Bars* bars, bool dkv) {
 }
 
 // Between dK/dV and dQ, by every thread of the CTA: each warp has waited for the copies and MMAs that it
-// started, so nobody uses a barrier any more, and all of them begin anew.
-__device__ __forceinline__ void turn_over(Bars* bars) {
+// started, so nobody uses a barrier any more, and all of them begin anew.  False where a wait ran out:
+// something may then still be under way, and the CTA does no more.
+__device__ __forceinline__ bool turn_over(Bars* bars) {
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) {
+  const bool go = *static_cast<volatile int*>(&bars->abort) == 0;
+  if (go && threadIdx.x == 0) {
     uint64_t* bar = reinterpret_cast<uint64_t*>(bars);
     for (uint32_t i = 0; i < offsetof(Bars, work) / 8; ++i) mbar_inval(smem_u32(bar + i));
     init_bars(bars, false);
   }
   __syncthreads();
   tc_fence_after();
+  return go;
 }
 
 template <int DP, bool BF16, bool DKV>
@@ -731,6 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_c
   Bars* bars = reinterpret_cast<Bars*>(base + L::bars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool both = gridDim.y == 1, dkv = blockIdx.y == 0;
+  // no piece yet, in either phase: the join reads every record, those of a CTA that gave up too
+  if (threadIdx.x < 4 && (both || (threadIdx.x < 2) == dkv))
+    a.records[2 * (blockIdx.x + (threadIdx.x < 2 ? 0 : gridDim.x)) + (threadIdx.x & 1)].used = 0;
   if (smem_u32(base) & 1023u) {  // the tiles' swizzle counts from 1 KB borders
     if (threadIdx.x == 0) atomicExch(a.s.status, kStatusTimeout);
     return;
@@ -763,13 +762,11 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_c
   if (warp >= kProducerWarp) {
     setmaxnreg_dec<kRegsOther>();
     if (dkv) other_warps<DP, BF16, true>(a, base, bars, tmem, g, rowbuf, warp, lane);
-    if (both) turn_over(bars);
-    if (both || !dkv) other_warps<DP, BF16, false>(a, base, bars, tmem, g, rowbuf, warp, lane);
+    if (both ? turn_over(bars) : !dkv) other_warps<DP, BF16, false>(a, base, bars, tmem, g, rowbuf, warp, lane);
   } else {
     setmaxnreg_inc<kRegsCompute>();
     if (dkv) compute_dkv<DP, BF16>(a, rowbuf, bars, tmem, g);
-    if (both) turn_over(bars);
-    if (both || !dkv) compute_dq<DP, BF16>(a, bars, tmem, g);
+    if (both ? turn_over(bars) : !dkv) compute_dq<DP, BF16>(a, bars, tmem, g);
   }
   tc_fence_before();
   __syncthreads();

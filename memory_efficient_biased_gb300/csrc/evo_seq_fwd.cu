@@ -75,12 +75,6 @@ static_assert(Layout<128>::total + 1024 <= 232448, "shared memory");
 __device__ __forceinline__ uint32_t col_s(uint32_t g) { return g * 128u; }
 __device__ __forceinline__ uint32_t col_o(uint32_t g) { return 256u + g * 128u; }
 
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const SeqFwdArgs& a) {
-  volatile int never = 0;
-  WaitGuard g{a.wait_ns, a.s.status, &never};
-  mbar_wait_inl(bar, parity, g);
-}
-
 // The next descriptor, read by every lane of a warp (or by one thread alone).
 template <bool WARP>
 __device__ __forceinline__ bool take(Bars* bars, uint32_t it, const WaitGuard& g, Work& w) {
@@ -177,9 +171,9 @@ __device__ __forceinline__ void producer(const SeqFwdArgs& a, uint8_t* base, Bar
   // every copy this warp started has landed before the CTA may exit
   __syncwarp();
   for (uint32_t x = use > L::kSlots ? use - L::kSlots : 0; x < use; ++x)
-    drain_wait(smem_u32(&bars->full[x % L::kSlots]), (x / L::kSlots) & 1, a);
+    drain_wait(smem_u32(&bars->full[x % L::kSlots]), (x / L::kSlots) & 1, g);
   for (int b = 0; b < 2; ++b)
-    if (queries[b] > 0) drain_wait(smem_u32(&bars->q_full[b]), (queries[b] - 1) & 1, a);
+    if (queries[b] > 0) drain_wait(smem_u32(&bars->q_full[b]), (queries[b] - 1) & 1, g);
 }
 
 // ------------------------------------------------------------ MMA (one warp per tile, one of its threads issuing)
@@ -271,7 +265,7 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
   }
   __syncwarp();
   if (elect_one()) umma_commit(smem_u32(&bars->drain[gq]));
-  drain_wait(smem_u32(&bars->drain[gq]), 0, a);
+  drain_wait(smem_u32(&bars->drain[gq]), 0, g);
 }
 
 // ------------------------------------------------------------ the walk, and V's release (one warp)

@@ -70,6 +70,16 @@ __device__ __forceinline__ int page_of(const SeqDesc& d, int b, int j) {
   return p;
 }
 
+// A wait that a CTA owes before it may leave, or begin its barriers anew: for its own copies and MMAs, which
+// write into its shared memory and its barriers.  It has a limit of its own: the caller's may be a
+// microsecond, and has just run out where a CTA gives up.
+constexpr uint64_t kDrainNs = 2000000000ull;
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const WaitGuard& g) {
+  volatile int never = 0;
+  const WaitGuard own{g.limit_ns > kDrainNs ? g.limit_ns : kDrainNs, g.status, &never};
+  if (!mbar_wait_inl(bar, parity, own)) *g.abort = 1;
+}
+
 struct AppendArgs {
   SeqDesc s;
   const uint16_t *k, *v;

@@ -70,11 +70,6 @@ struct CachedKeyBlocks {
   }
 };
 
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const SeqWeightsArgs& a) {
-  volatile int never = 0;
-  WaitGuard g{a.wait_ns, a.s.status, &never};
-  mbar_wait_inl(bar, parity, g);
-}
 template <bool WARP>
 __device__ __forceinline__ bool take(Bars* bars, uint32_t it, const WaitGuard& g, Work& w) {
   const uint32_t s = it % kDescs;
@@ -127,8 +122,8 @@ __device__ __forceinline__ void producer(const SeqWeightsArgs& a, uint8_t* base,
   }
   __syncwarp();
   for (uint32_t x = n > kSlots ? n - kSlots : 0; x < n; ++x)
-    drain_wait(smem_u32(&bars->q_full[x % kSlots]), (x / kSlots) & 1, a);
-  for (uint32_t x = keys > 2 ? keys - 2 : 0; x < keys; ++x) drain_wait(smem_u32(&bars->k_full[x & 1]), (x >> 1) & 1, a);
+    drain_wait(smem_u32(&bars->q_full[x % kSlots]), (x / kSlots) & 1, g);
+  for (uint32_t x = keys > 2 ? keys - 2 : 0; x < keys; ++x) drain_wait(smem_u32(&bars->k_full[x & 1]), (x >> 1) & 1, g);
 }
 
 template <int DP, bool BF16>
@@ -168,7 +163,7 @@ __device__ __forceinline__ void mma(const SeqWeightsArgs& a, uint8_t* base, Bars
   }
   __syncwarp();
   if (elect_one()) umma_commit(smem_u32(&bars->drain));
-  drain_wait(smem_u32(&bars->drain), 0, a);
+  drain_wait(smem_u32(&bars->drain), 0, g);
 }
 
 // -log2e·lse of each tile of queries; -inf (P = 0) for a row that saw nothing.
