@@ -58,8 +58,10 @@ struct Bars {
   uint64_t second_done;                              // dS·(Q or K), and all before it, is done
   uint64_t acc_full, acc_free, drain;
   Work work[kDescs];
+  uint32_t loads_a, loads_b, loads_own;  // copies that the producer asked for
   uint32_t tmem_slot;
   int abort;
+  int go;  // dQ's phase begins
 };
 
 template <int DP>
@@ -147,12 +149,7 @@ __device__ __forceinline__ void producer(const SeqBwdArgs& a, uint8_t* base, Bar
       ++nb;
     }
   }
-  // every copy has landed before the CTA may exit
-  for (uint32_t x = na > kASlots ? na - kASlots : 0; x < na; ++x)
-    drain_wait(smem_u32(&bars->a_full[x % kASlots]), (x / kASlots) & 1, g);
-  for (uint32_t x = nb > kBSlots ? nb - kBSlots : 0; x < nb; ++x)
-    drain_wait(smem_u32(&bars->b_full[x % kBSlots]), (x / kBSlots) & 1, g);
-  if (own > 0) drain_wait(smem_u32(&bars->own_full), (own - 1) & 1, g);
+  bars->loads_a = na, bars->loads_b = nb, bars->loads_own = own;
 }
 
 // ------------------------------------------------------------ the walk, and the streamed tiles' release
@@ -333,7 +330,6 @@ __device__ __forceinline__ void mma_dkv(const SeqBwdArgs& a, uint8_t* base, Bars
   }
   __syncwarp();
   if (elect_one()) umma_commit(smem_u32(&bars->drain));
-  drain_wait(smem_u32(&bars->drain), 0, g);
 }
 
 template <int DP, bool BF16>
@@ -400,7 +396,6 @@ __device__ __forceinline__ void mma_dq(const SeqBwdArgs& a, uint8_t* base, Bars*
   }
   __syncwarp();
   if (elect_one()) umma_commit(smem_u32(&bars->drain));
-  drain_wait(smem_u32(&bars->drain), 0, g);
 }
 
 // ------------------------------------------------------------ compute (warps 0..7)
@@ -683,21 +678,38 @@ __device__ __forceinline__ void init_bars(Bars* bars, bool dkv) {
   fence_barrier_init();
 }
 
-// Between dK/dV and dQ, by every thread of the CTA: each warp has waited for the copies and MMAs that it
-// started, so nobody uses a barrier any more, and all of them begin anew.  False where a wait ran out:
-// something may then still be under way, and the CTA does no more.
-__device__ __forceinline__ bool turn_over(Bars* bars) {
+// By one warp, when every role has ended.  (Every tile that was loaded was let go by a commit; where the
+// CTA gave up some were not.)
+__device__ __forceinline__ void drain_all(Bars* bars, const WaitGuard& g) {
+  const uint32_t all = *g.abort ? 0u : ~0u;
+  const Owed owed[] = {{bars->a_full, kASlots, bars->loads_a},       {bars->b_full, kBSlots, bars->loads_b},
+                       {&bars->own_full, 1, bars->loads_own},        {bars->a_empty, kASlots, bars->loads_a & all},
+                       {&bars->second_done, 1, bars->loads_a & all}, {bars->b_empty, kBSlots, bars->loads_b & all},
+                       {&bars->own_empty, 1, bars->loads_own & all}, {&bars->drain, 1, 1}};
+  drain(owed, g);
+}
+
+// Between dK/dV and dQ, by every thread of the CTA: nothing is under way, so nobody uses a barrier any more,
+// and all of them begin anew.  False where a wait ran out: something may then still be to come, and the
+// CTA does no more.
+template <bool COMPUTE>
+__device__ __forceinline__ bool turn_over(Bars* bars, const WaitGuard& g) {
   tc_fence_before();
   __syncthreads();
-  const bool go = *static_cast<volatile int*>(&bars->abort) == 0;
-  if (go && threadIdx.x == 0) {
-    uint64_t* bar = reinterpret_cast<uint64_t*>(bars);
-    for (uint32_t i = 0; i < offsetof(Bars, work) / 8; ++i) mbar_inval(smem_u32(bar + i));
-    init_bars(bars, false);
+  if (!COMPUTE && threadIdx.x >> 5 == kMmaWarp) {
+    drain_all(bars, g);
+    if ((threadIdx.x & 31) == 0) {
+      bars->go = *g.abort == 0;  // (one word that does not change: `abort` may, as soon as the first warp goes on)
+      if (bars->go) {
+        uint64_t* bar = reinterpret_cast<uint64_t*>(bars);
+        for (uint32_t i = 0; i < offsetof(Bars, work) / 8; ++i) mbar_inval(smem_u32(bar + i));
+        init_bars(bars, false);
+      }
+    }
   }
   __syncthreads();
   tc_fence_after();
-  return go;
+  return bars->go != 0;
 }
 
 template <int DP, bool BF16, bool DKV>
@@ -762,17 +774,20 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_bwd_kernel(const __grid_c
   if (warp >= kProducerWarp) {
     setmaxnreg_dec<kRegsOther>();
     if (dkv) other_warps<DP, BF16, true>(a, base, bars, tmem, g, rowbuf, warp, lane);
-    if (both ? turn_over(bars) : !dkv) other_warps<DP, BF16, false>(a, base, bars, tmem, g, rowbuf, warp, lane);
+    if (both ? turn_over<false>(bars, g) : !dkv) other_warps<DP, BF16, false>(a, base, bars, tmem, g, rowbuf, warp, lane);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+      drain_all(bars, g);
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
   } else {
     setmaxnreg_inc<kRegsCompute>();
     if (dkv) compute_dkv<DP, BF16>(a, rowbuf, bars, tmem, g);
-    if (both ? turn_over(bars) : !dkv) compute_dq<DP, BF16>(a, bars, tmem, g);
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kMmaWarp) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (both ? turn_over<true>(bars, g) : !dkv) compute_dq<DP, BF16>(a, bars, tmem, g);
+    tc_fence_before();
+    __syncthreads();
   }
 }
 

@@ -58,6 +58,7 @@ struct Bars {
   Work work[kDescs];
   float2 merge[kTile];  // (m, l) of the second warpgroup's share of a single tile
   int dirty[kDescs];  // a V tile of the item held values that were taken out
+  uint32_t tiles, queries[2];  // K and V tiles and Q tiles that the producer asked for
   uint32_t tmem_slot;
   int abort;
 };
@@ -168,12 +169,7 @@ __device__ __forceinline__ void producer(const SeqFwdArgs& a, uint8_t* base, Bar
     }
     if (!ok) break;
   }
-  // every copy this warp started has landed before the CTA may exit
-  __syncwarp();
-  for (uint32_t x = use > L::kSlots ? use - L::kSlots : 0; x < use; ++x)
-    drain_wait(smem_u32(&bars->full[x % L::kSlots]), (x / L::kSlots) & 1, g);
-  for (int b = 0; b < 2; ++b)
-    if (queries[b] > 0) drain_wait(smem_u32(&bars->q_full[b]), (queries[b] - 1) & 1, g);
+  if (lane == 0) bars->tiles = use, bars->queries[0] = queries[0], bars->queries[1] = queries[1];
 }
 
 // ------------------------------------------------------------ MMA (one warp per tile, one of its threads issuing)
@@ -265,7 +261,6 @@ __device__ __forceinline__ void mma(const SeqFwdArgs& a, uint8_t* base, Bars* ba
   }
   __syncwarp();
   if (elect_one()) umma_commit(smem_u32(&bars->drain[gq]));
-  drain_wait(smem_u32(&bars->drain[gq]), 0, g);
 }
 
 // ------------------------------------------------------------ the walk, and V's release (one warp)
@@ -731,15 +726,27 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_fwd_kernel(const __grid_c
     } else {
       mma<DP, BF16>(a, base, bars, tmem, static_cast<uint32_t>(uniform(warp) - kMmaWarp), g);
     }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+      const uint32_t all = bars->abort ? 0u : ~0u;  // (a CTA that gave up did not let go of every tile)
+      const Owed owed[] = {{bars->full, L::kSlots, bars->tiles},
+                           {bars->empty, L::kSlots, bars->tiles & all},
+                           {&bars->q_full[0], 1, bars->queries[0]},
+                           {&bars->q_full[1], 1, bars->queries[1]},
+                           {&bars->q_empty[0], 1, bars->queries[0] & all},
+                           {&bars->q_empty[1], 1, bars->queries[1] & all},
+                           {&bars->drain[0], 1, 1},
+                           {&bars->drain[1], 1, 1}};
+      drain(owed, g);
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
     softmax<DP, BF16, SCORES>(a, base, bars, tmem, g);
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kMmaWarp) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tc_fence_before();
+    __syncthreads();
   }
 }
 

@@ -1,6 +1,6 @@
-// evo_seq_index.h — index arithmetic of the causal-sequence kernels that has to hold up to the
-// longest sequences (2^31 keys) and the widest groups (128 heads).  Plain C++: compiled for the host
-// too, where no sequence of that length is needed to check it.
+// evo_seq_index.h — index arithmetic of the causal-sequence kernels that no run on a GPU checks well: it has
+// to hold up to the longest sequences (2^31 keys) and the widest groups (128 heads), and a wait must be for
+// the phase that it means.  Plain C++, compiled for the host too.
 #pragma once
 
 #if defined(__CUDACC__)
@@ -19,5 +19,9 @@ EVO_HD int first_row(int ahead, int TQ, int group) { return (ahead > -TQ ? ahead
 // Rows of a tile of TQ tokens that hold a token, where the sequence ends `left` tokens behind the
 // tile's first one (up to 2^31: counted within the tile before the product).
 EVO_HD int tile_rows(int left, int TQ, int group) { return (left < TQ ? left : TQ) * group; }
+
+// The newest of the phases, counted from 0, that slot i of a ring has gone through after `uses` > i uses
+// (the slots take turns, a phase each).
+EVO_HD unsigned newest_phase(unsigned uses, unsigned slots, unsigned i) { return (uses - 1 - i) / slots; }
 
 }  // namespace evo

@@ -70,14 +70,36 @@ __device__ __forceinline__ int page_of(const SeqDesc& d, int b, int j) {
   return p;
 }
 
-// A wait that a CTA owes before it may leave, or begin its barriers anew: for its own copies and MMAs, which
-// write into its shared memory and its barriers.  It has a limit of its own: the caller's may be a
-// microsecond, and has just run out where a CTA gives up.
+// What may still be under way when every role of a CTA has ended, and has to be over before its shared
+// memory is anybody else's or its barriers begin anew: copies, MMAs, and the arrivals of the MMAs' last commits
+// at barriers that no one else waits on (a commit's arrival may come later than that of a commit behind it).
+// Each is a ring of barriers that has gone through `uses` phases.
+struct Owed {
+  uint64_t* bars;
+  uint32_t slots, uses;
+};
+// Waits for the newest phase of every barrier, one a lane (at most 32).  The limit is not the caller's alone: that
+// may be a microsecond, and has just run out where a CTA gives up.
 constexpr uint64_t kDrainNs = 2000000000ull;
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, const WaitGuard& g) {
-  volatile int never = 0;
-  const WaitGuard own{g.limit_ns > kDrainNs ? g.limit_ns : kDrainNs, g.status, &never};
-  if (!mbar_wait_inl(bar, parity, own)) *g.abort = 1;
+template <int N>
+__device__ __forceinline__ void drain(const Owed (&owed)[N], const WaitGuard& g) {
+  const int lane = threadIdx.x & 31;
+  uint32_t bar = 0, phase = 0, base = 0;
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    const uint32_t i = lane - base;  // (wraps below the ring's first lane)
+    if (i < owed[r].slots && i < owed[r].uses) {
+      bar = smem_u32(owed[r].bars + i);
+      phase = newest_phase(owed[r].uses, owed[r].slots, i);
+    }
+    base += owed[r].slots;
+  }
+  if (bar) {
+    volatile int never = 0;
+    const WaitGuard own{g.limit_ns > kDrainNs ? g.limit_ns : kDrainNs, g.status, &never};
+    if (!mbar_wait_inl(bar, phase & 1, own)) *g.abort = 1;
+  }
+  __syncwarp();
 }
 
 struct AppendArgs {

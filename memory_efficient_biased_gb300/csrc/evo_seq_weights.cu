@@ -29,6 +29,7 @@ struct Bars {
   uint64_t half_full, half_free, drain;
   Work work[kDescs];
   float half[kTile];  // the second warpgroup's sums, one per key
+  uint32_t loads, keys;  // tiles of queries and keys that the producer asked for
   uint32_t tmem_slot;
   int abort;
 };
@@ -120,10 +121,7 @@ __device__ __forceinline__ void producer(const SeqWeightsArgs& a, uint8_t* base,
       }
     }
   }
-  __syncwarp();
-  for (uint32_t x = n > kSlots ? n - kSlots : 0; x < n; ++x)
-    drain_wait(smem_u32(&bars->q_full[x % kSlots]), (x / kSlots) & 1, g);
-  for (uint32_t x = keys > 2 ? keys - 2 : 0; x < keys; ++x) drain_wait(smem_u32(&bars->k_full[x & 1]), (x >> 1) & 1, g);
+  if (lane == 0) bars->loads = n, bars->keys = keys;
 }
 
 template <int DP, bool BF16>
@@ -163,7 +161,6 @@ __device__ __forceinline__ void mma(const SeqWeightsArgs& a, uint8_t* base, Bars
   }
   __syncwarp();
   if (elect_one()) umma_commit(smem_u32(&bars->drain));
-  drain_wait(smem_u32(&bars->drain), 0, g);
 }
 
 // -log2e·lse of each tile of queries; -inf (P = 0) for a row that saw nothing.
@@ -357,6 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1) evo_seq_weights_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
+    const uint32_t all = bars->abort ? 0u : ~0u;  // (a CTA that gave up did not let go of every tile)
+    const Owed owed[] = {{bars->q_full, kSlots, bars->loads},        {bars->k_full, 2, bars->keys},
+                         {bars->q_empty, kSlots, bars->loads & all}, {bars->k_empty, 2, bars->keys & all},
+                         {&bars->drain, 1, 1}};
+    drain(owed, g);
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }

@@ -11,6 +11,7 @@ SOURCE = """
 #include "evo_seq_index.h"
 extern "C" int first_row(int ahead, int TQ, int group) { return evo::first_row(ahead, TQ, group); }
 extern "C" int tile_rows(int left, int TQ, int group) { return evo::tile_rows(left, TQ, group); }
+extern "C" unsigned newest_phase(unsigned uses, unsigned slots, unsigned i) { return evo::newest_phase(uses, slots, i); }
 """
 GROUPS = (1, 2, 3, 8, 96, 127, 128)
 
@@ -42,3 +43,13 @@ def test_tile_rows(lib):
         TQ = 128 // G
         for left in [2 ** 31 - 1025, min(2 ** 31 // G + 1, 2 ** 31 - 1025), 2 ** 25, 2 ** 24 + 1, *range(1, 300)]:
             assert lib.tile_rows(left, TQ, G) == min(left, TQ) * G, (G, left)
+
+
+def test_newest_phase(lib):
+    """What a CTA waits for before it leaves: each slot's newest phase, and never one that was not begun."""
+    for slots in (1, 2, 3, 4, 5, 10):
+        phases = [-1] * slots
+        for uses in range(1, 60):
+            phases[(uses - 1) % slots] += 1
+            for i in range(min(slots, uses)):
+                assert lib.newest_phase(uses, slots, i) == phases[i], (uses, slots, i)
