@@ -25,7 +25,8 @@
  * and, for a gradient dO: delta_i = dO_i·O_i, dP_ij = dO_i·v_j,
  * dS_ij = P_ij (dP_ij - delta_i), dQ_i = s Σ_j dS_ij k_j,
  * dK_j = s Σ_h Σ_i dS_ij q_i and dV_j = Σ_h Σ_i P_ij dO_i over the heads h of a
- * group.  A row that sees no key gives O = 0 and lse = -inf.
+ * group.  A row that sees no key, or none with a score above -inf, gives O = 0 and
+ * lse = -inf, and no key a weight.
  *
  * Layouts.  All device memory.
  *     q, out, dout, dq        [tokens, q_heads, head_dim]   dtype

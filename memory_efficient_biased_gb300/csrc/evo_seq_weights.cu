@@ -163,7 +163,7 @@ __device__ __forceinline__ void mma(const SeqWeightsArgs& a, uint8_t* base, Bars
   if (elect_one()) umma_commit(smem_u32(&bars->drain));
 }
 
-// -log2e·lse of each tile of queries; -inf (P = 0) for a row that saw nothing.
+// -log2e·lse of each tile of queries; -inf (P = 0) for a row that saw nothing, or nothing but -inf.
 __device__ __forceinline__ void rows(const SeqWeightsArgs& a, float* buf, Bars* bars, const WaitGuard& g, int lane) {
   const SeqDesc& s = a.s;
   int dt[4], head[4];
@@ -395,9 +395,11 @@ __global__ void __launch_bounds__(256) evo_scores_sum_kernel(const __grid_consta
       const float z = a.lse[static_cast<size_t>(h) * s.tokens + row] * kSeqLog2e;
       const float4 x = *reinterpret_cast<const float4*>(a.scores + (row * s.q_heads + h) * a.scores_ld + key);
       const float xs[4] = {x.x, x.y, x.z, x.w};
+      // where every score that the row sees is -inf, it gives no weight (and -inf - z would be no number)
+      const int last = z == -INFINITY ? -1 : seen;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (e <= seen) sum[e] += ex2(xs[e] - z);
+        if (e <= last) sum[e] += ex2(xs[e] - z);
     }
   }
   float* w = a.weights + (static_cast<size_t>(b) * s.kv_heads + hk) * a.weights_len + key;

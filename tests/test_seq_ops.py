@@ -937,3 +937,22 @@ def test_a_wait_that_runs_out():
         for x, y in zip(got, want):
             # (another share of the work: other sums' order)
             assert torch.allclose(x.float(), y.float(), rtol=2.0 ** -6, atol=2.0 ** -6), b
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_rows_of_minus_infinity_give_no_weight(dtype):
+    """A row whose every visible score is -inf gives 0, -inf and no weight, whether the weights are summed from the
+    forward's scores (a token a sequence) or from scores formed again (many), beside rows as usual."""
+    for chunks, ctx in (([1, 1, 1], [200, 131, 90]), ([40, 50, 30], [200, 131, 90])):
+        q, kp, vp, table, cu, lens, ks, vs = c = paged_case(chunks, ctx, 4, 2, 64, 16, dtype, seed=81)
+        r = slice(int(cu[1]), int(cu[2]))
+        q[r, :, 0] = 1.0
+        ks[1][:, :, 0] = float("-inf")
+        S.fill_cache(kp, vp, table, 1, ks[1], vs[1])
+        w0 = torch.rand(3, 2, 210)
+        w = w0.cuda()
+        out, lse = Q.evo_paged_fwd(q.cuda(), kp.cuda(), vp.cuda(), cu.cuda(), lens.cuda(), table.cuda(), weights=w)
+        assert E.evo_attn_device_status() == 0
+        assert torch.all(out[r] == 0) and torch.all(lse[:, r] == float("-inf"))
+        assert torch.equal(w[1].cpu(), w0[1])
+        check_paged(c, chunks, ctx, out, lse, 64 ** -0.5, dtype, w0, w, skip=(1,))
