@@ -102,7 +102,8 @@ typedef struct {
 } evo_cache_shape_t;
 
 /* Per-call options; NULL or all zero (but size) = the defaults.
- *   scale          s above; 0 = head_dim^-1/2, otherwise finite and positive
+ *   scale          s above; 0 = head_dim^-1/2, otherwise positive, and s·log2 e finite
+ *                  (s below 2.358e38)
  *   wait_limit_ns  bound on every device-side wait (0 = 2e9, below 1000 = 1000).  A kernel that gave
  *                  up still waits for its own copies and products, up to 2 s whatever the limit.
  *   status         device int set to EVO_ERR_DEVICE_TIMEOUT or EVO_ERR_BAD_INDEX

@@ -23,7 +23,8 @@ struct Opts {
 bool read_opts(const evo_seq_options_t* o, Opts* c) {
   if (!o) return true;
   if (o->size < sizeof(evo_seq_options_t) || o->flags != 0 || o->reserved != 0) return false;
-  if (o->scale != 0.0f && !(std::isfinite(o->scale) && o->scale > 0.0f)) return false;
+  // (the kernels work with scale · log2 e, which has to be a number too)
+  if (o->scale != 0.0f && !(std::isfinite(o->scale * kSeqLog2e) && o->scale > 0.0f)) return false;
   c->scale = o->scale;
   if (o->wait_limit_ns) c->wait_ns = o->wait_limit_ns < 1000 ? 1000 : o->wait_limit_ns;
   c->status = o->status;

@@ -78,6 +78,7 @@ def load():
 # is as it should be passes in one line (append and attention of one token, on an Arm host: 37 us with a function for
 # each question, 34 so).
 _Tensor = torch.Tensor
+_MOST_SCALE = 2.358e38  # times log2 e it is still a float32
 
 
 def _options(scale, wait_limit_ns, status, dev):
@@ -87,9 +88,9 @@ def _options(scale, wait_limit_ns, status, dev):
         _flat(status, "status", None, torch.int32, dev)
         if status.numel() < 1:
             raise ValueError("status must have an element")
-    # as the float32 it becomes: a 0 would mean the default
-    if scale is not None and not (0.0 < ctypes.c_float(scale).value < float("inf")):
-        raise ValueError(f"scale must be finite and positive, got {scale}")
+    # as the float32 it becomes: a 0 would mean the default, and the kernels multiply it by log2 e
+    if scale is not None and not (0.0 < ctypes.c_float(scale).value <= _MOST_SCALE):
+        raise ValueError(f"scale must be positive and at most {_MOST_SCALE}, got {scale}")
     if not 0 <= wait_limit_ns < 1 << 64:
         raise ValueError(f"wait_limit_ns must be an unsigned 64-bit number, got {wait_limit_ns}")
     o = SeqOptions(ctypes.sizeof(SeqOptions), 0, scale or 0.0, 0, int(wait_limit_ns),

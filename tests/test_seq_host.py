@@ -256,3 +256,15 @@ def test_packed_rows():
             assert p.data_ptr() % 16 == 0 and p.is_contiguous() and torch.equal(p, t)
         for t in (fused, fused[:, 2:4], fused[::2]):
             assert _packed_rows(t) is t
+
+
+@pytest.mark.parametrize("call", [fwd, bwd, paged])
+def test_scale_times_log2e_is_a_number(lib, call):
+    """The kernels work with scale · log2 e in float32: a scale that is a number only without it is refused."""
+    for scale in (2.36e38, 3.0e38, 3.4028234e38):
+        assert call(lib, o=opts(scale=scale)) == 10, scale
+        with pytest.raises(ValueError):
+            Q._options(scale, 0, None, -1)
+    for scale in (2.357e38, 1e-40):
+        assert call(lib, o=opts(scale=scale)) in REACH, scale
+        assert Q._options(scale, 0, None, -1)._obj.scale == ctypes.c_float(scale).value
