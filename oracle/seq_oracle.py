@@ -3,8 +3,8 @@ attention over packed prompts and its gradients, attention of new tokens over
 a paged cache with the sums of its weights, and eviction by those sums.
 
 TEST INFRASTRUCTURE ONLY, like ``evo_oracle``; it shares no code with the CUDA
-library.  Sequences are lists of numpy arrays here: offsets, pages and tables are
-resolved by the caller or by the functions at the end.
+library.  Sequences are numpy arrays here: offsets, pages and tables are resolved by
+the caller.
 
 Pins: tests/test_seq_oracle.py (differences, a loop over single scores, closed
 forms and invariants).
@@ -71,10 +71,3 @@ def choose(weights, length, budget, recent):
     # larger weights first, a NaN behind every number, the older of two equal ones first
     order = sorted(old, key=lambda j: (-value[j][0], value[j][1], j))
     return sorted(order[:budget - recent]) + list(range(length - recent, length))
-
-
-def place_rows(pages, table, length):
-    """[num_pages, page, ...] and one sequence's table -> its rows [length, ...]."""
-    page = pages.shape[1]
-    return np.stack([pages[table[j // page], j % page] for j in range(length)]) if length else \
-        np.zeros((0,) + pages.shape[2:], pages.dtype)

@@ -841,7 +841,8 @@ def check_long(q, k, v, times, L, out, lse, w, scale, dtype):
     adds = (L / 128 + 256) * 2.0 ** -24
     S.assert_close(S.f64(lse[:, 0]), z, es + 2.0 ** -19 * (1 + np.abs(z)) + adds, "lse")
     rp = 2 * es + 2.0 ** -18 * (1 + np.abs(z)) + 2 * adds
-    S.assert_close(S.f64(out[0]), (p * times) @ v, (2 * u + rp[:, None]) * ((p * times) @ np.abs(v)), "out")
+    S.assert_close(S.f64(out[0]), (p * times) @ v, (2 * u + rp[:, None]) * ((p * times) @ np.abs(v)) +
+                   L * S.TINY[dtype] * np.max(np.abs(v)), "out")
     if w is not None:
         want, bound = p.sum(0), (p * (rp[:, None] + G * 2.0 ** -24)).sum(0)
         rows = k.shape[0]
@@ -956,3 +957,54 @@ def test_rows_of_minus_infinity_give_no_weight(dtype):
         assert torch.all(out[r] == 0) and torch.all(lse[:, r] == float("-inf"))
         assert torch.equal(w[1].cpu(), w0[1])
         check_paged(c, chunks, ctx, out, lse, 64 ** -0.5, dtype, w0, w, skip=(1,))
+
+
+@pytest.mark.parametrize("L,G,D,page,room", [(40000, 8, 128, 16, True), (40000, 20, 64, 64, False),
+                                             (131071, 4, 128, 128, True), (131071, 1, 72, 16, False)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_one_long_context_over_every_sm(L, G, D, page, room, dtype):
+    """One token, one kv head, one sequence: an item cut into a piece for every CTA, more than the join looks at in
+    one go; the weights from the forward's scores (a cache with room) and formed again (a small one)."""
+    k, v, kp, vp, table, times = long_cache(L, page, D, dtype, 91)
+    if room:  # pages in no table
+        kp, vp = (torch.cat([x, x.new_full((-(-L // page), page, 1, D), float("nan"))]) for x in (kp, vp))
+    q = S.normal(np.random.default_rng(92), 1, G, D, dtype=dtype, sigma=1.5)
+    d = (q.cuda(), kp, vp, S.offsets([1]).cuda(), torch.tensor([L], dtype=torch.int32).cuda(), table)
+    w = torch.zeros(1, 1, L + 5, device="cuda")
+    need = [Q.evo_paged_fwd_workspace_bytes(1, 1, G, 1, D, kp.shape[0], page, table.shape[1], n) for n in (0, L + 5)]
+    assert (need[1] > need[0]) == room
+    out, lse = Q.evo_paged_fwd(*d, weights=w)
+    out2, lse2 = Q.evo_paged_fwd(*d)
+    assert E.evo_attn_device_status() == 0
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    check_long(S.f64(q[0]), k, v, times, L, out, lse, w[0, 0], D ** -0.5, dtype)
+
+
+def test_evict_more_pages_than_the_moves_hold():
+    """4375 pages of one sequence, places read and written beyond the first 4096 of them."""
+    ctx, budget, recent = [70000], 66000, 100
+    case = evict_case(ctx, 1, 8, 16, BF, seed=93)
+    d = [x.cuda() for x in case[:5]]
+    kept = Q.evo_cache_evict(*d, budget, recent)
+    assert E.evo_attn_device_status() == 0
+    check_evict(case, ctx, budget, recent, [d[0].cpu(), d[1].cpu(), d[3], d[4].cpu()], kept.cpu())
+
+
+def test_rejected_sequences_get_no_gradient():
+    """Rows of a sequence with a bad offset keep what the gradients held, the good one in front is as usual."""
+    q, k, v, do, _ = prompt_inputs([64], 2, 1, 64, BF)
+    d = [x.cuda() for x in (q, k, v, do)]
+    for cu, good in (([0, 40, 30], 40), ([-4, 64], 0), ([0, 65], 0), ([0, 20, 2000000000], 20)):
+        cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        out, lse = torch.full_like(d[0], 7.0), torch.full((2, 64), 7.0, device="cuda")
+        mine = torch.zeros(1, dtype=torch.int32, device="cuda")
+        Q.evo_prompt_fwd(*d[:3], cud, out=out, lse=lse, status=mine)
+        grads = [torch.full_like(x, 7.0) for x in d[:3]]
+        Q.evo_prompt_bwd(*d[:3], cud, out, lse, d[3], *grads, status=mine)
+        assert int(mine) == 13
+        for t in [out] + grads:
+            assert torch.all(t[good:] == 7), cu
+        if good:
+            r = slice(0, good)
+            S.check_gradients(S.f64(q[r]), S.f64(k[r]), S.f64(v[r]), S.f64(do[r]), [S.f64(x[r]) for x in grads], 64 ** -0.5, BF)
+    assert E.evo_attn_device_status() == 0
