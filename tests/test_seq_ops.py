@@ -929,9 +929,12 @@ def test_a_wait_that_runs_out():
         yield Q.evo_paged_fwd(q, kp, vp, cu, lens, table, weights=w, **kw)
 
     mine = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gave_up = []
     for _ in calls(1, mine):
-        assert int(mine) == 8
+        gave_up.append(int(mine))
         mine.zero_()
+    # (a wait looks at its limit between some hundred tries: the forward's search may end within them)
+    assert gave_up[1] == 8 and set(gave_up) <= {0, 8}, gave_up
     usual = list(calls(0, mine))
     assert int(mine) == 0 and E.evo_attn_device_status() == 0
     for b, (got, want) in enumerate(zip(usual, (ref, gref, ref))):
