@@ -65,6 +65,11 @@
  * sequence's last token, in its last page or in the next sequence, may be
  * anything, NaN and infinities included.
  *
+ * Products take their operands in dtype and sum in fp32: P and dS are rounded to
+ * dtype in between, and delta is formed from the rounded O.  With fp16 a dS beyond
+ * 65504 becomes infinite (and so do the gradients that it enters) and steps
+ * below 2^-24 are lost: dO should be scaled to stay within them.
+ *
  * Every sum is formed in a fixed order: a call repeated on the same device
  * gives the same bytes.  Calls are asynchronous on `stream`, take no memory of
  * their own and keep nothing; a workspace's contents need not be initialised,
@@ -119,7 +124,11 @@ typedef struct {
 } evo_seq_options_t;
 
 /* Bytes of device workspace (256-byte aligned) that the calls need; 0 on a bad
- * shape.  They depend on the shape and on the current device's number of SMs. */
+ * shape.  They depend on the shape and on the current device's number of SMs.
+ * With weights and few rows a key (tokens * group up to 16 * seqs) there is room in it
+ * for the scores, 4 bytes for every token, query head and place that the table (or
+ * weights_len, if that is less) can hold, as long as that is at most a quarter of the
+ * cache's bytes; beyond, the keys are read a second time instead. */
 EVO_API size_t evo_prompt_fwd_workspace_bytes(evo_seq_shape_t shape);
 EVO_API size_t evo_prompt_bwd_workspace_bytes(evo_seq_shape_t shape);
 EVO_API size_t evo_paged_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache_shape_t cache,
