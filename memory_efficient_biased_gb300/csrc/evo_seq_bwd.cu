@@ -58,7 +58,8 @@ struct Bars {
   uint64_t b_full[kBSlots], b_empty[kBSlots];        // streamed: dO or V
   uint64_t ready[kReady];                            // a pair of streamed tiles, cleaned
   uint64_t rows_full[2], rows_empty[2];              // dK/dV: (lse, delta) of a tile of queries
-  uint64_t s_full[2], dp_full, p_ready, dp_free, ds_ready;
+  uint64_t s_full[2], dp_full, p_ready, dp_free;
+  uint64_t ds_ready[2];                              // dQ: by turns; dK/dV: the first
   uint64_t second_done;                              // dS·(Q or K), and all before it, is done
   uint64_t acc_full, acc_free, drain;
   Work work[kDescs];
@@ -316,7 +317,7 @@ __device__ __forceinline__ void mma_dkv(const SeqBwdArgs& a, uint8_t* base, Bars
       }
       __syncwarp();
       if (j + 1 < j1 && !issue_s(n + 1)) { ok = false; break; }
-      if (!mbar_wait_warp_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
+      if (!mbar_wait_warp_inl(smem_u32(&bars->ds_ready[0]), n & 1, g)) { ok = false; break; }
       tc_fence_after();
       if (elect_one()) {
         gather<DP>(tmem + kColK, tmem + (n & 1) * 128 + 32, smem_u32(base + L::a + as * L::kTB), id_g, j > j0);
@@ -381,7 +382,10 @@ __device__ __forceinline__ void mma_dq(const SeqBwdArgs& a, uint8_t* base, Bars*
     for (int j = j0; j < j1; ++j, ++n) {
       const uint32_t as = n % kASlots;
       if (j + 1 < j1 && (!issue_s(n + 1) || !issue_dp(n + 1))) { ok = false; break; }
-      if (!mbar_wait_warp_inl(smem_u32(&bars->ds_ready), n & 1, g)) { ok = false; break; }
+      // Two barriers by turns: S and dP of tile n + 1 are on their way already, so that its dS may be
+      // complete before this warp has looked for dS of n, and a wait by parity would miss a phase
+      // that the next one has passed.  With two, the compute warps need S of n + 2 first, issued behind this.
+      if (!mbar_wait_warp_inl(smem_u32(&bars->ds_ready[n & 1]), (n >> 1) & 1, g)) { ok = false; break; }
       if (j == j0 && !mbar_wait_warp_inl(smem_u32(&bars->acc_free), (it & 1) ^ 1, g)) { ok = false; break; }
       tc_fence_after();
       if (elect_one()) {
@@ -566,7 +570,7 @@ __device__ __forceinline__ void compute_dkv(const SeqBwdArgs& a, const float* ro
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_u32(&bars->ds_ready));
+        mbar_arrive(smem_u32(&bars->ds_ready[0]));
         mbar_arrive(smem_u32(&bars->rows_empty[st]));
       }
     }
@@ -637,7 +641,7 @@ __device__ __forceinline__ void compute_dq(const SeqBwdArgs& a, Bars* bars, uint
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->ds_ready));
+      if (lane == 0) mbar_arrive(smem_u32(&bars->ds_ready[n & 1]));
     }
     if (!ok || !mbar_wait_warp_inl(smem_u32(&bars->acc_full), it & 1, g)) break;
     tc_fence_after();
@@ -670,10 +674,10 @@ __device__ __forceinline__ void init_bars(Bars* bars, bool dkv) {
     mbar_init(smem_u32(&bars->rows_full[i]), 1);
     mbar_init(smem_u32(&bars->rows_empty[i]), 8);
     mbar_init(smem_u32(&bars->s_full[i]), 1);
+    mbar_init(smem_u32(&bars->ds_ready[i]), 8);
   }
   mbar_init(smem_u32(&bars->dp_full), 1);
   mbar_init(smem_u32(&bars->p_ready), 8);
-  mbar_init(smem_u32(&bars->ds_ready), 8);
   mbar_init(smem_u32(&bars->dp_free), 8);
   mbar_init(smem_u32(&bars->second_done), 1);
   mbar_init(smem_u32(&bars->acc_full), 1);
