@@ -12,7 +12,12 @@
  *                      included) over that cache, and, where asked for, the sum
  *                      of the attention weight every cached key received;
  *   evo_cache_evict    the cache cut down, in place, to the keys that received
- *                      the most weight and the newest ones.
+ *                      the most weight and the newest ones;
+ *   evo_rotary         queries and keys turned by their positions, in front of
+ *                      either attention, and gradients turned back;
+ *   evo_cache8_append / evo_cache8_read / evo_paged8_fwd  a cache in 8 bits with a
+ *                      scale for each block of tokens and head: rows into it,
+ *                      rows out of it, and attention over it.
  *
  * What they compute.  Sequence b has n_b new tokens, the last of its L_b
  * tokens (for a prompt n_b = L_b).  Its new token i sits at position
@@ -185,6 +190,90 @@ EVO_API evo_status_t evo_cache_evict(void* k_pages, void* v_pages, const int32_t
                                      float* weights, int64_t weights_len, int32_t* kept, int64_t budget,
                                      int64_t recent, evo_seq_shape_t shape, evo_cache_shape_t cache,
                                      evo_dtype_t dtype, const evo_seq_options_t* opts, void* stream);
+
+/* ---------------------------------------------------------------- rotary positions
+ *
+ * Feature pair i < rotary_dim / 2 of every head of token t is turned by the angle
+ * a = positions[t] * inv_freq[i] and multiplied by `factor`:
+ *
+ *     y1 = factor (x1 cos a - x2 sin a)      y2 = factor (x2 cos a + x1 sin a)
+ *
+ * Pair i is the features (i, i + rotary_dim / 2), with EVO_ROTARY_INTERLEAVED
+ * (2i, 2i + 1); features from rotary_dim on pass unchanged.  EVO_ROTARY_INVERSE turns
+ * by -a: with it the call takes the gradients of its outputs to those of its inputs.
+ * Contexts longer than trained on are a matter of inv_freq and factor.  Angles are
+ * formed modulo a turn in 64-bit integers: position and frequency lose nothing up
+ * to positions of 2^31 (an error of 2^-52 turns a position).  fp32 arithmetic, rounded once. */
+#define EVO_ROTARY_INTERLEAVED 1u
+#define EVO_ROTARY_INVERSE 2u
+typedef struct {
+  int64_t rotary_dim;   /* even, 2 .. head_dim                                */
+  uint32_t flags;
+  float factor;         /* finite; 0 = 1                                      */
+  int64_t q_out, k_out; /* token strides of the outputs, as evo_seq_strides_t */
+} evo_rotary_t;
+
+/* q [tokens, q_heads, head_dim] and k [tokens, kv_heads, head_dim] (k and k_out may
+ * be NULL: q alone) into q_out and k_out.  An output may be its own input, with the same
+ * stride, and overlaps no other tensor of the call.  positions [tokens] int32, of either sign;
+ * inv_freq [rotary_dim / 2] float64, finite.  q_heads 1 to 65535, kv_heads up to 16384, neither a
+ * multiple of the other; shape.seqs is not used, of the strides q and k are. */
+EVO_API evo_status_t evo_rotary(const void* q, const void* k, const int32_t* positions, const double* inv_freq,
+                                void* q_out, void* k_out, evo_seq_shape_t shape, const evo_rotary_t* rotary,
+                                evo_dtype_t dtype, const evo_seq_strides_t* strides, void* stream);
+
+/* ---------------------------------------------------------------- a cache in 8 bits
+ *
+ *     k_pages, v_pages    [num_pages, page_size, kv_heads, head_dim]  e4m3 (1 + 4 + 3 bits,
+ *         bias 7, no infinities, 0x7f and 0xff are NaN)
+ *     k_scales, v_scales  [num_pages, kv_heads, page_size / scale_block] float32: a code
+ *         stands for code * scale of its block of scale_block tokens and head
+ *
+ * head_dim is a multiple of 16, scale_block 16, 32, 64 or 128 and divides page_size;
+ * everything else (tables, lengths, offsets, what is checked on the device) is as for
+ * the 16-bit cache.
+ *
+ * Appending: a block's scale is the least power of two s, 2^-64 at the least, with |x| <= 448 s
+ * for the block's new values x, and not below the scale that tokens from before left the
+ * block with.  Where it grows, their codes are rescaled: exactly, but for what falls
+ * below the smallest code, 2^-9 of the new scale.  A code is x (1 / s) rounded to nearest even.  A value
+ * that is not finite is stored as NaN and does not enter the scale.  Where a block's first
+ * token is new, what its scale held before does not matter.
+ *
+ * Scales that others wrote may be any positive finite number.  Reading rounds code * scale to
+ * dtype (for scales that are powers of two exact within its range) and saturates at its largest
+ * finite number.  Attention takes code * scale as it is. */
+typedef struct {
+  int64_t num_pages, page_size, pages_per_seq;
+  int64_t scale_block;
+  int64_t k_page_stride, v_page_stride; /* in elements: multiples of 16, at least a page, below 2^36; 0 = packed */
+} evo_cache8_shape_t;
+
+/* As evo_cache_append; k and v are in dtype.  No two sequences of a call may write
+ * into the same block. */
+EVO_API evo_status_t evo_cache8_append(const void* k, const void* v, const int32_t* cu_seqlens,
+                                       const int32_t* seq_lens, const int32_t* block_table, void* k_pages,
+                                       void* v_pages, float* k_scales, float* v_scales, evo_seq_shape_t shape,
+                                       evo_cache8_shape_t cache, evo_dtype_t dtype, const evo_seq_strides_t* strides,
+                                       const evo_seq_options_t* opts, void* stream);
+
+/* The last tokens of every sequence out of the cache: the rows cu_seqlens[b] ..
+ * cu_seqlens[b+1] - 1 of k and v become the last of sequence b's seq_lens[b] tokens, as the
+ * rows of an append would be.  A row at a negative position or on a bad page becomes zeros. */
+EVO_API evo_status_t evo_cache8_read(const void* k_pages, const void* v_pages, const float* k_scales,
+                                     const float* v_scales, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                     const int32_t* block_table, void* k, void* v, evo_seq_shape_t shape,
+                                     evo_cache8_shape_t cache, evo_dtype_t dtype, const evo_seq_strides_t* strides,
+                                     const evo_seq_options_t* opts, void* stream);
+
+/* As evo_paged_fwd without weights; q and out are in dtype. */
+EVO_API size_t evo_paged8_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache8_shape_t cache);
+EVO_API evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                    const float* v_scales, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                    const int32_t* block_table, void* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, evo_seq_shape_t shape, evo_cache8_shape_t cache,
+                                    evo_dtype_t dtype, const evo_seq_strides_t* strides,
+                                    const evo_seq_options_t* opts, void* stream);
 
 #ifdef __cplusplus
 }

@@ -118,3 +118,29 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     being captured: PyTorch ties the accumulation of a leaf's gradient to the stream on which
     the leaf was first used, and a capture that meets another stream's work ends with an error."""
     return PromptAttentionFunction.apply(q, k, v, cu_seqlens, scale)
+
+
+class RotaryFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, interleaved, factor):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.how = {"interleaved": interleaved, "factor": factor}
+        q, k = Q.evo_rotary(_packed_rows(q), None if k is None else _packed_rows(k), positions, inv_freq, **ctx.how)
+        return q, k
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk):
+        positions, inv_freq = ctx.saved_tensors
+        # (autograd gives zeros for an output that nothing used)
+        dq, dk = Q.evo_rotary(_packed_rows(dq), None if dk is None else _packed_rows(dk), positions, inv_freq,
+                              inverse=True, **ctx.how)
+        return dq, dk, None, None, None, None
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor, *,
+           interleaved: bool = False, factor: float = 1.0):
+    """Rotary positions, differentiable: q [T, Hq, D] and k [T, Hk, D] (or None) turned by positions [T] int32
+    times inv_freq [rotary_dim / 2] float64 (``evo_seq.rotary_frequencies``); (q, k), as
+    ``prompt_attention`` takes them.  Strided token rows are read in place."""
+    return RotaryFunction.apply(q, k, positions, inv_freq, interleaved, factor)

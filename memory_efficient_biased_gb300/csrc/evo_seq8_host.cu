@@ -1,0 +1,177 @@
+// evo_seq8_host.cu — the C ABI of the 8-bit cache (include/evo_seq.h): argument validation,
+// workspace sizes and dispatch to the kernels.
+#include "evo_seq8_internal.h"
+#include "evo_seq_check.h"
+
+namespace evo {
+namespace {
+
+// The cache's pages as bytes, its scales, and the same as the 16-bit cache's shape (for desc).
+struct Checked {
+  int64_t k_page, v_page, scales;  // strides of the pages; scales of each of k and v
+  evo_cache_shape_t as16;
+};
+evo_status_t check_cache8(const evo_cache8_shape_t& c, const evo_seq_shape_t& s, Checked* o) {
+  const bool block_ok = c.scale_block == 16 || c.scale_block == 32 || c.scale_block == 64 || c.scale_block == 128;
+  if (s.head_dim % 16 || !page_size_ok(c.page_size) || !block_ok || c.page_size % c.scale_block || c.num_pages < 1 ||
+      c.num_pages > (int64_t(1) << 31) - 2 || c.pages_per_seq < 1 || c.pages_per_seq > (int64_t(1) << 31) - 1)
+    return EVO_ERR_BAD_SHAPE;
+  const int64_t packed = c.page_size * s.kv_heads * s.head_dim;
+  o->k_page = c.k_page_stride ? c.k_page_stride : packed;
+  o->v_page = c.v_page_stride ? c.v_page_stride : packed;
+  for (int64_t p : {o->k_page, o->v_page})
+    if (p < packed || p % 16 || p >= kMaxStride) return EVO_ERR_BAD_LAYOUT;
+  o->scales = c.num_pages * s.kv_heads * (c.page_size / c.scale_block);
+  o->as16 = evo_cache_shape_t{c.num_pages, c.page_size, c.pages_per_seq, 0, 0};
+  return EVO_OK;
+}
+
+Span pages8(const void* p, const evo_cache8_shape_t& c, const evo_seq_shape_t& s, int64_t stride) {
+  const int64_t piece = c.page_size * s.kv_heads * s.head_dim;
+  return {p, size_t(c.num_pages - 1) * size_t(stride) + size_t(piece), stride, piece};
+}
+
+Cache8 cache_of(const void* k_pages, const void* v_pages, const float* k_scales, const float* v_scales,
+                const evo_cache8_shape_t& c, const Checked& k) {
+  Cache8 o{};
+  o.k_pages = static_cast<uint8_t*>(const_cast<void*>(k_pages));
+  o.v_pages = static_cast<uint8_t*>(const_cast<void*>(v_pages));
+  o.k_scales = const_cast<float*>(k_scales);
+  o.v_scales = const_cast<float*>(v_scales);
+  o.k_page = k.k_page, o.v_page = k.v_page;
+  o.block = static_cast<int>(c.scale_block);
+  o.blocks = static_cast<int>(c.page_size / c.scale_block);
+  return o;
+}
+
+// What an append and a read check alike.
+evo_status_t rows_call(bool append, const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                       const int32_t* block_table, const void* k_pages, const void* v_pages, const float* k_scales,
+                       const float* v_scales, evo_seq_shape_t shape, const evo_cache8_shape_t& cache, evo_dtype_t dtype,
+                       const evo_seq_strides_t* strides, const evo_seq_options_t* opts, void* stream) {
+  Opts o;
+  if (!read_opts(opts, &o)) return EVO_ERR_BAD_ARGUMENT;
+  if (dtype != EVO_F16 && dtype != EVO_BF16) return EVO_ERR_BAD_DTYPE;
+  evo_status_t st = check_seq_shape(shape, false);
+  if (st != EVO_OK) return st;
+  shape.q_heads = shape.kv_heads;
+  Strides t;
+  Checked c;
+  if ((st = check_cache8(cache, shape, &c)) != EVO_OK) return st;
+  evo_seq_strides_t only{};
+  if (strides) only.k = strides->k, only.v = strides->v;
+  if (!read_strides(&only, shape, &t)) return EVO_ERR_BAD_LAYOUT;
+  if (shape.tokens == 0 || shape.seqs == 0) return EVO_OK;
+  if (!k || !v || !cu_seqlens || !seq_lens || !block_table || !k_pages || !v_pages || !k_scales || !v_scales)
+    return EVO_ERR_NULL_POINTER;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(cu_seqlens, 4) ||
+      !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(k_scales, 4) || !aligned(v_scales, 4) ||
+      !aligned(o.status, 4))
+    return EVO_ERR_MISALIGNED;
+  const int64_t nk = shape.kv_heads * shape.head_dim;
+  const Span plan[] = {flat(cu_seqlens, size_t(shape.seqs + 1) * 4), flat(seq_lens, size_t(shape.seqs) * 4),
+                       flat(block_table, size_t(shape.seqs) * size_t(cache.pages_per_seq) * 4)};
+  const Span rows[] = {strided(k, shape.tokens, t.k, nk), strided(v, shape.tokens, t.v, nk)};
+  const Span held[] = {pages8(k_pages, cache, shape, c.k_page), pages8(v_pages, cache, shape, c.v_page),
+                       flat(k_scales, size_t(c.scales) * 4), flat(v_scales, size_t(c.scales) * 4)};
+  // what is written overlaps neither what is read nor itself
+  if (append ? aliased(plan, held) || aliased(rows, held) : aliased(plan, rows) || aliased(held, rows)) return EVO_ERR_ALIASING;
+  int sms = 0;
+  int* fallback = nullptr;
+  if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
+  Cache8Args a{};
+  a.s = desc(shape, cu_seqlens, seq_lens, block_table, &c.as16, -1, o.status ? o.status : fallback);
+  a.c = cache_of(k_pages, v_pages, k_scales, v_scales, cache, c);
+  a.k = static_cast<uint16_t*>(const_cast<void*>(k));
+  a.v = static_cast<uint16_t*>(const_cast<void*>(v));
+  a.k_stride = t.k, a.v_stride = t.v;
+  const bool bf16 = dtype == EVO_BF16;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = append ? launch_cache8_append(a, bf16, cs) : launch_cache8_read(a, bf16, cs);
+  return e == cudaSuccess ? EVO_OK : cuda_fail(append ? "8-bit cache append launch" : "8-bit cache read launch", e);
+}
+
+}  // namespace
+}  // namespace evo
+
+using namespace evo;
+
+extern "C" {
+
+evo_status_t evo_cache8_append(const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                               const int32_t* block_table, void* k_pages, void* v_pages, float* k_scales,
+                               float* v_scales, evo_seq_shape_t shape, evo_cache8_shape_t cache, evo_dtype_t dtype,
+                               const evo_seq_strides_t* strides, const evo_seq_options_t* opts, void* stream) {
+  return rows_call(true, k, v, cu_seqlens, seq_lens, block_table, k_pages, v_pages, k_scales, v_scales, shape, cache,
+                   dtype, strides, opts, stream);
+}
+
+evo_status_t evo_cache8_read(const void* k_pages, const void* v_pages, const float* k_scales, const float* v_scales,
+                             const int32_t* cu_seqlens, const int32_t* seq_lens, const int32_t* block_table, void* k,
+                             void* v, evo_seq_shape_t shape, evo_cache8_shape_t cache, evo_dtype_t dtype,
+                             const evo_seq_strides_t* strides, const evo_seq_options_t* opts, void* stream) {
+  return rows_call(false, k, v, cu_seqlens, seq_lens, block_table, k_pages, v_pages, k_scales, v_scales, shape, cache,
+                   dtype, strides, opts, stream);
+}
+
+size_t evo_paged8_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache8_shape_t cache) {
+  Checked c;
+  if (check_seq_shape(shape, true) != EVO_OK || check_cache8(cache, shape, &c) != EVO_OK) return 0;
+  return seq_fwd_workspace(fwd_ctas(num_sms(), shape, cache.page_size * cache.pages_per_seq),
+                           static_cast<int>(shape.head_dim), nullptr, nullptr);
+}
+
+evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                            const float* v_scales, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                            const int32_t* block_table, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            evo_seq_shape_t shape, evo_cache8_shape_t cache, evo_dtype_t dtype,
+                            const evo_seq_strides_t* strides, const evo_seq_options_t* opts, void* stream) {
+  Opts o;
+  if (!read_opts(opts, &o)) return EVO_ERR_BAD_ARGUMENT;
+  if (dtype != EVO_F16 && dtype != EVO_BF16) return EVO_ERR_BAD_DTYPE;
+  evo_status_t st = check_seq_shape(shape, true);
+  if (st != EVO_OK) return st;
+  Checked c;
+  if ((st = check_cache8(cache, shape, &c)) != EVO_OK) return st;
+  evo_seq_strides_t only{};
+  if (strides) only.q = strides->q, only.out = strides->out;
+  Strides t;
+  if (!read_strides(&only, shape, &t)) return EVO_ERR_BAD_LAYOUT;
+  if (shape.tokens == 0 || shape.seqs == 0) return EVO_OK;
+  if (!q || !k_pages || !v_pages || !k_scales || !v_scales || !cu_seqlens || !seq_lens || !block_table || !out || !lse ||
+      !workspace)
+    return EVO_ERR_NULL_POINTER;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) || !aligned(k_scales, 4) ||
+      !aligned(v_scales, 4) || !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4) ||
+      !aligned(lse, 4) || !aligned(workspace, 256) || !aligned(o.status, 4))
+    return EVO_ERR_MISALIGNED;
+  if (workspace_bytes < evo_paged8_fwd_workspace_bytes(shape, cache)) return EVO_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t T = shape.tokens, nq = shape.q_heads * shape.head_dim;
+  const Span in[] = {strided(q, T, t.q, nq),
+                     pages8(k_pages, cache, shape, c.k_page),
+                     pages8(v_pages, cache, shape, c.v_page),
+                     flat(k_scales, size_t(c.scales) * 4),
+                     flat(v_scales, size_t(c.scales) * 4),
+                     flat(cu_seqlens, size_t(shape.seqs + 1) * 4),
+                     flat(seq_lens, size_t(shape.seqs) * 4),
+                     flat(block_table, size_t(shape.seqs) * size_t(cache.pages_per_seq) * 4)};
+  const Span outs[] = {strided(out, T, t.out, nq), flat(lse, size_t(T) * shape.q_heads * 4),
+                       flat(workspace, workspace_bytes)};
+  if (aliased(in, outs)) return EVO_ERR_ALIASING;
+  int sms = 0;
+  int* fallback = nullptr;
+  if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
+  Seq8FwdArgs a{};
+  a.s = desc(shape, cu_seqlens, seq_lens, block_table, &c.as16, -1, o.status ? o.status : fallback);
+  a.c = cache_of(k_pages, v_pages, k_scales, v_scales, cache, c);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = t.q;
+  a.out = static_cast<uint16_t*>(out);
+  a.out_stride = t.out;
+  a.lse = lse;
+  a.scale_log2 = scale_of(o, shape) * kSeqLog2e;
+  const cudaError_t e = launch_paged8_fwd(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EVO_OK : cuda_fail("8-bit cache attention launch", e);
+}
+
+}  // extern "C"

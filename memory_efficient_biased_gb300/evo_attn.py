@@ -40,7 +40,8 @@ EXPORTED = ("evo_attn_abi_version", "evo_status_string", "evo_attn_fwd", "evo_at
             "evo_attn_bwd_opts", "evo_attn_bwd_status",
             # include/evo_seq.h, bound in evo_seq.py
             "evo_prompt_fwd_workspace_bytes", "evo_prompt_bwd_workspace_bytes", "evo_paged_fwd_workspace_bytes",
-            "evo_prompt_fwd", "evo_prompt_bwd", "evo_cache_append", "evo_paged_fwd", "evo_cache_evict")
+            "evo_prompt_fwd", "evo_prompt_bwd", "evo_cache_append", "evo_paged_fwd", "evo_cache_evict", "evo_rotary",
+            "evo_cache8_append", "evo_cache8_read", "evo_paged8_fwd_workspace_bytes", "evo_paged8_fwd")
 OPT_SKIP_MASKED_TILES, OPT_NO_DBIAS2 = 1, 2  # evo_options_t flags
 
 _DTYPE_CODE = {torch.float16: 0, torch.bfloat16: 1}

@@ -4,7 +4,11 @@ marshalling only, like ``evo_attn``.
 ``evo_prompt_fwd`` / ``evo_prompt_bwd``: attention over packed prompts and its
 gradients (differentiable as ``autograd.prompt_attention``);
 ``evo_cache_append`` / ``evo_paged_fwd`` / ``evo_cache_evict``: a paged cache, the
-attention of new tokens over it, and its eviction by accumulated attention weight.
+attention of new tokens over it, and its eviction by accumulated attention weight;
+``evo_rotary``: rotary positions of queries and keys, and of their gradients
+(differentiable as ``autograd.rotary``), with ``rotary_frequencies`` for long contexts;
+``evo_cache8_append`` / ``evo_cache8_read`` / ``evo_paged8_fwd``: a cache in 8 bits with a
+scale for each block of tokens and head.
 The header states what each computes, its layouts and its limits.
 
 Tensors live on the current CUDA device.  With ``stream`` the call, and what it
@@ -18,6 +22,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 from typing import Optional
 
 import torch
@@ -39,6 +44,19 @@ class SeqStrides(ctypes.Structure):
 class CacheShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("num_pages", "page_size", "pages_per_seq", "k_page_stride",
                                                "v_page_stride")]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int64), ("flags", ctypes.c_uint32), ("factor", ctypes.c_float),
+                ("q_out", ctypes.c_int64), ("k_out", ctypes.c_int64)]
+
+
+ROTARY_INTERLEAVED, ROTARY_INVERSE = 1, 2  # evo_rotary_t flags
+
+
+class Cache8Shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("num_pages", "page_size", "pages_per_seq", "scale_block",
+                                               "k_page_stride", "v_page_stride")]
 
 
 class SeqOptions(ctypes.Structure):
@@ -66,7 +84,12 @@ def load():
             ("evo_prompt_bwd", i32, [vp] * 11 + [sz, SeqShape] + tail),
             ("evo_cache_append", i32, [vp] * 7 + [SeqShape, CacheShape] + tail),
             ("evo_paged_fwd", i32, [vp] * 9 + [i64, vp, sz, SeqShape, CacheShape] + tail),
-            ("evo_cache_evict", i32, [vp] * 5 + [i64, vp, i64, i64, SeqShape, CacheShape, i32, opts, vp])):
+            ("evo_cache_evict", i32, [vp] * 5 + [i64, vp, i64, i64, SeqShape, CacheShape, i32, opts, vp]),
+            ("evo_rotary", i32, [vp] * 6 + [SeqShape, ctypes.POINTER(Rotary), i32, strides, vp]),
+            ("evo_cache8_append", i32, [vp] * 9 + [SeqShape, Cache8Shape] + tail),
+            ("evo_cache8_read", i32, [vp] * 9 + [SeqShape, Cache8Shape] + tail),
+            ("evo_paged8_fwd_workspace_bytes", sz, [SeqShape, Cache8Shape]),
+            ("evo_paged8_fwd", i32, [vp] * 11 + [sz, SeqShape, Cache8Shape] + tail)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
     _bound = lib
@@ -165,8 +188,8 @@ def _pages(k_pages):
     return k_pages.shape
 
 
-def _page_stride(t, name: str, shape, dtype, dev: int) -> int:
-    """Checks the pages of one cache; their stride (0 = packed)."""
+def _page_stride(t, name: str, shape, dtype, dev: int, step: int = 8) -> int:
+    """Checks the pages of one cache; their stride (0 = packed), a multiple of ``step``."""
     if (isinstance(t, _Tensor) and t.get_device() == dev and t.dtype == dtype and t.is_contiguous()
             and t.shape == shape):
         return 0
@@ -178,21 +201,26 @@ def _page_stride(t, name: str, shape, dtype, dev: int) -> int:
     if t.shape[0] <= 1 or t.is_contiguous():
         return 0
     stride, packed = t.stride(0), t.shape[1] * t.shape[2] * t.shape[3]
-    if stride < packed or stride % 8:  # (0, an expanded page, would read as packed)
-        raise ValueError(f"{name} has page stride {stride}: at least {packed} and a multiple of 8 is needed")
+    if stride < packed or stride % step:  # (0, an expanded page, would read as packed)
+        raise ValueError(f"{name} has page stride {stride}: at least {packed} and a multiple of {step} is needed")
     return stride
 
 
 def _cache(k_pages, v_pages, block_table, seqs, dtype, dev: int) -> CacheShape:
     shape = k_pages.shape
     sk, sv = _page_stride(k_pages, "k_pages", shape, dtype, dev), _page_stride(v_pages, "v_pages", shape, dtype, dev)
+    return CacheShape(shape[0], shape[1], _columns(block_table, seqs, dev), sk, sv)
+
+
+def _columns(block_table, seqs, dev: int) -> int:
+    """Checks the table; pages a sequence."""
     if not isinstance(block_table, _Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor [seqs, pages_per_seq]")
     _flat(block_table, "block_table", None, torch.int32, dev)
     rows, columns = block_table.shape
     if seqs is not None and rows != seqs:
         raise ValueError(f"block_table has {rows} rows, expected {seqs}")
-    return CacheShape(shape[0], shape[1], columns, sk, sv)
+    return columns
 
 
 def _device_and_stream(t, stream):
@@ -399,3 +427,188 @@ def evo_cache_evict(k_pages, v_pages, block_table, seq_lens, weights, budget: in
                                  weights.data_ptr(), n, kept.data_ptr(), budget, recent, SeqShape(0, B, Hk, Hk, D),
                                  cache, _DTYPE_CODE[dt], _options(None, 0, status, dev), sp), "evo_cache_evict")
     return kept
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none", stretch: float = 1.0,
+                       trained: Optional[int] = None, fast: float = 32.0, slow: float = 1.0, device=None):
+    """(inv_freq [rotary_dim / 2] float64, factor) for ``evo_rotary``: pair i turns by
+    base^(-2i / rotary_dim) a position.  For contexts ``stretch`` times as long as trained on, ``scaling``
+        "linear"  divides every frequency by stretch (positions interpolated);
+        "base"    raises the base to base · stretch^(R / (R - 2)): the slowest pair turns
+                  stretch times more slowly, the fastest as before;
+        "parts"   divides by stretch the pairs that turn fewer than ``slow`` times within the ``trained`` tokens,
+                  leaves those that turn more than ``fast`` times, goes over linearly in between,
+                  and returns the factor 0.1 ln(stretch) + 1 (otherwise 1)."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError(f"rotary_dim must be even and positive, got {rotary_dim}")
+    if not (base > 0 and stretch > 0 and math.isfinite(base) and math.isfinite(stretch)):
+        raise ValueError(f"base and stretch must be positive and finite, got {base} and {stretch}")
+    if scaling not in ("none", "linear", "base", "parts"):
+        raise ValueError(f"scaling must be none, linear, base or parts, got {scaling!r}")
+    if scaling == "base" and rotary_dim > 2:
+        base = base * stretch ** (rotary_dim / (rotary_dim - 2))
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    f = base ** (-2.0 * i / rotary_dim)
+    if scaling == "linear":
+        return f / stretch, 1.0
+    if scaling != "parts":
+        return f, 1.0
+    if trained is None or trained < 1 or not fast > slow:
+        raise ValueError(f"scaling by parts needs trained >= 1 and fast > slow, got {trained}, {fast} and {slow}")
+    keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+    return f * keep + f / stretch * (1.0 - keep), 0.1 * math.log(stretch) + 1.0
+
+
+def evo_rotary(q, k, positions, inv_freq, q_out=None, k_out=None, stream=None, *, interleaved: bool = False,
+               inverse: bool = False, factor: float = 1.0):
+    """q [T,Hq,D] and k [T,Hk,D] (or None) turned by positions [T] int32 times inv_freq
+    [rotary_dim / 2] float64; (q_out, k_out).  An output may be its own input.  ``inverse`` turns back: the
+    gradients of the outputs become those of the inputs."""
+    if not isinstance(q, _Tensor) or q.dim() != 3 or q.dtype not in _DTYPE_CODE:
+        raise ValueError("q must be a float16 or bfloat16 tensor [tokens, heads, head_dim]")
+    T, Hq, D = rows = q.shape
+    dev, sp = _device_and_stream(q, stream)
+    dt, sq, Hk, sk, keys = q.dtype, _rows(q, "q", rows, q.dtype, dev), 0, 0, None
+    if k is not None:
+        if not isinstance(k, _Tensor) or k.dim() != 3 or k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"k must be a tensor [{T}, heads, {D}]")
+        keys, Hk = k.shape, k.shape[1]
+        sk = _rows(k, "k", keys, dt, dev)
+    elif k_out is not None:
+        raise ValueError("k_out is given without k")
+    _flat(positions, "positions", (T,), torch.int32, dev)
+    if not isinstance(inv_freq, _Tensor) or inv_freq.dim() != 1 or not 1 <= inv_freq.shape[0] <= D // 2:
+        raise ValueError(f"inv_freq must be a tensor of 1 to {D // 2} frequencies")
+    _flat(inv_freq, "inv_freq", None, torch.float64, dev)
+    if not math.isfinite(ctypes.c_float(factor).value) or ctypes.c_float(factor).value == 0.0:
+        raise ValueError(f"factor must be finite and not 0, got {factor}")
+    so, to = 0, 0
+    with _on(stream):
+        if q_out is None:
+            q_out = torch.empty(rows, dtype=dt, device=q.device)
+        else:
+            so = _rows(q_out, "q_out", rows, dt, dev)
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(keys, dtype=dt, device=q.device)
+            else:
+                to = _rows(k_out, "k_out", keys, dt, dev)
+    flags = (ROTARY_INTERLEAVED if interleaved else 0) | (ROTARY_INVERSE if inverse else 0)
+    strides = SeqStrides(sq, sk) if sq or sk else None
+    _done((_bound or load()).evo_rotary(q.data_ptr(), _p(k), positions.data_ptr(), inv_freq.data_ptr(), q_out.data_ptr(),
+                                        _p(k_out), SeqShape(T, 0, Hq, Hk, D),
+                                        Rotary(2 * inv_freq.shape[0], flags, factor, so, to), _DTYPE_CODE[dt], strides, sp),
+          "evo_rotary")
+    return q_out, k_out
+
+
+def _pages8(k_pages):
+    if not isinstance(k_pages, _Tensor) or k_pages.dim() != 4 or k_pages.dtype != torch.float8_e4m3fn:
+        raise ValueError("k_pages must be a float8_e4m3fn tensor [num_pages, page_size, kv_heads, head_dim]")
+    return k_pages.shape
+
+
+def _cache8(k_pages, v_pages, k_scales, v_scales, block_table, seqs, dev: int) -> Cache8Shape:
+    shape, dt = k_pages.shape, k_pages.dtype
+    P, page, Hk, _ = shape
+    sk = _page_stride(k_pages, "k_pages", shape, dt, dev, 16)
+    sv = _page_stride(v_pages, "v_pages", shape, dt, dev, 16)
+    n = k_scales.shape[2] if isinstance(k_scales, _Tensor) and k_scales.dim() == 3 else 0
+    if n < 1 or page % n:
+        raise ValueError("k_scales must be a tensor [num_pages, kv_heads, page_size / scale_block]")
+    _flat(k_scales, "k_scales", (P, Hk, n), torch.float32, dev)
+    _flat(v_scales, "v_scales", (P, Hk, n), torch.float32, dev)
+    return Cache8Shape(P, page, _columns(block_table, seqs, dev), page // n, sk, sv)
+
+
+def evo_cache8_append(k, v, cu_seqlens, seq_lens, k_pages, v_pages, k_scales, v_scales, block_table, stream=None, *,
+                      status: Optional[torch.Tensor] = None):
+    """``evo_cache_append`` into a cache in 8 bits: pages float8_e4m3fn
+    [num_pages, page_size, Hkv, D], scales float32 [num_pages, Hkv, page_size / scale_block]."""
+    if not isinstance(k, _Tensor) or k.dim() != 3 or k.dtype not in _DTYPE_CODE:
+        raise ValueError("k must be a float16 or bfloat16 tensor [tokens, heads, head_dim]")
+    dev, sp = _device_and_stream(k, stream)
+    T, Hk, D = keys = k.shape
+    dt, B = k.dtype, _offsets(cu_seqlens, dev)
+    if tuple(_pages8(k_pages)[2:]) != (Hk, D):
+        raise ValueError(f"k has {Hk} heads of {D}, the cache {tuple(k_pages.shape[2:])}")
+    cache = _cache8(k_pages, v_pages, k_scales, v_scales, block_table, B, dev)
+    _flat(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    sk, sv = _rows(k, "k", keys, dt, dev), _rows(v, "v", keys, dt, dev)
+    strides = SeqStrides(0, sk, sv) if sk or sv else None
+    _done((_bound or load()).evo_cache8_append(
+        k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+        k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), SeqShape(T, B, Hk, Hk, D),
+        cache, _DTYPE_CODE[dt], strides, _options(None, 0, status, dev), sp), "evo_cache8_append")
+
+
+def evo_cache8_read(k_pages, v_pages, k_scales, v_scales, cu_seqlens, seq_lens, block_table, tokens: int,
+                    dtype: torch.dtype = torch.bfloat16, k=None, v=None, stream=None, *,
+                    status: Optional[torch.Tensor] = None):
+    """The last tokens of every sequence out of a cache in 8 bits, as rows (k, v) [tokens,Hkv,D] of
+    ``dtype``: rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 are the last of sequence b's seq_lens[b].
+    Rows in no sequence keep what k and v held (new ones are uninitialised there)."""
+    _, _, Hk, D = _pages8(k_pages)
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"dtype must be float16 or bfloat16, got {dtype}")
+    dev, sp = _device_and_stream(k_pages, stream)
+    B, T = _offsets(cu_seqlens, dev), int(tokens)
+    if T < 0:
+        raise ValueError(f"tokens must not be negative, got {tokens}")
+    cache = _cache8(k_pages, v_pages, k_scales, v_scales, block_table, B, dev)
+    _flat(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    sk, sv, keys = 0, 0, (T, Hk, D)
+    with _on(stream):
+        if k is None:
+            k = torch.empty(keys, dtype=dtype, device=k_pages.device)
+        else:
+            sk = _rows(k, "k", keys, dtype, dev)
+        if v is None:
+            v = torch.empty(keys, dtype=dtype, device=k_pages.device)
+        else:
+            sv = _rows(v, "v", keys, dtype, dev)
+    strides = SeqStrides(0, sk, sv) if sk or sv else None
+    _done((_bound or load()).evo_cache8_read(
+        k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), cu_seqlens.data_ptr(),
+        seq_lens.data_ptr(), block_table.data_ptr(), k.data_ptr(), v.data_ptr(), SeqShape(T, B, Hk, Hk, D), cache,
+        _DTYPE_CODE[dtype], strides, _options(None, 0, status, dev), sp), "evo_cache8_read")
+    return k, v
+
+
+def evo_paged8_fwd_workspace_bytes(tokens, seqs, q_heads, kv_heads, head_dim, num_pages, page_size, pages_per_seq,
+                                   scale_block) -> int:
+    return int(load().evo_paged8_fwd_workspace_bytes(SeqShape(tokens, seqs, q_heads, kv_heads, head_dim),
+                                                     Cache8Shape(num_pages, page_size, pages_per_seq, scale_block, 0, 0)))
+
+
+def evo_paged8_fwd(q, k_pages, v_pages, k_scales, v_scales, cu_seqlens, seq_lens, block_table, out=None, lse=None,
+                   workspace=None, stream=None, *, scale: Optional[float] = None, wait_limit_ns: int = 0,
+                   status: Optional[torch.Tensor] = None):
+    """Attention of the new tokens q [T,Hq,D] over a cache in 8 bits that already holds them;
+    (out, lse [Hq,T] fp32)."""
+    _, _, Hk, d = _pages8(k_pages)
+    T, Hq, D = _queries(q, Hk, d, "the cache")
+    dev, sp = _device_and_stream(q, stream)
+    dt, rows = q.dtype, q.shape
+    B = _offsets(cu_seqlens, dev)
+    cache = _cache8(k_pages, v_pages, k_scales, v_scales, block_table, B, dev)
+    _flat(seq_lens, "seq_lens", (B,), torch.int32, dev)
+    sq, so = _rows(q, "q", rows, dt, dev), 0
+    opts = None if scale is status is None and not wait_limit_ns else _options(scale, wait_limit_ns, status, dev)
+    shape, lib = SeqShape(T, B, Hq, Hk, D), _bound or load()
+    with _on(stream):
+        if out is None:
+            out = torch.empty(rows, dtype=dt, device=q.device)
+        else:
+            so = _rows(out, "out", rows, dt, dev)
+        if lse is None:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        else:
+            _flat(lse, "lse", (Hq, T), torch.float32, dev)
+        ws, size = _workspace(workspace, lib.evo_paged8_fwd_workspace_bytes(shape, cache), q, dev)
+    strides = SeqStrides(sq, 0, 0, so) if sq or so else None
+    _done(lib.evo_paged8_fwd(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                             v_scales.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+                             out.data_ptr(), lse.data_ptr(), ws.data_ptr(), size, shape, cache, _DTYPE_CODE[dt],
+                             strides, opts, sp), "evo_paged8_fwd")
+    return out, lse

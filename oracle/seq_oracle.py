@@ -71,3 +71,54 @@ def choose(weights, length, budget, recent):
     # larger weights first, a NaN behind every number, the older of two equal ones first
     order = sorted(old, key=lambda j: (-value[j][0], value[j][1], j))
     return sorted(order[:budget - recent]) + list(range(length - recent, length))
+
+
+def rotate(x, positions, inv_freq, interleaved=False, factor=1.0, inverse=False):
+    """x [T, H, D], positions [T], inv_freq [R/2]: every feature pair as a complex number, times
+    factor·exp(±i angle); features from R on unchanged."""
+    R = 2 * len(inv_freq)
+    a = np.asarray(positions, np.float64)[:, None] * np.asarray(inv_freq, np.float64)[None]
+    turn = (factor * np.exp((-1j if inverse else 1j) * a))[:, None, :]
+    out = np.array(x, np.float64)
+    one, two = (slice(0, R, 2), slice(1, R, 2)) if interleaved else (slice(0, R // 2), slice(R // 2, R))
+    z = (out[..., one] + 1j * out[..., two]) * turn
+    out[..., one], out[..., two] = z.real, z.imag
+    return out
+
+
+# What the codes 0 .. 126 of e4m3 stand for (127 is NaN; 128 + c is -c).
+E4M3 = np.array([(c % 8) * 2.0 ** -9 if c < 8 else (8 + c % 8) * 2.0 ** (c // 8 - 10) for c in range(127)])
+
+
+def round_e4m3(x):
+    """The nearest value of e4m3, of two the one of the even code; NaN stays NaN.  |x| <= 448."""
+    x = np.asarray(x, np.float64)
+    a = np.minimum(np.abs(np.where(np.isnan(x), 0.0, x)), E4M3[-1])
+    hi = np.clip(np.searchsorted(E4M3, a), 1, 126)
+    lo = hi - 1
+    up, down = E4M3[hi] - a, a - E4M3[lo]
+    code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    return np.where(np.isnan(x), np.nan, np.sign(x) * E4M3[code])
+
+
+def scale8(most):
+    """The least power of two s, 2^-64 at the least, with most <= 448 s."""
+    s = 2.0 ** -64
+    while most > 448.0 * s:
+        s *= 2.0
+    return s
+
+
+def append8(codes, scales, new, first, block):
+    """One sequence and head of keys or values of a cache in 8 bits, in place: codes [places, D] as the
+    values they stand for, scales [places / block], new [n, D] from place first on."""
+    end = first + len(new)
+    for at in range(first // block * block, end, block):
+        lo, hi = max(at, first), min(at + block, end)
+        rows = np.where(np.isfinite(new[lo - first:hi - first]), new[lo - first:hi - first], np.nan)
+        s = scale8(np.nanmax(np.abs(rows), initial=0.0) if np.isfinite(rows).any() else 0.0)
+        if lo > at:
+            s = max(s, scales[at // block])
+            codes[at:lo] = round_e4m3(codes[at:lo] * (scales[at // block] / s))
+        codes[lo:hi] = round_e4m3(rows / s)
+        scales[at // block] = s
