@@ -240,7 +240,7 @@ EVO_API evo_status_t evo_rotary(const void* q, const void* k, const int32_t* pos
  * that is not finite is stored as NaN and does not enter the scale.  Where a block's first
  * token is new, what its scale held before does not matter.
  *
- * Scales that others wrote may be any positive finite number.  Reading rounds code * scale to
+ * Scales that others wrote may be any numbers from 2^-64 to 2^120.  Reading rounds code * scale to
  * dtype (for scales that are powers of two exact within its range) and saturates at its largest
  * finite number.  Attention takes code * scale as it is. */
 typedef struct {

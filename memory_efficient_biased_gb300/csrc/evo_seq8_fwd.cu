@@ -11,7 +11,7 @@ namespace {
 
 template <bool BF16>
 __global__ void __launch_bounds__(256) evo_paged8_rows_kernel(const __grid_constant__ Seq8FwdArgs a) {
-  const SeqDesc& s = a.s;
+  const SeqDesc& s = a.f.s;
   const Cache8& c = a.c;
   if (blockIdx.x == 0) check_seqs(s);
   const int lane = threadIdx.x & 31, d = lane * 4;
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(256) evo_paged8_rows_kernel(const __grid_const
       float y = x[0] * k[0] + x[1] * k[1] + x[2] * k[2] + x[3] * k[3];
 #pragma unroll
       for (int w = 16; w > 0; w >>= 1) y += __shfl_xor_sync(0xffffffffu, y, w);
-      y *= sk * a.scale_log2;
+      y *= sk * a.f.scale_log2;
       if (y == -INFINITY) continue;
       const float big = fmaxf(m, y), f = m == -INFINITY ? 0.0f : ex2(m - big), w = ex2(y - big);
       m = y != y ? y : big;  // (a NaN score makes the row NaN)
@@ -59,16 +59,16 @@ __global__ void __launch_bounds__(256) evo_paged8_rows_kernel(const __grid_const
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     if (has)
-      *reinterpret_cast<uint2*>(a.out + t * a.out_stride + static_cast<long long>(h) * s.D + d) =
+      *reinterpret_cast<uint2*>(a.f.out + t * a.f.out_stride + static_cast<long long>(h) * s.D + d) =
           l == 0.0f ? make_uint2(0u, 0u) : make_uint2(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv));
-    if (lane == 0) a.lse[static_cast<size_t>(h) * s.tokens + t] = l == 0.0f ? -INFINITY : (m + lg2(l)) * kSeqLn2;
+    if (lane == 0) a.f.lse[static_cast<size_t>(h) * s.tokens + t] = l == 0.0f ? -INFINITY : (m + lg2(l)) * kSeqLn2;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_paged8_fwd(const Seq8FwdArgs& a, bool bf16, cudaStream_t st) {
-  const long long blocks = (static_cast<long long>(a.s.tokens) * a.s.q_heads + 7) / 8;
+cudaError_t launch_paged8_rows(const Seq8FwdArgs& a, bool bf16, cudaStream_t st) {
+  const long long blocks = (static_cast<long long>(a.f.s.tokens) * a.f.s.q_heads + 7) / 8;
   const unsigned grid = static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20));
   if (bf16)
     evo_paged8_rows_kernel<true><<<grid, 256, 0, st>>>(a);

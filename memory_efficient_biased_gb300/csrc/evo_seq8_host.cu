@@ -44,6 +44,29 @@ Cache8 cache_of(const void* k_pages, const void* v_pages, const float* k_scales,
   return o;
 }
 
+// Pages as (D, kv_heads, page, num_pages), box (DP, 1, min(page, 128), 1): a row of codes is a swizzled row of the tile.
+bool map_pages8(CUtensorMap* m, const void* p, const evo_seq_shape_t& s, const evo_cache8_shape_t& c, int64_t stride) {
+  const int64_t D = s.head_dim, DP = D <= 64 ? 64 : 128;
+  cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(s.kv_heads), cuuint64_t(c.page_size), cuuint64_t(c.num_pages)};
+  cuuint64_t st[3] = {cuuint64_t(D), cuuint64_t(s.kv_heads * D), cuuint64_t(stride)};
+  cuuint32_t box[4] = {cuuint32_t(DP), 1, cuuint32_t(c.page_size < kTile ? c.page_size : kTile), 1};
+  return host_encode(m, p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, st, box,
+                     DP == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+}
+
+// Which kernel: up to 16 rows a sequence and kv head on the average, and a token's heads in one tile of 16.
+bool few_rows(const evo_seq_shape_t& s) {
+  const int64_t G = s.q_heads / s.kv_heads;
+  return G <= 16 && s.tokens * G <= 16 * s.seqs;
+}
+// CTAs of a launch: as fwd_ctas, for items of W tokens.
+int few_ctas(int sms, const evo_seq_shape_t& s, int64_t max_kv) {
+  const double W = 16 / (s.q_heads / s.kv_heads);
+  const double units = (double(s.tokens) / W + double(s.seqs)) * (double(max_kv) + 2 * kTile) * double(s.kv_heads);
+  return units < double(sms) * kTile ? static_cast<int>(units / kTile) + 1 : sms;
+}
+
 // What an append and a read check alike.
 evo_status_t rows_call(bool append, const void* k, const void* v, const int32_t* cu_seqlens, const int32_t* seq_lens,
                        const int32_t* block_table, const void* k_pages, const void* v_pages, const float* k_scales,
@@ -117,8 +140,9 @@ evo_status_t evo_cache8_read(const void* k_pages, const void* v_pages, const flo
 size_t evo_paged8_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache8_shape_t cache) {
   Checked c;
   if (check_seq_shape(shape, true) != EVO_OK || check_cache8(cache, shape, &c) != EVO_OK) return 0;
-  return seq_fwd_workspace(fwd_ctas(num_sms(), shape, cache.page_size * cache.pages_per_seq),
-                           static_cast<int>(shape.head_dim), nullptr, nullptr);
+  const int64_t max_kv = cache.page_size * cache.pages_per_seq;
+  const int ctas = few_rows(shape) ? few_ctas(num_sms(), shape, max_kv) : fwd_ctas(num_sms(), shape, max_kv);
+  return seq_fwd_workspace(ctas, static_cast<int>(shape.head_dim), nullptr, nullptr);
 }
 
 evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
@@ -162,15 +186,29 @@ evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pa
   int* fallback = nullptr;
   if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
   Seq8FwdArgs a{};
-  a.s = desc(shape, cu_seqlens, seq_lens, block_table, &c.as16, -1, o.status ? o.status : fallback);
+  a.f.s = desc(shape, cu_seqlens, seq_lens, block_table, &c.as16, -1, o.status ? o.status : fallback);
   a.c = cache_of(k_pages, v_pages, k_scales, v_scales, cache, c);
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = t.q;
-  a.out = static_cast<uint16_t*>(out);
-  a.out_stride = t.out;
-  a.lse = lse;
-  a.scale_log2 = scale_of(o, shape) * kSeqLog2e;
-  const cudaError_t e = launch_paged8_fwd(a, dtype == EVO_BF16, static_cast<cudaStream_t>(stream));
+  a.f.out = static_cast<uint16_t*>(out);
+  a.f.out_stride = t.out;
+  a.f.lse = lse;
+  a.f.scale_log2 = scale_of(o, shape) * kSeqLog2e;
+  a.f.wait_ns = o.wait_ns;
+  a.f.TQ = kTile / a.f.s.group;
+  const bool bf16 = dtype == EVO_BF16;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (few_rows(shape)) {
+    if (!map_pages8(&a.f.tk, k_pages, shape, cache, c.k_page) || !map_pages8(&a.f.tv, v_pages, shape, cache, c.v_page))
+      return EVO_ERR_CUDA;
+    a.f.W = 16 / a.f.s.group;
+    const int ctas = few_ctas(sms, shape, cache.page_size * cache.pages_per_seq);
+    seq_fwd_workspace(ctas, static_cast<int>(shape.head_dim), &a.f, static_cast<uint8_t*>(workspace));
+    e = launch_paged8_few(a, ctas, bf16, cs);
+  } else {
+    e = launch_paged8_rows(a, bf16, cs);
+  }
   return e == cudaSuccess ? EVO_OK : cuda_fail("8-bit cache attention launch", e);
 }
 

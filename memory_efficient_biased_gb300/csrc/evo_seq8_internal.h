@@ -21,14 +21,11 @@ struct Cache8Args {  // append and read
 };
 
 struct Seq8FwdArgs {
-  SeqDesc s;
+  SeqFwdArgs f;  // tk, tv: pages of bytes as (D, kv_heads, page, num_pages); W, TQ: the kernel's own, TQ as the join
+                 // takes it (128 / group)
   Cache8 c;
   const uint16_t* q;
   long long q_stride;
-  uint16_t* out;
-  long long out_stride;
-  float* lse;
-  float scale_log2;  // scale · log2 e
 };
 
 // Place of the scale of token j (of page p) and head h.
@@ -65,6 +62,7 @@ __device__ __forceinline__ uint2 codes_of_f32(const float (&x)[8]) {
 
 cudaError_t launch_cache8_append(const Cache8Args& a, bool bf16, cudaStream_t st);
 cudaError_t launch_cache8_read(const Cache8Args& a, bool bf16, cudaStream_t st);
-cudaError_t launch_paged8_fwd(const Seq8FwdArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_paged8_few(const Seq8FwdArgs& a, int ctas, bool bf16, cudaStream_t st);
+cudaError_t launch_paged8_rows(const Seq8FwdArgs& a, bool bf16, cudaStream_t st);
 
 }  // namespace evo

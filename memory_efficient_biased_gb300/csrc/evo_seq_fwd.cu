@@ -832,8 +832,7 @@ template <int DP, bool BF16>
 cudaError_t launch_t(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
   const cudaError_t e = a.scores ? launch_k<DP, BF16, true>(a, ctas, st) : launch_k<DP, BF16, false>(a, ctas, st);
   if (e != cudaSuccess || a.s.max_kv <= kTile) return e;  // one key tile: nothing is cut
-  evo_seq_join_kernel<DP, BF16><<<dim3(ctas, 256 / kJoinRows), 256, 0, st>>>(a, ctas);
-  return cudaGetLastError();
+  return launch_seq_join(a, ctas, BF16, st);
 }
 
 }  // namespace
@@ -855,6 +854,21 @@ size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws) {
     a->part_o = reinterpret_cast<float*>(po);
   }
   return off;
+}
+
+cudaError_t launch_seq_join(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st) {
+  const dim3 grid(ctas, 256 / kJoinRows);
+  if (a.s.D <= 64) {
+    if (bf16)
+      evo_seq_join_kernel<64, true><<<grid, 256, 0, st>>>(a, ctas);
+    else
+      evo_seq_join_kernel<64, false><<<grid, 256, 0, st>>>(a, ctas);
+  } else if (bf16) {
+    evo_seq_join_kernel<128, true><<<grid, 256, 0, st>>>(a, ctas);
+  } else {
+    evo_seq_join_kernel<128, false><<<grid, 256, 0, st>>>(a, ctas);
+  }
+  return cudaGetLastError();
 }
 
 cudaError_t launch_seq_fwd(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st) {
