@@ -162,10 +162,10 @@ __global__ void __launch_bounds__(256) evo_read8_kernel(const __grid_constant__ 
     const uint4 x = *reinterpret_cast<const uint4*>(page + (static_cast<long long>(j % s.page) * chunks + n) * 16);
     const float scale = (kv ? c.v_scales : c.k_scales)[scale_at(c, s, p, n / per, j)];
     constexpr float most = BF16 ? 3.38953139e38f : 65504.0f;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const uint2 w[4] = {f16x4_of_codes(x.x), f16x4_of_codes(x.y), f16x4_of_codes(x.z), f16x4_of_codes(x.w)};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float2 f = unpack2<false>(f16x2_of_e4m3x2((e & 1) ? w[e >> 1] >> 16 : w[e >> 1]));
+      float2 f = unpack2<false>((e & 1) ? w[e >> 1].y : w[e >> 1].x);
       f = make_float2(f.x * scale, f.y * scale);
       // (comparisons that a NaN passes unchanged)
       f.x = f.x > most ? most : (f.x < -most ? -most : f.x);

@@ -14,10 +14,11 @@
 // in registers are read once from the staged tile and widened on their way into the product: 2 bytes. The
 // products need 16 rows · 23 = 370 multiply-adds a clock and SM, a third of what mma.sync has.
 //
-// Roles (9 warps, one CTA per SM, persistent over its share of the work, evo_seq_sched.cuh):
-//   warps 0-7  16 keys of every tile of 128 each, which share their scales; M, l and O of their own,
-//              joined at the end of an item
-//   warp 8     the walk over the work; K and V tiles by TMA (a page is a box), scales by cp.async
+// Roles (13 warps, one CTA per SM, persistent over its share of the work, evo_seq_sched.cuh):
+//   warps 0-11  32 keys at a time each (16 share their scales), in turns; M, l and O of their own, joined at the end of an
+//               item.  Three a scheduler, for what a warp waits for between its products; that takes q out of their
+//               registers, into shared memory
+//   warp 12     the walk over the work; keys and values by TMA (a page is a box), scales by cp.async
 //
 // Fragments.  Inside a product the order of the features (scores) and of the keys (P·V) is free, so a lane takes 16
 // bytes next to each other: of key g for the scores (lane = 4 g + c: features 16 c .. and 64 + 16 c ..), of keys
@@ -29,23 +30,26 @@
 namespace evo {
 namespace {
 
-constexpr int kRows = 16, kWarps = 8, kThreads = 32 * (kWarps + 1), kDescs = 4;
+constexpr int kRows = 16, kWarps = 12, kThreads = 32 * (kWarps + 2), kDescs = 4;
+constexpr int kKeys = 16, kGroups = kTile / kKeys;  // keys that a warp takes at a time, warps to a tile
+constexpr int kStages = 6;                          // tiles
 
 template <int DP>
 struct Layout {
-  static constexpr uint32_t kTB = kTile * DP;  // one tile of codes
-  static constexpr int kStages = DP == 128 ? 4 : 8;
-  static constexpr int kPitch = DP + 4;        // floats between rows of a warp's O
-  static constexpr uint32_t ring = 0, merge = kStages * 2 * kTB, bars = merge + kWarps * kRows * kPitch * 4;
+  static constexpr uint32_t kTB = kTile * DP;     // codes of a tile's keys, and of its values
+  static constexpr int kPitch = DP / 4 + 4;       // floats between rows of a quarter of a warp's O
+  static constexpr uint32_t ring = 0, merge = kStages * 2 * kTB, q = merge + kWarps * kRows * kPitch * 4;
+  static constexpr uint32_t bars = q + kRows * DP * 2;
 };
 
 struct Bars {
   uint64_t desc_full[kDescs], desc_empty[kDescs];
-  uint64_t full[8], empty[8];
-  uint64_t merge_full, merge_empty;
+  uint64_t full[kStages], empty[kStages];
+  uint64_t merge_full, merge_empty, q_full;
+  alignas(8) float scales[kStages][2][8];  // of a stage: keys and values, 16 tokens each
   Work work[kDescs];
-  float scales[8][2][8];          // of a stage: keys and values, 16 tokens each
   float2 ml[kWarps][kRows];
+  float unit[kRows];              // scale · log2 e, and the power of two that q was divided by
   uint32_t tiles;
   int abort;
 };
@@ -69,18 +73,89 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 // Bytes of four codes that are NaN, as 0xff.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
-// ------------------------------------------------------------ walk and loads (one warp)
+// Codes that are NaN taken out of the values of 16 keys, in the layout of P·V (key: the lane's first), and NaN put into
+// the features of the rows that see them: the product of ones (a key that a row sees) and ones (a code that is NaN)
+// counts them.
+template <int COLS>
+__device__ __forceinline__ void nan_values(uint32_t (&v)[4][COLS / 4], float (&o)[COLS][4], int key, int pos0, int pos1) {
+  constexpr uint32_t one = 0x3c00u;  // 1 in fp16
+  uint32_t seen[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int at = key + 8 * (e >> 1), pos = (e & 1) ? pos1 : pos0;
+    seen[e] = (at <= pos ? one : 0u) | (at + 4 <= pos ? one << 16 : 0u);
+  }
+#pragma unroll
+  for (int e = 0; e < COLS / 4; ++e) {
+    uint32_t bad[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      bad[i] = nan_bytes(v[i][e]);
+      v[i][e] &= ~bad[i];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      auto pair = [&](int i) {
+        return ((bad[i] >> (8 * k)) & 1u ? one : 0u) | ((bad[i + 1] >> (8 * k)) & 1u ? one << 16 : 0u);
+      };
+      float count[4] = {};
+      mma16816(count, seen, pair(0), pair(2));
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (count[x] > 0.0f) o[4 * e + k][x] = NAN;
+    }
+  }
+}
+
+// ------------------------------------------------------------ walk, loads, scales (a warp each for loads and scales)
+// The pages of an item's tiles, looked up a batch of tiles at a time, a page a lane, and a batch ahead, and
+// looked over only when their turn comes: looked up tile by tile, the table's latency under load was what a tile took.
+struct Pages {
+  const SeqDesc& s;
+  const int* table;
+  int pages, j1, kv_end;   // pages of a tile
+  int now, next, in;       // in: tiles of the batch that are done
+
+  __device__ __forceinline__ Pages(const SeqDesc& s, const Work& w, int pages)
+      : s(s), table(s.table + static_cast<size_t>(w.b) * s.pages_per_seq), pages(pages), j1(w.j1), kv_end(w.kv_end), in(0) {
+    now = look_up(w.j0);
+    next = look_up(w.j0 + 32 / pages);
+    now = look_over(w.j0, now);
+  }
+  __device__ __forceinline__ int place(int j) const {  // of this lane's page in the batch that begins at tile j
+    const int lane = threadIdx.x & 31;
+    j += lane / pages;
+    return j < j1 ? j * kTile + lane % pages * s.page : kv_end;
+  }
+  __device__ __forceinline__ int look_up(int j) const {
+    const int at = place(j);
+    return at < kv_end ? table[at / s.page] : s.num_pages;
+  }
+  __device__ __forceinline__ int look_over(int j, int p) const {  // (a page past the keys, or a bad one, reads as zeros)
+    if (p >= 0 && p < s.num_pages) return p;
+    if (place(j) < kv_end) report_bad_index(s.status);
+    return s.num_pages;
+  }
+  __device__ __forceinline__ int of(int i) const { return __shfl_sync(0xffffffffu, now, in * pages + i); }  // page i of the tile
+  __device__ __forceinline__ void step(int j) {  // tile j is done
+    if (++in == 32 / pages) {
+      in = 0;
+      now = look_over(j + 1, next);
+      next = look_up(j + 1 + 32 / pages);
+    }
+  }
+};
+
 template <int DP>
 __device__ __forceinline__ void produce(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
   using L = Layout<DP>;
   const SeqDesc& s = a.f.s;
-  const Cache8& c = a.c;
   Walk<QueryBlocks> walk;
   walk.init(s, QueryBlocks{a.f.W}, blockIdx.x, gridDim.x);
   PieceRecord* rec = a.f.records + 2 * blockIdx.x;
   if (lane < 2) rec[lane].used = 0;
   __syncwarp();
-  const int box = s.page < kTile ? s.page : kTile, boxes = kTile / box;
+  const int box = s.page < kTile ? s.page : kTile, pages = kTile / box;  // a copy's rows, copies (and pages) of a tile
   uint32_t use = 0;
   for (uint32_t it = 0;; ++it) {
     const Work w = walk.next();
@@ -92,35 +167,56 @@ __device__ __forceinline__ void produce(const Seq8FwdArgs& a, uint8_t* base, Bar
       mbar_arrive(smem_u32(&bars->desc_full[d]));
     }
     if (w.stop) break;
-    // this lane's page of a tile (a page past the keys, or a bad one, reads as zeros)
-    auto page = [&](int j) -> int {
-      const int key = j * kTile + lane * box;
-      if (lane >= boxes || key >= w.kv_end) return s.num_pages;
-      const int p = page_of(s, w.b, key);
-      return p < 0 ? s.num_pages : p;
-    };
-    int mine = page(w.j0);
+    Pages look(s, w, pages);
+    int first = s.page > kTile ? (w.j0 * kTile) % s.page : 0;  // row of the page that the tile begins at
     bool ok = true;
     for (int j = w.j0; j < w.j1; ++j, ++use) {
-      const int cur = mine;
-      if (j + 1 < w.j1) mine = page(j + 1);
-      const uint32_t st = use % L::kStages;
-      if (!mbar_wait_warp_inl(smem_u32(&bars->empty[st]), ((use / L::kStages) & 1) ^ 1, g)) { ok = false; break; }
+      const uint32_t st = use % kStages;
+      if (!mbar_wait_warp_inl(smem_u32(&bars->empty[st]), ((use / kStages) & 1) ^ 1, g)) { ok = false; break; }
       const uint32_t full = smem_u32(&bars->full[st]), dst = smem_u32(base + L::ring + st * 2 * L::kTB);
-      if (lane == 0) mbar_arrive_expect_tx(full, 2 * L::kTB);
-      __syncwarp();
-      const int first = boxes == 1 ? (j * kTile) % s.page : 0;
-      if (lane < boxes) {
-        tma_load_4d(dst + lane * box * DP, &a.f.tk, full, 0, w.kvh, first, cur);
-        tma_load_4d(dst + L::kTB + lane * box * DP, &a.f.tv, full, 0, w.kvh, first, cur);
+      if (elect_one()) mbar_arrive_expect_tx(full, 2 * L::kTB);
+      for (int b = 0; b < pages; ++b) {
+        const int p = look.of(b);
+        if (elect_one()) {
+          tma_load_4d(dst + b * box * DP, &a.f.tk, full, 0, w.kvh, first, p);
+          tma_load_4d(dst + L::kTB + b * box * DP, &a.f.tv, full, 0, w.kvh, first, p);
+        }
       }
-      // the scale of 16 tokens: lanes 0-7 keys, 8-15 values
-      const int part = lane & 7, token = part * 16;
-      const int p = __shfl_sync(0xffffffffu, cur, token / box);
+      __syncwarp();
+      if (s.page > kTile && (first += kTile) == s.page) first = 0;
+      look.step(j);
+    }
+    if (!ok) break;
+  }
+  if (lane == 0) bars->tiles = use;
+}
+
+// The scales of a tile: lanes 0-7 keys, 8-15 values, 16 tokens each.
+__device__ __forceinline__ void fetch_scales(const Seq8FwdArgs& a, Bars* bars, const WaitGuard& g, int lane) {
+  const SeqDesc& s = a.f.s;
+  const Cache8& c = a.c;
+  const int pages = s.page < kTile ? kTile / s.page : 1, part = lane & 7, shift = __ffs(c.block) - 1;
+  const int mine = part * pages / 8, token = pages == 1 ? part * 16 : part % (8 / pages) * 16;  // page of the tile, place there
+  const float* scales = lane & 8 ? c.v_scales : c.k_scales;
+  uint32_t use = 0;
+  for (uint32_t it = 0;; ++it) {
+    const uint32_t d = it % kDescs;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->desc_full[d]), (it / kDescs) & 1, g)) return;
+    const Work w = bars->work[d];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->desc_empty[d]));
+    if (w.stop) return;
+    Pages look(s, w, pages);
+    int first = s.page > kTile ? (w.j0 * kTile) % s.page : 0;
+    for (int j = w.j0; j < w.j1; ++j, ++use) {
+      const uint32_t st = use % kStages;
+      const int p = look.of(mine);
+      const float* from = scales + (static_cast<long long>(p) * s.kv_heads + w.kvh) * c.blocks + ((first + token) >> shift);
+      if (!mbar_wait_warp_inl(smem_u32(&bars->empty[st]), ((use / kStages) & 1) ^ 1, g)) return;
       if (lane < 16) {
+        const uint32_t full = smem_u32(&bars->full[st]);
         float* to = &bars->scales[st][lane >> 3][part];
-        if (p < s.num_pages && j * kTile + token < w.kv_end) {
-          const float* from = (lane >> 3 ? c.v_scales : c.k_scales) + scale_at(c, s, p, w.kvh, first + token);
+        if (p < s.num_pages && j * kTile + part * 16 < w.kv_end) {
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
         } else {
@@ -129,10 +225,10 @@ __device__ __forceinline__ void produce(const Seq8FwdArgs& a, uint8_t* base, Bar
         }
       }
       __syncwarp();
+      if (s.page > kTile && (first += kTile) == s.page) first = 0;
+      look.step(j);
     }
-    if (!ok) break;
   }
-  if (lane == 0) bars->tiles = use;
 }
 
 // ------------------------------------------------------------ compute (warps 0..7)
@@ -142,8 +238,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
   constexpr int kHalves = DP / 64, kCols = DP / 8;  // 16-byte pieces a lane of a key, tiles of eight features
   const SeqDesc& s = a.f.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
-  // rows gr and gr + 8: token within the item, head within the group
-  const int G = s.group, dt0 = gr / G, dt1 = (gr + 8) / G, h0 = gr % G, h1 = (gr + 8) % G;
+  const int G = s.group, dt0 = gr / G, dt1 = (gr + 8) / G;  // rows gr and gr + 8: token within the item
   float* mine = reinterpret_cast<float*>(base + L::merge) + warp * kRows * L::kPitch;
   uint32_t use = 0, merges = 0;
   for (uint32_t it = 0;; ++it) {
@@ -153,77 +248,115 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->desc_empty[ds]));
     if (w.stop) return;
-    const bool live0 = dt0 < w.nt, live1 = dt1 < w.nt;  // (nt <= 16 / G: rows past the item's are none's)
-    // ---- q: features 64 i + 16 c + 4 k + (0, 1 | 2, 3) are elements (2c, 2c + 1 | 2c + 8, 2c + 9) of step 4 i + k
-    uint32_t q[4 * kHalves][4];
-    float unit[2] = {1.0f, 1.0f};
-    {
-      uint2 x[2][4 * kHalves];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const size_t row = static_cast<size_t>(w.row0) + w.t0 + (r ? dt1 : dt0);
-        const uint16_t* from = a.q + row * a.q_stride + static_cast<size_t>(w.kvh * G + (r ? h1 : h0)) * s.D + 16 * c;
-#pragma unroll
-        for (int k = 0; k < 4 * kHalves; ++k) {
-          const int at = 64 * (k >> 2) + 4 * (k & 3);
-          x[r][k] = make_uint2(0u, 0u);
-          if ((r ? live1 : live0) && 16 * c + at < s.D) x[r][k] = *reinterpret_cast<const uint2*>(from + at);
-        }
-      }
+    // ---- q in fp16, a row a warp: features 64 i + 16 c + 4 k + (0, 1 | 2, 3) of row r become elements
+    // (2c, 2c + 1 | 2c + 8, 2c + 9) of step 4 i + k, where lane 4 (r % 8) + c takes them for its product.  (The last item's
+    // q is nobody's any more: every warp has joined its share of it.)
+    for (int r = warp; r < kRows; r += kWarps) {
+      uint2 x = make_uint2(0u, 0u);
+      if (4 * lane < s.D && r / G < w.nt)
+        x = *reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(w.row0) + w.t0 + r / G) * a.q_stride +
+                                            static_cast<size_t>(w.kvh * G + r % G) * s.D + 4 * lane);
+      float unit = a.f.scale_log2;
       if constexpr (BF16) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          uint32_t most = 0;  // magnitudes, as two 16-bit numbers
-#pragma unroll
-          for (int k = 0; k < 4 * kHalves; ++k)
-            most = __vmaxu2(__vmaxu2(most, x[r][k].x & 0x7fff7fffu), x[r][k].y & 0x7fff7fffu);
-          most = max(most & 0xffffu, most >> 16);
-          most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-          most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-          const uint32_t e = min(max(most >> 7, 1u), 253u);
-          const float down = __uint_as_float((254u - e) << 23);
-          unit[r] = __uint_as_float(e << 23);
-#pragma unroll
-          for (int k = 0; k < 4 * kHalves; ++k) {
-            const float2 f0 = unpack2<true>(x[r][k].x), f1 = unpack2<true>(x[r][k].y);
-            x[r][k] = make_uint2(pack2<false>(f0.x * down, f0.y * down), pack2<false>(f1.x * down, f1.y * down));
-          }
-        }
+        uint32_t most = __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu);  // magnitudes, as two 16-bit numbers
+        most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+        const uint32_t e = min(max(most >> 7, 1u), 253u);
+        const float down = __uint_as_float((254u - e) << 23);
+        unit *= __uint_as_float(e << 23);
+        const float2 f0 = unpack2<true>(x.x), f1 = unpack2<true>(x.y);
+        x = make_uint2(pack2<false>(f0.x * down, f0.y * down), pack2<false>(f1.x * down, f1.y * down));
       }
-#pragma unroll
-      for (int k = 0; k < 4 * kHalves; ++k) q[k][0] = x[0][k].x, q[k][1] = x[1][k].x, q[k][2] = x[0][k].y, q[k][3] = x[1][k].y;
+      if (4 * lane < DP) {
+        uint32_t* to = reinterpret_cast<uint32_t*>(base + L::q) +
+                       (((lane >> 4) * 4 + (lane & 3)) * 32 + (r & 7) * 4 + ((lane >> 2) & 3)) * 4 + (r >> 3);
+        to[0] = x.x;
+        to[2] = x.y;
+      }
+      if (lane == 0) bars->unit[r] = unit;
     }
-    unit[0] *= a.f.scale_log2;
-    unit[1] *= a.f.scale_log2;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
+    if (!mbar_wait_warp_inl(smem_u32(&bars->q_full), it & 1, g)) return;
+    const float unit0 = bars->unit[gr], unit1 = bars->unit[gr + 8];
+    const uint32_t qs = smem_u32(base + L::q) + lane * 16;
     const int pos0 = w.pos + dt0, pos1 = w.pos + dt1;
     float o[kCols][4] = {};
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    for (int j = w.j0; j < w.j1; ++j, ++use) {
-      const uint32_t st = use % L::kStages;
-      if (!mbar_wait_warp_inl(smem_u32(&bars->full[st]), (use / L::kStages) & 1, g)) return;
-      const int key0 = j * kTile + warp * 16;
+    // The 16 keys that are this warp's: every twelfth of all that the CTA walks over.  (A stage is either always one
+    // of those that a warp looks at, or never: 12 times 16 keys are a tile and a half, and there are six stages.)
+    const uint32_t end = (use + static_cast<uint32_t>(w.j1 - w.j0)) * kGroups;
+    uint32_t n16 = use * kGroups;
+    n16 += (warp + kWarps - n16 % kWarps) % kWarps;
+    for (; n16 < end; n16 += kWarps) {
+      const uint32_t tile = n16 / kGroups, st = tile % kStages;
+      if (!mbar_wait_warp_inl(smem_u32(&bars->full[st]), (tile / kStages) & 1, g)) return;
+      const int part = static_cast<int>(n16 % kGroups), key0 = (w.j0 + static_cast<int>(tile - use)) * kTile + part * kKeys;
       if (key0 >= w.kv_end) {
         if (lane == 0) mbar_arrive(smem_u32(&bars->empty[st]));
         continue;
       }
-      const uint32_t kt = smem_u32(base + L::ring + st * 2 * L::kTB) + warp * 16 * DP, vt = kt + L::kTB;
-      const float ks = bars->scales[st][0][warp], vs = bars->scales[st][1][warp];
+      const uint32_t kt = smem_u32(base + L::ring + 2 * st * L::kTB) + part * kKeys * DP, vt = kt + L::kTB;
+      const float ks = bars->scales[st][0][part], vs = bars->scales[st][1][part];
       // ---- scores: column g of tile n is key 8 n + (g / 2) + 4 (g % 2)
-      float sc[2][kHalves][4] = {};
+      float t[2][4] = {};  // tile n: (row gr: keys 8n + c, 8n + c + 4), (row gr + 8: the same)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int r = 8 * n + (gr >> 1) + 4 * (gr & 1);
-        const uint32_t row = kt + r * DP;
+      for (int i = 0; i < kHalves; ++i) {
+        uint32_t u[2][4];
 #pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
+        for (int n = 0; n < 2; ++n) {
+          const int r = 8 * n + (gr >> 1) + 4 * (gr & 1);
           const uint32_t piece = DP == 128 ? static_cast<uint32_t>((c + 4 * i) ^ (r & 7)) : static_cast<uint32_t>(c ^ ((r >> 1) & 3));
-          const uint4 x = lds128(row + piece * 16);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+          const uint4 x = lds128(kt + r * DP + piece * 16);
+          u[n][0] = x.x, u[n][1] = x.y, u[n][2] = x.z, u[n][3] = x.w;
+        }
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma16816(sc[n][i], q[4 * i + k], f16x2_of_e4m3x2(u[k]), f16x2_of_e4m3x2(u[k] >> 16));
+        for (int k = 0; k < 4; ++k) {
+          const uint4 x = lds128(qs + (4 * i + k) * 512);
+          const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint2 f = f16x4_of_codes(u[n][k]);
+            mma16816(t[n], q, f.x, f.y);
+          }
         }
       }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[n][e] *= (e < 2 ? unit0 : unit1) * ks;
+      const bool edge = key0 + kKeys - 1 > w.pos;  // some row does not see some key
+      if (edge) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + 8 * n + c + 4 * (e & 1) > (e < 2 ? pos0 : pos1)) t[n][e] = -INFINITY;
+      }
+      const float lv = lg2(vs), iv = ex2(-lv);
+      float a0 = fmaxf(fmaxf(t[0][0], t[0][1]), fmaxf(t[1][0], t[1][1])) + lv;
+      float a1 = fmaxf(fmaxf(t[0][2], t[0][3]), fmaxf(t[1][2], t[1][3])) + lv;
+      // (the lanes that share rows need one M for them only where it moves)
+      if (__any_sync(0xffffffffu, a0 > m0 || a1 > m1)) {
+        a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
+        a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
+        a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
+        a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
+        const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
+        const float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - n1);
+        m0 = n0, m1 = n1;
+        l0 *= f0, l1 *= f1;
+#pragma unroll
+        for (int n = 0; n < kCols; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
+      }
+      const float b0 = lv - (m0 == -INFINITY ? 0.0f : m0), b1 = lv - (m1 == -INFINITY ? 0.0f : m1);
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[n][e] = ex2(t[n][e] + (e < 2 ? b0 : b1));
+      l0 = fmaf((t[0][0] + t[0][1]) + (t[1][0] + t[1][1]), iv, l0);
+      l1 = fmaf((t[0][2] + t[0][3]) + (t[1][2] + t[1][3]), iv, l1);
+      const uint32_t p[4] = {pack2<false>(t[0][0], t[0][1]), pack2<false>(t[0][2], t[0][3]), pack2<false>(t[1][0], t[1][1]),
+                             pack2<false>(t[1][2], t[1][3])};
       // ---- values: keys c, c + 4, c + 8, c + 12, features 16 G(g) .. (8 g ..)
       uint32_t v[4][kCols / 4];
 #pragma unroll
@@ -241,57 +374,9 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->empty[st]));
-      float t[2][4];  // tile n: (row gr: keys 8n + c, 8n + c + 4), (row gr + 8: the same)
-      const float k0 = unit[0] * ks, k1 = unit[1] * ks;
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = sc[n][0][e];
-          if constexpr (kHalves == 2) x += sc[n][1][e];
-          t[n][e] = x * (e < 2 ? k0 : k1);
-        }
-      const bool edge = key0 + 15 > w.pos;  // some row does not see some key
       if (edge) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key0 + 8 * n + c + 4 * (e & 1) > (e < 2 ? pos0 : pos1)) t[n][e] = -INFINITY;
-      }
-      float a0 = fmaxf(fmaxf(t[0][0], t[0][1]), fmaxf(t[1][0], t[1][1]));
-      float a1 = fmaxf(fmaxf(t[0][2], t[0][3]), fmaxf(t[1][2], t[1][3]));
-      a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
-      a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
-      a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
-      a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
-      const float lv = lg2(vs), iv = ex2(-lv);
-      a0 += lv;
-      a1 += lv;
-      if (__any_sync(0xffffffffu, a0 > m0 || a1 > m1)) {
-        const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
-        const float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - n1);
-        m0 = n0, m1 = n1;
-        l0 *= f0, l1 *= f1;
-#pragma unroll
-        for (int n = 0; n < kCols; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
-      }
-      const float b0 = lv - (m0 == -INFINITY ? 0.0f : m0), b1 = lv - (m1 == -INFINITY ? 0.0f : m1);
-      float p0 = 0.0f, p1 = 0.0f;
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[n][e] = ex2(t[n][e] + (e < 2 ? b0 : b1));
-        p0 += t[n][0] + t[n][1];
-        p1 += t[n][2] + t[n][3];
-      }
-      l0 = fmaf(p0, iv, l0);
-      l1 = fmaf(p1, iv, l1);
-      const uint32_t p[4] = {pack2<false>(t[0][0], t[0][1]), pack2<false>(t[0][2], t[0][3]), pack2<false>(t[1][0], t[1][1]),
-                             pack2<false>(t[1][2], t[1][3])};
-      uint32_t lost = 0;
-      if (edge) {
-        // rows behind the last key that anyone sees: nothing; codes that are NaN: taken out, and put back below where they are seen
+        // rows behind the last key that anyone sees: nothing; codes that are NaN: taken out, and put back where they are seen
+        uint32_t lost = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -299,48 +384,21 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
             if (key0 + c + 4 * i >= w.kv_end) v[i][e] = 0u;
             lost |= nan_bytes(v[i][e]);
           }
-      }
-      const bool dirty = edge && __any_sync(0xffffffffu, lost != 0);
-      if (dirty) {
-        // Which rows see a NaN, and in which feature: the product of ones (a key that a row sees) and ones (a code that is NaN).
-        uint32_t seen[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at = key0 + 8 * (e >> 1) + c, pos = (e & 1) ? pos1 : pos0;
-          seen[e] = (at <= pos ? 0x3c00u : 0u) | (at + 4 <= pos ? 0x3c000000u : 0u);
-        }
-#pragma unroll
-        for (int e = 0; e < kCols / 4; ++e) {
-          uint32_t bad[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            bad[i] = nan_bytes(v[i][e]);
-            v[i][e] &= ~bad[i];
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t one = 0x3c00u;
-            const uint32_t w0 = ((bad[0] >> (8 * k)) & 1u ? one : 0u) | ((bad[1] >> (8 * k)) & 1u ? one << 16 : 0u);
-            const uint32_t w1 = ((bad[2] >> (8 * k)) & 1u ? one : 0u) | ((bad[3] >> (8 * k)) & 1u ? one << 16 : 0u);
-            float count[4] = {};
-            mma16816(count, seen, w0, w1);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (count[x] > 0.0f) o[4 * e + k][x] = NAN;
-          }
-        }
+        if (__any_sync(0xffffffffu, lost != 0)) nan_values<kCols>(v, o, key0 + c, pos0, pos1);
       }
       // ---- O: bytes of keys (c, c + 4) and (c + 8, c + 12) paired, feature by feature
 #pragma unroll
       for (int e = 0; e < kCols / 4; ++e) {
         const uint32_t x0 = __byte_perm(v[0][e], v[1][e], 0x5140), x1 = __byte_perm(v[0][e], v[1][e], 0x7362);
         const uint32_t y0 = __byte_perm(v[2][e], v[3][e], 0x5140), y1 = __byte_perm(v[2][e], v[3][e], 0x7362);
-        mma16816(o[4 * e], p, f16x2_of_e4m3x2(x0), f16x2_of_e4m3x2(y0));
-        mma16816(o[4 * e + 1], p, f16x2_of_e4m3x2(x0 >> 16), f16x2_of_e4m3x2(y0 >> 16));
-        mma16816(o[4 * e + 2], p, f16x2_of_e4m3x2(x1), f16x2_of_e4m3x2(y1));
-        mma16816(o[4 * e + 3], p, f16x2_of_e4m3x2(x1 >> 16), f16x2_of_e4m3x2(y1 >> 16));
+        const uint2 f0 = f16x4_of_codes(x0), f1 = f16x4_of_codes(x1), g0 = f16x4_of_codes(y0), g1 = f16x4_of_codes(y1);
+        mma16816(o[4 * e], p, f0.x, g0.x);
+        mma16816(o[4 * e + 1], p, f0.y, g0.y);
+        mma16816(o[4 * e + 2], p, f1.x, g1.x);
+        mma16816(o[4 * e + 3], p, f1.y, g1.y);
       }
     }
+    use += static_cast<uint32_t>(w.j1 - w.j0);
     // ---- the warps' shares joined
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
@@ -351,67 +409,80 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
       bars->ml[warp][gr] = make_float2(m0, l0);
       bars->ml[warp][gr + 8] = make_float2(m1, l1);
     }
-    // tile n, elements 0 | 1: feature n of piece G(2 c) = c | G(2 c + 1) = 4 + c (D up to 64: 8 (2 c) | 8 (2 c + 1))
+    // Tile n holds, as elements 0 | 1 of a row, feature n of piece G(2 c) = c | G(2 c + 1) = 4 + c (D up to 64: of the eight
+    // features 2 c | 2 c + 1): a quarter of the tiles, and with it of the features, at a time.
+    const int r = threadIdx.x >> 4, piece = (threadIdx.x >> 1) & 7, two = (threadIdx.x & 1) * (DP / 64);  // row, features
+    const bool out = r < kRows && r / G < w.nt;  // (rows past the item's are none's)
+    const size_t row = static_cast<size_t>(w.row0) + w.t0 + r / G, at = (static_cast<size_t>(blockIdx.x) * 2 + w.slot) * 256 + r;
+    const int h = w.kvh * G + r % G;
+    float f[kWarps], big = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int k = 0; k < 4; ++k) {
+      constexpr int kN = kCols / 4;  // tiles of a quarter: 4, or 2
+      if (k > 0 && !mbar_wait_warp_inl(smem_u32(&bars->merge_empty), (merges & 1) ^ 1, g)) return;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float* to = mine + (gr + 8 * half) * L::kPitch + (DP == 128 ? 16 * (c + 4 * x) : 8 * (2 * c + x));
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int n = 0; n < kCols; n += 4)
-          *reinterpret_cast<float4*>(to + n) = make_float4(o[n][2 * half + x], o[n + 1][2 * half + x], o[n + 2][2 * half + x],
-                                                           o[n + 3][2 * half + x]);
+        for (int x = 0; x < 2; ++x) {
+          float* to = mine + (gr + 8 * half) * L::kPitch + (DP == 128 ? c + 4 * x : 2 * c + x) * kN;
+          if constexpr (kN == 4)
+            *reinterpret_cast<float4*>(to) = make_float4(o[4 * k][2 * half + x], o[4 * k + 1][2 * half + x],
+                                                         o[4 * k + 2][2 * half + x], o[4 * k + 3][2 * half + x]);
+          else
+            *reinterpret_cast<float2*>(to) = make_float2(o[2 * k][2 * half + x], o[2 * k + 1][2 * half + x]);
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->merge_full));
+      if (!mbar_wait_warp_inl(smem_u32(&bars->merge_full), merges & 1, g)) return;
+      ++merges;
+      if (out) {
+        if (k == 0) {
+          float2 ml[kWarps];
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) {
+            ml[i] = bars->ml[i][r];
+            if (ml[i].y != 0.0f) big = fmaxf(big, ml[i].x);
+          }
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) {
+            // (a share that saw a NaN may have no maximum: its l is NaN, whatever it is scaled by)
+            f[i] = ml[i].y == 0.0f ? 0.0f : (big == -INFINITY ? 1.0f : ex2(ml[i].x - big));
+            if (ml[i].y != 0.0f) l += ml[i].y * f[i];
+          }
+        }
+        // this thread's features of the quarter: two of a piece of four (one of two)
+        constexpr int kF = DP / 64;
+        float x[2] = {0.0f, 0.0f};
+        const float* from = reinterpret_cast<const float*>(base + L::merge) + r * L::kPitch + piece * kN + two;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i)
+#pragma unroll
+          for (int e = 0; e < kF; ++e) x[e] = fmaf(from[i * kRows * L::kPitch + e], f[i], x[e]);
+        const int d = piece * (DP / 8) + k * kN + two;
+        if (w.slot < 0) {
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          const uint32_t y = l == 0.0f ? 0u : pack2<BF16>(x[0] * inv, x[1] * inv);
+          uint16_t* to = a.f.out + row * a.f.out_stride + static_cast<size_t>(h) * s.D + d;
+          if (d < s.D) {
+            if constexpr (kF == 2)
+              *reinterpret_cast<uint32_t*>(to) = y;
+            else
+              *to = static_cast<uint16_t>(y);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < kF; ++e) a.f.part_o[at * DP + d + e] = x[e];
+        }
       }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars->merge_full));
-    if (!mbar_wait_warp_inl(smem_u32(&bars->merge_full), merges & 1, g)) return;
-    ++merges;
-    const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 8;  // row, eight features
-    if (d0 < DP && r / G < w.nt) {
-      float2 ml[kWarps];
-      float big = -INFINITY, l = 0.0f, f[kWarps];
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        ml[i] = bars->ml[i][r];
-        if (ml[i].y != 0.0f) big = fmaxf(big, ml[i].x);
-      }
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        // (a share that saw a NaN may have no maximum: its l is NaN, whatever it is scaled by)
-        f[i] = ml[i].y == 0.0f ? 0.0f : (big == -INFINITY ? 1.0f : ex2(ml[i].x - big));
-        if (ml[i].y != 0.0f) l += ml[i].y * f[i];
-      }
-      float x[8] = {};
-      const float* from = reinterpret_cast<const float*>(base + L::merge) + r * L::kPitch + d0;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        const float4 y0 = *reinterpret_cast<const float4*>(from + i * kRows * L::kPitch);
-        const float4 y1 = *reinterpret_cast<const float4*>(from + i * kRows * L::kPitch + 4);
-        if (f[i] == 0.0f && ml[i].y == 0.0f) continue;
-        x[0] = fmaf(y0.x, f[i], x[0]), x[1] = fmaf(y0.y, f[i], x[1]), x[2] = fmaf(y0.z, f[i], x[2]), x[3] = fmaf(y0.w, f[i], x[3]);
-        x[4] = fmaf(y1.x, f[i], x[4]), x[5] = fmaf(y1.y, f[i], x[5]), x[6] = fmaf(y1.z, f[i], x[6]), x[7] = fmaf(y1.w, f[i], x[7]);
-      }
-      const size_t row = static_cast<size_t>(w.row0) + w.t0 + r / G;
-      const int h = w.kvh * G + r % G;
-      if (w.slot < 0) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint32_t y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = l == 0.0f ? 0u : pack2<BF16>(x[2 * e] * inv, x[2 * e + 1] * inv);
-        if (d0 < s.D)
-          *reinterpret_cast<uint4*>(a.f.out + row * a.f.out_stride + static_cast<size_t>(h) * s.D + d0) =
-              make_uint4(y[0], y[1], y[2], y[3]);
-        if (d0 == 0) a.f.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
-      } else {
-        const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + w.slot) * 256 + r;
-        float4* to = reinterpret_cast<float4*>(a.f.part_o + at * DP + d0);
-        to[0] = make_float4(x[0], x[1], x[2], x[3]);
-        to[1] = make_float4(x[4], x[5], x[6], x[7]);
-        if (d0 == 0) a.f.part_ml[at] = make_float2(big, l);
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->merge_empty));
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars->merge_empty));
+    if (out && piece == 0 && two == 0 && (threadIdx.x & 1) == 0) {
+      if (w.slot < 0)
+        a.f.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
+      else
+        a.f.part_ml[at] = make_float2(big, l);
+    }
   }
 }
 
@@ -427,14 +498,15 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
     bars->tiles = 0;
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(smem_u32(&bars->desc_full[i]), 1);
-      mbar_init(smem_u32(&bars->desc_empty[i]), kWarps);
+      mbar_init(smem_u32(&bars->desc_empty[i]), kWarps + 1);
     }
-    for (int i = 0; i < L::kStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&bars->full[i]), 17);  // the copies' bytes, and a lane for each scale
-      mbar_init(smem_u32(&bars->empty[i]), kWarps);
+      mbar_init(smem_u32(&bars->empty[i]), kGroups);
     }
     mbar_init(smem_u32(&bars->merge_full), kWarps);
     mbar_init(smem_u32(&bars->merge_empty), kWarps);
+    mbar_init(smem_u32(&bars->q_full), kWarps);
     fence_barrier_init();
   }
   if (warp == kWarps && lane == 0) {
@@ -445,11 +517,13 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
   const WaitGuard g{a.f.wait_ns, a.f.s.status, &bars->abort};
   if (warp == kWarps)
     produce<DP>(a, base, bars, g, lane);
+  else if (warp == kWarps + 1)
+    fetch_scales(a, bars, g, lane);
   else
     compute<DP, BF16>(a, base, bars, g);
   __syncthreads();
   if (warp == kWarps) {
-    const Owed owed[] = {{bars->full, L::kStages, bars->tiles}};
+    const Owed owed[] = {{bars->full, kStages, bars->tiles}};
     drain(owed, g);
   }
 }

@@ -40,8 +40,8 @@ __global__ void __launch_bounds__(256) evo_paged8_rows_kernel(const __grid_const
         if (has) {
           const uint32_t ku = *reinterpret_cast<const uint32_t*>(c.k_pages + p * c.k_page + at);
           const uint32_t vu = *reinterpret_cast<const uint32_t*>(c.v_pages + p * c.v_page + at);
-          const float2 k0 = unpack2<false>(f16x2_of_e4m3x2(ku)), k1 = unpack2<false>(f16x2_of_e4m3x2(ku >> 16));
-          const float2 v0 = unpack2<false>(f16x2_of_e4m3x2(vu)), v1 = unpack2<false>(f16x2_of_e4m3x2(vu >> 16));
+          const uint2 k2 = f16x4_of_codes(ku), v2 = f16x4_of_codes(vu);
+          const float2 k0 = unpack2<false>(k2.x), k1 = unpack2<false>(k2.y), v0 = unpack2<false>(v2.x), v1 = unpack2<false>(v2.y);
           k[0] = k0.x, k[1] = k0.y, k[2] = k1.x, k[3] = k1.y;
           v[0] = v0.x, v[1] = v0.y, v[2] = v1.x, v[3] = v1.y;
         }

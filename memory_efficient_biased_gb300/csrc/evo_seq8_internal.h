@@ -33,10 +33,13 @@ __device__ __forceinline__ long long scale_at(const Cache8& c, const SeqDesc& s,
   return (static_cast<long long>(p) * s.kv_heads + h) * c.blocks + (j % s.page) / c.block;
 }
 
-// Two codes (the lower byte first) as a pair of f16, exactly; NaN stays NaN.
-__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(codes));
+// Four codes as two pairs of f16 (bytes 0 and 1, bytes 2 and 3), exactly; NaN stays NaN.
+__device__ __forceinline__ uint2 f16x4_of_codes(uint32_t codes) {
+  uint2 r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(codes));
   return r;
 }
 // x (lower byte) and y rounded to e4m3, nearest even; NaN stays NaN, what is beyond 448 becomes 448.
@@ -48,11 +51,10 @@ __device__ __forceinline__ uint32_t e4m3x2_of_f32(float x, float y) {
 // Eight codes as numbers.
 __device__ __forceinline__ void f32_of_codes(uint2 codes, float (&x)[8]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? codes.x : codes.y;
-    const float2 f = unpack2<false>(f16x2_of_e4m3x2((i & 1) ? w >> 16 : w));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+  for (int i = 0; i < 2; ++i) {
+    const uint2 w = f16x4_of_codes(i ? codes.y : codes.x);
+    const float2 f = unpack2<false>(w.x), h = unpack2<false>(w.y);
+    x[4 * i] = f.x, x[4 * i + 1] = f.y, x[4 * i + 2] = h.x, x[4 * i + 3] = h.y;
   }
 }
 __device__ __forceinline__ uint2 codes_of_f32(const float (&x)[8]) {
