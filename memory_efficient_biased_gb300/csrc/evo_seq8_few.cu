@@ -24,8 +24,7 @@
 // bytes next to each other: of key g for the scores (lane = 4 g + c: features 16 c .. and 64 + 16 c ..), of keys
 // c, c + 4, c + 8, c + 12 for P·V (features 16 G(g) ..), whose bytes are paired by permutes.  Key (g / 2) + 4 (g % 2) stands
 // in column g of the scores and G(g) = (g % 2) 4 + g / 2, so that with the tiles' 128-byte swizzle no read meets a bank twice.
-#include "evo_seq8_internal.h"
-#include "evo_seq_sched.cuh"
+#include "evo_seq8_pages.cuh"
 
 namespace evo {
 namespace {
@@ -108,44 +107,6 @@ __device__ __forceinline__ void nan_values(uint32_t (&v)[4][COLS / 4], float (&o
 }
 
 // ------------------------------------------------------------ walk, loads, scales (a warp each for loads and scales)
-// The pages of an item's tiles, looked up a batch of tiles at a time, a page a lane, and a batch ahead, and
-// looked over only when their turn comes: looked up tile by tile, the table's latency under load was what a tile took.
-struct Pages {
-  const SeqDesc& s;
-  const int* table;
-  int pages, j1, kv_end;   // pages of a tile
-  int now, next, in;       // in: tiles of the batch that are done
-
-  __device__ __forceinline__ Pages(const SeqDesc& s, const Work& w, int pages)
-      : s(s), table(s.table + static_cast<size_t>(w.b) * s.pages_per_seq), pages(pages), j1(w.j1), kv_end(w.kv_end), in(0) {
-    now = look_up(w.j0);
-    next = look_up(w.j0 + 32 / pages);
-    now = look_over(w.j0, now);
-  }
-  __device__ __forceinline__ int place(int j) const {  // of this lane's page in the batch that begins at tile j
-    const int lane = threadIdx.x & 31;
-    j += lane / pages;
-    return j < j1 ? j * kTile + lane % pages * s.page : kv_end;
-  }
-  __device__ __forceinline__ int look_up(int j) const {
-    const int at = place(j);
-    return at < kv_end ? table[at / s.page] : s.num_pages;
-  }
-  __device__ __forceinline__ int look_over(int j, int p) const {  // (a page past the keys, or a bad one, reads as zeros)
-    if (p >= 0 && p < s.num_pages) return p;
-    if (place(j) < kv_end) report_bad_index(s.status);
-    return s.num_pages;
-  }
-  __device__ __forceinline__ int of(int i) const { return __shfl_sync(0xffffffffu, now, in * pages + i); }  // page i of the tile
-  __device__ __forceinline__ void step(int j) {  // tile j is done
-    if (++in == 32 / pages) {
-      in = 0;
-      now = look_over(j + 1, next);
-      next = look_up(j + 1 + 32 / pages);
-    }
-  }
-};
-
 template <int DP>
 __device__ __forceinline__ void produce(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
   using L = Layout<DP>;
@@ -195,9 +156,8 @@ __device__ __forceinline__ void produce(const Seq8FwdArgs& a, uint8_t* base, Bar
 __device__ __forceinline__ void fetch_scales(const Seq8FwdArgs& a, Bars* bars, const WaitGuard& g, int lane) {
   const SeqDesc& s = a.f.s;
   const Cache8& c = a.c;
-  const int pages = s.page < kTile ? kTile / s.page : 1, part = lane & 7, shift = __ffs(c.block) - 1;
-  const int mine = part * pages / 8, token = pages == 1 ? part * 16 : part % (8 / pages) * 16;  // page of the tile, place there
-  const float* scales = lane & 8 ? c.v_scales : c.k_scales;
+  const int pages = s.page < kTile ? kTile / s.page : 1;
+  const ScaleLane mine(s, c, lane);
   uint32_t use = 0;
   for (uint32_t it = 0;; ++it) {
     const uint32_t d = it % kDescs;
@@ -210,13 +170,13 @@ __device__ __forceinline__ void fetch_scales(const Seq8FwdArgs& a, Bars* bars, c
     int first = s.page > kTile ? (w.j0 * kTile) % s.page : 0;
     for (int j = w.j0; j < w.j1; ++j, ++use) {
       const uint32_t st = use % kStages;
-      const int p = look.of(mine);
-      const float* from = scales + (static_cast<long long>(p) * s.kv_heads + w.kvh) * c.blocks + ((first + token) >> shift);
+      const int p = look.of(mine.page);
+      const float* from = mine.at(s, c, w.kvh, p, first);
       if (!mbar_wait_warp_inl(smem_u32(&bars->empty[st]), ((use / kStages) & 1) ^ 1, g)) return;
       if (lane < 16) {
         const uint32_t full = smem_u32(&bars->full[st]);
-        float* to = &bars->scales[st][lane >> 3][part];
-        if (p < s.num_pages && j * kTile + part * 16 < w.kv_end) {
+        float* to = &bars->scales[st][lane >> 3][mine.part];
+        if (p < s.num_pages && j * kTile + mine.part * 16 < w.kv_end) {
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
         } else {
@@ -538,7 +498,7 @@ cudaError_t launch_t(const Seq8FwdArgs& a, int ctas, cudaStream_t st) {
   static_assert(smem <= 232448, "shared memory");
   kern<<<ctas, kThreads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.f.s.max_kv <= kTile) return e;  // one key tile: nothing is cut
-  return launch_seq_join(a.f, ctas, BF16, st);
+  return launch_seq_join(a.f, ctas, kRows, BF16, st);
 }
 
 }  // namespace

@@ -56,13 +56,14 @@ bool map_pages8(CUtensorMap* m, const void* p, const evo_seq_shape_t& s, const e
 }
 
 // Which kernel: up to 16 rows a sequence and kv head on the average, and a token's heads in one tile of 16.
+constexpr int kFewRows = 16;
 bool few_rows(const evo_seq_shape_t& s) {
   const int64_t G = s.q_heads / s.kv_heads;
-  return G <= 16 && s.tokens * G <= 16 * s.seqs;
+  return G <= kFewRows && s.tokens * G <= kFewRows * s.seqs;
 }
 // CTAs of a launch: as fwd_ctas, for items of W tokens.
 int few_ctas(int sms, const evo_seq_shape_t& s, int64_t max_kv) {
-  const double W = 16 / (s.q_heads / s.kv_heads);
+  const double W = kFewRows / (s.q_heads / s.kv_heads);
   const double units = (double(s.tokens) / W + double(s.seqs)) * (double(max_kv) + 2 * kTile) * double(s.kv_heads);
   return units < double(sms) * kTile ? static_cast<int>(units / kTile) + 1 : sms;
 }
@@ -198,16 +199,21 @@ evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pa
   a.f.TQ = kTile / a.f.s.group;
   const bool bf16 = dtype == EVO_BF16;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (!map_pages8(&a.f.tk, k_pages, shape, cache, c.k_page) || !map_pages8(&a.f.tv, v_pages, shape, cache, c.v_page))
+    return EVO_ERR_CUDA;
+  const bool few = few_rows(shape);
+  const int64_t max_kv = cache.page_size * cache.pages_per_seq;
+  const int ctas = few ? few_ctas(sms, shape, max_kv) : fwd_ctas(sms, shape, max_kv);
+  seq_fwd_workspace(ctas, static_cast<int>(shape.head_dim), &a.f, static_cast<uint8_t*>(workspace));
   cudaError_t e;
-  if (few_rows(shape)) {
-    if (!map_pages8(&a.f.tk, k_pages, shape, cache, c.k_page) || !map_pages8(&a.f.tv, v_pages, shape, cache, c.v_page))
-      return EVO_ERR_CUDA;
-    a.f.W = 16 / a.f.s.group;
-    const int ctas = few_ctas(sms, shape, cache.page_size * cache.pages_per_seq);
-    seq_fwd_workspace(ctas, static_cast<int>(shape.head_dim), &a.f, static_cast<uint8_t*>(workspace));
+  if (few) {
+    a.f.W = kFewRows / a.f.s.group;
     e = launch_paged8_few(a, ctas, bf16, cs);
   } else {
-    e = launch_paged8_rows(a, bf16, cs);
+    a.f.W = 2 * a.f.TQ;
+    a.f.out32 = aligned(out, 32) && t.out % 16 == 0;
+    if (!map_q(&a.f.tq, q, bf16, shape, t.q, a.f.TQ)) return EVO_ERR_CUDA;
+    e = launch_paged8_tiles(a, ctas, bf16, cs);
   }
   return e == cudaSuccess ? EVO_OK : cuda_fail("8-bit cache attention launch", e);
 }

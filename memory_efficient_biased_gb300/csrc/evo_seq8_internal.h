@@ -21,10 +21,9 @@ struct Cache8Args {  // append and read
 };
 
 struct Seq8FwdArgs {
-  SeqFwdArgs f;  // tk, tv: pages of bytes as (D, kv_heads, page, num_pages); W, TQ: the kernel's own, TQ as the join
-                 // takes it (128 / group)
+  SeqFwdArgs f;  // tk, tv: pages of bytes as (D, kv_heads, page, num_pages); TQ = 128 / group, W: tokens of an item
   Cache8 c;
-  const uint16_t* q;
+  const uint16_t* q;   // few rows
   long long q_stride;
 };
 
@@ -65,6 +64,6 @@ __device__ __forceinline__ uint2 codes_of_f32(const float (&x)[8]) {
 cudaError_t launch_cache8_append(const Cache8Args& a, bool bf16, cudaStream_t st);
 cudaError_t launch_cache8_read(const Cache8Args& a, bool bf16, cudaStream_t st);
 cudaError_t launch_paged8_few(const Seq8FwdArgs& a, int ctas, bool bf16, cudaStream_t st);
-cudaError_t launch_paged8_rows(const Seq8FwdArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_paged8_tiles(const Seq8FwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 
 }  // namespace evo

@@ -34,8 +34,7 @@
 // TFLOP/s of the scores that are seen (66 % of cuBLAS).  There a pair of tiles takes 3500 cycles a key
 // tile, the chain S (800), max (500), exponentials (850), P·V and back (1150); its MMAs alone take 2560
 // (80 each instead of 64: both operands from shared memory ask for all of its 128 bytes a cycle).
-#include "evo_seq_internal.h"
-#include "evo_seq_sched.cuh"
+#include "evo_seq_fwd.cuh"
 
 namespace evo {
 namespace {
@@ -44,7 +43,6 @@ constexpr int kThreads = 384;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kWalkWarp = 11;
 constexpr uint32_t kRegsLaunch = 168, kRegsSoftmax = 200, kRegsOther = 104;
 static_assert(128 * kRegsOther + 256 * kRegsSoftmax <= kThreads * kRegsLaunch, "register split exceeds the launch");
-constexpr float kMoveLog2 = 8.0f;  // the reference moves only past this margin
 constexpr int kDescs = 4, kReady = 8, kMaxSlots = 10;
 static_assert(kReady >= kMaxSlots / 2 + 1, "a V tile's release must not lap the MMA threads");
 
@@ -73,9 +71,6 @@ struct Layout {
 };
 static_assert(Layout<128>::total + 1024 <= 232448, "shared memory");
 
-__device__ __forceinline__ uint32_t col_s(uint32_t g) { return g * 128u; }
-__device__ __forceinline__ uint32_t col_o(uint32_t g) { return 256u + g * 128u; }
-
 // The next descriptor, read by every lane of a warp (or by one thread alone).
 template <bool WARP>
 __device__ __forceinline__ bool take(Bars* bars, uint32_t it, const WaitGuard& g, Work& w) {
@@ -89,22 +84,6 @@ __device__ __forceinline__ bool take(Bars* bars, uint32_t it, const WaitGuard& g
 __device__ __forceinline__ void give_back(Bars* bars, uint32_t it) {
   mbar_arrive(smem_u32(&bars->desc_empty[it % kDescs]));
 }
-// One tile of queries: its key tiles alternate between the warpgroups.
-__device__ __forceinline__ bool single(const Work& w, int TQ) { return w.nt <= TQ; }
-// The key tiles of this piece that warpgroup g works on: from, from + step, ... below to.
-struct Share {
-  int from, to, step;
-};
-__device__ __forceinline__ Share share_of(const Work& w, int g, int TQ) {
-  if (single(w, TQ)) return Share{w.j0 + g, w.j1, 2};
-  int kt = w.kt;
-  if (g == 0) {
-    const int end = w.pos + TQ;
-    kt = end > 0 ? (end + kTile - 1) / kTile : 1;
-  }
-  return Share{w.j0, kt < w.j1 ? kt : w.j1, 1};
-}
-
 // ------------------------------------------------------------ producer (one warp)
 template <int DP>
 __device__ __forceinline__ void producer(const SeqFwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
@@ -361,12 +340,6 @@ __device__ __forceinline__ void walk(const SeqFwdArgs& a, uint8_t* base, Bars* b
 }
 
 // ------------------------------------------------------------ softmax (warps 0..7)
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-
 // Max of 32 scores (columns c0..), those past column `lim` taken out when MASK.
 template <bool MASK>
 __device__ __forceinline__ void chunk_max(uint32_t (&y)[32], int lim, float& mt) {
@@ -392,21 +365,6 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&y)[32], float2 sl2, f
     rs = add2(rs, make_float2(p0, p1));
     pp[x >> 1] = pack2<BF16>(p0, p1);
   }
-}
-
-// This thread's row of an accumulator times alpha.  Warp-collective.
-template <int DP>
-__device__ __forceinline__ void rescale(uint32_t ocol, float alpha) {
-#pragma unroll 1
-  for (int c = 0; c < DP / 16; ++c) {
-    uint32_t x[16];
-    tmem_ld16(ocol + c * 16, x);
-    tmem_wait_ld(x);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-    tmem_st16(ocol + c * 16, x);
-  }
-  tmem_wait_st();
 }
 
 // 64 scores, times s·log2 e, for the sums of the weights.
@@ -832,7 +790,7 @@ template <int DP, bool BF16>
 cudaError_t launch_t(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
   const cudaError_t e = a.scores ? launch_k<DP, BF16, true>(a, ctas, st) : launch_k<DP, BF16, false>(a, ctas, st);
   if (e != cudaSuccess || a.s.max_kv <= kTile) return e;  // one key tile: nothing is cut
-  return launch_seq_join(a, ctas, BF16, st);
+  return launch_seq_join(a, ctas, 256, BF16, st);
 }
 
 }  // namespace
@@ -856,8 +814,8 @@ size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws) {
   return off;
 }
 
-cudaError_t launch_seq_join(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st) {
-  const dim3 grid(ctas, 256 / kJoinRows);
+cudaError_t launch_seq_join(const SeqFwdArgs& a, int ctas, int rows, bool bf16, cudaStream_t st) {
+  const dim3 grid(ctas, (rows + kJoinRows - 1) / kJoinRows);
   if (a.s.D <= 64) {
     if (bf16)
       evo_seq_join_kernel<64, true><<<grid, 256, 0, st>>>(a, ctas);

@@ -184,8 +184,9 @@ size_t prompt_bwd_workspace(int ctas, const SeqDesc& s, SeqBwdArgs* a, uint8_t* 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_seq_fwd(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st);
-// Joins the pieces that cut items left in a forward's workspace (a: s, TQ, out, lse, records, part_ml, part_o).
-cudaError_t launch_seq_join(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st);
+// Joins the pieces, of at most `rows` rows, that cut items left in a forward's workspace (a: s, TQ, out, lse, records,
+// part_ml, part_o).
+cudaError_t launch_seq_join(const SeqFwdArgs& a, int ctas, int rows, bool bf16, cudaStream_t st);
 cudaError_t launch_seq_weights(const SeqWeightsArgs& a, int ctas, bool bf16, cudaStream_t st);
 cudaError_t launch_prompt_bwd(const SeqBwdArgs& a, int ctas, int rows, bool bf16, cudaStream_t st);
 
