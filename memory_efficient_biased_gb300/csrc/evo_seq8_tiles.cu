@@ -352,9 +352,10 @@ __device__ __forceinline__ void widen(const Seq8FwdArgs& a, uint8_t* base, Bars*
 }
 
 // ------------------------------------------------------------ softmax (warps 0..7)
-// The maximum of t + log2 s_v over 32 scores (columns c0.. of the row, lim the last that it sees), 16 of which share scales.
+// The maximum of t + log2 s_v over 32 scores (columns c0.. of the row, lim the last that it sees), 16 of which share scales:
+// f = s_k · what turns the row's products into scores, lv = log2 s_v.
 template <bool MASK>
-__device__ __forceinline__ void chunk_max(uint32_t (&y)[32], int lim, const float* sk, const float* lv, float unit, float& mt) {
+__device__ __forceinline__ void chunk_max(uint32_t (&y)[32], int lim, const float* f, const float* lv, float& mt) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float mx[2] = {-INFINITY, -INFINITY};
@@ -366,18 +367,17 @@ __device__ __forceinline__ void chunk_max(uint32_t (&y)[32], int lim, const floa
       }
       mx[(x >> 1) & 1] = max3(mx[(x >> 1) & 1], __uint_as_float(y[x]), __uint_as_float(y[x + 1]));
     }
-    mt = fmaxf(mt, fmaf(fmaxf(mx[0], mx[1]), fmaxf(sk[h] * unit, 1.2e-38f), lv[h]));
+    mt = fmaxf(mt, fmaf(fmaxf(mx[0], mx[1]), f[h], lv[h]));
   }
 }
 
 // P' = 2^(t + log2 s_v - M) of 32 scores, packed, and the sum of P' / s_v.
-__device__ __forceinline__ void chunk_exp(const uint32_t (&y)[32], const float* sk, const float* lv, const float* iv, float unit,
-                                          float m, uint32_t (&pp)[16], float& l) {
+__device__ __forceinline__ void chunk_exp(const uint32_t (&y)[32], const float* f, const float* lv, const float* iv, float m,
+                                          uint32_t (&pp)[16], float& l) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    // (a factor that underflows would make an unseen score's -inf a NaN)
-    const float f = fmaxf(sk[h] * unit, 1.2e-38f), b = lv[h] - m;
-    const float2 f2 = make_float2(f, f), b2 = make_float2(b, b);
+    const float b = lv[h] - m;
+    const float2 f2 = make_float2(f[h], f[h]), b2 = make_float2(b, b);
     float2 rs = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int x = 16 * h; x < 16 * h + 16; x += 2) {
@@ -459,16 +459,19 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
         continue;
       }
       next += sh.step;
+      if (!mbar_wait_warp_inl(sc_full, sc_phase, g)) { ok = false; break; }
+      float f[8], lv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = bars->scales[slot][0][e], lv[e] = bars->scales[slot][1][e];
+      const float* iv = bars->scales[slot][2];
       if (!mbar_wait_warp_inl(smem_u32(&bars->s_full[gq]), u & 1, g)) { ok = false; break; }
       tc_fence_after();
-      if (!mbar_wait_warp_inl(sc_full, sc_phase, g)) { ok = false; break; }
       if constexpr (BF16) {
         if (!begun) {  // (written before the first scores were formed)
           unit = a.f.scale_log2 * bars->unit[it % kDescs][(one ? 0 : gq * 128) + r];
           begun = true;
         }
       }
-      const float *sk = bars->scales[slot][0], *lv = bars->scales[slot][1], *iv = bars->scales[slot][2];
       uint32_t ya[64], yb[64];
       uint32_t(&y0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[0]);
       uint32_t(&y1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[32]);
@@ -476,22 +479,24 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
       uint32_t(&y3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&yb[32]);
       float mt = -INFINITY;
       tmem_ld64(scol, ya);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = fmaxf(f[e] * unit, 1.2e-38f);  // (one that underflows would make -inf a NaN)
       tmem_wait_ld(ya);
       tmem_ld64(scol + 64, yb);
       if (w.pos + first >= j * kTile + kTile - 1) {
         // the tile's first token sees the whole key tile: no row needs its mask
-        chunk_max<false>(y0, 0, sk, lv, unit, mt);
-        chunk_max<false>(y1, 0, sk + 2, lv + 2, unit, mt);
+        chunk_max<false>(y0, 0, f, lv, mt);
+        chunk_max<false>(y1, 0, f + 2, lv + 2, mt);
         tmem_wait_ld(yb);
-        chunk_max<false>(y2, 0, sk + 4, lv + 4, unit, mt);
-        chunk_max<false>(y3, 0, sk + 6, lv + 6, unit, mt);
+        chunk_max<false>(y2, 0, f + 4, lv + 4, mt);
+        chunk_max<false>(y3, 0, f + 6, lv + 6, mt);
       } else {
         const int lim = pos - j * kTile;
-        chunk_max<true>(y0, lim, sk, lv, unit, mt);
-        chunk_max<true>(y1, lim - 32, sk + 2, lv + 2, unit, mt);
+        chunk_max<true>(y0, lim, f, lv, mt);
+        chunk_max<true>(y1, lim - 32, f + 2, lv + 2, mt);
         tmem_wait_ld(yb);
-        chunk_max<true>(y2, lim - 64, sk + 4, lv + 4, unit, mt);
-        chunk_max<true>(y3, lim - 96, sk + 6, lv + 6, unit, mt);
+        chunk_max<true>(y2, lim - 64, f + 4, lv + 4, mt);
+        chunk_max<true>(y3, lim - 96, f + 6, lv + 6, mt);
       }
       bool moved = false;
       float alpha = 1.0f;
@@ -511,19 +516,19 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
       uint32_t pp[32];
       uint32_t(&p0)[16] = *reinterpret_cast<uint32_t(*)[16]>(&pp[0]);
       uint32_t(&p1)[16] = *reinterpret_cast<uint32_t(*)[16]>(&pp[16]);
-      chunk_exp(y0, sk, lv, iv, unit, m, p0, l);
-      chunk_exp(y1, sk + 2, lv + 2, iv + 2, unit, m, p1, l);
+      chunk_exp(y0, f, lv, iv, m, p0, l);
+      chunk_exp(y1, f + 2, lv + 2, iv + 2, m, p1, l);
       tmem_st32(scol, pp);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->p_half[gq]));
-      chunk_exp(y2, sk + 4, lv + 4, iv + 4, unit, m, p0, l);
+      chunk_exp(y2, f + 4, lv + 4, iv + 4, m, p0, l);
       if (j < both) {  // handed over a little early
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->turn[gq ^ 1]));
       }
-      chunk_exp(y3, sk + 6, lv + 6, iv + 6, unit, m, p1, l);
+      chunk_exp(y3, f + 6, lv + 6, iv + 6, m, p1, l);
       if (j < both) ++turns;
       tmem_st32(scol + 32, pp);
       tmem_wait_st();
