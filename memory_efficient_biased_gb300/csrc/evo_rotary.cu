@@ -8,7 +8,8 @@
 //
 // Work.  A thread keeps one token and VEC pairs, whose sines and cosines it forms once, and takes
 // every heads_apart-th head of q and then of k: its loads and stores are VEC elements wide, and a
-// head's threads lie next to each other.  F is formed once a block, in shared memory, as its few operations in 64 bits are
+// head's threads lie next to each other.  Features that pass are copied by threads behind all of
+// these (in the same warps, the two paths one behind the other, a half turned head took twice the time).  F is formed once a block, in shared memory, as its few operations in 64 bits are
 // the dearest here (a GB300 issues two a clock and SM).
 //
 // Bound by the bytes: every element read and written once.
@@ -26,8 +27,9 @@ struct RotaryArgs {
   const int* positions;
   const double* inv_freq;
   int tokens, q_heads, heads, D, half;  // heads: of q and k together
-  int units;                            // threads a head: pairs, then (not in place) the features that pass
+  int pairs, passing;                   // threads a head: for its pairs, and (not in place) for the features that pass
   int heads_apart;                      // threads a token and unit
+  long long turning;                    // threads that turn pairs; those behind them copy
   float factor, sine;                   // sine: ±factor
 };
 
@@ -81,20 +83,25 @@ __global__ void __launch_bounds__(kRotaryThreads) evo_rotary_kernel(const __grid
     turn[i] = static_cast<unsigned long long>((x - floor(x)) * 18446744073709551616.0);
   }
   __syncthreads();
-  const long long id = static_cast<long long>(blockIdx.x) * kRotaryThreads + threadIdx.x;
-  const int unit = static_cast<int>(id % a.units);
-  const long long rest = id / a.units;
+  long long id = static_cast<long long>(blockIdx.x) * kRotaryThreads + threadIdx.x;
+  const bool copy = id >= a.turning;
+  if (copy) id -= a.turning;
+  if (copy && a.passing == 0) return;
+  const int units = copy ? a.passing : a.pairs;
+  const long long rest = id / units;
+  const int unit = static_cast<int>(id - rest * units);
   const long long t = rest / a.heads_apart;
   if (t >= a.tokens) return;
-  const int first = static_cast<int>(rest % a.heads_apart), pairs = a.half / VEC;
+  const int first = static_cast<int>(rest - t * a.heads_apart);
   auto in = [&](int h) {
     return h < a.q_heads ? a.q + t * a.q_stride + h * a.D : a.k + t * a.k_stride + (h - a.q_heads) * a.D;
   };
   auto out = [&](int h) {
     return h < a.q_heads ? a.q_out + t * a.q_out_stride + h * a.D : a.k_out + t * a.k_out_stride + (h - a.q_heads) * a.D;
   };
-  if (unit >= pairs) {  // features that pass
-    const int at = 2 * a.half + (unit - pairs) * VEC;
+  if (copy) {
+    const int at = 2 * a.half + unit * VEC;
+#pragma unroll 8
     for (int h = first; h < a.heads; h += a.heads_apart)
       *reinterpret_cast<typename Pack<VEC>::T*>(out(h) + at) = *reinterpret_cast<const typename Pack<VEC>::T*>(in(h) + at);
     return;
@@ -144,7 +151,7 @@ __global__ void __launch_bounds__(kRotaryThreads) evo_rotary_kernel(const __grid
 
 template <bool BF16, bool INTERLEAVED, int VEC>
 cudaError_t launch_rotary_t(const RotaryArgs& a, cudaStream_t st) {
-  const long long threads = static_cast<long long>(a.tokens) * a.units * a.heads_apart;
+  const long long threads = a.turning + static_cast<long long>(a.tokens) * a.passing * a.heads_apart;
   evo_rotary_kernel<BF16, INTERLEAVED, VEC>
       <<<static_cast<unsigned>((threads + kRotaryThreads - 1) / kRotaryThreads), kRotaryThreads, 0, st>>>(a);
   return cudaGetLastError();
@@ -208,12 +215,14 @@ extern "C" evo_status_t evo_rotary(const void* q, const void* k, const int32_t* 
   // the widest accesses that the pairs allow (rows and heads start on 16 bytes)
   const int vec = a.half % 8 == 0 ? 8 : a.half % 4 == 0 ? 4 : a.half % 2 == 0 ? 2 : 1;
   const bool in_place = q_self && (!k || k_self);
-  a.units = a.half / vec + (in_place ? 0 : (a.D - 2 * a.half) / vec);
+  a.pairs = a.half / vec;
+  a.passing = in_place ? 0 : (a.D - 2 * a.half) / vec;
   // A thread takes about ten heads, for the cost of its sines, while there are enough threads to fill the SMs.
-  const int64_t fill = int64_t(sms) * 2048, per = T * a.units;
+  const int64_t fill = int64_t(sms) * 2048, per = T * (a.pairs + a.passing);
   int64_t apart = (a.heads + 9) / 10;
   if (per * apart < fill) apart = (fill + per - 1) / per;
   a.heads_apart = static_cast<int>(apart < a.heads ? apart : a.heads);
+  a.turning = T * a.pairs * a.heads_apart;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = bf16 ? (inter ? launch_rotary_v<true, true>(a, vec, st) : launch_rotary_v<true, false>(a, vec, st))
                              : (inter ? launch_rotary_v<false, true>(a, vec, st) : launch_rotary_v<false, false>(a, vec, st));

@@ -29,7 +29,7 @@
 namespace evo {
 namespace {
 
-constexpr int kRows = 16, kWarps = 12, kThreads = 32 * (kWarps + 2), kDescs = 4;
+constexpr int kRows = kFewRows, kWarps = 12, kThreads = 32 * (kWarps + 2), kDescs = 4;
 constexpr int kKeys = 16, kGroups = kTile / kKeys;  // keys that a warp takes at a time, warps to a tile
 constexpr int kStages = 6;                          // tiles
 
@@ -107,14 +107,14 @@ __device__ __forceinline__ void nan_values(uint32_t (&v)[4][COLS / 4], float (&o
 }
 
 // ------------------------------------------------------------ walk, loads, scales (a warp each for loads and scales)
-template <int DP>
+template <int DP, class Blocks>
 __device__ __forceinline__ void produce(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
   using L = Layout<DP>;
   const SeqDesc& s = a.f.s;
-  Walk<QueryBlocks> walk;
-  walk.init(s, QueryBlocks{a.f.W}, blockIdx.x, gridDim.x);
+  Walk<Blocks> walk;
+  walk.init(s, Blocks{a.f.W}, blockIdx.x, gridDim.x);
   PieceRecord* rec = a.f.records + 2 * blockIdx.x;
-  if (lane < 2) rec[lane].used = 0;
+  if (!a.whole && lane < 2) rec[lane].used = 0;
   __syncwarp();
   const int box = s.page < kTile ? s.page : kTile, pages = kTile / box;  // a copy's rows, copies (and pages) of a tile
   uint32_t use = 0;
@@ -373,7 +373,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
     // features 2 c | 2 c + 1): a quarter of the tiles, and with it of the features, at a time.
     const int r = threadIdx.x >> 4, piece = (threadIdx.x >> 1) & 7, two = (threadIdx.x & 1) * (DP / 64);  // row, features
     const bool out = r < kRows && r / G < w.nt;  // (rows past the item's are none's)
-    const size_t row = static_cast<size_t>(w.row0) + w.t0 + r / G, at = (static_cast<size_t>(blockIdx.x) * 2 + w.slot) * 256 + r;
+    const size_t row = static_cast<size_t>(w.row0) + w.t0 + r / G, at = (static_cast<size_t>(blockIdx.x) * 2 + w.slot) * kRows + r;
     const int h = w.kvh * G + r % G;
     float f[kWarps], big = -INFINITY, l = 0.0f;
 #pragma unroll
@@ -475,12 +475,16 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
   }
   __syncthreads();
   const WaitGuard g{a.f.wait_ns, a.f.s.status, &bars->abort};
-  if (warp == kWarps)
-    produce<DP>(a, base, bars, g, lane);
-  else if (warp == kWarps + 1)
+  if (warp == kWarps) {
+    if (a.whole)
+      produce<DP, WholeBlocks>(a, base, bars, g, lane);
+    else
+      produce<DP, QueryBlocks>(a, base, bars, g, lane);
+  } else if (warp == kWarps + 1) {
     fetch_scales(a, bars, g, lane);
-  else
+  } else {
     compute<DP, BF16>(a, base, bars, g);
+  }
   __syncthreads();
   if (warp == kWarps) {
     const Owed owed[] = {{bars->full, kStages, bars->tiles}};
@@ -497,8 +501,8 @@ cudaError_t launch_t(const Seq8FwdArgs& a, int ctas, cudaStream_t st) {
   constexpr size_t smem = Layout<DP>::bars + sizeof(Bars) + 1024;
   static_assert(smem <= 232448, "shared memory");
   kern<<<ctas, kThreads, smem, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.f.s.max_kv <= kTile) return e;  // one key tile: nothing is cut
-  return launch_seq_join(a.f, ctas, kRows, BF16, st);
+  if ((e = cudaGetLastError()) != cudaSuccess || a.whole) return e;
+  return launch_seq_join(a.f, ctas, BF16, st);
 }
 
 }  // namespace

@@ -55,17 +55,31 @@ bool map_pages8(CUtensorMap* m, const void* p, const evo_seq_shape_t& s, const e
                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
-// Which kernel: up to 16 rows a sequence and kv head on the average, and a token's heads in one tile of 16.
-constexpr int kFewRows = 16;
-bool few_rows(const evo_seq_shape_t& s) {
-  const int64_t G = s.q_heads / s.kv_heads;
-  return G <= kFewRows && s.tokens * G <= kFewRows * s.seqs;
+// Which kernel (few rows a key: up to 16 a sequence and kv head on the average, and a token's heads in one tile of
+// 16), and its launch.
+struct Plan {
+  bool few, whole;
+  int ctas, rows;  // rows: of a piece
+};
+constexpr int64_t kWholeKeys = 1024;
+Plan plan(int sms, const evo_seq_shape_t& s, const evo_cache8_shape_t& c) {
+  const int64_t G = s.q_heads / s.kv_heads, max_kv = c.page_size * c.pages_per_seq;
+  Plan p{};
+  p.few = G <= kFewRows && s.tokens * G <= kFewRows * s.seqs;
+  if (!p.few) {
+    p.ctas = fwd_ctas(sms, s, max_kv);
+    p.rows = 256;
+    return p;
+  }
+  p.rows = kFewRows;
+  const double items = (double(s.tokens) / double(kFewRows / G) + double(s.seqs)) * double(s.kv_heads);
+  p.whole = max_kv <= kTile || (max_kv <= kWholeKeys && items <= sms);
+  const double most = p.whole ? items : items * (double(max_kv) / kTile + 2);  // CTAs that the work can fill
+  p.ctas = most < sms ? static_cast<int>(most) + 1 : sms;
+  return p;
 }
-// CTAs of a launch: as fwd_ctas, for items of W tokens.
-int few_ctas(int sms, const evo_seq_shape_t& s, int64_t max_kv) {
-  const double W = kFewRows / (s.q_heads / s.kv_heads);
-  const double units = (double(s.tokens) / W + double(s.seqs)) * (double(max_kv) + 2 * kTile) * double(s.kv_heads);
-  return units < double(sms) * kTile ? static_cast<int>(units / kTile) + 1 : sms;
+size_t workspace_of(const Plan& p, const evo_seq_shape_t& s, SeqFwdArgs* a, void* ws) {
+  return seq_fwd_workspace(p.whole ? 0 : p.ctas, static_cast<int>(s.head_dim), a, static_cast<uint8_t*>(ws), p.rows);
 }
 
 // What an append and a read check alike.
@@ -111,7 +125,7 @@ evo_status_t rows_call(bool append, const void* k, const void* v, const int32_t*
   a.k_stride = t.k, a.v_stride = t.v;
   const bool bf16 = dtype == EVO_BF16;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = append ? launch_cache8_append(a, bf16, cs) : launch_cache8_read(a, bf16, cs);
+  const cudaError_t e = append ? launch_cache8_append(a, bf16, cs) : launch_cache8_read(a, sms, bf16, cs);
   return e == cudaSuccess ? EVO_OK : cuda_fail(append ? "8-bit cache append launch" : "8-bit cache read launch", e);
 }
 
@@ -141,9 +155,7 @@ evo_status_t evo_cache8_read(const void* k_pages, const void* v_pages, const flo
 size_t evo_paged8_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache8_shape_t cache) {
   Checked c;
   if (check_seq_shape(shape, true) != EVO_OK || check_cache8(cache, shape, &c) != EVO_OK) return 0;
-  const int64_t max_kv = cache.page_size * cache.pages_per_seq;
-  const int ctas = few_rows(shape) ? few_ctas(num_sms(), shape, max_kv) : fwd_ctas(num_sms(), shape, max_kv);
-  return seq_fwd_workspace(ctas, static_cast<int>(shape.head_dim), nullptr, nullptr);
+  return workspace_of(plan(num_sms(), shape, cache), shape, nullptr, nullptr);
 }
 
 evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
@@ -201,19 +213,18 @@ evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pa
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (!map_pages8(&a.f.tk, k_pages, shape, cache, c.k_page) || !map_pages8(&a.f.tv, v_pages, shape, cache, c.v_page))
     return EVO_ERR_CUDA;
-  const bool few = few_rows(shape);
-  const int64_t max_kv = cache.page_size * cache.pages_per_seq;
-  const int ctas = few ? few_ctas(sms, shape, max_kv) : fwd_ctas(sms, shape, max_kv);
-  seq_fwd_workspace(ctas, static_cast<int>(shape.head_dim), &a.f, static_cast<uint8_t*>(workspace));
+  const Plan p = plan(sms, shape, cache);
+  workspace_of(p, shape, &a.f, workspace);
+  a.whole = p.whole;
   cudaError_t e;
-  if (few) {
+  if (p.few) {
     a.f.W = kFewRows / a.f.s.group;
-    e = launch_paged8_few(a, ctas, bf16, cs);
+    e = launch_paged8_few(a, p.ctas, bf16, cs);
   } else {
     a.f.W = 2 * a.f.TQ;
     a.f.out32 = aligned(out, 32) && t.out % 16 == 0;
     if (!map_q(&a.f.tq, q, bf16, shape, t.q, a.f.TQ)) return EVO_ERR_CUDA;
-    e = launch_paged8_tiles(a, ctas, bf16, cs);
+    e = launch_paged8_tiles(a, p.ctas, bf16, cs);
   }
   return e == cudaSuccess ? EVO_OK : cuda_fail("8-bit cache attention launch", e);
 }

@@ -18,13 +18,18 @@ struct Cache8Args {  // append and read
   Cache8 c;
   uint16_t *k, *v;   // rows: read by an append, written by a read
   long long k_stride, v_stride;
+  int tokens_a_warp;   // read
+  uint32_t per_magic;  // read: ceil(2^32 / (16-code pieces of a head)), for exact quotients below 2^29
 };
+
+constexpr int kFewRows = 16;  // rows of a tile of the kernel for few rows a key
 
 struct Seq8FwdArgs {
   SeqFwdArgs f;  // tk, tv: pages of bytes as (D, kv_heads, page, num_pages); TQ = 128 / group, W: tokens of an item
   Cache8 c;
   const uint16_t* q;   // few rows
   long long q_stride;
+  int whole;           // few rows: no item is cut, and nothing is joined
 };
 
 // Place of the scale of token j (of page p) and head h.
@@ -62,7 +67,7 @@ __device__ __forceinline__ uint2 codes_of_f32(const float (&x)[8]) {
 }
 
 cudaError_t launch_cache8_append(const Cache8Args& a, bool bf16, cudaStream_t st);
-cudaError_t launch_cache8_read(const Cache8Args& a, bool bf16, cudaStream_t st);
+cudaError_t launch_cache8_read(const Cache8Args& a, int sms, bool bf16, cudaStream_t st);
 cudaError_t launch_paged8_few(const Seq8FwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 cudaError_t launch_paged8_tiles(const Seq8FwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 

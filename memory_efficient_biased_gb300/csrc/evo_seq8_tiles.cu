@@ -733,7 +733,7 @@ cudaError_t launch_t(const Seq8FwdArgs& a, int ctas, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   kern<<<ctas, kThreads, Layout<DP>::total + 1024, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.f.s.max_kv <= kTile) return e;  // one key tile: nothing is cut
-  return launch_seq_join(a.f, ctas, 256, BF16, st);
+  return launch_seq_join(a.f, ctas, BF16, st);
 }
 
 }  // namespace

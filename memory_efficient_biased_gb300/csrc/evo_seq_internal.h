@@ -137,8 +137,9 @@ struct SeqFwdArgs {
   long long out_stride;
   float* lse;
   PieceRecord* records;  // workspace: two per CTA, and one for the sums of the scores
-  float2* part_ml;       // ... [ctas][2][256] (m, l)
-  float* part_o;         // ... [ctas][2][256][DP], not yet divided by l
+  int piece_rows;        // rows of a piece (256, or the 8-bit cache's 16)
+  float2* part_ml;       // ... [ctas][2][piece_rows] (m, l)
+  float* part_o;         // ... [ctas][2][piece_rows][DP], not yet divided by l
   float* scores;         // nullable: s·log2e·S left behind for the weights, [tokens][q_heads][scores_ld]
   long long scores_ld;   // max_kv rounded up to whole tiles
   uint64_t wait_ns;
@@ -160,7 +161,7 @@ struct SeqWeightsArgs {
   uint64_t wait_ns;
 };
 // Bytes of the workspace for `ctas` CTAs; with a and ws, a's pointers into it.
-size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws);
+size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws, int piece_rows = 256);
 
 // The prompt's backward on the tensor cores (tk, tv as the prompt forward's).
 struct SeqBwdArgs {
@@ -184,9 +185,8 @@ size_t prompt_bwd_workspace(int ctas, const SeqDesc& s, SeqBwdArgs* a, uint8_t* 
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t st);
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
 cudaError_t launch_seq_fwd(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st);
-// Joins the pieces, of at most `rows` rows, that cut items left in a forward's workspace (a: s, TQ, out, lse, records,
-// part_ml, part_o).
-cudaError_t launch_seq_join(const SeqFwdArgs& a, int ctas, int rows, bool bf16, cudaStream_t st);
+// Joins the pieces that cut items left in a forward's workspace (a: s, TQ, out, lse, and the workspace's).
+cudaError_t launch_seq_join(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 cudaError_t launch_seq_weights(const SeqWeightsArgs& a, int ctas, bool bf16, cudaStream_t st);
 cudaError_t launch_prompt_bwd(const SeqBwdArgs& a, int ctas, int rows, bool bf16, cudaStream_t st);
 

@@ -85,6 +85,13 @@ struct QueryBlocks {
   __device__ __forceinline__ int tile(const Work&, long long keys) const { return static_cast<int>(keys / kTile); }
 };
 
+// The same blocks, none of them cut: each counts alike, and a CTA takes whole ones.
+struct WholeBlocks : QueryBlocks {
+  __device__ __forceinline__ int cost() const { return 0; }
+  __device__ __forceinline__ long long of(const Seq&, int) const { return kTile; }
+  __device__ __forceinline__ long long before(const Seq&, int p) const { return static_cast<long long>(p) * kTile; }
+};
+
 // Tiles of 128 keys under the tiles of TQ query tokens that see them (dK and dV of a prompt).
 // Work: t0, nt the keys; j0, j1, kt tiles of queries.
 struct KeyBlocks {
@@ -107,6 +114,15 @@ struct KeyBlocks {
     return static_cast<int>((w.t0 + tokens) / TQ);
   }
 };
+
+// A CTA's share of the units: at least a tile, or whole blocks.
+template <class Blocks>
+__device__ __forceinline__ long long share_of_cta(const Blocks&, long long units) {
+  return units < kTile ? kTile : units;
+}
+__device__ __forceinline__ long long share_of_cta(const WholeBlocks&, long long units) {
+  return (units + kTile - 1) / kTile * kTile;
+}
 
 // The walk of one CTA over its share; run by one whole warp (every lane holds the state).
 template <class Blocks>
@@ -151,8 +167,7 @@ struct Walk {
       report_bad_index(desc.status);
       all = 0;
     }
-    long long share = (all + ctas - 1) / ctas;
-    if (share < kTile) share = kTile;
+    const long long share = share_of_cta(k, (all + ctas - 1) / ctas);
     const long long x0 = share * cta;
     left = all - x0 < share ? all - x0 : share;
     b = desc.seqs;
