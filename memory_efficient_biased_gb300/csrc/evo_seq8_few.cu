@@ -14,41 +14,45 @@
 // in registers are read once from the staged tile and widened on their way into the product: 2 bytes. The
 // products need 16 rows · 23 = 370 multiply-adds a clock and SM, a third of what mma.sync has.
 //
-// Roles (13 warps, one CTA per SM, persistent over its share of the work, evo_seq_sched.cuh):
+// Roles (16 warps, one CTA per SM, persistent over its share of the work, evo_seq_sched.cuh):
 //   warps 0-11  32 keys at a time each (16 share their scales), in turns; M, l and O of their own, joined at the end of an
 //               item.  Three a scheduler, for what a warp waits for between its products; that takes q out of their
 //               registers, into shared memory
-//   warp 12     the walk over the work; keys and values by TMA (a page is a box), scales by cp.async
+//   warps 12-15 the walk over the work, and keys by TMA (a page is a box); values; scales by cp.async; q, an item ahead.
+//               A warp each: what one of them did for a tile, beside three busy warps, took longer than the tile
 //
 // Fragments.  Inside a product the order of the features (scores) and of the keys (P·V) is free, so a lane takes 16
 // bytes next to each other: of key g for the scores (lane = 4 g + c: features 16 c .. and 64 + 16 c ..), of keys
 // c, c + 4, c + 8, c + 12 for P·V (features 16 G(g) ..), whose bytes are paired by permutes.  Key (g / 2) + 4 (g % 2) stands
 // in column g of the scores and G(g) = (g % 2) 4 + g / 2, so that with the tiles' 128-byte swizzle no read meets a bank twice.
+#include <type_traits>
+
 #include "evo_seq8_pages.cuh"
 
 namespace evo {
 namespace {
 
-constexpr int kRows = kFewRows, kWarps = 12, kThreads = 32 * (kWarps + 2), kDescs = 4;
-constexpr int kKeys = 16, kGroups = kTile / kKeys;  // keys that a warp takes at a time, warps to a tile
+constexpr int kRows = kFewRows, kWarps = 12, kThreads = 32 * (kWarps + 4), kDescs = 4;
+constexpr int kKeys = 16, kGroups = kTile / kKeys;  // keys that a warp takes at a time, times that a tile is
 constexpr int kStages = 6;                          // tiles
+constexpr int kJoined = 4;                          // rows whose shares are joined at a time, a warp each
 
 template <int DP>
 struct Layout {
   static constexpr uint32_t kTB = kTile * DP;     // codes of a tile's keys, and of its values
-  static constexpr int kPitch = DP / 4 + 4;       // floats between rows of a quarter of a warp's O
-  static constexpr uint32_t ring = 0, merge = kStages * 2 * kTB, q = merge + kWarps * kRows * kPitch * 4;
-  static constexpr uint32_t bars = q + kRows * DP * 2;
+  static constexpr int kPitch = DP + 4;           // floats between rows of O to join: O, then M and l
+  static constexpr uint32_t kQ = kRows * DP * 2;
+  static constexpr uint32_t ring = 0, merge = kStages * 2 * kTB, q = merge + kWarps * kJoined * kPitch * 4;
+  static constexpr uint32_t bars = q + 2 * kQ;
 };
 
 struct Bars {
   uint64_t desc_full[kDescs], desc_empty[kDescs];
   uint64_t full[kStages], empty[kStages];
-  uint64_t merge_full, merge_empty, q_full;
+  uint64_t merge_full, merge_empty, q_full[2], q_empty[2];
   alignas(8) float scales[kStages][2][8];  // of a stage: keys and values, 16 tokens each
   Work work[kDescs];
-  float2 ml[kWarps][kRows];
-  float unit[kRows];              // scale · log2 e, and the power of two that q was divided by
+  float unit[2][kRows];           // scale · log2 e, and the power of two that q was divided by
   uint32_t tiles;
   int abort;
 };
@@ -106,17 +110,50 @@ __device__ __forceinline__ void nan_values(uint32_t (&v)[4][COLS / 4], float (&o
   }
 }
 
-// ------------------------------------------------------------ walk, loads, scales (a warp each for loads and scales)
+// ------------------------------------------------------------ walk, loads, scales and q (a warp each)
+// The next descriptor, for a warp that takes each one; false: no more work, or given up.
+__device__ __forceinline__ bool take(Bars* bars, uint32_t it, const WaitGuard& g, Work& w) {
+  const uint32_t d = it % kDescs;
+  if (!mbar_wait_warp_inl(smem_u32(&bars->desc_full[d]), (it / kDescs) & 1, g)) return false;
+  w = bars->work[d];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bars->desc_empty[d]));
+  return !w.stop;
+}
+
+// One item's tiles of keys, or of values, into the ring.
+template <int DP>
+__device__ __forceinline__ bool load_tiles(const Seq8FwdArgs& a, const CUtensorMap* map, uint32_t to, Bars* bars, const Work& w,
+                                           uint32_t& use, const WaitGuard& g) {
+  using L = Layout<DP>;
+  const SeqDesc& s = a.f.s;
+  const int box = s.page < kTile ? s.page : kTile, pages = kTile / box;  // a copy's rows, copies (and pages) of a tile
+  Pages look(s, w, pages);
+  int first = s.page > kTile ? (w.j0 * kTile) % s.page : 0;  // row of the page that the tile begins at
+  for (int j = w.j0; j < w.j1; ++j, ++use) {
+    const uint32_t st = use % kStages;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->empty[st]), ((use / kStages) & 1) ^ 1, g)) return false;
+    const uint32_t full = smem_u32(&bars->full[st]), dst = to + st * 2 * L::kTB;
+    if (elect_one()) mbar_arrive_expect_tx(full, L::kTB);
+    for (int b = 0; b < pages; ++b) {
+      const int p = look.of(b);
+      if (elect_one()) tma_load_4d(dst + b * box * DP, map, full, 0, w.kvh, first, p);
+    }
+    __syncwarp();
+    if (s.page > kTile && (first += kTile) == s.page) first = 0;
+    look.step(j);
+  }
+  return true;
+}
+
 template <int DP, class Blocks>
 __device__ __forceinline__ void produce(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
   using L = Layout<DP>;
-  const SeqDesc& s = a.f.s;
   Walk<Blocks> walk;
-  walk.init(s, Blocks{a.f.W}, blockIdx.x, gridDim.x);
+  walk.init(a.f.s, Blocks{a.f.W}, blockIdx.x, gridDim.x);
   PieceRecord* rec = a.f.records + 2 * blockIdx.x;
   if (!a.whole && lane < 2) rec[lane].used = 0;
   __syncwarp();
-  const int box = s.page < kTile ? s.page : kTile, pages = kTile / box;  // a copy's rows, copies (and pages) of a tile
   uint32_t use = 0;
   for (uint32_t it = 0;; ++it) {
     const Work w = walk.next();
@@ -127,45 +164,27 @@ __device__ __forceinline__ void produce(const Seq8FwdArgs& a, uint8_t* base, Bar
       if (!w.stop && w.slot >= 0) rec[w.slot] = PieceRecord{1, w.j1 == w.kt, w.b, w.kvh, w.row0, w.t0, w.nt, 0};
       mbar_arrive(smem_u32(&bars->desc_full[d]));
     }
-    if (w.stop) break;
-    Pages look(s, w, pages);
-    int first = s.page > kTile ? (w.j0 * kTile) % s.page : 0;  // row of the page that the tile begins at
-    bool ok = true;
-    for (int j = w.j0; j < w.j1; ++j, ++use) {
-      const uint32_t st = use % kStages;
-      if (!mbar_wait_warp_inl(smem_u32(&bars->empty[st]), ((use / kStages) & 1) ^ 1, g)) { ok = false; break; }
-      const uint32_t full = smem_u32(&bars->full[st]), dst = smem_u32(base + L::ring + st * 2 * L::kTB);
-      if (elect_one()) mbar_arrive_expect_tx(full, 2 * L::kTB);
-      for (int b = 0; b < pages; ++b) {
-        const int p = look.of(b);
-        if (elect_one()) {
-          tma_load_4d(dst + b * box * DP, &a.f.tk, full, 0, w.kvh, first, p);
-          tma_load_4d(dst + L::kTB + b * box * DP, &a.f.tv, full, 0, w.kvh, first, p);
-        }
-      }
-      __syncwarp();
-      if (s.page > kTile && (first += kTile) == s.page) first = 0;
-      look.step(j);
-    }
-    if (!ok) break;
+    if (w.stop || !load_tiles<DP>(a, &a.f.tk, smem_u32(base + L::ring), bars, w, use, g)) break;
   }
   if (lane == 0) bars->tiles = use;
 }
 
-// The scales of a tile: lanes 0-7 keys, 8-15 values, 16 tokens each.
+template <int DP>
+__device__ __forceinline__ void load_values(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g) {
+  uint32_t use = 0;
+  Work w;
+  for (uint32_t it = 0; take(bars, it, g, w); ++it)
+    if (!load_tiles<DP>(a, &a.f.tv, smem_u32(base + Layout<DP>::ring + Layout<DP>::kTB), bars, w, use, g)) return;
+}
+
 __device__ __forceinline__ void fetch_scales(const Seq8FwdArgs& a, Bars* bars, const WaitGuard& g, int lane) {
   const SeqDesc& s = a.f.s;
   const Cache8& c = a.c;
   const int pages = s.page < kTile ? kTile / s.page : 1;
   const ScaleLane mine(s, c, lane);
   uint32_t use = 0;
-  for (uint32_t it = 0;; ++it) {
-    const uint32_t d = it % kDescs;
-    if (!mbar_wait_warp_inl(smem_u32(&bars->desc_full[d]), (it / kDescs) & 1, g)) return;
-    const Work w = bars->work[d];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars->desc_empty[d]));
-    if (w.stop) return;
+  Work w;
+  for (uint32_t it = 0; take(bars, it, g, w); ++it) {
     Pages look(s, w, pages);
     int first = s.page > kTile ? (w.j0 * kTile) % s.page : 0;
     for (int j = w.j0; j < w.j1; ++j, ++use) {
@@ -191,6 +210,49 @@ __device__ __forceinline__ void fetch_scales(const Seq8FwdArgs& a, Bars* bars, c
   }
 }
 
+// The items' q in fp16, an item ahead: features 64 i + 16 c + 4 k + (0, 1 | 2, 3) of row r become elements
+// (2c, 2c + 1 | 2c + 8, 2c + 9) of step 4 i + k, where lane 4 (r % 8) + c takes them for its product.
+template <int DP, bool BF16>
+__device__ __forceinline__ void fetch_q(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
+  const SeqDesc& s = a.f.s;
+  const int G = s.group;
+  Work w;
+  for (uint32_t it = 0; take(bars, it, g, w); ++it) {
+    const uint32_t b = it & 1;
+    if (!mbar_wait_warp_inl(smem_u32(&bars->q_empty[b]), ((it >> 1) & 1) ^ 1, g)) return;
+    uint2 x[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      x[r] = make_uint2(0u, 0u);
+      if (4 * lane < s.D && r < w.nt * G)
+        x[r] = *reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(w.row0) + w.t0 + r / G) * a.q_stride +
+                                               static_cast<size_t>(w.kvh * G + r % G) * s.D + 4 * lane);
+    }
+    uint32_t* to = reinterpret_cast<uint32_t*>(base + Layout<DP>::q + b * Layout<DP>::kQ) +
+                   (((lane >> 4) * 4 + (lane & 3)) * 32 + ((lane >> 2) & 3)) * 4;
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      float unit = a.f.scale_log2;
+      if constexpr (BF16) {
+        uint32_t most = __vmaxu2(x[r].x & 0x7fff7fffu, x[r].y & 0x7fff7fffu);  // magnitudes, as two 16-bit numbers
+        most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+        const uint32_t e = min(max(most >> 7, 1u), 253u);
+        const float down = __uint_as_float((254u - e) << 23);
+        unit *= __uint_as_float(e << 23);
+        const float2 f0 = unpack2<true>(x[r].x), f1 = unpack2<true>(x[r].y);
+        x[r] = make_uint2(pack2<false>(f0.x * down, f0.y * down), pack2<false>(f1.x * down, f1.y * down));
+      }
+      if (4 * lane < DP) {
+        to[(r & 7) * 16 + (r >> 3)] = x[r].x;
+        to[(r & 7) * 16 + (r >> 3) + 2] = x[r].y;
+      }
+      if (lane == 0) bars->unit[b][r] = unit;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[b]));
+  }
+}
+
 // ------------------------------------------------------------ compute (warps 0..7)
 template <int DP, bool BF16>
 __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g) {
@@ -199,46 +261,12 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
   const SeqDesc& s = a.f.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
   const int G = s.group, dt0 = gr / G, dt1 = (gr + 8) / G;  // rows gr and gr + 8: token within the item
-  float* mine = reinterpret_cast<float*>(base + L::merge) + warp * kRows * L::kPitch;
   uint32_t use = 0, merges = 0;
-  for (uint32_t it = 0;; ++it) {
-    const uint32_t ds = it % kDescs;
-    if (!mbar_wait_warp_inl(smem_u32(&bars->desc_full[ds]), (it / kDescs) & 1, g)) return;
-    const Work w = bars->work[ds];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars->desc_empty[ds]));
-    if (w.stop) return;
-    // ---- q in fp16, a row a warp: features 64 i + 16 c + 4 k + (0, 1 | 2, 3) of row r become elements
-    // (2c, 2c + 1 | 2c + 8, 2c + 9) of step 4 i + k, where lane 4 (r % 8) + c takes them for its product.  (The last item's
-    // q is nobody's any more: every warp has joined its share of it.)
-    for (int r = warp; r < kRows; r += kWarps) {
-      uint2 x = make_uint2(0u, 0u);
-      if (4 * lane < s.D && r / G < w.nt)
-        x = *reinterpret_cast<const uint2*>(a.q + (static_cast<size_t>(w.row0) + w.t0 + r / G) * a.q_stride +
-                                            static_cast<size_t>(w.kvh * G + r % G) * s.D + 4 * lane);
-      float unit = a.f.scale_log2;
-      if constexpr (BF16) {
-        uint32_t most = __vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu);  // magnitudes, as two 16-bit numbers
-        most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
-        const uint32_t e = min(max(most >> 7, 1u), 253u);
-        const float down = __uint_as_float((254u - e) << 23);
-        unit *= __uint_as_float(e << 23);
-        const float2 f0 = unpack2<true>(x.x), f1 = unpack2<true>(x.y);
-        x = make_uint2(pack2<false>(f0.x * down, f0.y * down), pack2<false>(f1.x * down, f1.y * down));
-      }
-      if (4 * lane < DP) {
-        uint32_t* to = reinterpret_cast<uint32_t*>(base + L::q) +
-                       (((lane >> 4) * 4 + (lane & 3)) * 32 + (r & 7) * 4 + ((lane >> 2) & 3)) * 4 + (r >> 3);
-        to[0] = x.x;
-        to[2] = x.y;
-      }
-      if (lane == 0) bars->unit[r] = unit;
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars->q_full));
-    if (!mbar_wait_warp_inl(smem_u32(&bars->q_full), it & 1, g)) return;
-    const float unit0 = bars->unit[gr], unit1 = bars->unit[gr + 8];
-    const uint32_t qs = smem_u32(base + L::q) + lane * 16;
+  Work w;
+  for (uint32_t it = 0; take(bars, it, g, w); ++it) {
+    if (!mbar_wait_warp_inl(smem_u32(&bars->q_full[it & 1]), (it >> 1) & 1, g)) return;
+    const float unit0 = bars->unit[it & 1][gr], unit1 = bars->unit[it & 1][gr + 8];
+    const uint32_t qs = smem_u32(base + L::q + (it & 1) * L::kQ) + lane * 16;
     const int pos0 = w.pos + dt0, pos1 = w.pos + dt1;
     float o[kCols][4] = {};
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
@@ -359,89 +387,79 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
       }
     }
     use += static_cast<uint32_t>(w.j1 - w.j0);
-    // ---- the warps' shares joined
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->q_empty[it & 1]));
+    // ---- the warps' shares joined, four rows at a time, each by one warp; the others go on
     l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (!mbar_wait_warp_inl(smem_u32(&bars->merge_empty), (merges & 1) ^ 1, g)) return;
-    if (c == 0) {
-      bars->ml[warp][gr] = make_float2(m0, l0);
-      bars->ml[warp][gr + 8] = make_float2(m1, l1);
-    }
-    // Tile n holds, as elements 0 | 1 of a row, feature n of piece G(2 c) = c | G(2 c + 1) = 4 + c (D up to 64: of the eight
-    // features 2 c | 2 c + 1): a quarter of the tiles, and with it of the features, at a time.
-    const int r = threadIdx.x >> 4, piece = (threadIdx.x >> 1) & 7, two = (threadIdx.x & 1) * (DP / 64);  // row, features
-    const bool out = r < kRows && r / G < w.nt;  // (rows past the item's are none's)
-    const size_t row = static_cast<size_t>(w.row0) + w.t0 + r / G, at = (static_cast<size_t>(blockIdx.x) * 2 + w.slot) * kRows + r;
-    const int h = w.kvh * G + r % G;
-    float f[kWarps], big = -INFINITY, l = 0.0f;
+    const int rows = w.nt * G;
+    for (int first = 0; first < rows; first += kJoined, ++merges) {
+      if (!mbar_wait_warp_inl(smem_u32(&bars->merge_empty), (merges & 1) ^ 1, g)) return;
+      // Tile n holds, as elements 0 | 1 of a row, feature n of piece G(2 c) = c | G(2 c + 1) = 4 + c (D up to 64: of the eight
+      // features 2 c | 2 c + 1).
+      if ((gr & 4) == (first & 4)) {
+        float* to = reinterpret_cast<float*>(base + L::merge) + (warp * kJoined + (gr & 3)) * L::kPitch;
+        auto put = [&](auto upper) {
+          constexpr bool up = decltype(upper)::value;
+          constexpr int e = up ? 2 : 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      constexpr int kN = kCols / 4;  // tiles of a quarter: 4, or 2
-      if (k > 0 && !mbar_wait_warp_inl(smem_u32(&bars->merge_empty), (merges & 1) ^ 1, g)) return;
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float* to = mine + (gr + 8 * half) * L::kPitch + (DP == 128 ? c + 4 * x : 2 * c + x) * kN;
-          if constexpr (kN == 4)
-            *reinterpret_cast<float4*>(to) = make_float4(o[4 * k][2 * half + x], o[4 * k + 1][2 * half + x],
-                                                         o[4 * k + 2][2 * half + x], o[4 * k + 3][2 * half + x]);
-          else
-            *reinterpret_cast<float2*>(to) = make_float2(o[2 * k][2 * half + x], o[2 * k + 1][2 * half + x]);
-        }
+            for (int n = 0; n < kCols; n += 4)
+              *reinterpret_cast<float4*>(to + (DP == 128 ? 16 * (c + 4 * x) : 8 * (2 * c + x)) + n) =
+                  make_float4(o[n][e + x], o[n + 1][e + x], o[n + 2][e + x], o[n + 3][e + x]);
+          if (c == 0) *reinterpret_cast<float2*>(to + DP) = up ? make_float2(m1, l1) : make_float2(m0, l0);
+        };
+        if (first < 8)
+          put(std::false_type{});
+        else
+          put(std::true_type{});
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->merge_full));
+      if (warp >= kJoined) continue;
       if (!mbar_wait_warp_inl(smem_u32(&bars->merge_full), merges & 1, g)) return;
-      ++merges;
-      if (out) {
-        if (k == 0) {
-          float2 ml[kWarps];
+      const int r = first + warp, d = 4 * lane;  // row, four features
+      if (r < rows && d < DP) {
+        const float* from = reinterpret_cast<const float*>(base + L::merge) + warp * L::kPitch;
+        float big = -INFINITY, l = 0.0f, f[kWarps];
 #pragma unroll
-          for (int i = 0; i < kWarps; ++i) {
-            ml[i] = bars->ml[i][r];
-            if (ml[i].y != 0.0f) big = fmaxf(big, ml[i].x);
-          }
-#pragma unroll
-          for (int i = 0; i < kWarps; ++i) {
-            // (a share that saw a NaN may have no maximum: its l is NaN, whatever it is scaled by)
-            f[i] = ml[i].y == 0.0f ? 0.0f : (big == -INFINITY ? 1.0f : ex2(ml[i].x - big));
-            if (ml[i].y != 0.0f) l += ml[i].y * f[i];
-          }
+        for (int i = 0; i < kWarps; ++i) {
+          const float2 ml = *reinterpret_cast<const float2*>(from + i * kJoined * L::kPitch + DP);
+          if (ml.y != 0.0f) big = fmaxf(big, ml.x);
         }
-        // this thread's features of the quarter: two of a piece of four (one of two)
-        constexpr int kF = DP / 64;
-        float x[2] = {0.0f, 0.0f};
-        const float* from = reinterpret_cast<const float*>(base + L::merge) + r * L::kPitch + piece * kN + two;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i)
+        for (int i = 0; i < kWarps; ++i) {
+          const float2 ml = *reinterpret_cast<const float2*>(from + i * kJoined * L::kPitch + DP);
+          // (a share that saw a NaN may have no maximum: its l is NaN, whatever it is scaled by)
+          f[i] = ml.y == 0.0f ? 0.0f : (big == -INFINITY ? 1.0f : ex2(ml.x - big));
+          if (ml.y != 0.0f) l += ml.y * f[i];
+        }
+        float x[4] = {};
 #pragma unroll
-          for (int e = 0; e < kF; ++e) x[e] = fmaf(from[i * kRows * L::kPitch + e], f[i], x[e]);
-        const int d = piece * (DP / 8) + k * kN + two;
+        for (int i = 0; i < kWarps; ++i) {
+          const float4 y = *reinterpret_cast<const float4*>(from + i * kJoined * L::kPitch + d);
+          x[0] = fmaf(y.x, f[i], x[0]), x[1] = fmaf(y.y, f[i], x[1]), x[2] = fmaf(y.z, f[i], x[2]), x[3] = fmaf(y.w, f[i], x[3]);
+        }
+        const size_t row = static_cast<size_t>(w.row0) + w.t0 + r / G;
+        const int h = w.kvh * G + r % G;
         if (w.slot < 0) {
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          const uint32_t y = l == 0.0f ? 0u : pack2<BF16>(x[0] * inv, x[1] * inv);
-          uint16_t* to = a.f.out + row * a.f.out_stride + static_cast<size_t>(h) * s.D + d;
-          if (d < s.D) {
-            if constexpr (kF == 2)
-              *reinterpret_cast<uint32_t*>(to) = y;
-            else
-              *to = static_cast<uint16_t>(y);
-          }
+          if (d < s.D)
+            *reinterpret_cast<uint2*>(a.f.out + row * a.f.out_stride + static_cast<size_t>(h) * s.D + d) =
+                l == 0.0f ? make_uint2(0u, 0u)
+                          : make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
+          if (lane == 0) a.f.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
         } else {
-#pragma unroll
-          for (int e = 0; e < kF; ++e) a.f.part_o[at * DP + d + e] = x[e];
+          const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + w.slot) * kRows + r;
+          *reinterpret_cast<float4*>(a.f.part_o + at * DP + d) = make_float4(x[0], x[1], x[2], x[3]);
+          if (lane == 0) a.f.part_ml[at] = make_float2(big, l);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->merge_empty));
-    }
-    if (out && piece == 0 && two == 0 && (threadIdx.x & 1) == 0) {
-      if (w.slot < 0)
-        a.f.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
-      else
-        a.f.part_ml[at] = make_float2(big, l);
     }
   }
 }
@@ -458,15 +476,18 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
     bars->tiles = 0;
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(smem_u32(&bars->desc_full[i]), 1);
-      mbar_init(smem_u32(&bars->desc_empty[i]), kWarps + 1);
+      mbar_init(smem_u32(&bars->desc_empty[i]), kWarps + 3);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&bars->full[i]), 17);  // the copies' bytes, and a lane for each scale
+      mbar_init(smem_u32(&bars->full[i]), 18);  // the copies' bytes (two warps), and a lane for each scale
       mbar_init(smem_u32(&bars->empty[i]), kGroups);
     }
     mbar_init(smem_u32(&bars->merge_full), kWarps);
-    mbar_init(smem_u32(&bars->merge_empty), kWarps);
-    mbar_init(smem_u32(&bars->q_full), kWarps);
+    mbar_init(smem_u32(&bars->merge_empty), kJoined);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars->q_full[i]), 1);
+      mbar_init(smem_u32(&bars->q_empty[i]), kWarps);
+    }
     fence_barrier_init();
   }
   if (warp == kWarps && lane == 0) {
@@ -481,7 +502,11 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
     else
       produce<DP, QueryBlocks>(a, base, bars, g, lane);
   } else if (warp == kWarps + 1) {
+    load_values<DP>(a, base, bars, g);
+  } else if (warp == kWarps + 2) {
     fetch_scales(a, bars, g, lane);
+  } else if (warp == kWarps + 3) {
+    fetch_q<DP, BF16>(a, base, bars, g, lane);
   } else {
     compute<DP, BF16>(a, base, bars, g);
   }
