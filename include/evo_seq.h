@@ -242,7 +242,7 @@ EVO_API evo_status_t evo_rotary(const void* q, const void* k, const int32_t* pos
  *
  * Scales that others wrote may be any numbers from 2^-64 to 2^120.  Reading rounds code * scale to
  * dtype (for scales that are powers of two exact within its range) and saturates at its largest
- * finite number.  Attention takes code * scale as it is. */
+ * finite number.  Attention takes code * scale as it is, or, with many rows a key, as reading gives it. */
 typedef struct {
   int64_t num_pages, page_size, pages_per_seq;
   int64_t scale_block;
@@ -266,7 +266,9 @@ EVO_API evo_status_t evo_cache8_read(const void* k_pages, const void* v_pages, c
                                      evo_cache8_shape_t cache, evo_dtype_t dtype, const evo_seq_strides_t* strides,
                                      const evo_seq_options_t* opts, void* stream);
 
-/* As evo_paged_fwd without weights; q and out are in dtype. */
+/* As evo_paged_fwd without weights; q and out are in dtype.  With many rows a key (tokens * group above 512 * seqs)
+ * the workspace has room for a copy in 16 bits of all that the table can hold, as long as that is at most
+ * 512 MB; otherwise codes are widened where they are used. */
 EVO_API size_t evo_paged8_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache8_shape_t cache);
 EVO_API evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
                                     const float* v_scales, const int32_t* cu_seqlens, const int32_t* seq_lens,

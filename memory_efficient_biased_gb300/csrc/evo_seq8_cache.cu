@@ -181,10 +181,57 @@ __device__ __forceinline__ uint32_t read2(uint32_t codes_f16, float scale) {
   return pack2<BF16>(f.x, f.y);
 }
 
+// One token's keys and values out of row r of page p (p < 0: zeros), by a warp: pieces of 16 codes, four a lane under way
+// together.
+struct RowShape {
+  int per, chunks, shift;  // pieces a head, and a row; log2 of the tokens a scale
+  uint32_t magic;          // ceil(2^32 / per), for exact quotients below 2^29
+  __device__ __forceinline__ RowShape(const SeqDesc& s, const Cache8& c) {
+    per = s.D / 16;
+    chunks = s.kv_heads * per;
+    shift = __ffs(c.block) - 1;
+    magic = 0xffffffffu / per + 1;
+  }
+};
+template <bool BF16>
+__device__ __forceinline__ void read_row(const SeqDesc& s, const Cache8& c, const RowShape& q, int p, int r, uint16_t* ko,
+                                         uint16_t* vo) {
+  const int lane = threadIdx.x & 31;
+  const uint8_t* kp = c.k_pages + p * c.k_page + static_cast<long long>(r) * q.chunks * 16;
+  const uint8_t* vp = c.v_pages + p * c.v_page + static_cast<long long>(r) * q.chunks * 16;
+  const long long scales = static_cast<long long>(p) * s.kv_heads * c.blocks + (r >> q.shift);
+  for (int n0 = lane; n0 < 2 * q.chunks; n0 += 128) {
+    uint4 x[4];
+    float scale[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = n0 + 32 * e, kv = n >= q.chunks, at = kv ? n - q.chunks : n;
+      x[e] = make_uint4(0u, 0u, 0u, 0u);
+      scale[e] = 0.0f;
+      if (p >= 0 && n < 2 * q.chunks) {
+        const int h = q.per == 1 ? at : static_cast<int>(__umulhi(static_cast<uint32_t>(at), q.magic));  // at / per
+        x[e] = __ldg(reinterpret_cast<const uint4*>((kv ? vp : kp) + at * 16));
+        scale[e] = __ldg((kv ? c.v_scales : c.k_scales) + scales + static_cast<long long>(h) * c.blocks);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = n0 + 32 * e, kv = n >= q.chunks, at = kv ? n - q.chunks : n;
+      if (n >= 2 * q.chunks) continue;
+      const uint2 w[4] = {f16x4_of_codes(x[e].x), f16x4_of_codes(x[e].y), f16x4_of_codes(x[e].z), f16x4_of_codes(x[e].w)};
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[2 * i] = read2<BF16>(w[i].x, scale[e]), o[2 * i + 1] = read2<BF16>(w[i].y, scale[e]);
+      uint16_t* to = (kv ? vo : ko) + at * 16;
+      *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(256) evo_read8_kernel(const __grid_constant__ Cache8Args a) {
   const SeqDesc& s = a.s;
-  const Cache8& c = a.c;
   if (blockIdx.x == 0) check_seqs(s);
   const int lane = threadIdx.x & 31, tokens = a.tokens_a_warp;
   const long long first = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * tokens;
@@ -198,35 +245,43 @@ __global__ void __launch_bounds__(256) evo_read8_kernel(const __grid_constant__ 
       if (t >= q.row0 && t < q.row0 + q.n) {
         const int j = q.pos0 + (t - q.row0);
         page = j < 0 ? -1 : page_of(s, b, j);
-        row = j % s.page;
+        row = j < 0 ? 0 : j % s.page;
       }
     }
   }
-  const int per = s.D / 16, chunks = s.kv_heads * per, shift = __ffs(c.block) - 1;
+  const RowShape shape(s, a.c);
   for (int i = 0; i < tokens; ++i) {
     const int p = __shfl_sync(0xffffffffu, page, i), r = __shfl_sync(0xffffffffu, row, i);
-    if (p == -2) continue;
-    const long long t = first + i;
-    const uint8_t* kp = c.k_pages + p * c.k_page + static_cast<long long>(r) * chunks * 16;
-    const uint8_t* vp = c.v_pages + p * c.v_page + static_cast<long long>(r) * chunks * 16;
-    uint16_t *ko = a.k + t * a.k_stride, *vo = a.v + t * a.v_stride;
-    const long long scales = static_cast<long long>(p) * s.kv_heads * c.blocks + (r >> shift);
-#pragma unroll 4
-    for (int n = lane; n < 2 * chunks; n += 32) {
-      const int kv = n >= chunks, at = kv ? n - chunks : n;
-      uint32_t o[8] = {};
-      if (p >= 0) {
-        const int h = per == 1 ? at : static_cast<int>(__umulhi(static_cast<uint32_t>(at), a.per_magic));  // at / per
-        const uint4 x = *reinterpret_cast<const uint4*>((kv ? vp : kp) + at * 16);
-        const float scale = (kv ? c.v_scales : c.k_scales)[scales + static_cast<long long>(h) * c.blocks];
-        const uint2 w[4] = {f16x4_of_codes(x.x), f16x4_of_codes(x.y), f16x4_of_codes(x.z), f16x4_of_codes(x.w)};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[2 * e] = read2<BF16>(w[e].x, scale), o[2 * e + 1] = read2<BF16>(w[e].y, scale);
+    if (p != -2) read_row<BF16>(s, a.c, shape, p, r, a.k + (first + i) * a.k_stride, a.v + (first + i) * a.v_stride);
+  }
+}
+
+// ------------------------------------------------------------------ a copy in 16 bits
+// Every sequence's pages as pages of 16 bits, one behind the other, with a table for them, for the attention of many
+// rows a key: page i of sequence b becomes page b · pages_per_seq + i.  The CTAs take the pages there are by turns,
+// a warp a token.  Rows behind a sequence's end stay as they are.
+template <bool BF16>
+__global__ void __launch_bounds__(256) evo_copy8_kernel(const __grid_constant__ Cache8Args a, int* table) {
+  const SeqDesc& s = a.s;
+  if (blockIdx.x == 0) check_seqs(s);
+  const int warp = threadIdx.x >> 5;
+  const RowShape shape(s, a.c);
+  const long long row = static_cast<long long>(s.kv_heads) * s.D;
+  unsigned turn = blockIdx.x;  // the first page of the sequence that is this CTA's
+  for (int b = 0; b < s.seqs; ++b) {
+    const Seq q = load_seq(s, b);
+    const unsigned n = q.n > 0 ? static_cast<unsigned>((q.kv + s.page - 1) / s.page) : 0u;
+    unsigned i = turn;
+    for (; i < n; i += gridDim.x) {
+      const int to = b * s.pages_per_seq + static_cast<int>(i), p = page_of(s, b, static_cast<int>(i) * s.page);
+      const int tokens = min(s.page, q.kv - static_cast<int>(i) * s.page);
+      if (threadIdx.x == 0) table[to] = to;
+      for (int r = warp; r < tokens; r += 8) {
+        const long long at = (static_cast<long long>(to) * s.page + r) * row;
+        read_row<BF16>(s, a.c, shape, p, r, a.k + at, a.v + at);
       }
-      uint16_t* to = (kv ? vo : ko) + at * 16;
-      *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    turn = i - n;  // (one behind the last page that was there: the turns go on in the next sequence)
   }
 }
 
@@ -245,8 +300,6 @@ cudaError_t launch_cache8_append(const Cache8Args& a, bool bf16, cudaStream_t st
 
 cudaError_t launch_cache8_read(const Cache8Args& args, int sms, bool bf16, cudaStream_t st) {
   Cache8Args a = args;
-  const uint32_t per = static_cast<uint32_t>(a.s.D / 16);
-  a.per_magic = per > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + per - 1) / per) : 0;
   // fewer tokens a warp where there would be fewer than two blocks an SM
   a.tokens_a_warp = kReadTokens;
   while (a.tokens_a_warp > 1 && a.s.tokens / (8 * a.tokens_a_warp) < 2 * sms) a.tokens_a_warp /= 2;
@@ -256,6 +309,16 @@ cudaError_t launch_cache8_read(const Cache8Args& args, int sms, bool bf16, cudaS
     evo_read8_kernel<true><<<grid, 256, 0, st>>>(a);
   else
     evo_read8_kernel<false><<<grid, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache8_copy(const Cache8Args& a, int* table, int sms, bool bf16, cudaStream_t st) {
+  const long long pages = static_cast<long long>(a.s.seqs) * a.s.pages_per_seq;
+  const unsigned grid = static_cast<unsigned>(pages < 6ll * sms ? pages : 6ll * sms);
+  if (bf16)
+    evo_copy8_kernel<true><<<grid, 256, 0, st>>>(a, table);
+  else
+    evo_copy8_kernel<false><<<grid, 256, 0, st>>>(a, table);
   return cudaGetLastError();
 }
 

@@ -55,13 +55,23 @@ bool map_pages8(CUtensorMap* m, const void* p, const evo_seq_shape_t& s, const e
                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
 }
 
-// Which kernel (few rows a key: up to 16 a sequence and kv head on the average, and a token's heads in one tile of
-// 16), and its launch.
+// Which kernels, and their launch.
+//   few    up to 16 rows a sequence and kv head on the average, and a token's heads in one tile of 16
+//   copy   many rows, and the codes are widened once, into the workspace, for the 16-bit forward; otherwise every block of 256
+//          rows widens them as it needs them.  The copy costs 6 bytes a code and a launch; widening in place what it takes
+//          beside the products.  So: from more than two blocks a sequence on, while the copy stays below 512 MB.  Measured,
+//          in place / copied: one block (2 x 64 tokens over 16384 each, group 4) 64 / 93 us, 3.5 blocks (455 tokens over
+//          12,291, head_dim 64) 44 / 40, 5.2 (1325 over 23,348) 232 / 167, 64 (4096 over 16,384) 970 / 758.
+//   whole  few rows, contexts of at most 1024 keys and no more items than SMs: no item is cut, nothing is joined.  An SM takes
+//          0.7 us a tile, a join 5 and a launch.
+size_t round_up(size_t bytes) { return (bytes + 255) & ~size_t(255); }
 struct Plan {
   bool few, whole;
   int ctas, rows;  // rows: of a piece
+  size_t copy;     // many rows: bytes of the keys' (and of the values') copy in 16 bits; 0: none is made
 };
-constexpr int64_t kWholeKeys = 1024;
+constexpr int64_t kWholeKeys = 1024, kCopyRows = 512;
+constexpr double kCopyBytes = 512.0 * 1024 * 1024;
 Plan plan(int sms, const evo_seq_shape_t& s, const evo_cache8_shape_t& c) {
   const int64_t G = s.q_heads / s.kv_heads, max_kv = c.page_size * c.pages_per_seq;
   Plan p{};
@@ -69,6 +79,8 @@ Plan plan(int sms, const evo_seq_shape_t& s, const evo_cache8_shape_t& c) {
   if (!p.few) {
     p.ctas = fwd_ctas(sms, s, max_kv);
     p.rows = 256;
+    const double copy = 2.0 * double(s.seqs) * double(max_kv) * double(s.kv_heads) * double(s.head_dim);
+    p.copy = s.tokens * G > kCopyRows * s.seqs && 2 * copy <= kCopyBytes ? round_up(static_cast<size_t>(copy)) : 0;
     return p;
   }
   p.rows = kFewRows;
@@ -78,7 +90,12 @@ Plan plan(int sms, const evo_seq_shape_t& s, const evo_cache8_shape_t& c) {
   p.ctas = most < sms ? static_cast<int>(most) + 1 : sms;
   return p;
 }
-size_t workspace_of(const Plan& p, const evo_seq_shape_t& s, SeqFwdArgs* a, void* ws) {
+size_t table_bytes(const evo_seq_shape_t& s, const evo_cache8_shape_t& c) { return round_up(size_t(s.seqs) * size_t(c.pages_per_seq) * 4); }
+evo_cache_shape_t copy_shape(const evo_seq_shape_t& s, const evo_cache8_shape_t& c) {
+  return {s.seqs * c.pages_per_seq, c.page_size, c.pages_per_seq, 0, 0};
+}
+size_t workspace_of(const Plan& p, const evo_seq_shape_t& s, const evo_cache8_shape_t& c, SeqFwdArgs* a, void* ws) {
+  if (p.copy) return 2 * p.copy + table_bytes(s, c) + evo_paged_fwd_workspace_bytes(s, copy_shape(s, c), 0);
   return seq_fwd_workspace(p.whole ? 0 : p.ctas, static_cast<int>(s.head_dim), a, static_cast<uint8_t*>(ws), p.rows);
 }
 
@@ -155,7 +172,7 @@ evo_status_t evo_cache8_read(const void* k_pages, const void* v_pages, const flo
 size_t evo_paged8_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache8_shape_t cache) {
   Checked c;
   if (check_seq_shape(shape, true) != EVO_OK || check_cache8(cache, shape, &c) != EVO_OK) return 0;
-  return workspace_of(plan(num_sms(), shape, cache), shape, nullptr, nullptr);
+  return workspace_of(plan(num_sms(), shape, cache), shape, cache, nullptr, nullptr);
 }
 
 evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
@@ -198,6 +215,23 @@ evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pa
   int sms = 0;
   int* fallback = nullptr;
   if ((st = host_device(&sms, &fallback)) != EVO_OK) return st;
+  const Plan p = plan(sms, shape, cache);
+  const bool bf16 = dtype == EVO_BF16;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (p.copy) {
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    Cache8Args w{};
+    w.s = desc(shape, cu_seqlens, seq_lens, block_table, &c.as16, -1, o.status ? o.status : fallback);
+    w.c = cache_of(k_pages, v_pages, k_scales, v_scales, cache, c);
+    w.k = reinterpret_cast<uint16_t*>(at);
+    w.v = reinterpret_cast<uint16_t*>(at + p.copy);
+    int* table = reinterpret_cast<int*>(at + 2 * p.copy);
+    const cudaError_t e = launch_cache8_copy(w, table, sms, bf16, cs);
+    if (e != cudaSuccess) return cuda_fail("8-bit cache copy launch", e);
+    const size_t used = 2 * p.copy + table_bytes(shape, cache);
+    return evo_paged_fwd(q, w.k, w.v, cu_seqlens, seq_lens, table, out, lse, nullptr, 0, at + used, workspace_bytes - used,
+                         shape, copy_shape(shape, cache), dtype, strides, opts, stream);
+  }
   Seq8FwdArgs a{};
   a.f.s = desc(shape, cu_seqlens, seq_lens, block_table, &c.as16, -1, o.status ? o.status : fallback);
   a.c = cache_of(k_pages, v_pages, k_scales, v_scales, cache, c);
@@ -209,12 +243,9 @@ evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pa
   a.f.scale_log2 = scale_of(o, shape) * kSeqLog2e;
   a.f.wait_ns = o.wait_ns;
   a.f.TQ = kTile / a.f.s.group;
-  const bool bf16 = dtype == EVO_BF16;
-  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (!map_pages8(&a.f.tk, k_pages, shape, cache, c.k_page) || !map_pages8(&a.f.tv, v_pages, shape, cache, c.v_page))
     return EVO_ERR_CUDA;
-  const Plan p = plan(sms, shape, cache);
-  workspace_of(p, shape, &a.f, workspace);
+  workspace_of(p, shape, cache, &a.f, workspace);
   a.whole = p.whole;
   cudaError_t e;
   if (p.few) {

@@ -13,13 +13,12 @@ struct Cache8 {
   int block, blocks;         // tokens a scale, scales a page and head
 };
 
-struct Cache8Args {  // append and read
+struct Cache8Args {  // append, read and copy
   SeqDesc s;
   Cache8 c;
-  uint16_t *k, *v;   // rows: read by an append, written by a read
+  uint16_t *k, *v;    // rows: read by an append, written by a read; a copy's pages
   long long k_stride, v_stride;
-  int tokens_a_warp;   // read
-  uint32_t per_magic;  // read: ceil(2^32 / (16-code pieces of a head)), for exact quotients below 2^29
+  int tokens_a_warp;  // read
 };
 
 constexpr int kFewRows = 16;  // rows of a tile of the kernel for few rows a key
@@ -68,6 +67,7 @@ __device__ __forceinline__ uint2 codes_of_f32(const float (&x)[8]) {
 
 cudaError_t launch_cache8_append(const Cache8Args& a, bool bf16, cudaStream_t st);
 cudaError_t launch_cache8_read(const Cache8Args& a, int sms, bool bf16, cudaStream_t st);
+cudaError_t launch_cache8_copy(const Cache8Args& a, int* table, int sms, bool bf16, cudaStream_t st);
 cudaError_t launch_paged8_few(const Seq8FwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 cudaError_t launch_paged8_tiles(const Seq8FwdArgs& a, int ctas, bool bf16, cudaStream_t st);
 

@@ -544,6 +544,68 @@ def test_paged8_past_32_bits_of_offset():
             a += m
 
 
+COPIED = [([300], [300], 8, 2, 128, 16, 16), ([200, 0, 260], [700, 33, 260], 16, 2, 64, 64, 32), ([33, 70], [500, 400], 64, 1, 80, 32, 32),
+          ([600, 1], [1400, 900], 4, 2, 128, 128, 128), ([180], [1025], 12, 4, 96, 384, 64), ([9], [64], 128, 1, 16, 16, 16)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("chunks,ctx,Hq,Hk,D,page,block", COPIED)
+def test_paged8_many_rows(chunks, ctx, Hq, Hk, D, page, block, dtype):
+    """More rows a key than two blocks: the codes are widened once, into the workspace; with a table too wide for that
+    (places for 2^20 tokens and more), where they are used.  Behind the sequences' ends the pages and scales hold NaN."""
+    rng = np.random.default_rng(sum(ctx) + 1)
+    cache = filled(rng, ctx, page, block, Hk, D)
+    for s in (cache.ks, cache.vs):
+        s[s == -7.0] = float("nan")
+    q = S.normal(rng, sum(chunks), Hq, D, dtype=dtype, sigma=1.3)
+    wide = torch.full((len(ctx), (1 << 28) // (Hk * D * page) + 1), -1, dtype=torch.int32, device="cuda")
+    wide[:, :cache.table.shape[1]] = cache.table
+    need = [Q.evo_paged8_fwd_workspace_bytes(sum(chunks), len(ctx), Hq, Hk, D, cache.k.shape[0], page, t.shape[1], block)
+            for t in (cache.table, wide)]
+    assert need[0] >= 4 * len(ctx) * max(ctx) * Hk * D and need[1] < 1 << 29
+    for table in (cache.table, wide):
+        args = q.cuda(), *cache.args(), S.offsets(chunks).cuda(), i32(ctx), table
+        out, lse = Q.evo_paged8_fwd(*args)
+        check_paged(cache, q, chunks, ctx, out, lse, D ** -0.5, dtype)
+        again = Q.evo_paged8_fwd(*args)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert E.evo_attn_device_status() == 0
+
+
+def test_paged8_many_rows_unseen_bad_and_captured():
+    """As above: NaN in later tokens of the chunk, a bad page, strided pages, a captured call replayed on a longer context."""
+    rng = np.random.default_rng(28)
+    chunks, ctx, Hq, Hk, D = [80, 70], [300, 90], 16, 1, 64
+    cache = filled(rng, ctx, 32, 16, Hk, D, interleaved=True)
+    clean = [cache.rows(b, n) for b, n in enumerate(ctx)]
+    q = S.normal(rng, 150, Hq, D, dtype=BF)
+    qd, cu, lens = q.cuda(), S.offsets(chunks).cuda(), i32(ctx)
+    p = int(cache.table[0, 299 // 32])
+    cache.v.view(torch.uint8)[p, 299 % 32, 0, 9] = NAN8
+    out, lse = Q.evo_paged8_fwd(qd, *cache.args(), cu, lens, cache.table)
+    C.check_attention(S.f64(q[:79]), clean[0][0][:299], clean[0][1][:299], S.f64(out[:79]), S.f64(lse[:, :79]), 0.125, BF)
+    C.check_attention(S.f64(q[80:]), *clean[1], S.f64(out[80:]), S.f64(lse[:, 80:]), 0.125, BF)
+    last = out[79].float()
+    assert torch.all(torch.isnan(last[:, 9])) and torch.all(torch.isfinite(last[:, :9])) and torch.all(torch.isfinite(last[:, 10:]))
+    cache.v.view(torch.uint8)[p, 299 % 32, 0, 9] = 0
+    table, status = cache.table.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    table[1, 0] = -5
+    out, lse = Q.evo_paged8_fwd(qd, *cache.args(), cu, lens, table, status=status)
+    assert int(status) == 13
+    C.check_attention(S.f64(q[:80]), *cache.rows(0, 300), S.f64(out[:80]), S.f64(lse[:, :80]), 0.125, BF)
+    ws = torch.empty(Q.evo_paged8_fwd_workspace_bytes(150, 2, Hq, Hk, D, cache.k.shape[0], 32, cache.table.shape[1], 16),
+                     dtype=torch.uint8, device="cuda")
+    o, z, g = torch.empty_like(out), torch.empty_like(lse), torch.cuda.CUDAGraph()
+    lens.sub_(10)
+    with torch.cuda.graph(g):
+        Q.evo_paged8_fwd(qd, *cache.args(), cu, lens, cache.table, out=o, lse=z, workspace=ws)
+    lens.add_(10)
+    ws.fill_(255)
+    g.replay()
+    check_paged(cache, q, chunks, ctx, o, z, 0.125, BF)
+    assert E.evo_attn_device_status() == 0
+
+
 def test_paged8_refusals():
     rng = np.random.default_rng(27)
     cache = filled(rng, [40], 16, 16, 2, 64)
