@@ -47,17 +47,17 @@ template <>
 struct Pack<1> { using T = uint16_t; };
 
 template <bool BF16, int N>
-__device__ __forceinline__ void load_row(const uint16_t* p, float (&x)[N]) {
+__device__ __forceinline__ void unpack_row(const typename Pack<N>::T& v, float (&x)[N]) {
   union {
     typename Pack<N>::T v;
     uint16_t e[N];
   } u;
-  u.v = *reinterpret_cast<const typename Pack<N>::T*>(p);
+  u.v = v;
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = to_f32<BF16>(u.e[i]);
 }
 template <bool BF16, int N>
-__device__ __forceinline__ void store_row(uint16_t* p, const float (&x)[N]) {
+__device__ __forceinline__ typename Pack<N>::T pack_row(const float (&x)[N]) {
   union {
     typename Pack<N>::T v;
     uint32_t w[(N + 1) / 2];
@@ -69,8 +69,11 @@ __device__ __forceinline__ void store_row(uint16_t* p, const float (&x)[N]) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) u.w[i] = pack2<BF16>(x[2 * i], x[2 * i + 1]);
   }
-  *reinterpret_cast<typename Pack<N>::T*>(p) = u.v;
+  return u.v;
 }
+
+constexpr int kAtOnce = 4;  // heads of a thread whose loads are under way together (the outputs may be the inputs: left to
+                            // the compiler, each head's loads waited for the stores of the one before)
 
 // VEC pairs a thread: their first and second features are VEC next to each other each (halves), or
 // 2 VEC next to each other, in turns (INTERLEAVED; two loads where VEC is 8).
@@ -99,11 +102,18 @@ __global__ void __launch_bounds__(kRotaryThreads) evo_rotary_kernel(const __grid
   auto out = [&](int h) {
     return h < a.q_heads ? a.q_out + t * a.q_out_stride + h * a.D : a.k_out + t * a.k_out_stride + (h - a.q_heads) * a.D;
   };
+  using T = typename Pack<VEC>::T;
   if (copy) {
     const int at = 2 * a.half + unit * VEC;
-#pragma unroll 8
-    for (int h = first; h < a.heads; h += a.heads_apart)
-      *reinterpret_cast<typename Pack<VEC>::T*>(out(h) + at) = *reinterpret_cast<const typename Pack<VEC>::T*>(in(h) + at);
+    for (int h0 = first; h0 < a.heads; h0 += 2 * kAtOnce * a.heads_apart) {
+      T x[2 * kAtOnce];
+#pragma unroll
+      for (int e = 0; e < 2 * kAtOnce; ++e)
+        if (const int h = h0 + e * a.heads_apart; h < a.heads) x[e] = __ldcs(reinterpret_cast<const T*>(in(h) + at));
+#pragma unroll
+      for (int e = 0; e < 2 * kAtOnce; ++e)
+        if (const int h = h0 + e * a.heads_apart; h < a.heads) *reinterpret_cast<T*>(out(h) + at) = x[e];
+    }
     return;
   }
   float c[VEC], s[VEC];
@@ -116,36 +126,42 @@ __global__ void __launch_bounds__(kRotaryThreads) evo_rotary_kernel(const __grid
     c[i] *= a.factor;
   }
   const int at = INTERLEAVED ? 2 * unit * VEC : unit * VEC, gap = INTERLEAVED ? VEC : a.half;
-#pragma unroll 4
-  for (int h = first; h < a.heads; h += a.heads_apart) {
-    float x[VEC], y[VEC];
-    const uint16_t* from = in(h) + at;
-    load_row<BF16, VEC>(from, x);
-    load_row<BF16, VEC>(from + gap, y);
-    if constexpr (!INTERLEAVED) {
+  for (int h0 = first; h0 < a.heads; h0 += kAtOnce * a.heads_apart) {
+    T lo[kAtOnce], hi[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float u = x[i], v = y[i];
-        x[i] = fmaf(u, c[i], -v * s[i]);
-        y[i] = fmaf(v, c[i], u * s[i]);
+    for (int e = 0; e < kAtOnce; ++e)
+      if (const int h = h0 + e * a.heads_apart; h < a.heads) {
+        lo[e] = __ldcs(reinterpret_cast<const T*>(in(h) + at));
+        hi[e] = __ldcs(reinterpret_cast<const T*>(in(h) + at + gap));
       }
-    } else if constexpr (VEC == 1) {
-      const float u = x[0], v = y[0];
-      x[0] = fmaf(u, c[0], -v * s[0]);
-      y[0] = fmaf(v, c[0], u * s[0]);
-    } else {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {  // pair i: elements 2i and 2i + 1 of x and y together
-        float(&z)[VEC] = i < VEC / 2 ? x : y;
-        const int e = 2 * i % VEC;
-        const float u = z[e], v = z[e + 1];
-        z[e] = fmaf(u, c[i], -v * s[i]);
-        z[e + 1] = fmaf(v, c[i], u * s[i]);
+    for (int e = 0; e < kAtOnce; ++e) {
+      const int h = h0 + e * a.heads_apart;
+      if (h >= a.heads) break;
+      float x[VEC], y[VEC];
+      unpack_row<BF16, VEC>(lo[e], x);
+      unpack_row<BF16, VEC>(hi[e], y);
+      if constexpr (!INTERLEAVED || VEC == 1) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float u = x[i], v = y[i];
+          x[i] = fmaf(u, c[i], -v * s[i]);
+          y[i] = fmaf(v, c[i], u * s[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {  // pair i: elements 2i and 2i + 1 of x and y together
+          float(&z)[VEC] = i < VEC / 2 ? x : y;
+          const int p = 2 * i % VEC;
+          const float u = z[p], v = z[p + 1];
+          z[p] = fmaf(u, c[i], -v * s[i]);
+          z[p + 1] = fmaf(v, c[i], u * s[i]);
+        }
       }
+      uint16_t* to = out(h) + at;
+      *reinterpret_cast<T*>(to) = pack_row<BF16, VEC>(x);
+      *reinterpret_cast<T*>(to + gap) = pack_row<BF16, VEC>(y);
     }
-    uint16_t* to = out(h) + at;
-    store_row<BF16, VEC>(to, x);
-    store_row<BF16, VEC>(to + gap, y);
   }
 }
 

@@ -61,8 +61,9 @@ __device__ __forceinline__ float2 finite2(uint32_t w, float otherwise) {
 
 // A warp's rows lie P lanes each, P the power of two that holds their 16-byte pieces, 32 / P rows at a time; the
 // largest magnitude is looked for in pairs of 16 bits, and only where that is no number among numbers
-// alone.  (4096 + 7,190 tokens of 8 heads of 128 in blocks of 64: 14 us, 5.0 TB/s; with a division for every
-// piece's row and comparisons in 32 bits 30.)
+// alone.  (10,188 tokens of 8 heads of 128 in blocks of 64: 16 us, 3.9 TB/s; with a division for every piece's row
+// and comparisons in 32 bits 29.  What bounds it now is latency and issue, 1.7 instructions a clock; several units a CTA,
+// which saves the lookups, and more CTAs an SM with fewer registers changed nothing.)
 template <bool BF16>
 __global__ void __launch_bounds__(kAppendThreads) evo_append8_kernel(const __grid_constant__ Cache8Args a) {
   __shared__ uint32_t warp_most[8];
@@ -83,19 +84,21 @@ __global__ void __launch_bounds__(kAppendThreads) evo_append8_kernel(const __gri
   const int p = page_of(s, b, start);
   if (p < 0) return;
   // (up to here every thread of the block went the same way)
-  const int team = c.block / 16, unit = blockIdx.y * (8 / team) + warp / team;
-  const bool work = unit < 2 * s.kv_heads;
-  const int kv = unit >= s.kv_heads, h = work ? (kv ? unit - s.kv_heads : unit) : 0;
+  const int team = c.block / 16, units = 8 / team;                               // warps a unit, units at a time
   const int per = s.D / 8, shift = per > 8 ? 4 : per > 4 ? 3 : per > 2 ? 2 : 1;  // pieces a row, log2 P
   const int piece = lane & ((1 << shift) - 1), step = 32 >> shift;               // of the row, and rows at a time
   const int place = (warp % team) * 16 + (lane >> shift), in_page = start % s.page;  // first row in the block
   const int steps = 1 << (shift - 1);
+  const int row = s.kv_heads * s.D;
+  const bool older = start < lo;
+  constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
+  const int unit = blockIdx.y * units + warp / team;
+  const bool work = unit < 2 * s.kv_heads, live = work && piece < per;
+  const int kv = unit >= s.kv_heads, h = work ? (kv ? unit - s.kv_heads : unit) : 0;
   const uint16_t* rows = (kv ? a.v : a.k) + static_cast<long long>(h) * s.D + piece * 8;
   const long long stride = kv ? a.v_stride : a.k_stride;
-  const int row = s.kv_heads * s.D;
   uint8_t* page = (kv ? c.v_pages + p * c.v_page : c.k_pages + p * c.k_page) + h * s.D + piece * 8;
   float* scale = (kv ? c.v_scales : c.k_scales) + scale_at(c, s, p, h, start);
-  const bool older = start < lo, live = work && piece < per;
   const float before = work && older ? *scale : 0.0f;
   uint4 x[8];
 #pragma unroll
@@ -103,14 +106,13 @@ __global__ void __launch_bounds__(kAppendThreads) evo_append8_kernel(const __gri
     const int j = start + place + r * step;
     x[r] = make_uint4(0u, 0u, 0u, 0u);
     if (live && r < steps && j >= lo && j < hi)
-      x[r] = *reinterpret_cast<const uint4*>(rows + (q.row0 + static_cast<long long>(j - q.pos0)) * stride);
+      x[r] = __ldcs(reinterpret_cast<const uint4*>(rows + (q.row0 + static_cast<long long>(j - q.pos0)) * stride));
   }
   uint32_t bits = 0;
 #pragma unroll
   for (int r = 0; r < 8; ++r) bits = larger(larger(larger(larger(bits, x[r].x), x[r].y), x[r].z), x[r].w);
-  bits = max(bits & 0xffffu, bits >> 16);
-  constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
-  const bool all_finite = __reduce_max_sync(0xffffffffu, bits) < inf;
+  bits = __reduce_max_sync(0xffffffffu, max(bits & 0xffffu, bits >> 16));
+  const bool all_finite = bits < inf;
   if (!all_finite) {
     bits = 0;
 #pragma unroll
@@ -122,8 +124,8 @@ __global__ void __launch_bounds__(kAppendThreads) evo_append8_kernel(const __gri
         bits = max(bits, max(l < inf ? l : 0u, u < inf ? u : 0u));
       }
     }
+    bits = __reduce_max_sync(0xffffffffu, bits);
   }
-  bits = __reduce_max_sync(0xffffffffu, bits);
   if (team > 1) {
     if (lane == 0) warp_most[warp] = bits;
     __syncthreads();
@@ -195,7 +197,7 @@ struct RowShape {
 };
 template <bool BF16>
 __device__ __forceinline__ void read_row(const SeqDesc& s, const Cache8& c, const RowShape& q, int p, int r, uint16_t* ko,
-                                         uint16_t* vo) {
+                                         uint16_t* vo, bool wide) {
   const int lane = threadIdx.x & 31;
   const uint8_t* kp = c.k_pages + p * c.k_page + static_cast<long long>(r) * q.chunks * 16;
   const uint8_t* vp = c.v_pages + p * c.v_page + static_cast<long long>(r) * q.chunks * 16;
@@ -210,7 +212,7 @@ __device__ __forceinline__ void read_row(const SeqDesc& s, const Cache8& c, cons
       scale[e] = 0.0f;
       if (p >= 0 && n < 2 * q.chunks) {
         const int h = q.per == 1 ? at : static_cast<int>(__umulhi(static_cast<uint32_t>(at), q.magic));  // at / per
-        x[e] = __ldg(reinterpret_cast<const uint4*>((kv ? vp : kp) + at * 16));
+        x[e] = __ldcs(reinterpret_cast<const uint4*>((kv ? vp : kp) + at * 16));
         scale[e] = __ldg((kv ? c.v_scales : c.k_scales) + scales + static_cast<long long>(h) * c.blocks);
       }
     }
@@ -223,8 +225,12 @@ __device__ __forceinline__ void read_row(const SeqDesc& s, const Cache8& c, cons
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[2 * i] = read2<BF16>(w[i].x, scale[e]), o[2 * i + 1] = read2<BF16>(w[i].y, scale[e]);
       uint16_t* to = (kv ? vo : ko) + at * 16;
-      *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+      if (wide) {
+        st_global_32(to, o);
+      } else {
+        *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(to + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
     }
   }
 }
@@ -252,7 +258,8 @@ __global__ void __launch_bounds__(256) evo_read8_kernel(const __grid_constant__ 
   const RowShape shape(s, a.c);
   for (int i = 0; i < tokens; ++i) {
     const int p = __shfl_sync(0xffffffffu, page, i), r = __shfl_sync(0xffffffffu, row, i);
-    if (p != -2) read_row<BF16>(s, a.c, shape, p, r, a.k + (first + i) * a.k_stride, a.v + (first + i) * a.v_stride);
+    if (p != -2) read_row<BF16>(s, a.c, shape, p, r, a.k + (first + i) * a.k_stride, a.v + (first + i) * a.v_stride,
+                                a.wide);
   }
 }
 
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(256) evo_copy8_kernel(const __grid_constant__ 
       if (threadIdx.x == 0) table[to] = to;
       for (int r = warp; r < tokens; r += 8) {
         const long long at = (static_cast<long long>(to) * s.page + r) * row;
-        read_row<BF16>(s, a.c, shape, p, r, a.k + at, a.v + at);
+        read_row<BF16>(s, a.c, shape, p, r, a.k + at, a.v + at, true);
       }
     }
     turn = i - n;  // (one behind the last page that was there: the turns go on in the next sequence)
@@ -289,8 +296,8 @@ __global__ void __launch_bounds__(256) evo_copy8_kernel(const __grid_constant__ 
 
 cudaError_t launch_cache8_append(const Cache8Args& a, bool bf16, cudaStream_t st) {
   const long long blocks = static_cast<long long>(a.s.tokens) / a.c.block + 2ll * a.s.seqs;
-  const int units = 8 / (a.c.block / 16);  // a CTA
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((2 * a.s.kv_heads + units - 1) / units));
+  const int units = 8 / (a.c.block / 16), groups = (2 * a.s.kv_heads + units - 1) / units;  // a CTA, CTAs a block
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(groups));
   if (bf16)
     evo_append8_kernel<true><<<grid, kAppendThreads, 0, st>>>(a);
   else
@@ -300,9 +307,9 @@ cudaError_t launch_cache8_append(const Cache8Args& a, bool bf16, cudaStream_t st
 
 cudaError_t launch_cache8_read(const Cache8Args& args, int sms, bool bf16, cudaStream_t st) {
   Cache8Args a = args;
-  // fewer tokens a warp where there would be fewer than two blocks an SM
+  // fewer tokens a warp where there would be fewer than six blocks an SM
   a.tokens_a_warp = kReadTokens;
-  while (a.tokens_a_warp > 1 && a.s.tokens / (8 * a.tokens_a_warp) < 2 * sms) a.tokens_a_warp /= 2;
+  while (a.tokens_a_warp > 1 && a.s.tokens / (8 * a.tokens_a_warp) < 6 * sms) a.tokens_a_warp /= 2;
   const long long tokens = 8ll * a.tokens_a_warp;
   const unsigned grid = static_cast<unsigned>((a.s.tokens + tokens - 1) / tokens);
   if (bf16)

@@ -96,7 +96,7 @@ evo_cache_shape_t copy_shape(const evo_seq_shape_t& s, const evo_cache8_shape_t&
 }
 size_t workspace_of(const Plan& p, const evo_seq_shape_t& s, const evo_cache8_shape_t& c, SeqFwdArgs* a, void* ws) {
   if (p.copy) return 2 * p.copy + table_bytes(s, c) + evo_paged_fwd_workspace_bytes(s, copy_shape(s, c), 0);
-  return seq_fwd_workspace(p.whole ? 0 : p.ctas, static_cast<int>(s.head_dim), a, static_cast<uint8_t*>(ws), p.rows);
+  return p.whole ? 0 : seq_fwd_workspace(p.ctas, static_cast<int>(s.head_dim), a, static_cast<uint8_t*>(ws), p.rows);
 }
 
 // What an append and a read check alike.
@@ -140,6 +140,7 @@ evo_status_t rows_call(bool append, const void* k, const void* v, const int32_t*
   a.k = static_cast<uint16_t*>(const_cast<void*>(k));
   a.v = static_cast<uint16_t*>(const_cast<void*>(v));
   a.k_stride = t.k, a.v_stride = t.v;
+  a.wide = aligned(k, 32) && aligned(v, 32) && t.k % 16 == 0 && t.v % 16 == 0;
   const bool bf16 = dtype == EVO_BF16;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e = append ? launch_cache8_append(a, bf16, cs) : launch_cache8_read(a, sms, bf16, cs);
@@ -192,14 +193,15 @@ evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pa
   Strides t;
   if (!read_strides(&only, shape, &t)) return EVO_ERR_BAD_LAYOUT;
   if (shape.tokens == 0 || shape.seqs == 0) return EVO_OK;
+  const size_t need = evo_paged8_fwd_workspace_bytes(shape, cache);
   if (!q || !k_pages || !v_pages || !k_scales || !v_scales || !cu_seqlens || !seq_lens || !block_table || !out || !lse ||
-      !workspace)
+      (need && !workspace))
     return EVO_ERR_NULL_POINTER;
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) || !aligned(k_scales, 4) ||
       !aligned(v_scales, 4) || !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4) ||
       !aligned(lse, 4) || !aligned(workspace, 256) || !aligned(o.status, 4))
     return EVO_ERR_MISALIGNED;
-  if (workspace_bytes < evo_paged8_fwd_workspace_bytes(shape, cache)) return EVO_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < need) return EVO_ERR_WORKSPACE_TOO_SMALL;
   const int64_t T = shape.tokens, nq = shape.q_heads * shape.head_dim;
   const Span in[] = {strided(q, T, t.q, nq),
                      pages8(k_pages, cache, shape, c.k_page),

@@ -19,6 +19,7 @@ struct Cache8Args {  // append, read and copy
   uint16_t *k, *v;    // rows: read by an append, written by a read; a copy's pages
   long long k_stride, v_stride;
   int tokens_a_warp;  // read
+  int wide;           // read: rows start at multiples of 32 bytes
 };
 
 constexpr int kFewRows = 16;  // rows of a tile of the kernel for few rows a key

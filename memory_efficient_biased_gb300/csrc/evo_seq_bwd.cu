@@ -407,12 +407,6 @@ __device__ __forceinline__ void mma_dq(const SeqBwdArgs& a, uint8_t* base, Bars*
 }
 
 // ------------------------------------------------------------ compute (warps 0..7)
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-
 // Columns [c0, c1) (N at a time; stops at D) of this thread's row of an accumulator: times f in the
 // result's type at `out`, or as they are at `part`.  Warp-collective.
 template <int N, bool BF16>

@@ -30,12 +30,6 @@ __device__ __forceinline__ Share share_of(const Work& w, int g, int TQ) {
   return Share{w.j0, kt < w.j1 ? kt : w.j1, 1};
 }
 
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-
 // This thread's row of an accumulator times alpha.  Warp-collective.
 template <int DP>
 __device__ __forceinline__ void rescale(uint32_t ocol, float alpha) {

@@ -144,9 +144,12 @@ def _flat(t, name: str, shape, dtype, dev: int):
 
 def _rows(t, name: str, shape, dtype, dev: int) -> int:
     """Checks a [tokens, heads, head_dim] tensor; its token stride (0 = packed)."""
-    if (isinstance(t, _Tensor) and t.get_device() == dev and t.dtype == dtype and t.is_contiguous()
-            and t.shape == shape):
-        return 0
+    if isinstance(t, _Tensor) and t.get_device() == dev and t.dtype == dtype and t.shape == shape:
+        if t.is_contiguous():
+            return 0
+        stride, head, one = t.stride()
+        if one == 1 and head == shape[2] and shape[0] > 1 and stride > head * shape[1] and stride % 8 == 0:
+            return stride
     _placed(t, name, dtype, dev)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -480,7 +483,7 @@ def evo_rotary(q, k, positions, inv_freq, q_out=None, k_out=None, stream=None, *
     if not isinstance(inv_freq, _Tensor) or inv_freq.dim() != 1 or not 1 <= inv_freq.shape[0] <= D // 2:
         raise ValueError(f"inv_freq must be a tensor of 1 to {D // 2} frequencies")
     _flat(inv_freq, "inv_freq", None, torch.float64, dev)
-    if not math.isfinite(ctypes.c_float(factor).value) or ctypes.c_float(factor).value == 0.0:
+    if factor != 1.0 and not (0.0 < abs(ctypes.c_float(factor).value) < math.inf):  # (as the float32 it becomes)
         raise ValueError(f"factor must be finite and not 0, got {factor}")
     so, to = 0, 0
     with _on(stream):
@@ -605,10 +608,11 @@ def evo_paged8_fwd(q, k_pages, v_pages, k_scales, v_scales, cu_seqlens, seq_lens
             lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
         else:
             _flat(lse, "lse", (Hq, T), torch.float32, dev)
-        ws, size = _workspace(workspace, lib.evo_paged8_fwd_workspace_bytes(shape, cache), q, dev)
+        need = lib.evo_paged8_fwd_workspace_bytes(shape, cache)
+        ws, size = _workspace(workspace, need, q, dev) if need or workspace is not None else (None, 0)
     strides = SeqStrides(sq, 0, 0, so) if sq or so else None
     _done(lib.evo_paged8_fwd(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
                              v_scales.data_ptr(), cu_seqlens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-                             out.data_ptr(), lse.data_ptr(), ws.data_ptr(), size, shape, cache, _DTYPE_CODE[dt],
+                             out.data_ptr(), lse.data_ptr(), _p(ws), size, shape, cache, _DTYPE_CODE[dt],
                              strides, opts, sp), "evo_paged8_fwd")
     return out, lse

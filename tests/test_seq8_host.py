@@ -121,6 +121,10 @@ def test_cache8_refusals(lib, call):
     if call is paged:
         assert call(lib, ws_bytes=8) == 5
         assert call(lib, ws=7 * A + 128) == 4
+        one = shape(T=2, B=2)  # single tokens over at most 64 places: no workspace
+        assert lib.evo_paged8_fwd_workspace_bytes(one, cache()) == 0
+        assert call(lib, s=one, ws=None) in REACH
+        assert call(lib, s=one, c=cache(cols=100), ws=None) == 1
         assert call(lib, s=shape(Hq=7), ws_bytes=1 << 30) == 2
         assert call(lib, s=shape(Hq=258), ws_bytes=1 << 30) == 2
         assert call(lib, strides=Q.SeqStrides(q=516)) == 12
@@ -143,6 +147,11 @@ def test_cache8_aliasing(lib):
 
 def test_workspace(lib):
     assert Q.evo_paged8_fwd_workspace_bytes(64, 2, 8, 2, 64, 10, 16, 4, 16) > 0
+    few, long = (Q.evo_paged8_fwd_workspace_bytes(2, 2, 8, 2, 64, 10, 16, n, 16) for n in (64, 65))
+    assert few == 0 and 0 < long < 1 << 23  # single tokens: 16 rows a piece, none where nothing is cut
+    # many rows: a copy of what the table can hold, up to 512 MB
+    room = [Q.evo_paged8_fwd_workspace_bytes(2000, 2, 8, 2, 64, 10, 16, n, 16) for n in (8, 1 << 15, (1 << 15) + 1)]
+    assert room[1] >= 1 << 29 > room[2] and room[0] >= 4 * 2 * 128 * 2 * 64
     assert Q.evo_paged8_fwd_workspace_bytes(64, 2, 8, 2, 72, 10, 16, 4, 16) == 0
     assert Q.evo_paged8_fwd_workspace_bytes(64, 2, 8, 2, 64, 10, 16, 4, 32) == 0
 
