@@ -53,7 +53,7 @@ struct Bars {
   alignas(8) float scales[kStages][2][8];  // of a stage: keys and values, 16 tokens each
   Work work[kDescs];
   float unit[2][kRows];           // scale · log2 e, and the power of two that q was divided by
-  uint32_t tiles;
+  uint32_t tiles[3];              // that were asked for: keys, values, scales
   int abort;
 };
 
@@ -166,15 +166,16 @@ __device__ __forceinline__ void produce(const Seq8FwdArgs& a, uint8_t* base, Bar
     }
     if (w.stop || !load_tiles<DP>(a, &a.f.tk, smem_u32(base + L::ring), bars, w, use, g)) break;
   }
-  if (lane == 0) bars->tiles = use;
+  if (lane == 0) bars->tiles[0] = use;
 }
 
 template <int DP>
-__device__ __forceinline__ void load_values(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g) {
+__device__ __forceinline__ void load_values(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int lane) {
   uint32_t use = 0;
   Work w;
   for (uint32_t it = 0; take(bars, it, g, w); ++it)
-    if (!load_tiles<DP>(a, &a.f.tv, smem_u32(base + Layout<DP>::ring + Layout<DP>::kTB), bars, w, use, g)) return;
+    if (!load_tiles<DP>(a, &a.f.tv, smem_u32(base + Layout<DP>::ring + Layout<DP>::kTB), bars, w, use, g)) break;
+  if (lane == 0) bars->tiles[1] = use;
 }
 
 __device__ __forceinline__ void fetch_scales(const Seq8FwdArgs& a, Bars* bars, const WaitGuard& g, int lane) {
@@ -184,14 +185,15 @@ __device__ __forceinline__ void fetch_scales(const Seq8FwdArgs& a, Bars* bars, c
   const ScaleLane mine(s, c, lane);
   uint32_t use = 0;
   Work w;
-  for (uint32_t it = 0; take(bars, it, g, w); ++it) {
+  bool ok = true;
+  for (uint32_t it = 0; ok && take(bars, it, g, w); ++it) {
     Pages look(s, w, pages);
     int first = s.page > kTile ? (w.j0 * kTile) % s.page : 0;
     for (int j = w.j0; j < w.j1; ++j, ++use) {
       const uint32_t st = use % kStages;
       const int p = look.of(mine.page);
       const float* from = mine.at(s, c, w.kvh, p, first);
-      if (!mbar_wait_warp_inl(smem_u32(&bars->empty[st]), ((use / kStages) & 1) ^ 1, g)) return;
+      if (!mbar_wait_warp_inl(smem_u32(&bars->empty[st]), ((use / kStages) & 1) ^ 1, g)) { ok = false; break; }
       if (lane < 16) {
         const uint32_t full = smem_u32(&bars->full[st]);
         float* to = &bars->scales[st][lane >> 3][mine.part];
@@ -208,6 +210,7 @@ __device__ __forceinline__ void fetch_scales(const Seq8FwdArgs& a, Bars* bars, c
       look.step(j);
     }
   }
+  if (lane == 0) bars->tiles[2] = use;
 }
 
 // The items' q in fp16, an item ahead: features 64 i + 16 c + 4 k + (0, 1 | 2, 3) of row r become elements
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     bars->abort = 0;
-    bars->tiles = 0;
+    bars->tiles[0] = bars->tiles[1] = bars->tiles[2] = 0;
     for (int i = 0; i < kDescs; ++i) {
       mbar_init(smem_u32(&bars->desc_full[i]), 1);
       mbar_init(smem_u32(&bars->desc_empty[i]), kWarps + 3);
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
     else
       produce<DP, QueryBlocks>(a, base, bars, g, lane);
   } else if (warp == kWarps + 1) {
-    load_values<DP>(a, base, bars, g);
+    load_values<DP>(a, base, bars, g, lane);
   } else if (warp == kWarps + 2) {
     fetch_scales(a, bars, g, lane);
   } else if (warp == kWarps + 3) {
@@ -512,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
   }
   __syncthreads();
   if (warp == kWarps) {
-    const Owed owed[] = {{bars->full, kStages, bars->tiles}};
+    // (where a warp gave up, another may have asked for a tile more)
+    const Owed owed[] = {{bars->full, kStages, max(bars->tiles[0], max(bars->tiles[1], bars->tiles[2]))}};
     drain(owed, g);
   }
 }

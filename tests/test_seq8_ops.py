@@ -606,6 +606,27 @@ def test_paged8_many_rows_unseen_bad_and_captured():
     assert E.evo_attn_device_status() == 0
 
 
+def test_paged8_gives_up_in_time():
+    """The least wait limit: a kernel may give up, says so, and leaves the GPU as it was; the next call is as usual."""
+    rng = np.random.default_rng(29)
+    ctx = [5000, 3000]
+    cache = filled(rng, ctx, 64, 64, 2, 128)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for chunks in ([1, 1], [40, 30]):
+        q = S.normal(rng, sum(chunks), 8, 128, dtype=BF)
+        args = q.cuda(), *cache.args(), S.offsets(chunks).cuda(), i32(ctx), cache.table
+        want = Q.evo_paged8_fwd(*args)
+        Q.evo_paged8_fwd(*args, wait_limit_ns=1, status=status)
+        assert int(status) in (0, 8)
+        status.zero_()
+        again = Q.evo_paged8_fwd(*args, wait_limit_ns=10 ** 9, status=status)
+        assert int(status) == 0
+        for x, y in zip(want, again):
+            assert torch.equal(x, y)
+        check_paged(cache, q, chunks, ctx, *again, 128 ** -0.5, BF)
+    assert E.evo_attn_device_status() == 0
+
+
 def test_paged8_refusals():
     rng = np.random.default_rng(27)
     cache = filled(rng, [40], 16, 16, 2, 64)
@@ -658,6 +679,48 @@ def test_serving_run(dtype):
             x = S.f64(x)
             assert np.all(np.abs(S.f64(got) - x) <= np.maximum(np.abs(x) * 2.0 ** -4, np.abs(x).max() / 224 * 2.0 ** -10))
     assert E.evo_attn_device_status() == 0
+
+
+def test_captured_step():
+    """Rotation, append, attention and read of one step captured once and replayed for token after token, the lengths and
+    positions counted up inside; a cache that begins empty."""
+    rng = np.random.default_rng(32)
+    Hq, Hk, D, B, steps = 8, 2, 128, 3, 40
+    caches = [C.Cache(np.random.default_rng(1), [steps] * B, 16, 16, Hk, D) for _ in range(2)]
+    f = Q.rotary_frequencies(D)[0].cuda()
+    rows = S.normal(rng, steps, B, (Hq + 2 * Hk) * D, dtype=BF).cuda()
+    cu = i32([0, 1, 2, 3])
+
+    def step(cache, qkv, lens, pos):
+        lens.add_(1)
+        q, k, v = qkv[:, :Hq * D].view(B, Hq, D), qkv[:, Hq * D:(Hq + Hk) * D].view(B, Hk, D), qkv[:, (Hq + Hk) * D:].view(B, Hk, D)
+        q, k = Q.evo_rotary(q, k, pos, f)
+        Q.evo_cache8_append(k, v, cu, lens, *cache.args(), cache.table)
+        out = Q.evo_paged8_fwd(q, *cache.args(), cu, lens, cache.table)
+        pos.add_(1)
+        return (*out, *Q.evo_cache8_read(*cache.args(), cu, lens, cache.table, B, BF))
+
+    one, lens, pos = rows[0].clone(), i32([0] * B), i32([0] * B)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):  # (the extension's first launches are no capture's)
+        step(C.Cache(np.random.default_rng(1), [steps] * B, 16, 16, Hk, D), one, i32([0] * B), i32([0] * B))
+    st.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(caches[0], one, lens, pos)
+    l2, p2 = i32([0] * B), i32([0] * B)
+    for i in range(steps):
+        one.copy_(rows[i])
+        g.replay()
+        want = step(caches[1], rows[i], l2, p2)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y), i
+    for x, y in zip(caches[0].args(), caches[1].args()):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    q = S.f64(Q.evo_rotary(rows[-1][:, :Hq * D].view(B, Hq, D), None, i32([steps - 1] * B), f)[0])
+    for b in range(B):
+        C.check_attention(q[b:b + 1], *caches[0].rows(b, steps), S.f64(got[0][b:b + 1]), S.f64(got[1][:, b:b + 1]), D ** -0.5, BF)
 
 
 def test_training_run():
