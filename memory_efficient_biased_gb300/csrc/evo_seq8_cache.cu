@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(kAppendThreads) evo_append8_kernel(const __gri
 // ------------------------------------------------------------------ read
 // A warp takes eight tokens next to each other: a lane each finds its sequence, page and place, then the warp
 // goes over the 16-code pieces of one token after the other, keys and values, which are next to each other in both.
-// Bound by the bytes: one read and two written an element.
+// Bound by the bytes: one read and two written an element.  10,460 tokens of 8 heads of 128: 14 us, 4.7 TB/s (loads one
+// by one between the stores 18; a thread a piece, each with its own search and divisions, 20).
 constexpr int kReadTokens = 8;
 
 // x times scale, at most `most` in magnitude, as a pair of the output's type.
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(256) evo_read8_kernel(const __grid_constant__ 
 // ------------------------------------------------------------------ a copy in 16 bits
 // Every sequence's pages as pages of 16 bits, one behind the other, with a table for them, for the attention of many
 // rows a key: page i of sequence b becomes page b · pages_per_seq + i.  The CTAs take the pages there are by turns,
-// a warp a token.  Rows behind a sequence's end stay as they are.
+// a warp a token.  Rows behind a sequence's end stay as they are.  (23,348 tokens of 8 heads of 128: 27 us, 5.3 TB/s.)
 template <bool BF16>
 __global__ void __launch_bounds__(256) evo_copy8_kernel(const __grid_constant__ Cache8Args a, int* table) {
   const SeqDesc& s = a.s;

@@ -15,16 +15,26 @@
 // products need 16 rows · 23 = 370 multiply-adds a clock and SM, a third of what mma.sync has.
 //
 // Roles (16 warps, one CTA per SM, persistent over its share of the work, evo_seq_sched.cuh):
-//   warps 0-11  32 keys at a time each (16 share their scales), in turns; M, l and O of their own, joined at the end of an
+//   warps 0-11  16 keys at a time each (they share their scales), in turns; M, l and O of their own, joined at the end of an
 //               item.  Three a scheduler, for what a warp waits for between its products; that takes q out of their
 //               registers, into shared memory
 //   warps 12-15 the walk over the work, and keys by TMA (a page is a box); values; scales by cp.async; q, an item ahead.
 //               A warp each: what one of them did for a tile, beside three busy warps, took longer than the tile
 //
+// What bounds it.  HBM: the 0.98 GB of four contexts of 120,000 tokens (8 kv heads of 128) take 72 to 79 us more than half
+// of them, 6.2 to 6.9 TB/s by the machine.  In front of that lie 10 to 12 us until the first tiles are there (offsets, table,
+// then 30 MB asked for at once on pages that no translation is held for), behind it 4 for the last tile and the joining of the
+// warps, 5 of CTAs that were served later than others, and the joining launch, 8: four contexts of 245,609 tokens in all
+// take 100 to 111 us (by the machine), 64 of 287,032 109 to 122, one of 777 12.  Steps: 16 keys a warp, eight warps, pages looked up
+// tile by tile 119 us; page table entries a batch ahead and a second loading warp 101; the warps' shares joined
+// for the live rows only 100, and the 64 contexts 136 -> 109.  No use: 32 keys a warp (fewer stages in flight), eight
+// warps with q in registers (104), the join set up early by a programmatic launch (+1).
+//
 // Fragments.  Inside a product the order of the features (scores) and of the keys (P·V) is free, so a lane takes 16
 // bytes next to each other: of key g for the scores (lane = 4 g + c: features 16 c .. and 64 + 16 c ..), of keys
 // c, c + 4, c + 8, c + 12 for P·V (features 16 G(g) ..), whose bytes are paired by permutes.  Key (g / 2) + 4 (g % 2) stands
-// in column g of the scores and G(g) = (g % 2) 4 + g / 2, so that with the tiles' 128-byte swizzle no read meets a bank twice.
+// in column g of the scores and G(g) = (g % 2) 4 + g / 2, so that with the tiles' 128-byte swizzle no read meets a bank twice
+// (head_dim up to 64: twice).
 #include <type_traits>
 
 #include "evo_seq8_pages.cuh"

@@ -8,6 +8,13 @@
 // The tensor core takes 16 bits from shared memory, so a tile of codes arrives in a staging buffer and four warps widen
 // it into the ring that the products read: 128 KB a pair of key tiles in and out of shared memory, beside the products' own 192.
 //
+// What bounds it: the chain scores, maximum, exponentials, P·V of a pair of tiles, as in the 16-bit forward, at 4600 to 4800
+// cycles instead of 3500: 700 of them are the widening's (1440 cycles a tile and warp, beside the softmax on the same
+// schedulers and the products on the same shared memory), 600 the scales'.  4096 tokens over 16,384 keys, 32 heads of 128: 970
+// us, where a copy widened beforehand and the 16-bit forward take 758; 2 x 64 tokens over 16,384 each 64 us, where those take 93.
+// No use: four slots and two staging buffers instead of three and three (1020), codes loaded into registers
+// instead of a staging buffer (2020: the loads' latency, and no registers to hide it in).
+//
 // Roles (16 warps, one CTA per SM, persistent over its share of the work):
 //   warps 0-3, 4-7  softmax of query tile 0 and 1, one thread per row
 //   warp 8          producer: Q tiles, and tiles of codes into the staging ring, by TMA (a page is a box)
