@@ -142,5 +142,6 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, 
            interleaved: bool = False, factor: float = 1.0):
     """Rotary positions, differentiable: q [T, Hq, D] and k [T, Hk, D] (or None) turned by positions [T] int32
     times inv_freq [rotary_dim / 2] float64 (``evo_seq.rotary_frequencies``); (q, k), as
-    ``prompt_attention`` takes them.  Strided token rows are read in place."""
+    ``prompt_attention`` takes them.  Strided token rows are read in place.  The gradients are not differentiable
+    themselves, and a captured backward needs its forward inside the same capture, as there."""
     return RotaryFunction.apply(q, k, positions, inv_freq, interleaved, factor)

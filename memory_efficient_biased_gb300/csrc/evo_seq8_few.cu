@@ -24,10 +24,11 @@
 // What bounds it.  HBM: the 0.98 GB of four contexts of 120,000 tokens (8 kv heads of 128) take 72 to 79 us more than half
 // of them, 6.2 to 6.9 TB/s by the machine.  In front of that lie 10 to 12 us until the first tiles are there (offsets, table,
 // then 30 MB asked for at once on pages that no translation is held for), behind it 4 for the last tile and the joining of the
-// warps, 5 of CTAs that were served later than others, and the joining launch, 8: four contexts of 245,609 tokens in all
-// take 100 to 111 us (by the machine), 64 of 287,032 109 to 122, one of 777 12.  Steps: 16 keys a warp, eight warps, pages looked up
+// warps, 5 of CTAs that were served later than others, and the joining launch, 3: four contexts of 245,609 tokens in all
+// take 94 to 104 us (by the machine), 64 of 287,032 107 to 120, one of 777 12, one of 2000 14.  Steps: 16 keys a warp, eight warps, pages looked up
 // tile by tile 119 us; page table entries a batch ahead and a second loading warp 101; the warps' shares joined
-// for the live rows only 100, and the 64 contexts 136 -> 109.  No use: 32 keys a warp (fewer stages in flight), eight
+// for the live rows only 100, and the 64 contexts 136 -> 109; the join that asks for everything at once 94 (one context
+// of 2000 21 -> 14).  No use: 32 keys a warp (fewer stages in flight), eight
 // warps with q in registers (104), the join set up early by a programmatic launch (+1).
 //
 // Fragments.  Inside a product the order of the features (scores) and of the keys (P·V) is free, so a lane takes 16
@@ -531,6 +532,73 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
   }
 }
 
+// ------------------------------------------------------------ join
+// The pieces of an item that the borders between CTAs cut, as in evo_seq_fwd.cu's join: the one that begins it (slot 1 of
+// CTA c), then slot 0 of c + 1, c + 2, ..., joined in that order, a warp a row.  Latency is what it costs, so the records, M and
+// l of 32 pieces and O of eight are asked for together, before it is known how many there are (what lies
+// behind the last is read and not used).
+constexpr int kAhead = 8;
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(32 * kRows) evo_paged8_join_kernel(const __grid_constant__ SeqFwdArgs a, int ctas) {
+  constexpr int kF = DP / 32;  // features a lane
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+  auto at = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * kRows + r; };
+  auto load_ml = [&](int p) { return c0 + p < ctas ? a.part_ml[at(p)] : make_float2(0.0f, 0.0f); };
+  struct alignas(4 * kF) Features {
+    float x[kF];
+  };
+  auto load_o = [&](int p0, Features (&o)[kAhead]) {
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p)
+      if (c0 + p0 + p < ctas) o[p] = *reinterpret_cast<const Features*>(a.part_o + at(p0 + p) * DP + lane * kF);
+  };
+  Features o[kAhead];
+  load_o(0, o);
+  float2 ml = load_ml(lane);
+  const PieceRecord first = a.records[2 * c0 + 1];
+  const int pieces = count_pieces(a.records, c0, ctas);
+  const int G = a.s.group;
+  if (!first.used || r >= first.nt * G) return;
+  float big = lane < pieces && ml.y != 0.0f ? ml.x : -INFINITY;
+  for (int base = 32; base < pieces; base += 32) {
+    const float2 more = base + lane < pieces ? load_ml(base + lane) : make_float2(0.0f, 0.0f);
+    if (more.y != 0.0f) big = fmaxf(big, more.x);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, x));
+  float sum[kF] = {}, l = 0.0f;
+  for (int p0 = 0; p0 < pieces; p0 += kAhead) {
+    if (p0 > 0) {
+      load_o(p0, o);
+      if (p0 % 32 == 0) ml = load_ml(p0 + lane);
+    }
+    // (a piece that saw a NaN may have no maximum: its l is NaN, whatever it is scaled by)
+    const float f_mine = p0 / 32 * 32 + lane < pieces && ml.y != 0.0f ? (big == -INFINITY ? 1.0f : ex2(ml.x - big)) : 0.0f;
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+      const float f = __shfl_sync(0xffffffffu, f_mine, (p0 + p) & 31), y = __shfl_sync(0xffffffffu, ml.y, (p0 + p) & 31);
+      if (p0 + p >= pieces || y == 0.0f) continue;  // (no key: nothing is there)
+      l += y * f;
+#pragma unroll
+      for (int e = 0; e < kF; ++e) sum[e] = fmaf(o[p].x[e], f, sum[e]);
+    }
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const size_t row = static_cast<size_t>(first.row0) + first.t0 + r / G;
+  const int h = first.kvh * G + r % G, d = lane * kF;
+  if (d < a.s.D) {
+    uint32_t v[kF / 2];
+#pragma unroll
+    for (int e = 0; e < kF / 2; ++e) v[e] = l == 0.0f ? 0u : pack2<BF16>(sum[2 * e] * inv, sum[2 * e + 1] * inv);
+    uint16_t* out = a.out + row * a.out_stride + static_cast<size_t>(h) * a.s.D + d;
+    if constexpr (kF == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(v[0], v[1]);
+    else
+      *reinterpret_cast<uint32_t*>(out) = v[0];
+  }
+  if (lane == 0) a.lse[static_cast<size_t>(h) * a.s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
+}
+
 template <int DP, bool BF16>
 cudaError_t launch_t(const Seq8FwdArgs& a, int ctas, cudaStream_t st) {
   auto kern = evo_paged8_few_kernel<DP, BF16>;
@@ -541,7 +609,8 @@ cudaError_t launch_t(const Seq8FwdArgs& a, int ctas, cudaStream_t st) {
   static_assert(smem <= 232448, "shared memory");
   kern<<<ctas, kThreads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.whole) return e;
-  return launch_seq_join(a.f, ctas, BF16, st);
+  evo_paged8_join_kernel<DP, BF16><<<ctas, 32 * kRows, 0, st>>>(a.f, ctas);
+  return cudaGetLastError();
 }
 
 }  // namespace

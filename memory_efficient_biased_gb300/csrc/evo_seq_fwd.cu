@@ -723,9 +723,9 @@ __global__ void __launch_bounds__(256) evo_seq_join_kernel(const __grid_constant
   if (!first.used) return;
   const SeqDesc& s = a.s;
   const int gq = i >> 7, r = i & 127, dt = r / s.group, tok = gq * a.TQ + dt;
-  const bool live = i < a.piece_rows && dt < a.TQ && tok < first.nt;
+  const bool live = dt < a.TQ && tok < first.nt;
   if (!__any_sync(0xffffffffu, live)) return;
-  auto at = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * a.piece_rows + i; };
+  auto at = [&](int p) { return (static_cast<size_t>(c0 + p) * 2 + (p == 0)) * 256 + i; };
   const int sub = threadIdx.x & 7;
   // (m, l) of eight pieces at a time, one a thread
   auto load_ml = [&](int base) {
@@ -795,7 +795,7 @@ cudaError_t launch_t(const SeqFwdArgs& a, int ctas, cudaStream_t st) {
 
 }  // namespace
 
-size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws, int piece_rows) {
+size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws, int rows) {
   const int DP = D <= 64 ? 64 : 128;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -804,10 +804,9 @@ size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws, int piece_
     return p;
   };
   uint8_t* rec = take((size_t(ctas) * 2 + 1) * sizeof(PieceRecord));
-  uint8_t* ml = take(size_t(ctas) * 2 * piece_rows * sizeof(float2));
-  uint8_t* po = take(size_t(ctas) * 2 * piece_rows * DP * sizeof(float));
+  uint8_t* ml = take(size_t(ctas) * 2 * rows * sizeof(float2));
+  uint8_t* po = take(size_t(ctas) * 2 * rows * DP * sizeof(float));
   if (a) {
-    a->piece_rows = piece_rows;
     a->records = reinterpret_cast<PieceRecord*>(rec);
     a->part_ml = reinterpret_cast<float2*>(ml);
     a->part_o = reinterpret_cast<float*>(po);
@@ -816,7 +815,7 @@ size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws, int piece_
 }
 
 cudaError_t launch_seq_join(const SeqFwdArgs& a, int ctas, bool bf16, cudaStream_t st) {
-  const dim3 grid(ctas, (a.piece_rows + kJoinRows - 1) / kJoinRows);
+  const dim3 grid(ctas, 256 / kJoinRows);
   if (a.s.D <= 64) {
     if (bf16)
       evo_seq_join_kernel<64, true><<<grid, 256, 0, st>>>(a, ctas);

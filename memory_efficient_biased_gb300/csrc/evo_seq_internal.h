@@ -137,9 +137,8 @@ struct SeqFwdArgs {
   long long out_stride;
   float* lse;
   PieceRecord* records;  // workspace: two per CTA, and one for the sums of the scores
-  int piece_rows;        // rows of a piece (256, or the 8-bit cache's 16)
-  float2* part_ml;       // ... [ctas][2][piece_rows] (m, l)
-  float* part_o;         // ... [ctas][2][piece_rows][DP], not yet divided by l
+  float2* part_ml;       // ... [ctas][2][256] (m, l); of few rows a key 16 instead of 256
+  float* part_o;         // ... [ctas][2][256][DP], not yet divided by l
   float* scores;         // nullable: s·log2e·S left behind for the weights, [tokens][q_heads][scores_ld]
   long long scores_ld;   // max_kv rounded up to whole tiles
   uint64_t wait_ns;
@@ -160,8 +159,8 @@ struct SeqWeightsArgs {
   float* part;           // ... [ctas][2][128]
   uint64_t wait_ns;
 };
-// Bytes of the workspace for `ctas` CTAs; with a and ws, a's pointers into it.
-size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws, int piece_rows = 256);
+// Bytes of the workspace for `ctas` CTAs and pieces of `rows` rows; with a and ws, a's pointers into it.
+size_t seq_fwd_workspace(int ctas, int D, SeqFwdArgs* a, uint8_t* ws, int rows = 256);
 
 // The prompt's backward on the tensor cores (tk, tv as the prompt forward's).
 struct SeqBwdArgs {

@@ -302,6 +302,53 @@ def test_append8_more_tokens_than_length_and_rows_outside():
     np.testing.assert_array_equal(S.f64(ko[4:12]), cache.rows(0, 8)[0])
 
 
+def test_append8_many_sequences():
+    """More sequences than three rounds of the search for a block's tell apart, most of them short, some empty."""
+    rng = np.random.default_rng(12)
+    n = 1500
+    had, new = rng.integers(0, 20, n), rng.integers(0, 4, n)
+    new[[0, 700, 1499]] = 0, 60, 33
+    ends = [int(x) for x in had + new]
+    cache = C.Cache(rng, [max(ends)] * n, 16, 16, 1, 16)
+    state = fresh_state(cache, 1, 16)
+    for sizes, lens in (([int(x) for x in had], [int(x) for x in had]), ([int(x) for x in new], ends)):
+        T = sum(sizes)
+        k, v = (S.normal(rng, T, 1, 16, dtype=BF, sigma=float(s)) for s in (1.0, 3.0))
+        Q.evo_cache8_append(k.cuda(), v.cuda(), S.offsets(sizes).cuda(), i32(lens), *cache.args(), cache.table)
+        expect_append(cache, state, k, v, sizes, lens)
+    assert_holds(cache, state)
+    ko, vo = Q.evo_cache8_read(*cache.args(), S.offsets(ends).cuda(), i32(ends), cache.table, sum(ends), BF)
+    a = 0
+    for b, e in enumerate(ends):
+        s = np.repeat(state[b][1], 16, 0)[:e, :, None]
+        np.testing.assert_array_equal(S.f64(ko[a:a + e]), state[b][0][:e] * s)
+        a += e
+    q = S.normal(rng, n, 2, 16, dtype=BF)
+    out, lse = Q.evo_paged8_fwd(q.cuda(), *cache.args(), i32(np.arange(n + 1)), i32(ends), cache.table)
+    for b in list(range(0, n, 37)) + [700, 1499]:
+        rows = cache.rows(b, ends[b])
+        C.check_attention(S.f64(q[b:b + 1]), *rows, S.f64(out[b:b + 1]), S.f64(lse[:, b:b + 1]), 0.25, BF, f"sequence {b}")
+    assert E.evo_attn_device_status() == 0
+
+
+def test_offsets_out_of_order_with_more_rows_than_tokens():
+    """Recorded; nothing is written that is not a row of the call or a page of the tables."""
+    rng = np.random.default_rng(13)
+    for Hq in (2, 8, 64):  # the three ways of the attention
+        cache = C.Cache(rng, [60] * 5, 16, 16, 1, 64)
+        k, v, q = (S.normal(rng, 60, h, 64, dtype=BF).cuda() for h in (1, 1, Hq))
+        cu, lens = i32([0, 60, 0, 60, 0, 60]), i32([60] * 5)
+        for call in (lambda s: Q.evo_cache8_append(k, v, cu, lens, *cache.args(), cache.table, status=s),
+                     lambda s: Q.evo_cache8_read(*cache.args(), cu, lens, cache.table, 60, BF, status=s),
+                     lambda s: Q.evo_paged8_fwd(q, *cache.args(), cu, lens, cache.table, status=s)):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            call(status)
+            assert int(status) == 13
+        rest = np.setdiff1d(np.arange(cache.k.shape[0]), cache.table.cpu().numpy())
+        assert torch.all(cache.k.view(torch.uint8)[torch.from_numpy(rest).cuda()] == NAN8)
+    assert E.evo_attn_device_status() == 0
+
+
 def test_bad_indices_are_recorded_and_leave_the_rest():
     rng = np.random.default_rng(11)
     for what in ("offset", "length", "long", "page"):
@@ -579,7 +626,9 @@ def test_paged8_many_rows_unseen_bad_and_captured():
     cache = filled(rng, ctx, 32, 16, Hk, D, interleaved=True)
     clean = [cache.rows(b, n) for b, n in enumerate(ctx)]
     q = S.normal(rng, 150, Hq, D, dtype=BF)
-    qd, cu, lens = q.cuda(), S.offsets(chunks).cuda(), i32(ctx)
+    wide = torch.zeros(150, 2 * Hq * D, dtype=BF, device="cuda")
+    wide[:, :Hq * D] = q.cuda().view(150, -1)
+    qd, cu, lens = wide[:, :Hq * D].view(150, Hq, D), S.offsets(chunks).cuda(), i32(ctx)
     p = int(cache.table[0, 299 // 32])
     cache.v.view(torch.uint8)[p, 299 % 32, 0, 9] = NAN8
     out, lse = Q.evo_paged8_fwd(qd, *cache.args(), cu, lens, cache.table)
@@ -595,7 +644,7 @@ def test_paged8_many_rows_unseen_bad_and_captured():
     C.check_attention(S.f64(q[:80]), *cache.rows(0, 300), S.f64(out[:80]), S.f64(lse[:, :80]), 0.125, BF)
     ws = torch.empty(Q.evo_paged8_fwd_workspace_bytes(150, 2, Hq, Hk, D, cache.k.shape[0], 32, cache.table.shape[1], 16),
                      dtype=torch.uint8, device="cuda")
-    o, z, g = torch.empty_like(out), torch.empty_like(lse), torch.cuda.CUDAGraph()
+    o, z, g = wide[:, Hq * D:].view(150, Hq, D), torch.empty_like(lse), torch.cuda.CUDAGraph()
     lens.sub_(10)
     with torch.cuda.graph(g):
         Q.evo_paged8_fwd(qd, *cache.args(), cu, lens, cache.table, out=o, lse=z, workspace=ws)
