@@ -14,7 +14,8 @@ namespace {
 // on, which the CTAs search; the numbers that are left over have no block.  (The search, not the
 // bytes, is what a step of single tokens waits for.)
 //
-// Bound by the bytes: two read and one written an element, and nothing else where the scale does not grow.
+// What it cannot do without: two bytes read and one written an element where the scale does not grow. 10,188 tokens of 8 heads of
+// 128, keys and values, take 16 us, where those bytes take 9: the lookups in front of the loads and 1.7 instructions a clock.
 constexpr int kAppendThreads = 256;
 
 __device__ __forceinline__ long long block_number(const SeqDesc& s, int block, int b) {
