@@ -240,9 +240,11 @@ EVO_API evo_status_t evo_rotary(const void* q, const void* k, const int32_t* pos
  * that is not finite is stored as NaN and does not enter the scale.  Where a block's first
  * token is new, what its scale held before does not matter.
  *
- * Scales that others wrote may be any numbers from 2^-64 to 2^120.  Reading rounds code * scale to
+ * Scales that others wrote may be 0 and any numbers from 2^-64 to 2^120.  Reading rounds code * scale to
  * dtype (for scales that are powers of two exact within its range) and saturates at its largest
- * finite number.  Attention takes code * scale as it is, or, with many rows a key, as reading gives it. */
+ * finite number.  Attention takes code * scale as it is (a value with a scale of 0 with 2^-64), or, with many
+ * rows a key, as reading gives it.  The scales of the values that a row sees lie within 2^90 of one another: a key whose
+ * scale is farther below another's may lose its weight. */
 typedef struct {
   int64_t num_pages, page_size, pages_per_seq;
   int64_t scale_block;

@@ -334,7 +334,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
           for (int e = 0; e < 4; ++e)
             if (key0 + 8 * n + c + 4 * (e & 1) > (e < 2 ? pos0 : pos1)) t[n][e] = -INFINITY;
       }
-      const float lv = lg2(vs), iv = ex2(-lv);
+      const float lv = log2_value_scale(vs), iv = ex2(-lv);
       float a0 = fmaxf(fmaxf(t[0][0], t[0][1]), fmaxf(t[1][0], t[1][1])) + lv;
       float a1 = fmaxf(fmaxf(t[0][2], t[0][3]), fmaxf(t[1][2], t[1][3])) + lv;
       // (the lanes that share rows need one M for them only where it moves)

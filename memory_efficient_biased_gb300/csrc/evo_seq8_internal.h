@@ -37,6 +37,13 @@ __device__ __forceinline__ long long scale_at(const Cache8& c, const SeqDesc& s,
   return (static_cast<long long>(p) * s.kv_heads + h) * c.blocks + (j % s.page) / c.block;
 }
 
+// log2 of a scale of values, -64 at the least (a block of zeros may have a scale of 0); NaN stays NaN.
+__device__ __forceinline__ float log2_value_scale(float s) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(lg2(s)), "f"(-64.0f));
+  return r;
+}
+
 // Four codes as two pairs of f16 (bytes 0 and 1, bytes 2 and 3), exactly; NaN stays NaN.
 __device__ __forceinline__ uint2 f16x4_of_codes(uint32_t codes) {
   uint2 r;

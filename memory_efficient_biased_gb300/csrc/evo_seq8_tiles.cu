@@ -261,7 +261,7 @@ __device__ __forceinline__ void walk(const Seq8FwdArgs& a, Bars* bars, const Wai
       if (lane < 8) {
         bars->scales[slot][0][lane] = now;
       } else if (lane < 16) {
-        const float lv = lg2(now);
+        const float lv = log2_value_scale(now);
         bars->scales[slot][1][lane - 8] = lv;
         bars->scales[slot][2][lane - 8] = ex2(-lv);
       }

@@ -454,6 +454,25 @@ def test_paged8_given_scales_and_scale():
         check_paged(cache, q, chunks, ctx, out, lse, float(np.float32(0.05)), dtype, vmax=vmax)
 
 
+@pytest.mark.parametrize("chunks,ctx", [([1, 2], [300, 77]), ([1], [3000]), ([60, 3], [300, 77]), ([300], [301])])
+def test_paged8_scales_of_zero(chunks, ctx):
+    """Blocks of zeros with a scale of 0, as others may write them, and as an append leaves them, 2^-64: their keys (the first of them
+    with large scores against the others') have weight, their values none.  The blocks of keys that are zero the same."""
+    rng = np.random.default_rng(26)
+    for zero in (0.0, 2.0 ** -64):
+        cache = C.Cache(rng, ctx, 32, 32, 2, 64)
+        for b, n in enumerate(ctx):
+            k, v = (rng.standard_normal((n, 2, 64)) for _ in "kv")
+            v[:32, 0] = v[-40:, 1] = k[32:64, 1] = 0.0
+            k[:32] *= 3.0
+            cache.fill(b, k, v)
+        for s in (cache.ks, cache.vs):
+            s[s == 2.0 ** -64] = zero
+        q = S.normal(rng, sum(chunks), 4, 64, dtype=BF)
+        out, lse = Q.evo_paged8_fwd(q.cuda(), *cache.args(), S.offsets(chunks).cuda(), i32(ctx), cache.table)
+        check_paged(cache, q, chunks, ctx, out, lse, 0.125, BF)
+
+
 def test_paged8_rising_scores():
     """A maximum that moves far, more than once, in some rows only."""
     rng = np.random.default_rng(22)
