@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kAppendThreads) evo_append8_kernel(const __gri
   float now = scale_for(to_f32<BF16>(static_cast<uint16_t>(bits)));
   if (before > now && before < INFINITY) now = before;  // (a block without tokens from before has 0 there)
   if (older && now != before && live) {
-    const float shrink = before > 0.0f && before < INFINITY ? before / now : 1.0f;
+    const float shrink = before >= 0.0f && before < INFINITY ? before / now : 1.0f;  // (0: they stand for 0)
     for (int r = 0; r < steps; ++r) {
       const int at = place + r * step;
       if (start + at >= lo) break;

@@ -267,6 +267,32 @@ def test_append8_extremes(dtype):
     assert torch.equal(torch.nan_to_num(vo, nan=7.0), torch.nan_to_num(ko.flip(0), nan=7.0))
 
 
+def test_append8_behind_scales_of_others():
+    """Tokens behind some whose scale is 0, and they 0 with it whatever their codes; whose scale is no power of two."""
+    rng = np.random.default_rng(27)
+    for block, old in ((16, 0.0), (64, 0.0), (64, 1.5 * 2.0 ** -12), (32, 1.25 * 2.0 ** 9)):
+        cache = C.Cache(rng, [60], 64, block, 2, 64)
+        cache.fill(0, *(rng.standard_normal((21, 2, 64)) for _ in "kv"))
+        for s in (cache.ks, cache.vs):
+            s[s > 0] = old
+        page = int(cache.table[0, 0])
+        state = fresh_state(cache, 2, 64)
+        for at, (pages, scales) in ((0, (cache.k, cache.ks)), (2, (cache.v, cache.vs))):
+            state[0][at][:] = C.value_of(pages, torch.ones_like(scales))[page]
+            state[0][at + 1][:] = scales[page].double().cpu().numpy().T
+        k, v = (S.normal(rng, 9, 2, 64, dtype=BF) for _ in "kv")
+        Q.evo_cache8_append(k.cuda(), v.cuda(), i32([0, 9]), i32([30]), *cache.args(), cache.table)
+        if old == 0.0:
+            expect_append(cache, state, k, v, [9], [30])
+            assert_holds(cache, state)
+        else:
+            got, want = cache.rows(0, 30), [np.concatenate([state[0][at][:21] * old, S.f64(x)]) for at, x in ((0, k), (2, v))]
+            for x, y, s in zip(got, want, (cache.ks, cache.vs)):
+                # a rounding to three bits, after one in 32 bits that may move it over a border
+                least = float(s[page].max()) * 2.0 ** -10
+                assert np.all(np.abs(x - y) <= np.abs(y) * (2.0 ** -4 + 2.0 ** -20) + least)
+
+
 def test_append8_strided_pages_and_rows():
     rng = np.random.default_rng(9)
     cache = C.Cache(rng, [100, 30], 32, 32, 2, 64, interleaved=True)
