@@ -56,7 +56,10 @@ bool map_pages8(CUtensorMap* m, const void* p, const evo_seq_shape_t& s, const e
 }
 
 // Which kernels, and their launch.
-//   few    up to 16 rows a sequence and kv head on the average, and a token's heads in one tile of 16
+//   few    up to 32 rows a sequence and kv head on the average, and a token's heads in one tile of 16.  The cache is then read
+//          twice, at 6 TB/s, where the other kernel widens it once, at 1.8.  Measured, 24 to 32 rows of few / of the other:
+//          16 contexts of 8192 (8 kv heads of 128) 111 / 150 us, 2 of 16,384 38 / 50, 32 of 2048 85 / 103, one of
+//          100,000 88 / 110, 64 of 700 95 / 102; 48 rows 156 / 152, 47 / 51, 102 / 104, 116 / 113, 129 / 103
 //   copy   many rows, and the codes are widened once, into the workspace, for the 16-bit forward; otherwise every block of 256
 //          rows widens them as it needs them.  The copy costs 6 bytes a code and a launch; widening in place what it takes
 //          beside the products.  So: from more than two blocks a sequence on, while the copy stays below 512 MB.  Measured,
@@ -75,7 +78,7 @@ constexpr double kCopyBytes = 512.0 * 1024 * 1024;
 Plan plan(int sms, const evo_seq_shape_t& s, const evo_cache8_shape_t& c) {
   const int64_t G = s.q_heads / s.kv_heads, max_kv = c.page_size * c.pages_per_seq;
   Plan p{};
-  p.few = G <= kFewRows && s.tokens * G <= kFewRows * s.seqs;
+  p.few = G <= kFewRows && s.tokens * G <= 2 * kFewRows * s.seqs;
   if (!p.few) {
     p.ctas = fwd_ctas(sms, s, max_kv);
     p.rows = 256;

@@ -438,7 +438,8 @@ PAGED = [([1], [1], 1, 1, 64, 16, 16), ([1], [777], 8, 2, 128, 16, 16), ([1, 1, 
          ([1, 0, 1], [513, 9, 64], 16, 1, 128, 128, 128), ([3, 1, 2], [300, 256, 2], 5, 1, 80, 32, 16),
          ([17, 5], [17, 400], 6, 2, 96, 16, 16), ([130, 1, 64], [130, 700, 333], 4, 2, 128, 64, 64),
          ([200], [900], 8, 1, 64, 384, 128), ([1, 40], [260, 41], 128, 1, 64, 16, 16), ([2, 1], [99, 130], 24, 1, 48, 32, 32),
-         ([1] * 40, [7 + 31 * i % 400 for i in range(40)], 8, 2, 16, 16, 16), ([5, 9], [600, 1300], 3, 3, 112, 1024, 64)]
+         ([1] * 40, [7 + 31 * i % 400 for i in range(40)], 8, 2, 16, 16, 16), ([5, 9], [600, 1300], 3, 3, 112, 1024, 64),
+         ([8, 5, 8], [3000, 900, 2500], 8, 2, 128, 64, 16), ([9, 8], [1700, 60], 8, 2, 64, 32, 32)]
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
