@@ -63,8 +63,10 @@ bool map_pages8(CUtensorMap* m, const void* p, const evo_seq_shape_t& s, const e
 //   copy   many rows, and the codes are widened once, into the workspace, for the 16-bit forward; otherwise every block of 256
 //          rows widens them as it needs them.  The copy costs 6 bytes a code and a launch; widening in place what it takes
 //          beside the products.  So: from more than two blocks a sequence on, while the copy stays below 512 MB.  Measured,
-//          in place / copied: one block (2 x 64 tokens over 16384 each, group 4) 64 / 93 us, 3.5 blocks (455 tokens over
-//          12,291, head_dim 64) 44 / 40, 5.2 (1325 over 23,348) 232 / 167, 64 (4096 over 16,384) 970 / 758.
+//          in place / copied, 8 kv heads with group 4 of 128 unless given: two contexts of 16,384 2 blocks each 88 / 110 us,
+//          4 150 / 163, 6 210 / 212, 8 271 / 265; one of 23,348 21 blocks 476 / 424, of 16,384 64 blocks 897 / 759;
+//          head_dim 64, one of 12,291 3.5 blocks 44 / 40, 4 of 5000 4 blocks 55 / 57.  Where most rows are those of few sequences,
+//          the average says too little of them: 5.2 blocks, 1325 tokens over 23,348 in all, 220 / 165; hence two, not six.
 //   whole  few rows, contexts of at most 1024 keys and no more items than SMs: no item is cut, nothing is joined.  An SM takes
 //          0.7 us a tile, a second launch 3 and the host 4 (777 keys of 8 heads: 12 us of GPU either way, 22 and 26 a call).
 size_t round_up(size_t bytes) { return (bytes + 255) & ~size_t(255); }

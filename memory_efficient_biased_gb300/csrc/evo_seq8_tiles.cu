@@ -8,12 +8,15 @@
 // The tensor core takes 16 bits from shared memory, so a tile of codes arrives in a staging buffer and four warps widen
 // it into the ring that the products read: 128 KB a pair of key tiles in and out of shared memory, beside the products' own 192.
 //
-// What bounds it: the chain scores, maximum, exponentials, P·V of a pair of tiles, as in the 16-bit forward, at 4600 to 4800
-// cycles instead of 3500: 700 of them are the widening's (1440 cycles a tile and warp, beside the softmax on the same
-// schedulers and the products on the same shared memory), 600 the scales'.  4096 tokens over 16,384 keys, 32 heads of 128: 970
-// us, where a copy widened beforehand and the 16-bit forward take 758; 2 x 64 tokens over 16,384 each 64 us, where those take 93.
-// No use: four slots and two staging buffers instead of three and three (1020), codes loaded into registers
-// instead of a staging buffer (2020: the loads' latency, and no registers to hide it in).
+// What bounds it: the chain scores, maximum, exponentials, P·V of a pair of tiles, as in the 16-bit forward, and the widening
+// beside it, on the same schedulers and the same shared memory.  4096 tokens over 16,384 keys, 32 heads of 128: 897 us, where a
+// copy widened beforehand and the 16-bit forward take 759; 2 x 64 tokens over 16,384 each 60 us, where those take 87; 16 x 16 tokens
+// over 8192 each 131 (a key tile and SM 2.0 us: the ring holds a tile and a half, and the next keys are widened when a
+// tile's P·V is done).  The widening is the better for having few loads under way: with two pieces of a row, and
+// what only the last tiles need in a loop of its own, 131; one 134, four 138, eight 136; four with the checks
+// in the same loop 151, all eight of them before the wait for the place they go to 203.
+// No use: four slots and two staging buffers instead of three and three, codes loaded into registers instead of a staging
+// buffer (twice as long: the loads' latency, and no registers to hide it in).
 //
 // Roles (16 warps, one CTA per SM, persistent over its share of the work):
 //   warps 0-3, 4-7  softmax of query tile 0 and 1, one thread per row
@@ -330,19 +333,25 @@ __device__ __forceinline__ void widen(const Seq8FwdArgs& a, uint8_t* base, Bars*
         uint8_t* to = base + L::ring + slot * L::kTB + r * 128;
         const bool none = kv && r >= last, some = kv && r >= all;
         bool lost = false;
-#pragma unroll 4
-        for (int i = 0; i < DP / 16; ++i) {
-          const int piece = DP == 128 ? (i ^ r) & 7 : (i ^ (r >> 1)) & 3;
-          uint4 x = *reinterpret_cast<const uint4*>(from + piece * 16);
-          if (some) {
-            const uint32_t n0 = nan_bytes(x.x), n1 = nan_bytes(x.y), n2 = nan_bytes(x.z), n3 = nan_bytes(x.w);
-            lost = lost || (!none && (n0 | n1 | n2 | n3));
-            x = none ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(x.x & ~n0, x.y & ~n1, x.z & ~n2, x.w & ~n3);
-          }
+        auto put = [&](int i, const uint4& x) {
           const uint2 f0 = f16x4_of_codes(x.x), f1 = f16x4_of_codes(x.y), f2 = f16x4_of_codes(x.z), f3 = f16x4_of_codes(x.w);
           uint8_t* half = to + (i >> 2) * L::kHalf;
           *reinterpret_cast<uint4*>(half + (((2 * i) ^ r) & 7) * 16) = make_uint4(f0.x, f0.y, f1.x, f1.y);
           *reinterpret_cast<uint4*>(half + (((2 * i + 1) ^ r) & 7) * 16) = make_uint4(f2.x, f2.y, f3.x, f3.y);
+        };
+        auto piece = [&](int i) { return *reinterpret_cast<const uint4*>(from + (DP == 128 ? (i ^ r) & 7 : (i ^ (r >> 1)) & 3) * 16); };
+        if (!some) {
+#pragma unroll 2
+          for (int i = 0; i < DP / 16; ++i) put(i, piece(i));
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < DP / 16; ++i) {
+            uint4 x = piece(i);
+            const uint32_t n0 = nan_bytes(x.x), n1 = nan_bytes(x.y), n2 = nan_bytes(x.z), n3 = nan_bytes(x.w);
+            lost = lost || (!none && (n0 | n1 | n2 | n3));
+            x = none ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(x.x & ~n0, x.y & ~n1, x.z & ~n2, x.w & ~n3);
+            put(i, x);
+          }
         }
         if (lost) bars->dirty[it % kDescs] = 1;
         fence_proxy_async_smem();

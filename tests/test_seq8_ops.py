@@ -638,14 +638,15 @@ def test_paged8_past_32_bits_of_offset():
 
 
 COPIED = [([300], [300], 8, 2, 128, 16, 16), ([200, 0, 260], [700, 33, 260], 16, 2, 64, 64, 32), ([33, 70], [500, 400], 64, 1, 80, 32, 32),
-          ([600, 1], [1400, 900], 4, 2, 128, 128, 128), ([180], [1025], 12, 4, 96, 384, 64), ([9], [64], 128, 1, 16, 16, 16)]
+          ([600, 1], [1400, 900], 4, 2, 128, 128, 128), ([180], [1025], 12, 4, 96, 384, 64), ([9], [64], 128, 1, 16, 16, 16),
+          ([500], [500], 8, 2, 128, 16, 16), ([300, 0, 301], [700, 33, 400], 16, 2, 112, 64, 32), ([30, 70], [1400, 900], 64, 2, 128, 128, 128)]
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("chunks,ctx,Hq,Hk,D,page,block", COPIED)
 def test_paged8_many_rows(chunks, ctx, Hq, Hk, D, page, block, dtype):
-    """More rows a key than two blocks: the codes are widened once, into the workspace; with a table too wide for that
-    (places for 2^20 tokens and more), where they are used.  Behind the sequences' ends the pages and scales hold NaN."""
+    """More rows a key than two blocks: the codes are widened once, into the workspace; with a
+    table too wide for that (places for 2^20 tokens and more), where they are used.  Behind the sequences' ends the pages and scales hold NaN."""
     rng = np.random.default_rng(sum(ctx) + 1)
     cache = filled(rng, ctx, page, block, Hk, D)
     for s in (cache.ks, cache.vs):
@@ -655,7 +656,8 @@ def test_paged8_many_rows(chunks, ctx, Hq, Hk, D, page, block, dtype):
     wide[:, :cache.table.shape[1]] = cache.table
     need = [Q.evo_paged8_fwd_workspace_bytes(sum(chunks), len(ctx), Hq, Hk, D, cache.k.shape[0], page, t.shape[1], block)
             for t in (cache.table, wide)]
-    assert need[0] >= 4 * len(ctx) * max(ctx) * Hk * D and need[1] < 1 << 29
+    copied = sum(chunks) * Hq // Hk > 512 * len(ctx)
+    assert (need[0] >= 4 * len(ctx) * max(ctx) * Hk * D if copied else need[0] <= need[1]) and need[1] < 1 << 29
     for table in (cache.table, wide):
         args = q.cuda(), *cache.args(), S.offsets(chunks).cuda(), i32(ctx), table
         out, lse = Q.evo_paged8_fwd(*args)
