@@ -3,10 +3,16 @@
 //
 // Mathematics, per row (token, head) and block of keys with scales s_k and s_v: S = q·code_k,
 // t = s_k s·log2e·S, P' = 2^(t + log2 s_v - M) with M the running maximum of t + log2 s_v, l = Σ P' / s_v and
-// O = Σ P' code_v; at the end O / l and lse = ln2·(M + log2 l).  The weight that a value enters with is
-// P' = P s_v: held against the largest such product it fits fp16 whatever the scales, and the codes
-// themselves, exact in fp16, are the other operand.  q is exact in fp16 too, for bf16 after its row
-// is brought to a largest magnitude of 1 to 2 by a power of two (what falls below 2^-24 of that is lost).
+// O = Σ P' code_v; at the end O / l and lse = ln2·(M + log2 l).  The codes are exact in fp16; so is q, for bf16 after its
+// row is brought to a largest magnitude of 1 to 2 by a power of two (what falls below 2^-24 of that is lost).
+//
+// Range.  The weight that a value enters with is P' = P s_v, held times 2^14: fp16 has 11 bits of it down to 2^-28 of the
+// largest, and loses it below 2^-39.  Among keys of like scales that loses weights below 2^-35 of the largest, less than l's own
+// rounding.  A key whose scale is far below another's may have a small P' and a large weight, though, and values of its own where
+// the other's codes are 0.  So 16 keys whose scale is below 2^-4 of the largest so far, and some of whose P' are below 2^-14 of the row's
+// largest, are held against their own largest: P' times 2^d, and O and l times 2^d before their product and 2^-d after it, d whole
+// (72 at the most: O below 2^50 stays finite).  That costs such keys a second time what they take; without them nothing (a product with
+// factors of its own for them beside the usual one took 7 to 14 % from all others, for the registers).
 //
 // Why mma.sync.  A byte of the cache has to be turned into 16 bits before a product of 16 bits
 // takes it.  tcgen05 would take it from shared memory: staged, read, written twice as wide and read by the product,
@@ -47,6 +53,8 @@ constexpr int kRows = kFewRows, kWarps = 12, kThreads = 32 * (kWarps + 4), kDesc
 constexpr int kKeys = 16, kGroups = kTile / kKeys;  // keys that a warp takes at a time, times that a tile is
 constexpr int kStages = 6;                          // tiles
 constexpr int kJoined = 4;                          // rows whose shares are joined at a time, a warp each
+constexpr float kHeld = 14.0f;  // log2 of what a row's largest P' is held as
+constexpr float kNear = 4.0f;   // log2 of how far scales of values lie apart and need no more than that
 
 template <int DP>
 struct Layout {
@@ -267,7 +275,27 @@ __device__ __forceinline__ void fetch_q(const Seq8FwdArgs& a, uint8_t* base, Bar
   }
 }
 
-// ------------------------------------------------------------ compute (warps 0..7)
+// ------------------------------------------------------------ compute (warps 0..11)
+template <int COLS>
+__device__ __forceinline__ void scale_rows(float (&o)[COLS][4], float& l0, float& l1, float f0, float f1) {
+  l0 *= f0, l1 *= f1;
+#pragma unroll
+  for (int n = 0; n < COLS; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
+}
+
+// By which power of two keys are held apart whose largest t + log2 s_v of this lane is x, in a row whose maximum is m: what brings the
+// four lanes' largest to M, and at most 2^72, or what l allows (O is below 2^23 a key).
+__device__ __forceinline__ float power_of_two(int d) { return __uint_as_float(static_cast<uint32_t>(127 + d) << 23); }
+__device__ __forceinline__ uint32_t apart_by(float m, float x, float l) {
+#pragma unroll
+  for (int i = 1; i < 4; i *= 2) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
+    l = fmaxf(l, __shfl_xor_sync(0xffffffffu, l, i));
+  }
+  const float d = fminf(fminf(m - x, 72.0f), 120.0f - lg2(l));
+  return x > -INFINITY && d > 0.0f ? static_cast<uint32_t>(d) : 0u;
+}
+
 template <int DP, bool BF16>
 __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g) {
   using L = Layout<DP>;
@@ -283,7 +311,8 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
     const uint32_t qs = smem_u32(base + L::q + (it & 1) * L::kQ) + lane * 16;
     const int pos0 = w.pos + dt0, pos1 = w.pos + dt1;
     float o[kCols][4] = {};
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // (O and l are held times 2^kHeld)
+    float top = -INFINITY;                                       // log2 of the largest scale of values so far
     // The 16 keys that are this warp's: every twelfth of all that the CTA walks over.  (A stage is either always one
     // of those that a warp looks at, or never: 12 times 16 keys are a tile and a half, and there are six stages.)
     const uint32_t end = (use + static_cast<uint32_t>(w.j1 - w.j0)) * kGroups;
@@ -346,11 +375,19 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
         const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
         const float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - n1);
         m0 = n0, m1 = n1;
-        l0 *= f0, l1 *= f1;
-#pragma unroll
-        for (int n = 0; n < kCols; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
+        scale_rows(o, l0, l1, f0, f1);
       }
-      const float b0 = lv - (m0 == -INFINITY ? 0.0f : m0), b1 = lv - (m1 == -INFINITY ? 0.0f : m1);
+      float b0 = (lv + kHeld) - (m0 == -INFINITY ? 0.0f : m0), b1 = (lv + kHeld) - (m1 == -INFINITY ? 0.0f : m1);
+      // Keys whose scale is small, and which lie so far below M that fp16 would lose of them, are held 2^d times as large, and
+      // so are O and l until their product is done (exactly: d is whole).
+      top = fmaxf(top, lv);
+      uint32_t apart = 0;  // d of both rows
+      if (lv < top - kNear && __any_sync(0xffffffffu, (a0 < m0 - kHeld && a0 > -INFINITY) || (a1 < m1 - kHeld && a1 > -INFINITY))) {
+        const uint32_t d0 = apart_by(m0, a0, l0), d1 = apart_by(m1, a1, l1);
+        apart = d0 | d1 << 8;
+        b0 += static_cast<float>(d0), b1 += static_cast<float>(d1);
+        scale_rows(o, l0, l1, power_of_two(d0), power_of_two(d1));
+      }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -399,6 +436,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
         mma16816(o[4 * e + 2], p, f1.x, g1.x);
         mma16816(o[4 * e + 3], p, f1.y, g1.y);
       }
+      if (apart) scale_rows(o, l0, l1, power_of_two(-static_cast<int>(apart & 0xffu)), power_of_two(-static_cast<int>(apart >> 8)));
     }
     use += static_cast<uint32_t>(w.j1 - w.j0);
     __syncwarp();
@@ -424,7 +462,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
             for (int n = 0; n < kCols; n += 4)
               *reinterpret_cast<float4*>(to + (DP == 128 ? 16 * (c + 4 * x) : 8 * (2 * c + x)) + n) =
                   make_float4(o[n][e + x], o[n + 1][e + x], o[n + 2][e + x], o[n + 3][e + x]);
-          if (c == 0) *reinterpret_cast<float2*>(to + DP) = up ? make_float2(m1, l1) : make_float2(m0, l0);
+          if (c == 0) *reinterpret_cast<float2*>(to + DP) = up ? make_float2(m1 - kHeld, l1) : make_float2(m0 - kHeld, l0);
         };
         if (first < 8)
           put(std::false_type{});

@@ -83,3 +83,59 @@ def check_attention(q, k, v, out, lse, scale, dtype, what="", vmax=None):
         big = 2 * np.max(np.abs(v[:, h // G]), initial=0.0) if vmax is None else vmax
         bound = (2 * u + rp[h][:, None]) * (p[h] @ np.abs(v[:, h // G])) + k.shape[0] * 2.0 ** -25 * big + S.TINY[dtype]
         S.assert_close(out[:, h], o[:, h], bound, f"{what} out head {h}")
+
+
+def coded(rng, ctx, page, block, heads, D, k, v, **kw):
+    """A Cache of sequences of ctx[b] tokens that holds what k(b, n) and v(b, n) give: (values [n, H, D] that are
+    numbers of e4m3, scales [ceil(n / block), H]), written as they are."""
+    cache = Cache(rng, ctx, page, block, heads, D, **kw)
+    for b, n in enumerate(ctx):
+        j = torch.arange(n, device="cuda")
+        at = cache.table[b].long()[j // page]
+        first = torch.arange(0, n, block, device="cuda")
+        first_at = cache.table[b].long()[first // page]
+        for pages, scales, make in ((cache.k, cache.ks, k), (cache.v, cache.vs, v)):
+            x, s = make(b, n)
+            codes = torch.from_numpy(np.ascontiguousarray(x, np.float32)).cuda().to(E4M3)
+            pages.view(torch.uint8)[at, j % page] = codes.view(torch.uint8)
+            scales[first_at, :, first % page // block] = torch.from_numpy(np.ascontiguousarray(s, np.float32)).cuda()
+    return cache
+
+
+def close_bounds(q, k, v, z, p, scale, dtype, few):
+    """How far out [n,Hq,D] and lse [Hq,n] may be off, from the weights themselves: sharper than check_attention, whose
+    last term takes the largest weight as 1 and every code as 448.  z, p: the oracle's lse and weights; few: the
+    kernel for few rows a key.
+
+    P is rounded by u_P: to fp16 (few), to dtype otherwise.  What is below fp16's normal numbers is held in steps of 2^-24:
+      few   the largest P s_v of a row is held as 2^14 to 2^15.  Keys of 16 next to each other share their scale and
+            are held against their own largest weight, 2^14, where they lie 2^14 or more below the row's largest and their scale
+            2^4 or more below the largest so far: 2^-25 of the 16's largest weight at the most.  Where their scale is not that
+            much smaller the steps are those of the row's largest: 2^-39 2^4 of the largest weight
+      many  fp16 alone: 2^-25 of the largest weight (the reference is at most the row's maximum)
+    times |v| of each key."""
+    es, u = S.score_error(q, k, scale), S.U[dtype]
+    G = q.shape[1] // k.shape[1]
+    zz = np.where(np.isfinite(z), np.abs(z), 0.0)
+    rp = 2 * es + 2.0 ** -18 * (1 + zz)
+    out = np.zeros(q.shape)
+    for h in range(q.shape[1]):
+        a, w = np.abs(v[:, h // G]), p[h]
+        bound = ((2.0 ** -11 if few else u) + u + rp[h][:, None]) * (w @ a) + S.TINY[dtype]
+        if few:
+            pad = -len(a) % 16
+            blocks = np.pad(a, ((0, pad), (0, 0))).reshape(-1, 16, a.shape[1]).sum(1)
+            most = np.pad(w, ((0, 0), (0, pad))).reshape(len(w), -1, 16).max(2)
+            bound = bound + 2.0 ** -25 * (most @ blocks) + 2.0 ** -35 * w.max(1)[:, None] * a.sum(0)
+        elif dtype == torch.float16:
+            bound = bound + 2.0 ** -25 * w.max(1)[:, None] * a.sum(0)
+        out[:, h] = bound
+    return out, es + 2.0 ** -19 * (1 + zz)
+
+
+def check_close(q, k, v, out, lse, scale, dtype, few, what=""):
+    """check_attention with the bounds above."""
+    o, z, _, p = O.attend(q, k, v, scale)
+    bound, lse_bound = close_bounds(q, k, v, z, p, scale, dtype, few)
+    S.assert_close(lse, z, lse_bound, f"{what} lse")
+    S.assert_close(out, o, bound, f"{what} out")

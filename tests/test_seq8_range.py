@@ -1,0 +1,102 @@
+"""GPU: attention over the 8-bit cache where weights and scales lie far apart, against the fp64 oracle
+within bounds that follow from the weights themselves (tests/seq8_util.py, close_bounds): few rows a key, and many over a copy."""
+import numpy as np
+import pytest
+import torch
+
+from memory_efficient_biased_gb300 import evo_attn as E
+from memory_efficient_biased_gb300 import evo_seq as Q
+from oracle import seq_oracle as O
+from tests import seq8_util as C
+from tests import seq_util as S
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+WAYS = ["few", "copied"]
+
+
+def attend(way, cache, ctx, q, Hk, scale=None):
+    """(out, lse) of the new tokens q [n, Hq, D] of one sequence, and that the call goes that way."""
+    n, Hq, D = q.shape
+    rows = n * Hq // Hk
+    assert rows <= 32 if way == "few" else rows > 512
+    cu, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [ctx]))
+    args = q.cuda(), *cache.args(), cu, lens, cache.table
+    out, lse = Q.evo_paged8_fwd(*args, scale=scale)
+    again = Q.evo_paged8_fwd(*args, scale=scale)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert E.evo_attn_device_status() == 0
+    return S.f64(out), S.f64(lse)
+
+
+def tokens_of(way, G):
+    return 32 // G if way == "few" else 512 // G + 1
+
+
+@pytest.mark.parametrize("apart", [12, 20, 40, 88])
+@pytest.mark.parametrize("order", ["large first", "small first", "mixed"])
+@pytest.mark.parametrize("way", WAYS)
+def test_blocks_of_equal_weight_and_scales_far_apart(way, order, apart):
+    """All keys alike (the same weight); half of the blocks have a scale 2^apart times the others' and codes of 0 in half of
+    the features: there the small blocks' values are all that there is.  (Few rows: an item that is not cut, several blocks a warp.)"""
+    rng = np.random.default_rng(apart)
+    Hq, Hk, D, ctx = 8, 2, 64, 1000 if way == "few" else 1500
+    n = -(-ctx // 16)
+    large = rng.random(n) < 0.5 if order == "mixed" else (np.arange(n) < n // 2) == (order == "large first")
+
+    def v(b, length):
+        x = O.round_e4m3(rng.uniform(1.0, 440.0, (length, Hk, D)))
+        x[np.repeat(large, 16)[:length], :, :D // 2] = 0.0
+        return x, np.repeat(np.where(large, 2.0 ** (apart // 2), 2.0 ** (apart // 2 - apart))[:, None], Hk, 1)
+
+    cache = C.coded(rng, [ctx], 64, 16, Hk, D, lambda b, length: (np.zeros((length, Hk, D)), np.ones((n, Hk))), v)
+    q = S.normal(rng, tokens_of(way, Hq // Hk), Hq, D, dtype=BF)
+    out, lse = attend(way, cache, ctx, q, Hk)
+    C.check_close(S.f64(q), *cache.rows(0, ctx), out, lse, D ** -0.5, BF, way == "few", way)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("way", ["few", "copied"])
+def test_one_key_of_large_weight_and_scale(way, dtype):
+    """One key with 2^13 times the weight and 2^12 times the scale of each of the others, and codes of 0 in half of the features."""
+    rng = np.random.default_rng(3)
+    Hq, Hk, D, ctx = 8, 1, 64, 20000 if way == "copied" else 131071
+    big, sign, n = ctx // 2 + 5, np.where(rng.random(D) < 0.5, -1.0, 1.0), -(-ctx // 16)
+
+    def k(b, length):
+        x = np.zeros((length, Hk, D))
+        x[big] = 9.0 * sign
+        return x, np.ones((n, Hk))
+
+    def v(b, length):
+        x, s = O.round_e4m3(rng.uniform(1.0, 4.0, (length, Hk, D))), np.full((n, Hk), 2.0 ** -4)
+        at = big // 16 * 16
+        s[at // 16] = 2.0 ** 8
+        x[at:at + 16] = 0.0
+        x[big, :, D // 2:] = 3.0
+        return x, s
+
+    cache = C.coded(rng, [ctx], 128, 16, Hk, D, k, v)
+    q = torch.from_numpy(np.ascontiguousarray(np.broadcast_to(sign / (9.0 * D), (tokens_of(way, Hq), Hq, D)), np.float32)).to(dtype)
+    scale = float(np.float32(13 * np.log(2.0)))
+    out, lse = attend(way, cache, ctx, q, Hk, scale)
+    C.check_close(S.f64(q), *cache.rows(0, ctx), out, lse, scale, dtype, way == "few", way)
+
+
+@pytest.mark.parametrize("dtype,lo,hi", [(BF, -44, 45), (FP, -14, 8)])
+@pytest.mark.parametrize("D,page,block", [(64, 64, 16), (128, 16, 16), (96, 128, 64)])
+@pytest.mark.parametrize("way", WAYS)
+def test_scales_of_any_size(way, D, page, block, dtype, lo, hi):
+    """Every block of values has a scale of its own, anywhere in the range; half of the codes are 0; scores spread over 30 powers
+    of two."""
+    rng = np.random.default_rng(D + page)
+    Hq, Hk, ctx = 8, 2, 1000 if way == "few" else 1777
+    n = -(-ctx // block)
+    make = lambda zeros, s: lambda b, length: (  # noqa: E731
+        O.round_e4m3(rng.standard_normal((length, Hk, D)) * 20.0) * (rng.random((length, Hk, D)) >= zeros), s)
+    cache = C.coded(rng, [ctx], page, block, Hk, D, make(0.0, 2.0 ** rng.integers(-6, -3, (n, Hk))),
+                    make(0.5, 2.0 ** rng.integers(lo, hi, (n, Hk))))
+    q = S.normal(rng, tokens_of(way, Hq // Hk), Hq, D, dtype=dtype, sigma=3.0)
+    out, lse = attend(way, cache, ctx, q, Hk)
+    C.check_close(S.f64(q), *cache.rows(0, ctx), out, lse, D ** -0.5, dtype, way == "few", way)
