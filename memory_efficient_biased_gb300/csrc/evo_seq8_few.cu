@@ -4,7 +4,7 @@
 // Mathematics, per row (token, head) and block of keys with scales s_k and s_v: S = q·code_k,
 // t = s_k s·log2e·S, P' = 2^(t + log2 s_v - M) with M the running maximum of t + log2 s_v, l = Σ P' / s_v and
 // O = Σ P' code_v; at the end O / l and lse = ln2·(M + log2 l).  The codes are exact in fp16; so is q, for bf16 after its
-// row is brought to a largest magnitude of 1 to 2 by a power of two (what falls below 2^-24 of that is lost).
+// row is brought to a largest magnitude of 2^14 to 2^15 by a power of two (what falls below 2^-39 of that is lost).
 //
 // Range.  The weight that a value enters with is P' = P s_v, held times 2^14: fp16 has 11 bits of it down to 2^-28 of the
 // largest, and loses it below 2^-39.  Among keys of like scales that loses weights below 2^-35 of the largest, less than l's own
@@ -53,6 +53,8 @@ constexpr int kRows = kFewRows, kWarps = 12, kThreads = 32 * (kWarps + 4), kDesc
 constexpr int kKeys = 16, kGroups = kTile / kKeys;  // keys that a warp takes at a time, times that a tile is
 constexpr int kStages = 6;                          // tiles
 constexpr int kJoined = 4;                          // rows whose shares are joined at a time, a warp each
+// bf16 queries in fp16: log2 of what a row's largest magnitude becomes (or up to twice that).  What is below 2^-39 of it is lost
+constexpr uint32_t kLift = 14;
 constexpr float kHeld = 14.0f;  // log2 of what a row's largest P' is held as
 constexpr float kNear = 4.0f;   // log2 of how far scales of values lie apart and need no more than that
 
@@ -258,9 +260,9 @@ __device__ __forceinline__ void fetch_q(const Seq8FwdArgs& a, uint8_t* base, Bar
       if constexpr (BF16) {
         uint32_t most = __vmaxu2(x[r].x & 0x7fff7fffu, x[r].y & 0x7fff7fffu);  // magnitudes, as two 16-bit numbers
         most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
-        const uint32_t e = min(max(most >> 7, 1u), 253u);
-        const float down = __uint_as_float((254u - e) << 23);
-        unit *= __uint_as_float(e << 23);
+        const uint32_t e = min(max(most >> 7, kLift + 1u), 254u);  // (an infinity stays one)
+        const float down = __uint_as_float((254u + kLift - e) << 23);
+        unit *= __uint_as_float((e - kLift) << 23);
         const float2 f0 = unpack2<true>(x[r].x), f1 = unpack2<true>(x[r].y);
         x[r] = make_uint2(pack2<false>(f0.x * down, f0.y * down), pack2<false>(f1.x * down, f1.y * down));
       }

@@ -113,9 +113,12 @@ def close_bounds(q, k, v, z, p, scale, dtype, few):
             2^4 or more below the largest so far: 2^-25 of the 16's largest weight at the most.  Where their scale is not that
             much smaller the steps are those of the row's largest: 2^-39 2^4 of the largest weight
       many  fp16 alone: 2^-25 of the largest weight (the reference is at most the row's maximum)
-    times |v| of each key."""
+    times |v| of each key.  bf16 queries lose what is below 2^-39 of their row's largest."""
     es, u = S.score_error(q, k, scale), S.U[dtype]
     G = q.shape[1] // k.shape[1]
+    if dtype == torch.bfloat16:
+        most = max(float(np.max(np.abs(k[:, h]).sum(-1))) for h in range(k.shape[1]))
+        es += scale * 2.0 ** -39 * float(np.max(np.abs(q))) * most
     zz = np.where(np.isfinite(z), np.abs(z), 0.0)
     rp = 2 * es + 2.0 ** -18 * (1 + zz)
     out = np.zeros(q.shape)

@@ -100,3 +100,22 @@ def test_scales_of_any_size(way, D, page, block, dtype, lo, hi):
     q = S.normal(rng, tokens_of(way, Hq // Hk), Hq, D, dtype=dtype, sigma=3.0)
     out, lse = attend(way, cache, ctx, q, Hk)
     C.check_close(S.f64(q), *cache.rows(0, ctx), out, lse, D ** -0.5, dtype, way == "few", way)
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_queries_with_one_large_feature(way):
+    """bf16 queries with a feature 2^20 times the others, where the keys have nothing: the others make the scores."""
+    rng = np.random.default_rng(6)
+    Hq, Hk, D, ctx = 8, 2, 128, 700
+    n = -(-ctx // 32)
+
+    def k(b, length):
+        x = O.round_e4m3(rng.standard_normal((length, Hk, D)))
+        x[:, :, 17] = 0.0
+        return x, np.ones((n, Hk))
+
+    cache = C.coded(rng, [ctx], 32, 32, Hk, D, k, lambda b, length: (O.round_e4m3(rng.standard_normal((length, Hk, D))), np.ones((n, Hk))))
+    q = S.normal(rng, tokens_of(way, Hq // Hk), Hq, D, dtype=BF)
+    q[:, :, 17] = 2.0 ** 20
+    out, lse = attend(way, cache, ctx, q, Hk)
+    C.check_close(S.f64(q), *cache.rows(0, ctx), out, lse, D ** -0.5, BF, way == "few", way)
