@@ -53,6 +53,16 @@ __device__ __forceinline__ uint2 f16x4_of_codes(uint32_t codes) {
       : "r"(codes));
   return r;
 }
+// A pair of codes in f16 as a pair of bf16, exactly (a bf16 is the upper half of an f32); NaN stays NaN.
+__device__ __forceinline__ uint32_t bf16x2_of_codes(uint32_t f16) {
+  const float2 f = unpack2<false>(f16);
+  return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 // x (lower byte) and y rounded to e4m3, nearest even; NaN stays NaN, what is beyond 448 becomes 448.
 __device__ __forceinline__ uint32_t e4m3x2_of_f32(float x, float y) {
   uint32_t r;

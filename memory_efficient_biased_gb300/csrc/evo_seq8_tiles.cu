@@ -1,20 +1,25 @@
 // evo_seq8_tiles.cu — attention over the 8-bit cache (include/evo_seq.h) for many rows a key, on tcgen05.
 //
-// Mathematics, rows, items and roles as in evo_seq_fwd.cu, with the scales of evo_seq8_few.cu: S = q·code_k,
-// t = s_k s·log2e·S, P' = 2^(t + log2 s_v - M), M following the maximum of t + log2 s_v, l = Σ P' / s_v and
-// O = Σ P' code_v; at the end O / l and lse = ln2·(M + log2 l).  Codes are exact in fp16, and so is q, for bf16
-// after its row is brought to a largest magnitude of 1 to 2 by a power of two; P' is rounded to fp16.
+// Mathematics, rows, items and roles as in evo_seq_fwd.cu, with scales: S = q·code_k, t = s_k s·log2e·S,
+// P' = 2^(t + log2 r_v - M), M following the maximum of t + log2 r_v, l = Σ P' / r_v and O = Σ P' v'; at the end O / l and
+// lse = ln2·(M + log2 l).  Operands are in q's type, which holds every code exactly, and P' is rounded to it, as in the
+// 16-bit forward.  What a value enters with is P' v':
+//   bf16  v' = code and r_v = s_v: bf16 holds P s_v whatever the scales
+//   fp16  v' = code times the power of two in s_v, as far as fp16 holds that exactly (2^-14 to 2^7), and r_v the rest of s_v (1 to 2 in
+//         that range).  With all of s_v in P', fp16 would lose keys whose scale is small beside another's, though their
+//         weight be as large
 //
 // The tensor core takes 16 bits from shared memory, so a tile of codes arrives in a staging buffer and four warps widen
 // it into the ring that the products read: 128 KB a pair of key tiles in and out of shared memory, beside the products' own 192.
 //
 // What bounds it: the chain scores, maximum, exponentials, P·V of a pair of tiles, as in the 16-bit forward, and the widening
-// beside it, on the same schedulers and the same shared memory.  4096 tokens over 16,384 keys, 32 heads of 128: 897 us, where a
-// copy widened beforehand and the 16-bit forward take 759; 2 x 64 tokens over 16,384 each 60 us, where those take 87; 16 x 16 tokens
-// over 8192 each 131 (a key tile and SM 2.0 us: the ring holds a tile and a half, and the next keys are widened when a
-// tile's P·V is done).  The widening is the better for having few loads under way: with two pieces of a row, and
-// what only the last tiles need in a loop of its own, 131; one 134, four 138, eight 136; four with the checks
-// in the same loop 151, all eight of them before the wait for the place they go to 203.
+// beside it, on the same schedulers and the same shared memory (bf16 / fp16).  4096 tokens over 16,384 keys, 32 heads of 128: 948 / 976 us,
+// where a copy widened beforehand and the 16-bit forward take 759; 2 x 64 tokens over 16,384 each 58 / 59 us, where those take 87;
+// 16 x 16 tokens over 8192 each 146 / 145 (a key tile and SM 2.2 us: the ring holds a tile and a half, and the next keys are
+// widened when a tile's P·V is done).  The widening is the better for few instructions and few loads under way: codes of bf16 take three
+// instructions a pair more than f16's (146 us where those took 132), fp16's product and the wait for its factor 7 us
+// each; one piece of a row at a time in bf16 146, two 144, four 155, but 4096 tokens 948, 976, 993; in fp16 154, 145, 163; loops of
+// their own for keys and values, 152 and 155; what only the last tiles need in a loop of its own.
 // No use: four slots and two staging buffers instead of three and three, codes loaded into registers instead of a staging
 // buffer (twice as long: the loads' latency, and no registers to hide it in).
 //
@@ -24,7 +29,7 @@
 //   warps 9, 10     the MMAs of tile 0 and 1
 //   warp 11         the walk over the work, and the tiles' scales
 //   warps 12-15     widening: a thread a row of K and V (rows of V that no query of the item sees become zeros, and
-//                   codes that are NaN and seen by some rows only are taken out, to be put back at the end), and of Q
+//                   codes that are NaN and seen by some rows only are taken out, to be put back at the end)
 // Tensor memory (512 columns): S_0, S_1 (128 each, P' in place of S as packed pairs), O_0, O_1.
 #include "evo_seq8_pages.cuh"
 #include "evo_seq_fwd.cuh"
@@ -40,15 +45,15 @@ constexpr int kDescs = 4, kScaleSlots = 8, kMaxSlots = 6;
 
 struct Bars {
   uint64_t desc_full[kDescs], desc_empty[kDescs];
-  uint64_t q_full[2], q_empty[2], q_ready[2];
+  uint64_t q_full[2], q_empty[2];
   uint64_t raw_full[kMaxSlots], raw_empty[kMaxSlots], full[kMaxSlots], empty[kMaxSlots];
   uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
   // turn: see the softmax; merge_full: the second warpgroup's share of a single tile is done
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2], drain[2], turn[2], merge_full;
-  alignas(16) float scales[kScaleSlots][3][8];  // of a key tile, 16 tokens each: s_k, log2 s_v, 1 / s_v
+  // of a key tile, 16 tokens each: s_k; log2 r_v and 1 / r_v; fp16: s_v / r_v, which V's codes are multiplied by
+  alignas(16) float scales[kScaleSlots][4][8];
   Work work[kDescs];
   float2 merge[kTile];       // (M, l) of the second warpgroup's share of a single tile
-  float unit[kDescs][256];   // bf16: what the rows of an item's q were divided by
   int dirty[kDescs];         // a V tile of the item held codes that were taken out
   uint32_t tiles, queries[2];  // tiles of codes and Q tiles that the producer asked for
   uint32_t tmem_slot;
@@ -131,9 +136,8 @@ __device__ __forceinline__ void mma(const Seq8FwdArgs& a, uint8_t* base, Bars* b
                                     const WaitGuard& g) {
   using L = Layout<DP>;
   const int steps = a.f.s.D / 16;  // of 16 features
-  const uint32_t id_s = idesc_f16(128, 128, false, false, false);
-  const uint32_t id_o = idesc_f16(128, steps * 16, false, false, true);
-  uint64_t* q_here = BF16 ? bars->q_ready : bars->q_full;
+  const uint32_t id_s = idesc_f16(128, 128, BF16, false, false);
+  const uint32_t id_o = idesc_f16(128, steps * 16, BF16, false, true);
   uint32_t n = 0, u = 0, it = 0, own = 0, queries[2] = {0, 0};
   bool ok = true;
   Work w;
@@ -149,7 +153,7 @@ __device__ __forceinline__ void mma(const Seq8FwdArgs& a, uint8_t* base, Bars* b
     // (the other tile's buffer too: it is released by both)
     for (uint32_t b = 0; b < 2; ++b)
       if (!one || b == qb) {
-        if (!mbar_wait_warp_inl(smem_u32(q_here + b), queries[b] & 1, g)) ok = false;
+        if (!mbar_wait_warp_inl(smem_u32(&bars->q_full[b]), queries[b] & 1, g)) ok = false;
         ++queries[b];
       }
     if (!ok) break;
@@ -217,6 +221,14 @@ __device__ __forceinline__ void mma(const Seq8FwdArgs& a, uint8_t* base, Bars* b
 }
 
 // ------------------------------------------------------------ the walk, and the scales (one warp)
+// fp16: what V's codes are multiplied by, the power of two in a block's scale, as far as the products are exact: codes of 448 just
+// fit 2^7, and steps of 2^-9 are kept at 2^-14.
+__device__ __forceinline__ float value_part(float s) {
+  const float power = __uint_as_float(__float_as_uint(s) & 0x7f800000u);
+  return fminf(fmaxf(power, 0x1p-14f), 0x1p7f);
+}
+
+template <bool BF16>
 __device__ __forceinline__ void walk(const Seq8FwdArgs& a, Bars* bars, const WaitGuard& g, int lane) {
   const SeqDesc& s = a.f.s;
   const Cache8& c = a.c;
@@ -264,9 +276,10 @@ __device__ __forceinline__ void walk(const Seq8FwdArgs& a, Bars* bars, const Wai
       if (lane < 8) {
         bars->scales[slot][0][lane] = now;
       } else if (lane < 16) {
-        const float lv = log2_value_scale(now);
+        const float part = BF16 ? 1.0f : value_part(now), lv = log2_value_scale(now) - lg2(part);
         bars->scales[slot][1][lane - 8] = lv;
         bars->scales[slot][2][lane - 8] = ex2(-lv);
+        bars->scales[slot][3][lane - 8] = part;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->scale_full[slot]));
@@ -282,66 +295,43 @@ template <int DP, bool BF16>
 __device__ __forceinline__ void widen(const Seq8FwdArgs& a, uint8_t* base, Bars* bars, const WaitGuard& g, int r) {
   using L = Layout<DP>;
   const int lane = r & 31;
-  uint32_t use = 0, queries[2] = {0, 0};
+  uint32_t use = 0, n = 0;
   Work w;
   for (uint32_t it = 0; take(bars, it, g, w); ++it) {
-    const bool one = single(w, a.f.TQ);
-    if constexpr (BF16) {
-      // this thread's row of q: divided by a power of two that brings its largest magnitude to 1 to 2
-      for (int t = 0; t < (one ? 1 : 2); ++t) {
-        const int b = one ? w.q : t;
-        if (!mbar_wait_warp_inl(smem_u32(&bars->q_full[b]), queries[b] & 1, g)) return;
-        ++queries[b];
-        if (r < a.f.TQ * a.f.s.group) {
-          uint8_t* row = base + L::q + b * L::kTB + r * 128;
-          uint32_t most = 0;  // magnitudes, as two 16-bit numbers (the order of a row's pieces does not matter)
-#pragma unroll 4
-          for (int i = 0; i < DP / 8; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4*>(row + (i >> 3) * L::kHalf + ((i ^ r) & 7) * 16);
-            most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-          }
-          most = max(most & 0xffffu, most >> 16);
-          const uint32_t e = most == 0 ? 127u : min(max(most >> 7, 1u), 253u);
-          const float down = __uint_as_float((254u - e) << 23);
-          bars->unit[it % kDescs][t * 128 + r] = __uint_as_float(e << 23);
-          auto narrow = [&](uint32_t v) {
-            const float2 f = unpack2<true>(v);
-            return pack2<false>(f.x * down, f.y * down);
-          };
-#pragma unroll 2
-          for (int i = 0; i < DP / 8; ++i) {
-            uint4* at = reinterpret_cast<uint4*>(row + (i >> 3) * L::kHalf + ((i ^ r) & 7) * 16);
-            const uint4 x = *at;
-            *at = make_uint4(narrow(x.x), narrow(x.y), narrow(x.z), narrow(x.w));
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->q_ready[b]));
-      }
-    }
-    for (int j = w.j0; j < w.j1; ++j) {
+    for (int j = w.j0; j < w.j1; ++j, ++n) {
       const int last = w.kv_end - j * kTile;  // rows of the tile that some query sees
       const int all = w.pos + 1 - j * kTile;  // ... that every query sees
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++use) {
         const uint32_t slot = use % L::kSlots;
+        uint32_t times = 0x3c003c00u;  // fp16: what the codes are multiplied by, for keys 1
+        if (!BF16 && kv) {
+          const uint32_t sc = n % kScaleSlots;
+          if (!mbar_wait_warp_inl(smem_u32(&bars->scale_full[sc]), (n / kScaleSlots) & 1, g)) return;
+          const float part = bars->scales[sc][3][r >> 4];
+          times = pack2<false>(part, part);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->scale_empty[sc]));
+        }
         if (!mbar_wait_warp_inl(smem_u32(&bars->raw_full[slot]), (use / L::kSlots) & 1, g)) return;
         if (!mbar_wait_warp_inl(smem_u32(&bars->empty[slot]), ((use / L::kSlots) & 1) ^ 1, g)) return;
         const uint8_t* from = base + L::raw + slot * L::kRaw + r * DP;
         uint8_t* to = base + L::ring + slot * L::kTB + r * 128;
         const bool none = kv && r >= last, some = kv && r >= all;
         bool lost = false;
+        auto four = [&](uint32_t codes) {
+          const uint2 f = f16x4_of_codes(codes);
+          return BF16 ? make_uint2(bf16x2_of_codes(f.x), bf16x2_of_codes(f.y)) : make_uint2(mul_f16x2(f.x, times), mul_f16x2(f.y, times));
+        };
         auto put = [&](int i, const uint4& x) {
-          const uint2 f0 = f16x4_of_codes(x.x), f1 = f16x4_of_codes(x.y), f2 = f16x4_of_codes(x.z), f3 = f16x4_of_codes(x.w);
+          const uint2 f0 = four(x.x), f1 = four(x.y), f2 = four(x.z), f3 = four(x.w);
           uint8_t* half = to + (i >> 2) * L::kHalf;
           *reinterpret_cast<uint4*>(half + (((2 * i) ^ r) & 7) * 16) = make_uint4(f0.x, f0.y, f1.x, f1.y);
           *reinterpret_cast<uint4*>(half + (((2 * i + 1) ^ r) & 7) * 16) = make_uint4(f2.x, f2.y, f3.x, f3.y);
         };
         auto piece = [&](int i) { return *reinterpret_cast<const uint4*>(from + (DP == 128 ? (i ^ r) & 7 : (i ^ (r >> 1)) & 3) * 16); };
         if (!some) {
-#pragma unroll 2
+#pragma unroll(BF16 ? 1 : 2)
           for (int i = 0; i < DP / 16; ++i) put(i, piece(i));
         } else {
 #pragma unroll 1
@@ -388,6 +378,7 @@ __device__ __forceinline__ void chunk_max(uint32_t (&y)[32], int lim, const floa
 }
 
 // P' = 2^(t + log2 s_v - M) of 32 scores, packed, and the sum of P' / s_v.
+template <bool BF16>
 __device__ __forceinline__ void chunk_exp(const uint32_t (&y)[32], const float* f, const float* lv, const float* iv, float m,
                                           uint32_t (&pp)[16], float& l) {
 #pragma unroll
@@ -400,7 +391,7 @@ __device__ __forceinline__ void chunk_exp(const uint32_t (&y)[32], const float* 
       const float2 t = fma2(make_float2(__uint_as_float(y[x]), __uint_as_float(y[x + 1])), f2, b2);
       const float p0 = ex2(t.x), p1 = ex2(t.y);
       rs = add2(rs, make_float2(p0, p1));
-      pp[x >> 1] = pack2<false>(p0, p1);
+      pp[x >> 1] = pack2<BF16>(p0, p1);
     }
     l = fmaf(rs.x + rs.y, iv[h], l);
   }
@@ -435,6 +426,7 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
   const uint32_t trow = tmem + (static_cast<uint32_t>(wq * 32) << 16);
   const uint32_t scol = trow + col_s(gq), ocol = trow + col_o(gq);
   const int dt = r / s.group, head = r % s.group;  // token within the tile, head within the group
+  const float scale_log2 = a.f.scale_log2;
   uint32_t u = 0, it = 0, merges = 0, turns = 0, n = 0;
   bool ok = true;
   Work w;
@@ -447,8 +439,8 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
     const bool live = dt < a.f.TQ && tok < w.nt;
     const bool any = __any_sync(0xffffffffu, live);
     const int pos = w.pos + tok;
-    float m = 0.0f, l = 0.0f, unit = a.f.scale_log2;
-    bool have = false, begun = false;
+    float m = 0.0f, l = 0.0f;
+    bool have = false;
     int next = sh.from;
     for (int j = w.j0; j < w.j1; ++j, ++n) {
       const uint32_t slot = n % kScaleSlots;
@@ -482,12 +474,6 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
       const float* iv = bars->scales[slot][2];
       if (!mbar_wait_warp_inl(smem_u32(&bars->s_full[gq]), u & 1, g)) { ok = false; break; }
       tc_fence_after();
-      if constexpr (BF16) {
-        if (!begun) {  // (written before the first scores were formed)
-          unit = a.f.scale_log2 * bars->unit[it % kDescs][(one ? 0 : gq * 128) + r];
-          begun = true;
-        }
-      }
       uint32_t ya[64], yb[64];
       uint32_t(&y0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[0]);
       uint32_t(&y1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&ya[32]);
@@ -496,7 +482,7 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
       float mt = -INFINITY;
       tmem_ld64(scol, ya);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = fmaxf(f[e] * unit, 1.2e-38f);  // (one that underflows would make -inf a NaN)
+      for (int e = 0; e < 8; ++e) f[e] = fmaxf(f[e] * scale_log2, 1.2e-38f);  // (one that underflows would make -inf a NaN)
       tmem_wait_ld(ya);
       tmem_ld64(scol + 64, yb);
       if (w.pos + first >= j * kTile + kTile - 1) {
@@ -532,19 +518,19 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
       uint32_t pp[32];
       uint32_t(&p0)[16] = *reinterpret_cast<uint32_t(*)[16]>(&pp[0]);
       uint32_t(&p1)[16] = *reinterpret_cast<uint32_t(*)[16]>(&pp[16]);
-      chunk_exp(y0, f, lv, iv, m, p0, l);
-      chunk_exp(y1, f + 2, lv + 2, iv + 2, m, p1, l);
+      chunk_exp<BF16>(y0, f, lv, iv, m, p0, l);
+      chunk_exp<BF16>(y1, f + 2, lv + 2, iv + 2, m, p1, l);
       tmem_st32(scol, pp);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->p_half[gq]));
-      chunk_exp(y2, f + 4, lv + 4, iv + 4, m, p0, l);
+      chunk_exp<BF16>(y2, f + 4, lv + 4, iv + 4, m, p0, l);
       if (j < both) {  // handed over a little early
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->turn[gq ^ 1]));
       }
-      chunk_exp(y3, f + 6, lv + 6, iv + 6, m, p1, l);
+      chunk_exp<BF16>(y3, f + 6, lv + 6, iv + 6, m, p1, l);
       if (j < both) ++turns;
       tmem_st32(scol + 32, pp);
       tmem_wait_st();
@@ -676,13 +662,12 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_tiles_kernel(const __g
     }
     for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(smem_u32(&bars->scale_full[i]), 1);
-      mbar_init(smem_u32(&bars->scale_empty[i]), 8);
+      mbar_init(smem_u32(&bars->scale_empty[i]), BF16 ? 8 : 12);  // eight softmax warps; fp16: those that widen
     }
     mbar_init(smem_u32(&bars->merge_full), 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->q_full[i]), 1);
       mbar_init(smem_u32(&bars->q_empty[i]), 2);  // both MMA warps
-      mbar_init(smem_u32(&bars->q_ready[i]), 4);
       mbar_init(smem_u32(&bars->s_full[i]), 1);
       mbar_init(smem_u32(&bars->p_half[i]), 4);
       mbar_init(smem_u32(&bars->p_full[i]), 4);
@@ -713,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_tiles_kernel(const __g
     } else if (warp == kProducerWarp) {
       producer<DP>(a, base, bars, g, lane);
     } else if (warp == kWalkWarp) {
-      walk(a, bars, g, lane);
+      walk<BF16>(a, bars, g, lane);
     } else {
       mma<DP, BF16>(a, base, bars, tmem, static_cast<uint32_t>(uniform(warp) - kMmaWarp), g);
     }

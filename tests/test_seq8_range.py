@@ -1,5 +1,6 @@
-"""GPU: attention over the 8-bit cache where weights and scales lie far apart, against the fp64 oracle
-within bounds that follow from the weights themselves (tests/seq8_util.py, close_bounds): few rows a key, and many over a copy."""
+"""GPU: attention over the 8-bit cache where weights and scales lie far apart, against the fp64 oracle within bounds that follow
+from the weights themselves (tests/seq8_util.py, close_bounds).  Every way of the attention: few rows a key; many in place
+(one tile of queries, two), as a table too wide for a copy makes them; many over a copy."""
 import numpy as np
 import pytest
 import torch
@@ -13,16 +14,20 @@ from tests import seq_util as S
 pytestmark = pytest.mark.gpu
 
 BF, FP = torch.bfloat16, torch.float16
-WAYS = ["few", "copied"]
+WAYS = ["few", "one tile", "two tiles", "copied"]
 
 
 def attend(way, cache, ctx, q, Hk, scale=None):
     """(out, lse) of the new tokens q [n, Hq, D] of one sequence, and that the call goes that way."""
     n, Hq, D = q.shape
-    rows = n * Hq // Hk
-    assert rows <= 32 if way == "few" else rows > 512
+    rows, cols = n * Hq // Hk, cache.table.shape[1]
+    assert rows <= 32 if way == "few" else rows > 512 if way == "copied" else 32 < rows <= 512
+    table = cache.table
+    if way in ("one tile", "two tiles"):  # 2^28 values, and more, of each of keys and values
+        table = torch.full((1, (1 << 28) // (Hk * D * cache.page) + 1), -1, dtype=torch.int32, device="cuda")
+        table[:, :cols] = cache.table
     cu, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [ctx]))
-    args = q.cuda(), *cache.args(), cu, lens, cache.table
+    args = q.cuda(), *cache.args(), cu, lens, table
     out, lse = Q.evo_paged8_fwd(*args, scale=scale)
     again = Q.evo_paged8_fwd(*args, scale=scale)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
@@ -31,7 +36,7 @@ def attend(way, cache, ctx, q, Hk, scale=None):
 
 
 def tokens_of(way, G):
-    return 32 // G if way == "few" else 512 // G + 1
+    return {"few": 32 // G, "one tile": 32 // G + 1, "two tiles": 512 // G, "copied": 512 // G + 1}[way]
 
 
 @pytest.mark.parametrize("apart", [12, 20, 40, 88])
@@ -57,7 +62,7 @@ def test_blocks_of_equal_weight_and_scales_far_apart(way, order, apart):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
-@pytest.mark.parametrize("way", ["few", "copied"])
+@pytest.mark.parametrize("way", ["few", "one tile", "copied"])
 def test_one_key_of_large_weight_and_scale(way, dtype):
     """One key with 2^13 times the weight and 2^12 times the scale of each of the others, and codes of 0 in half of the features."""
     rng = np.random.default_rng(3)
