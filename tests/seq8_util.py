@@ -142,3 +142,12 @@ def check_close(q, k, v, out, lse, scale, dtype, few, what=""):
     bound, lse_bound = close_bounds(q, k, v, z, p, scale, dtype, few)
     S.assert_close(lse, z, lse_bound, f"{what} lse")
     S.assert_close(out, o, bound, f"{what} out")
+
+
+def flat_rows(rng, n, D):
+    """Keys [n, D] of e4m3 whose scores lie close together, and values that are positive in the features of their own
+    tile of 128 keys and 0 in the others, so that each tile alone makes a good part of some features (D of 2 a tile):
+    no tile can be left out, or counted twice, without that."""
+    tile = np.arange(n) // 128
+    v = np.where((np.arange(D)[None] % (D // 2)) == (tile % (D // 2))[:, None], rng.uniform(1.0, 2.0, (n, D)), 0.0)
+    return O.round_e4m3(rng.standard_normal((n, D))), O.round_e4m3(v)

@@ -1,5 +1,6 @@
-"""GPU: attention over the 8-bit cache where weights and scales lie far apart, against the fp64 oracle within bounds that follow
-from the weights themselves (tests/seq8_util.py, close_bounds).  Every way of the attention: few rows a key; many in place
+"""GPU: attention over the 8-bit cache where weights and scales lie far apart, and over long contexts with flat scores, against the
+fp64 oracle within bounds that follow from the weights themselves (tests/seq8_util.py, close_bounds; what they notice:
+tests/test_seq8_checks.py).  Every way of the attention: few rows a key; many in place
 (one tile of queries, two), as a table too wide for a copy makes them; many over a copy."""
 import numpy as np
 import pytest
@@ -124,3 +125,37 @@ def test_queries_with_one_large_feature(way):
     q[:, :, 17] = 2.0 ** 20
     out, lse = attend(way, cache, ctx, q, Hk)
     C.check_close(S.f64(q), *cache.rows(0, ctx), out, lse, D ** -0.5, BF, way == "few", way)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("way,ctx", [("few", 131071), ("few", 70003), ("one tile", 131071), ("two tiles", 30011), ("copied", 30011)])
+def test_long_flat_contexts(way, ctx, dtype):
+    """Contexts over every SM, every tile with a part in the result that cannot be missed."""
+    rng = np.random.default_rng(ctx)
+    Hq, Hk, D = 8, 1, 64
+    k, v = C.flat_rows(rng, ctx, D)
+    ones = np.ones((-(-ctx // 64), Hk))
+    cache = C.coded(rng, [ctx], 64, 64, Hk, D, lambda b, n: (k[:, None], ones * 2.0 ** -5), lambda b, n: (v[:, None], ones))
+    q = S.normal(rng, tokens_of(way, Hq), Hq, D, dtype=dtype)
+    out, lse = attend(way, cache, ctx, q, Hk)
+    C.check_close(S.f64(q), *cache.rows(0, ctx), out, lse, D ** -0.5, dtype, way == "few", way)
+
+
+def test_long_flat_contexts_together():
+    """Several of them of uneven lengths in a call, items and pieces on every SM."""
+    rng = np.random.default_rng(12)
+    Hq, Hk, D, ctx = 4, 2, 64, [9001, 40007, 128, 17, 22222]
+    flat = [[C.flat_rows(rng, n, D) for _ in range(Hk)] for n in ctx]
+    ones = lambda n, s: np.full((-(-n // 16), Hk), s)  # noqa: E731
+    cache = C.coded(rng, ctx, 16, 16, Hk, D, lambda b, n: (np.stack([x[0] for x in flat[b]], 1), ones(n, 2.0 ** -5)),
+                    lambda b, n: (np.stack([x[1] for x in flat[b]], 1), ones(n, 1.0)))
+    for chunks in ([1] * 5, [9, 30, 5, 17, 60]):
+        q = S.normal(rng, sum(chunks), Hq, D, dtype=BF)
+        lens = torch.tensor(ctx, dtype=torch.int32, device="cuda")
+        out, lse = Q.evo_paged8_fwd(q.cuda(), *cache.args(), S.offsets(chunks).cuda(), lens, cache.table)
+        a = 0
+        for b, n in enumerate(chunks):
+            C.check_close(S.f64(q[a:a + n]), *cache.rows(b, ctx[b]), S.f64(out[a:a + n]), S.f64(lse[:, a:a + n]), D ** -0.5, BF,
+                          chunks[0] == 1, f"sequence {b}")
+            a += n
+    assert E.evo_attn_device_status() == 0
