@@ -566,8 +566,13 @@ __global__ void __launch_bounds__(kThreads, 1) evo_paged8_few_kernel(const __gri
   }
   __syncthreads();
   if (warp == kWarps) {
-    // (where a warp gave up, another may have asked for a tile more)
-    const Owed owed[] = {{bars->full, kStages, max(bars->tiles[0], max(bars->tiles[1], bars->tiles[2]))}};
+    // Where a warp gave up, another may have asked for tiles more (fewer than there are stages): the arrivals that
+    // are missing at their barriers, without which no wait for those copies would end before its limit.
+    const uint32_t uses = max(bars->tiles[0], max(bars->tiles[1], bars->tiles[2]));
+    for (int i = 0; i < 3; ++i)
+      for (uint32_t use = bars->tiles[i]; use < uses; ++use)
+        if (lane < (i < 2 ? 1 : 16)) mbar_arrive(smem_u32(&bars->full[use % kStages]));
+    const Owed owed[] = {{bars->full, kStages, uses}};
     drain(owed, g);
   }
 }
