@@ -273,8 +273,10 @@ EVO_API evo_status_t evo_cache8_read(const void* k_pages, const void* v_pages, c
 
 /* As evo_paged_fwd without weights; q and out are in dtype.  With many rows a key (tokens * group above 512 * seqs)
  * the workspace has room for a copy in 16 bits of all that the table can hold, as long as that is at most
- * 512 MB; otherwise codes are widened where they are used.  Short contexts (max 1024 places in the table) with
- * few rows need no workspace: 0, and NULL will do.  (A bad shape gives 0 too, and the call says so.) */
+ * 512 MB; otherwise codes are widened where they are used.  With few rows (tokens * group up to 32 * seqs, group up to
+ * 16) short contexts need no workspace: 0, and NULL will do.  Those are tables of at most 128 places, and of at most 1024 where
+ * the call has no more than a kv head's 16 rows for every SM: kv_heads * (tokens / floor(16 / group) + seqs) up to their
+ * number.  (A bad shape gives 0 too, and the call says so.) */
 EVO_API size_t evo_paged8_fwd_workspace_bytes(evo_seq_shape_t shape, evo_cache8_shape_t cache);
 EVO_API evo_status_t evo_paged8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
                                     const float* v_scales, const int32_t* cu_seqlens, const int32_t* seq_lens,
