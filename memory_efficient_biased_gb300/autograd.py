@@ -143,5 +143,8 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, 
     """Rotary positions, differentiable: q [T, Hq, D] and k [T, Hk, D] (or None) turned by positions [T] int32
     times inv_freq [rotary_dim / 2] float64 (``evo_seq.rotary_frequencies``); (q, k), as
     ``prompt_attention`` takes them.  Strided token rows are read in place.  The gradients are not differentiable
-    themselves, and a captured backward needs its forward inside the same capture, as there."""
+    themselves, and a captured backward needs its forward inside the same capture, as there.  Frequencies get no
+    gradient: some that require one are refused."""
+    if isinstance(inv_freq, torch.Tensor) and inv_freq.requires_grad:
+        raise ValueError("inv_freq gets no gradient here: give it detached")
     return RotaryFunction.apply(q, k, positions, inv_freq, interleaved, factor)
