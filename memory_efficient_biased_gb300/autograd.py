@@ -145,6 +145,6 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, 
     ``prompt_attention`` takes them.  Strided token rows are read in place.  The gradients are not differentiable
     themselves, and a captured backward needs its forward inside the same capture, as there.  Frequencies get no
     gradient: some that require one are refused."""
-    if isinstance(inv_freq, torch.Tensor) and inv_freq.requires_grad:
+    if isinstance(inv_freq, torch.Tensor) and inv_freq.requires_grad and torch.is_grad_enabled():
         raise ValueError("inv_freq gets no gradient here: give it detached")
     return RotaryFunction.apply(q, k, positions, inv_freq, interleaved, factor)

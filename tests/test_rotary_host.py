@@ -13,3 +13,5 @@ def test_frequencies_that_require_a_gradient_are_refused():
         rotary(q, None, pos, f)
     with pytest.raises(ValueError, match="CUDA"):  # (as any call without a GPU)
         rotary(q, None, pos, f.detach())
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):  # no gradients are asked for
+        rotary(q, None, pos, f)
