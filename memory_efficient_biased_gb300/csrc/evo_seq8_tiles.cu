@@ -5,7 +5,7 @@
 // lse = ln2·(M + log2 l).  Operands are in q's type, which holds every code exactly, and P' is rounded to it, as in the
 // 16-bit forward.  What a value enters with is P' v':
 //   bf16  v' = code and r_v = s_v: bf16 holds P s_v whatever the scales
-//   fp16  v' = code times the power of two in s_v, as far as fp16 holds that exactly (2^-14 to 2^7), and r_v the rest of s_v (1 to 2 in
+//   fp16  v' = code times the power of two in s_v, as far as fp16 goes (2^-24 to 2^7), and r_v the rest of s_v (1 to 2 in
 //         that range).  With all of s_v in P', fp16 would lose keys whose scale is small beside another's, though their
 //         weight be as large
 //
@@ -221,11 +221,11 @@ __device__ __forceinline__ void mma(const Seq8FwdArgs& a, uint8_t* base, Bars* b
 }
 
 // ------------------------------------------------------------ the walk, and the scales (one warp)
-// fp16: what V's codes are multiplied by, the power of two in a block's scale, as far as the products are exact: codes of 448 just
-// fit 2^7, and steps of 2^-9 are kept at 2^-14.
+// fp16: what V's codes are multiplied by, the power of two in a block's scale as far as fp16 goes: codes of 448 just fit 2^7, and
+// below 2^-15 the products are rounded to steps of 2^-24, as reading rounds them.
 __device__ __forceinline__ float value_part(float s) {
   const float power = __uint_as_float(__float_as_uint(s) & 0x7f800000u);
-  return fminf(fmaxf(power, 0x1p-14f), 0x1p7f);
+  return fminf(fmaxf(power, 0x1p-24f), 0x1p7f);
 }
 
 template <bool BF16>

@@ -113,7 +113,7 @@ def close_bounds(q, k, v, z, p, scale, dtype, few):
             2^4 or more below the largest so far: 2^-25 of the 16's largest weight at the most.  Where their scale is not that
             much smaller the steps are those of the row's largest: 2^-39 2^4 of the largest weight
       many  fp16 alone: 2^-25 of the largest weight (the reference is at most the row's maximum)
-    times |v| of each key.  bf16 queries lose what is below 2^-39 of their row's largest."""
+    times |v| of each key.  With fp16 and many rows values are in steps of 2^-24 too.  bf16 queries lose what is below 2^-39 of their row's largest."""
     es, u = S.score_error(q, k, scale), S.U[dtype]
     G = q.shape[1] // k.shape[1]
     if dtype == torch.bfloat16:
@@ -131,7 +131,7 @@ def close_bounds(q, k, v, z, p, scale, dtype, few):
             most = np.pad(w, ((0, 0), (0, pad))).reshape(len(w), -1, 16).max(2)
             bound = bound + 2.0 ** -25 * (most @ blocks) + 2.0 ** -35 * w.max(1)[:, None] * a.sum(0)
         elif dtype == torch.float16:
-            bound = bound + 2.0 ** -25 * w.max(1)[:, None] * a.sum(0)
+            bound = bound + 2.0 ** -25 * w.max(1)[:, None] * a.sum(0) + 2.0 ** -25
         out[:, h] = bound
     return out, es + 2.0 ** -19 * (1 + zz)
 

@@ -90,7 +90,7 @@ def test_one_key_of_large_weight_and_scale(way, dtype):
     C.check_close(S.f64(q), *cache.rows(0, ctx), out, lse, scale, dtype, way == "few", way)
 
 
-@pytest.mark.parametrize("dtype,lo,hi", [(BF, -44, 45), (FP, -14, 8)])
+@pytest.mark.parametrize("dtype,lo,hi", [(BF, -44, 45), (FP, -14, 8), (FP, -33, 8), (FP, -33, -23)])
 @pytest.mark.parametrize("D,page,block", [(64, 64, 16), (128, 16, 16), (96, 128, 64)])
 @pytest.mark.parametrize("way", WAYS)
 def test_scales_of_any_size(way, D, page, block, dtype, lo, hi):
@@ -159,3 +159,29 @@ def test_long_flat_contexts_together():
                           chunks[0] == 1, f"sequence {b}")
             a += n
     assert E.evo_attn_device_status() == 0
+
+
+def test_fp16_many_keys_of_small_weight_and_scale():
+    """In front of each head's keys one of 2^17.5 times the weight and 2^20 times the scale of each of the others, whose values are all
+    that there is in half of the features.  (More heads than SMs: one reference for most of a head's keys.)"""
+    rng = np.random.default_rng(8)
+    Hk, G, D, ctx = 160, 8, 64, 4096
+    sign, n = np.where(rng.random(D) < 0.5, -1.0, 1.0), ctx // 16
+
+    def k(b, length):
+        x = np.zeros((length, Hk, D))
+        x[3] = 9.0 * sign
+        return x, np.ones((n, Hk))
+
+    def v(b, length):
+        x, s = np.repeat(O.round_e4m3(rng.uniform(200.0, 440.0, (length, 1, D))), Hk, 1), np.full((n, Hk), 2.0 ** -20)
+        s[0] = 1.0
+        x[:16] = 0.0
+        x[3, :, D // 2:] = 3.0
+        return x, s
+
+    cache = C.coded(rng, [ctx], 128, 16, Hk, D, k, v)
+    q = torch.from_numpy(np.ascontiguousarray(np.broadcast_to(sign / (9.0 * D), (tokens_of("one tile", G), G * Hk, D)), np.float32)).to(FP)
+    scale = float(np.float32(17.5 * np.log(2.0)))
+    out, lse = attend("one tile", cache, ctx, q, Hk, scale)
+    C.check_close(S.f64(q), *cache.rows(0, ctx), out, lse, scale, FP, False)
