@@ -15,7 +15,8 @@ namespace {
 // bytes, is what a step of single tokens waits for.)
 //
 // What it cannot do without: two bytes read and one written an element where the scale does not grow. 10,188 tokens of 8 heads of
-// 128, keys and values, take 16 us, where those bytes take 9: the lookups in front of the loads and 1.7 instructions a clock.
+// 128, keys and values, take 16 us, where those bytes take 9: a CTA's search, length, table, rows and stores wait for one another, and
+// the three CTAs of an SM hold too little of it under way (28 % of DRAM's throughput, 1.7 of 4 instructions a clock).
 constexpr int kAppendThreads = 256;
 
 __device__ __forceinline__ long long block_number(const SeqDesc& s, int block, int b) {
@@ -63,7 +64,7 @@ __device__ __forceinline__ float2 finite2(uint32_t w, float otherwise) {
 // A warp's rows lie P lanes each, P the power of two that holds their 16-byte pieces, 32 / P rows at a time; the
 // largest magnitude is looked for in pairs of 16 bits, and only where that is no number among numbers
 // alone.  (10,188 tokens of 8 heads of 128 in blocks of 64: 16 us, 3.9 TB/s; with a division for every piece's row
-// and comparisons in 32 bits 29.  What bounds it now is latency and issue, 1.7 instructions a clock; several units a CTA,
+// and comparisons in 32 bits 29.  What bounds it now is latency, as above; several units a CTA,
 // which saves the lookups, and more CTAs an SM with fewer registers changed nothing.)
 template <bool BF16>
 __global__ void __launch_bounds__(kAppendThreads) evo_append8_kernel(const __grid_constant__ Cache8Args a) {
@@ -169,8 +170,9 @@ __global__ void __launch_bounds__(kAppendThreads) evo_append8_kernel(const __gri
 // ------------------------------------------------------------------ read
 // A warp takes eight tokens next to each other: a lane each finds its sequence, page and place, then the warp
 // goes over the 16-code pieces of one token after the other, keys and values, which are next to each other in both.
-// Bound by the bytes: one read and two written an element.  10,460 tokens of 8 heads of 128: 14 us, 4.7 TB/s (loads one
-// by one between the stores 18; a thread a piece, each with its own search and divisions, 20).
+// One byte read and two written an element: 10,460 tokens of 8 heads of 128 take 14 us, where those bytes take 9.5 (loads one
+// by one between the stores 18; a thread a piece, each with its own search and divisions, 20).  What bounds it is latency, the searches
+// and table entries in front of a warp's loads: 17 % of DRAM's throughput (the writes stay in L2), 1.7 of 4 instructions a clock.
 constexpr int kReadTokens = 8;
 
 // x times scale, at most `most` in magnitude, as a pair of the output's type.

@@ -31,7 +31,7 @@
 // of them, 6.2 to 6.9 TB/s by the machine.  In front of that lie 10 to 12 us until the first tiles are there (offsets, table,
 // then 30 MB asked for at once on pages that no translation is held for), behind it 4 for the last tile and the joining of the
 // warps, 5 of CTAs that were served later than others, and the joining launch, 3: four contexts of 245,609 tokens in all
-// take 94 to 104 us (by the machine), 64 of 287,032 107 to 120, one of 777 12, one of 2000 14.  Steps: 16 keys a warp, eight warps, pages looked up
+// take 94 to 106 us (by the machine), 64 of 287,032 107 to 120, one of 777 12, one of 2000 14.  Steps: 16 keys a warp, eight warps, pages looked up
 // tile by tile 119 us; page table entries a batch ahead and a second loading warp 101; the warps' shares joined
 // for the live rows only 100, and the 64 contexts 136 -> 109; the join that asks for everything at once 94 (one context
 // of 2000 21 -> 14).  No use: 32 keys a warp (fewer stages in flight), eight

@@ -57,16 +57,18 @@ bool map_pages8(CUtensorMap* m, const void* p, const evo_seq_shape_t& s, const e
 
 // Which kernels, and their launch.
 //   few    up to 32 rows a sequence and kv head on the average, and a token's heads in one tile of 16.  The cache is then read
-//          twice, at 6 TB/s, where the other kernel widens it once, at 1.8.  Measured, 24 to 32 rows of few / of the other:
-//          16 contexts of 8192 (8 kv heads of 128) 111 / 150 us, 2 of 16,384 38 / 50, 32 of 2048 85 / 103, one of
-//          100,000 88 / 110, 64 of 700 95 / 102; 48 rows 156 / 152, 47 / 51, 102 / 104, 116 / 113, 129 / 103
+//          twice, at 6 TB/s, where the other kernel widens it once, at 1.8.  Measured, 32 rows of few / of the other:
+//          16 contexts of 8192 (8 kv heads of 128) 112 / 143 us, 2 of 16,384 43 / 47, 32 of 2048 92 / 95, one of
+//          100,000 89 / 112, 64 of 700 107 / 100; 48 rows 158 / 145, 52 / 48, 106 / 96, 119 / 114, 139 / 101.  The average says nothing
+//          of uneven batches: one chunk of 512 tokens over 16,000 beside 128 single tokens over 2000 each goes to few and takes 814
+//          us, 496 the other way, its parts by themselves 142 and 127
 //   copy   many rows, and the codes are widened once, into the workspace, for the 16-bit forward; otherwise every block of 256
 //          rows widens them as it needs them.  The copy costs 6 bytes a code and a launch; widening in place what it takes
-//          beside the products.  So: from more than two blocks a sequence on, while the copy stays below 512 MB.  Measured,
-//          in place / copied, 8 kv heads with group 4 of 128 unless given: two contexts of 16,384 2 blocks each 88 / 110 us,
-//          4 150 / 163, 6 210 / 212, 8 271 / 265; one of 23,348 21 blocks 476 / 424, of 16,384 64 blocks 897 / 759;
-//          head_dim 64, one of 12,291 3.5 blocks 44 / 40, 4 of 5000 4 blocks 55 / 57.  Where most rows are those of few sequences,
-//          the average says too little of them: 5.2 blocks, 1325 tokens over 23,348 in all, 220 / 165; hence two, not six.
+//          beside the products.  So: from more than two blocks a sequence on, while the copy of all that the table can hold stays below
+//          512 MB.  Measured, in place / copied, 8 kv heads with group 4 of 128 unless given: two contexts of 16,384 4 blocks each
+//          155 / 164 us, 6 221 / 215, 8 286 / 266; one of 23,348 21 blocks 509 / 424, of 16,384 64 blocks 948 / 767;
+//          head_dim 64, one of 12,291 3.5 blocks 63 / 63, of 5000 4 blocks 37 / 43.  Where most rows are those of few sequences,
+//          the average says too little of them: 5.2 blocks, 1325 tokens over 23,348 in all, 200 / 168; hence two, not six.
 //   whole  few rows, contexts of at most 1024 keys and no more items than SMs: no item is cut, nothing is joined.  An SM takes
 //          0.7 us a tile, a second launch 3 and the host 4 (777 keys of 8 heads: 12 us of GPU either way, 22 and 26 a call).
 size_t round_up(size_t bytes) { return (bytes + 255) & ~size_t(255); }

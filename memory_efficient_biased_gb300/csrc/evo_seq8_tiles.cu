@@ -14,7 +14,7 @@
 //
 // What bounds it: the chain scores, maximum, exponentials, P·V of a pair of tiles, as in the 16-bit forward, and the widening
 // beside it, on the same schedulers and the same shared memory (bf16 / fp16).  4096 tokens over 16,384 keys, 32 heads of 128: 948 / 976 us,
-// where a copy widened beforehand and the 16-bit forward take 759; 2 x 64 tokens over 16,384 each 58 / 59 us, where those take 87;
+// where a copy widened beforehand and the 16-bit forward take 767; 2 x 64 tokens over 16,384 each 58 / 59 us, where those take 87;
 // 16 x 16 tokens over 8192 each 146 / 145 (a key tile and SM 2.2 us: the ring holds a tile and a half, and the next keys are
 // widened when a tile's P·V is done).  The widening is the better for few instructions and few loads under way: codes of bf16 take three
 // instructions a pair more than f16's (146 us where those took 132), fp16's product and the wait for its factor 7 us
