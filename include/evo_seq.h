@@ -246,8 +246,9 @@ EVO_API evo_status_t evo_rotary(const void* q, const void* k, const int32_t* pos
  * evo_paged8_fwd), as reading gives it: for scales as an append writes them and values within dtype's normal numbers the
  * same.  P is rounded to dtype, with few rows a key to fp16 whatever dtype is; bf16 queries then
  * lose what is below 2^-39 of their row's largest.  The scales of the values that a row sees lie within 2^90 of one
- * another: a key whose scale is farther below another's may lose its weight.  With fp16 and many rows a key values are taken in
- * steps of 2^-24, and some beyond 65504 may cost those beside them their precision. */
+ * another: a key whose scale is farther below another's may lose its weight.  With many rows a key sums of q times codes have to
+ * be float32 numbers (bf16: |q| below 2^111, as head_dim is at most 128); with fp16 values are taken in steps of 2^-24
+ * then, and some beyond 65504 may cost those beside them their precision. */
 typedef struct {
   int64_t num_pages, page_size, pages_per_seq;
   int64_t scale_block;
