@@ -2,7 +2,7 @@
 // or a few of them, with their group's heads in 16 rows.
 //
 // Mathematics, per row (token, head) and block of keys with scales s_k and s_v: S = q·code_k,
-// t = s_k s·log2e·S, P' = 2^(t + log2 s_v - M) with M the running maximum of t + log2 s_v, l = Σ P' / s_v and
+// t = s_k s·log2e·S, P' = 2^(t + log2 s_v - M) with M the running maximum of t + log2 s_v rounded up, l = Σ P' / s_v and
 // O = Σ P' code_v; at the end O / l and lse = ln2·(M + log2 l).  The codes are exact in fp16; so is q, for bf16 after its
 // row is brought to a largest magnitude of 2^14 to 2^15 by a power of two (what falls below 2^-39 of that is lost).
 //
@@ -287,15 +287,14 @@ __device__ __forceinline__ void scale_rows(float (&o)[COLS][4], float& l0, float
 
 // By which power of two keys are held apart whose largest t + log2 s_v of this lane is x, in a row whose maximum is m: what brings the
 // four lanes' largest to M, and at most 2^72, or what l allows (O is below 2^23 a key).
-__device__ __forceinline__ float power_of_two(int d) { return __uint_as_float(static_cast<uint32_t>(127 + d) << 23); }
-__device__ __forceinline__ uint32_t apart_by(float m, float x, float l) {
+__device__ __forceinline__ float apart_by(float m, float x, float l) {
 #pragma unroll
   for (int i = 1; i < 4; i *= 2) {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, i));
     l = fmaxf(l, __shfl_xor_sync(0xffffffffu, l, i));
   }
   const float d = fminf(fminf(m - x, 72.0f), 120.0f - lg2(l));
-  return x > -INFINITY && d > 0.0f ? static_cast<uint32_t>(d) : 0u;
+  return x > -INFINITY && d > 0.0f ? floorf(d) : 0.0f;
 }
 
 template <int DP, bool BF16>
@@ -374,7 +373,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
         a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
         a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
         a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
-        const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
+        const float n0 = ceilf(fmaxf(m0, a0)), n1 = ceilf(fmaxf(m1, a1));  // (whole: log2 s_v - M then loses nothing of t)
         const float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - n1);
         m0 = n0, m1 = n1;
         scale_rows(o, l0, l1, f0, f1);
@@ -385,9 +384,9 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
       top = fmaxf(top, lv);
       uint32_t apart = 0;  // d of both rows
       if (lv < top - kNear && __any_sync(0xffffffffu, (a0 < m0 - kHeld && a0 > -INFINITY) || (a1 < m1 - kHeld && a1 > -INFINITY))) {
-        const uint32_t d0 = apart_by(m0, a0, l0), d1 = apart_by(m1, a1, l1);
-        apart = d0 | d1 << 8;
-        b0 += static_cast<float>(d0), b1 += static_cast<float>(d1);
+        const float d0 = apart_by(m0, a0, l0), d1 = apart_by(m1, a1, l1);
+        apart = static_cast<uint32_t>(d0) | static_cast<uint32_t>(d1) << 8;
+        b0 += d0, b1 += d1;
         scale_rows(o, l0, l1, power_of_two(d0), power_of_two(d1));
       }
 #pragma unroll
@@ -438,7 +437,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
         mma16816(o[4 * e + 2], p, f1.x, g1.x);
         mma16816(o[4 * e + 3], p, f1.y, g1.y);
       }
-      if (apart) scale_rows(o, l0, l1, power_of_two(-static_cast<int>(apart & 0xffu)), power_of_two(-static_cast<int>(apart >> 8)));
+      if (apart) scale_rows(o, l0, l1, power_of_two(-static_cast<float>(apart & 0xffu)), power_of_two(-static_cast<float>(apart >> 8)));
     }
     use += static_cast<uint32_t>(w.j1 - w.j0);
     __syncwarp();
@@ -505,7 +504,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
             *reinterpret_cast<uint2*>(a.f.out + row * a.f.out_stride + static_cast<size_t>(h) * s.D + d) =
                 l == 0.0f ? make_uint2(0u, 0u)
                           : make_uint2(pack2<BF16>(x[0] * inv, x[1] * inv), pack2<BF16>(x[2] * inv, x[3] * inv));
-          if (lane == 0) a.f.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
+          if (lane == 0) a.f.lse[static_cast<size_t>(h) * s.tokens + row] = lse_of(big, l);
         } else {
           const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + w.slot) * kRows + r;
           *reinterpret_cast<float4*>(a.f.part_o + at * DP + d) = make_float4(x[0], x[1], x[2], x[3]);
@@ -641,7 +640,7 @@ __global__ void __launch_bounds__(32 * kRows) evo_paged8_join_kernel(const __gri
     else
       *reinterpret_cast<uint32_t*>(out) = v[0];
   }
-  if (lane == 0) a.lse[static_cast<size_t>(h) * a.s.tokens + row] = l == 0.0f ? -INFINITY : (big + lg2(l)) * kSeqLn2;
+  if (lane == 0) a.lse[static_cast<size_t>(h) * a.s.tokens + row] = lse_of(big, l);
 }
 
 template <int DP, bool BF16>

@@ -44,6 +44,21 @@ __device__ __forceinline__ float log2_value_scale(float s) {
   return r;
 }
 
+// ln2 (m + log2 l), for a whole m: l is a sum of weights over the scales of values, so both may be large and cancel.  The whole part of
+// log2 l is added to m exactly (lg2 alone would be 2^-22 of it off).
+__device__ __forceinline__ float whole_log2(float l) {  // 0 for what is no normal number below 2^126
+  const uint32_t u = __float_as_uint(l);
+  return u - 0x00800000u < 0x7e000000u ? static_cast<float>(static_cast<int>(u >> 23) - 127) : 0.0f;
+}
+__device__ __forceinline__ float power_of_two(float d) {  // d whole, -126 to 127
+  return __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(d)) << 23);
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+  if (l == 0.0f) return -INFINITY;
+  const float e = whole_log2(l);
+  return ((m + e) + lg2(l * power_of_two(-e))) * kSeqLn2;
+}
+
 // Four codes as two pairs of f16 (bytes 0 and 1, bytes 2 and 3), exactly; NaN stays NaN.
 __device__ __forceinline__ uint2 f16x4_of_codes(uint32_t codes) {
   uint2 r;

@@ -1,7 +1,7 @@
 // evo_seq8_tiles.cu — attention over the 8-bit cache (include/evo_seq.h) for many rows a key, on tcgen05.
 //
 // Mathematics, rows, items and roles as in evo_seq_fwd.cu, with scales: S = q·code_k, t = s_k s·log2e·S,
-// P' = 2^(t + log2 r_v - M), M following the maximum of t + log2 r_v, l = Σ P' / r_v and O = Σ P' v'; at the end O / l and
+// P' = 2^(t + log2 r_v - M), M following the maximum of t + log2 r_v, rounded up, l = Σ P' / r_v and O = Σ P' v'; at the end O / l and
 // lse = ln2·(M + log2 l).  Operands are in q's type, which holds every code exactly, and P' is rounded to it, as in the
 // 16-bit forward.  What a value enters with is P' v':
 //   bf16  v' = code and r_v = s_v: bf16 holds P s_v whatever the scales
@@ -504,8 +504,9 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
       float alpha = 1.0f;
       if (mt != -INFINITY && (!have || mt > m + kMoveLog2)) {
         moved = have;
-        alpha = have ? ex2(m - mt) : 1.0f;
-        m = mt;
+        const float up = ceilf(mt);  // (whole: log2 r_v - M then loses nothing of t)
+        alpha = have ? ex2(m - up) : 1.0f;
+        m = up;
         have = true;
       }
       // O so far is complete: this tile's S was issued behind the previous P·V
@@ -570,7 +571,7 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
       }
       if (worked && any) {
         const bool dirty = bars->dirty[it % kDescs] != 0;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l, unit = power_of_two(-whole_log2(l));
         uint16_t* out = a.f.out + row * a.f.out_stride + static_cast<size_t>(h) * s.D;
         const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (w.slot > 0)) * 256 + gq * 128 + r;
         float* part = a.f.part_o + prow * DP;
@@ -613,8 +614,10 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
               }
             } else {
 #pragma unroll
-              for (int e = 0; e < 64; e += 8) {
-                const uint32_t(&o)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&x[e]);
+              for (int e = 0; e < 64; e += 8) {  // (a piece's l is kept as 1 to 2, so that its m is one of weights)
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(x[e + i]) * unit);
                 st_global_32(part + c + e, o);
               }
             }
@@ -630,9 +633,10 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
       }
       if (live) {
         if (w.slot < 0)
-          a.f.lse[static_cast<size_t>(h) * s.tokens + row] = l == 0.0f ? -INFINITY : (m + lg2(l)) * kSeqLn2;
+          a.f.lse[static_cast<size_t>(h) * s.tokens + row] = lse_of(m, l);
         else
-          a.f.part_ml[(static_cast<size_t>(blockIdx.x) * 2 + w.slot) * 256 + gq * 128 + r] = make_float2(m, l);
+          a.f.part_ml[(static_cast<size_t>(blockIdx.x) * 2 + w.slot) * 256 + gq * 128 + r] =
+              make_float2(m + whole_log2(l), l * power_of_two(-whole_log2(l)));
       }
     }
     __syncwarp();

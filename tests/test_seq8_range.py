@@ -161,6 +161,25 @@ def test_long_flat_contexts_together():
     assert E.evo_attn_device_status() == 0
 
 
+@pytest.mark.parametrize("power", [-60, -20, 40, 100])
+@pytest.mark.parametrize("way", WAYS)
+def test_scales_far_from_one(way, power):
+    """All scales of values alike and far from 1: the log-sum-exp, and P, know nothing of them.  Contexts of a few keys (a wide range of
+    lse's relative precision), and ones that are cut."""
+    rng = np.random.default_rng(100 + power)
+    Hq, Hk, D = 8, 2, 64
+    for ctx in (1, 7, 900, 5000):
+        n = -(-ctx // 16)
+        cache = C.coded(rng, [ctx], 64, 16, Hk, D, lambda b, length: (O.round_e4m3(rng.standard_normal((length, Hk, D))), np.full((n, Hk), 2.0 ** -6)),
+                        lambda b, length: (O.round_e4m3(rng.standard_normal((length, Hk, D)) * 9), np.full((n, Hk), 2.0 ** power)))
+        tokens = tokens_of(way, Hq // Hk)
+        q = S.normal(rng, tokens, Hq, D, dtype=BF)
+        out, lse = attend(way, cache, ctx, q, Hk)
+        see = min(ctx, tokens)  # (more tokens than keys: the first of them see none)
+        C.check_close(S.f64(q)[tokens - see:], *cache.rows(0, ctx), out[tokens - see:], lse[:, tokens - see:], D ** -0.5, BF, way == "few", way)
+        assert np.all(out[:tokens - see] == 0) and np.all(lse[:, :tokens - see] == -np.inf)
+
+
 def test_fp16_many_keys_of_small_weight_and_scale():
     """In front of each head's keys one of 2^17.5 times the weight and 2^20 times the scale of each of the others, whose values are all
     that there is in half of the features.  (More heads than SMs: one reference for most of a head's keys.)"""
