@@ -6,8 +6,8 @@
 // O = Σ P' code_v; at the end O / l and lse = ln2·(M + log2 l).  The codes are exact in fp16; so is q, for bf16 after its
 // row is brought to a largest magnitude of 2^14 to 2^15 by a power of two (what falls below 2^-39 of that is lost).
 //
-// Range.  The weight that a value enters with is P' = P s_v, held times 2^14: fp16 has 11 bits of it down to 2^-28 of the
-// largest, and loses it below 2^-39.  Among keys of like scales that loses weights below 2^-35 of the largest, less than l's own
+// Range.  The weight that a value enters with is P' = P s_v, the largest held as 2^13 to 2^14: fp16 has 11 bits of it down to
+// 2^-27 of that, and loses it below 2^-38.  Among keys of like scales that loses weights below 2^-34 of the largest, less than l's own
 // rounding.  A key whose scale is far below another's may have a small P' and a large weight, though, and values of its own where
 // the other's codes are 0.  So 16 keys whose scale is below 2^-4 of the largest so far, and some of whose P' are below 2^-14 of the row's
 // largest, are held against their own largest: P' times 2^d, and O and l times 2^d before their product and 2^-d after it, d whole
@@ -55,7 +55,7 @@ constexpr int kStages = 6;                          // tiles
 constexpr int kJoined = 4;                          // rows whose shares are joined at a time, a warp each
 // bf16 queries in fp16: log2 of what a row's largest magnitude becomes (or up to twice that).  What is below 2^-39 of it is lost
 constexpr uint32_t kLift = 14;
-constexpr float kHeld = 14.0f;  // log2 of what a row's largest P' is held as
+constexpr float kHeld = 14.0f;  // log2 of what a row's largest P' is held as, or up to half of it
 constexpr float kNear = 4.0f;   // log2 of how far scales of values lie apart and need no more than that
 
 template <int DP>
