@@ -2,13 +2,14 @@
 // or a few of them, with their group's heads in 16 rows.
 //
 // Mathematics, per row (token, head) and block of keys with scales s_k and s_v: S = q·code_k,
-// t = s_k s·log2e·S, P' = 2^(t + log2 s_v - M) with M the running maximum of t + log2 s_v rounded up, l = Σ P' / s_v and
+// t = s_k s·log2e·S, P' = 2^(t + log2 s_v - M) with M the running maximum of t + log2 s_v, l = Σ P' / s_v and
 // O = Σ P' code_v; at the end O / l and lse = ln2·(M + log2 l).  The codes are exact in fp16; so is q, for bf16 after its
 // row is brought to a largest magnitude of 2^14 to 2^15 by a power of two (what falls below 2^-39 of that is lost).
 //
-// Range.  The weight that a value enters with is P' = P s_v, the largest held as 2^13 to 2^14: fp16 has 11 bits of it down to
-// 2^-27 of that, and loses it below 2^-38.  Among keys of like scales that loses weights below 2^-34 of the largest, less than l's own
-// rounding.  A key whose scale is far below another's may have a small P' and a large weight, though, and values of its own where
+// Range.  The weight that a value enters with is P' = P s_v, held times 2^14: fp16 has 11 bits of it down to 2^-28 of the
+// largest, and loses it below 2^-39.  Among keys of like scales that loses weights below 2^-35 of the largest, less than l's own
+// rounding.  (M is not rounded up to a whole number: the largest weight, a power of two, is then held exactly, which takes a fifth off
+// the error of rows that few keys make.)  A key whose scale is far below another's may have a small P' and a large weight, though, and values of its own where
 // the other's codes are 0.  So 16 keys whose scale is below 2^-4 of the largest so far, and some of whose P' are below 2^-14 of the row's
 // largest, are held against their own largest: P' times 2^d, and O and l times 2^d before their product and 2^-d after it, d whole
 // (72 at the most: O below 2^50 stays finite).  That costs such keys a second time what they take; without them nothing (a product with
@@ -55,7 +56,7 @@ constexpr int kStages = 6;                          // tiles
 constexpr int kJoined = 4;                          // rows whose shares are joined at a time, a warp each
 // bf16 queries in fp16: log2 of what a row's largest magnitude becomes (or up to twice that).  What is below 2^-39 of it is lost
 constexpr uint32_t kLift = 14;
-constexpr float kHeld = 14.0f;  // log2 of what a row's largest P' is held as, or up to half of it
+constexpr float kHeld = 14.0f;  // log2 of what a row's largest P' is held as
 constexpr float kNear = 4.0f;   // log2 of how far scales of values lie apart and need no more than that
 
 template <int DP>
@@ -285,7 +286,7 @@ __device__ __forceinline__ void scale_rows(float (&o)[COLS][4], float& l0, float
   for (int n = 0; n < COLS; ++n) o[n][0] *= f0, o[n][1] *= f0, o[n][2] *= f1, o[n][3] *= f1;
 }
 
-// By which power of two keys are held apart whose largest t + log2 s_v of this lane is x, in a row whose maximum is m: what brings the
+// By which power of two keys are held apart whose largest t + log2 s_v of this lane is x, in a row whose maximum is m (both less kHeld): what brings the
 // four lanes' largest to M, and at most 2^72, or what l allows (O is below 2^23 a key).
 __device__ __forceinline__ float apart_by(float m, float x, float l) {
 #pragma unroll
@@ -312,7 +313,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
     const uint32_t qs = smem_u32(base + L::q + (it & 1) * L::kQ) + lane * 16;
     const int pos0 = w.pos + dt0, pos1 = w.pos + dt1;
     float o[kCols][4] = {};
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // (O and l are held times 2^kHeld)
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // m: M - kHeld
     float top = -INFINITY;                                       // log2 of the largest scale of values so far
     // The 16 keys that are this warp's: every twelfth of all that the CTA walks over.  (A stage is either always one
     // of those that a warp looks at, or never: 12 times 16 keys are a tile and a half, and there are six stages.)
@@ -365,20 +366,20 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
             if (key0 + 8 * n + c + 4 * (e & 1) > (e < 2 ? pos0 : pos1)) t[n][e] = -INFINITY;
       }
       const float lv = log2_value_scale(vs), iv = ex2(-lv);
-      float a0 = fmaxf(fmaxf(t[0][0], t[0][1]), fmaxf(t[1][0], t[1][1])) + lv;
-      float a1 = fmaxf(fmaxf(t[0][2], t[0][3]), fmaxf(t[1][2], t[1][3])) + lv;
+      float a0 = fmaxf(fmaxf(t[0][0], t[0][1]), fmaxf(t[1][0], t[1][1])) + (lv - kHeld);
+      float a1 = fmaxf(fmaxf(t[0][2], t[0][3]), fmaxf(t[1][2], t[1][3])) + (lv - kHeld);
       // (the lanes that share rows need one M for them only where it moves)
       if (__any_sync(0xffffffffu, a0 > m0 || a1 > m1)) {
         a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 1));
         a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 1));
         a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
         a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
-        const float n0 = ceilf(fmaxf(m0, a0)), n1 = ceilf(fmaxf(m1, a1));  // (whole: log2 s_v - M then loses nothing of t)
+        const float n0 = fmaxf(m0, a0), n1 = fmaxf(m1, a1);
         const float f0 = m0 == -INFINITY ? 0.0f : ex2(m0 - n0), f1 = m1 == -INFINITY ? 0.0f : ex2(m1 - n1);
         m0 = n0, m1 = n1;
         scale_rows(o, l0, l1, f0, f1);
       }
-      float b0 = (lv + kHeld) - (m0 == -INFINITY ? 0.0f : m0), b1 = (lv + kHeld) - (m1 == -INFINITY ? 0.0f : m1);
+      float b0 = lv - (m0 == -INFINITY ? 0.0f : m0), b1 = lv - (m1 == -INFINITY ? 0.0f : m1);
       // Keys whose scale is small, and which lie so far below M that fp16 would lose of them, are held 2^d times as large, and
       // so are O and l until their product is done (exactly: d is whole).
       top = fmaxf(top, lv);
@@ -463,7 +464,7 @@ __device__ __forceinline__ void compute(const Seq8FwdArgs& a, uint8_t* base, Bar
             for (int n = 0; n < kCols; n += 4)
               *reinterpret_cast<float4*>(to + (DP == 128 ? 16 * (c + 4 * x) : 8 * (2 * c + x)) + n) =
                   make_float4(o[n][e + x], o[n + 1][e + x], o[n + 2][e + x], o[n + 3][e + x]);
-          if (c == 0) *reinterpret_cast<float2*>(to + DP) = up ? make_float2(m1 - kHeld, l1) : make_float2(m0 - kHeld, l0);
+          if (c == 0) *reinterpret_cast<float2*>(to + DP) = up ? make_float2(m1, l1) : make_float2(m0, l0);
         };
         if (first < 8)
           put(std::false_type{});

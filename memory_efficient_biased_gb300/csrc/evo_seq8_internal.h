@@ -44,8 +44,8 @@ __device__ __forceinline__ float log2_value_scale(float s) {
   return r;
 }
 
-// ln2 (m + log2 l), for a whole m: l is a sum of weights over the scales of values, so both may be large and cancel.  The whole part of
-// log2 l is added to m exactly (lg2 alone would be 2^-22 of it off).
+// ln2 (m + log2 l): l is a sum of weights over the scales of values, so both may be large and cancel.  The whole part of log2 l
+// is added to m by itself, which loses nothing then (lg2 alone would be 2^-22 of it off).
 __device__ __forceinline__ float whole_log2(float l) {  // 0 for what is no normal number below 2^126
   const uint32_t u = __float_as_uint(l);
   return u - 0x00800000u < 0x7e000000u ? static_cast<float>(static_cast<int>(u >> 23) - 127) : 0.0f;

@@ -1,7 +1,7 @@
 // evo_seq8_tiles.cu — attention over the 8-bit cache (include/evo_seq.h) for many rows a key, on tcgen05.
 //
 // Mathematics, rows, items and roles as in evo_seq_fwd.cu, with scales: S = q·code_k, t = s_k s·log2e·S,
-// P' = 2^(t + log2 r_v - M), M following the maximum of t + log2 r_v, rounded up, l = Σ P' / r_v and O = Σ P' v'; at the end O / l and
+// P' = 2^(t + log2 r_v - M), M following the maximum of t + log2 r_v, l = Σ P' / r_v and O = Σ P' v'; at the end O / l and
 // lse = ln2·(M + log2 l).  Operands are in q's type, which holds every code exactly, and P' is rounded to it, as in the
 // 16-bit forward.  What a value enters with is P' v':
 //   bf16  v' = code and r_v = s_v: bf16 holds P s_v whatever the scales
@@ -504,9 +504,8 @@ __device__ __forceinline__ void softmax(const Seq8FwdArgs& a, Bars* bars, uint32
       float alpha = 1.0f;
       if (mt != -INFINITY && (!have || mt > m + kMoveLog2)) {
         moved = have;
-        const float up = ceilf(mt);  // (whole: log2 r_v - M then loses nothing of t)
-        alpha = have ? ex2(m - up) : 1.0f;
-        m = up;
+        alpha = have ? ex2(m - mt) : 1.0f;
+        m = mt;
         have = true;
       }
       // O so far is complete: this tile's S was issued behind the previous P·V

@@ -108,10 +108,10 @@ def close_bounds(q, k, v, z, p, scale, dtype, few):
     kernel for few rows a key.
 
     P is rounded by u_P: to fp16 (few), to dtype otherwise.  What is below fp16's normal numbers is held in steps of 2^-24:
-      few   the largest P s_v of a row is held as 2^13 to 2^14.  Keys of 16 next to each other share their scale and
+      few   the largest P s_v of a row is held as 2^14.  Keys of 16 next to each other share their scale and
             are held against their own largest weight, as 2^13 to 2^14, where they lie 2^14 or more below the row's largest and their
             scale 2^4 or more below the largest so far; otherwise theirs is 1 or more: half a step is 2^-25 of the 16's largest
-            weight at the most.  Where their scale is not that much smaller it is 2^-25 2^-13 2^4 of the row's largest weight
+            weight at the most.  Where their scale is not that much smaller it is 2^-25 2^-14 2^4 of the row's largest weight
       many  fp16 alone: 2^-25 of the largest weight (the reference is at most the row's maximum)
     times |v| of each key.  With fp16 and many rows values are in steps of 2^-24 too.  bf16 queries lose what is below 2^-39 of their row's largest."""
     es, u = S.score_error(q, k, scale), S.U[dtype]
@@ -129,7 +129,7 @@ def close_bounds(q, k, v, z, p, scale, dtype, few):
             pad = -len(a) % 16
             blocks = np.pad(a, ((0, pad), (0, 0))).reshape(-1, 16, a.shape[1]).sum(1)
             most = np.pad(w, ((0, 0), (0, pad))).reshape(len(w), -1, 16).max(2)
-            bound = bound + 2.0 ** -25 * (most @ blocks) + 2.0 ** -34 * w.max(1)[:, None] * a.sum(0)
+            bound = bound + 2.0 ** -25 * (most @ blocks) + 2.0 ** -35 * w.max(1)[:, None] * a.sum(0)
         elif dtype == torch.float16:
             bound = bound + 2.0 ** -25 * w.max(1)[:, None] * a.sum(0) + 2.0 ** -25
         out[:, h] = bound
